@@ -88,6 +88,7 @@ typedef enum {
 #define MR_MAX_EXPERTS 2304
 #define MR_MAX_TOPK 36
 #define MR_MAX_GROUPS 32
+#define MR_MAX_FEATURES 65536 /* columns of the expert-side operators */
 
 /*
  * router_topk_fwd — score, select and emit the top-K experts of each token.
@@ -398,6 +399,137 @@ MR_API int router_aux_loss_bwd(const float* grad_loss, const int32_t* tokens_per
 MR_API int router_aux_loss_fwd_noalloc(const float* aux_scores, const uint8_t* routing_map, int T,
                                        int E, int K, float coeff, float* loss,
                                        int32_t* tokens_per_expert, mr_stream_t stream);
+
+/*
+ * The expert-side operators: what runs on the rows that router_expert_maps
+ * (or router_topk_fwd_maps) orders by expert.  A layer is
+ *   router_topk_fwd_compact, router_expert_maps    weights, maps
+ *   router_expert_matmul (x by permuted_to_unpermuted), an activation,
+ *   router_expert_matmul (on permuted rows)        the experts
+ *   router_combine_fwd                             the weighted sum
+ * and its gradients run back through router_combine_bwd,
+ * router_expert_matmul_bwd_input / _bwd_weight and, for the tokens' own
+ * gradient, router_combine_fwd without weights (the sum over a token's
+ * copies).
+ *
+ * Shared rules.  P is the number of permuted rows, T K for a full batch;
+ * expert e owns rows [offset[e], offset[e + 1]) of expert_first_token_offset
+ * [E + 1] (device memory, read by the kernels; values outside [0, P] or out of
+ * order are clamped).  Rows of the [P, ...] outputs that no expert owns (at
+ * and behind offset[E]) are left as they were.  Sums are fp32 whatever the
+ * types, with one rounding at the store; repeated calls give the same bits.
+ * Nothing is allocated and no workspace is needed.  A NaN or infinity stays
+ * in the output rows (weight gradient: the experts) whose inputs hold it.
+ * MR_ERR_INVALID: a negative size, E, N, D or K < 1, unknown dtypes, a NULL
+ * tensor that the call reads or writes.  MR_ERR_UNSUPPORTED: E >
+ * MR_MAX_EXPERTS, K > MR_MAX_TOPK, N or D > MR_MAX_FEATURES.
+ */
+
+/*
+ * router_expert_matmul — every expert's weight times its rows:
+ *   out[p, n] = sum_d weight[e, n, d] x[row(p), d],   p owned by e
+ * with row(p) = permuted_to_unpermuted[p] mod T when the map is given (x is
+ * [T, D], read through the map: no permuted copy is needed), else p (x is
+ * [P, D]).  The map's entries for owned rows must not be negative (their
+ * outputs are unspecified, nothing out of range is read).
+ *
+ * x       [T, D] or [P, D] dtype, input
+ * weight  [E, N, D] dtype, input
+ * out     [P, N] out_dtype, output
+ * P = 0 is a no-op.  MR_ERR_INVALID also for a map with T = 0 and P > 0.
+ * fp32 operands are multiplied in fp32 on the vector units.
+ */
+MR_API int router_expert_matmul(const void* x, mr_dtype dtype, const void* weight,
+                                const int32_t* expert_first_token_offset,
+                                const int32_t* permuted_to_unpermuted, int T, int P, int E, int N,
+                                int D, void* out, mr_dtype out_dtype, mr_stream_t stream);
+
+/*
+ * router_expert_matmul_bwd_input — its gradient by the rows:
+ *   grad_x[p, d] = sum_n grad_out[p, n] weight[e, n, d]
+ * on permuted rows: with a forward that read tokens through the map, a
+ * token's gradient is the sum over its K rows (router_combine_fwd without
+ * weights).
+ *
+ * grad_out [P, N] dtype, weight [E, N, D] dtype, grad_x [P, D] out_dtype.
+ */
+MR_API int router_expert_matmul_bwd_input(const void* grad_out, mr_dtype dtype,
+                                          const void* weight,
+                                          const int32_t* expert_first_token_offset, int P, int E,
+                                          int N, int D, void* grad_x, mr_dtype out_dtype,
+                                          mr_stream_t stream);
+
+/*
+ * router_expert_matmul_bwd_weight — its gradient by the weights:
+ *   grad_weight[e, n, d] = sum_{p owned by e} grad_out[p, n] x[row(p), d]
+ * every element is written: an expert without rows gets zeros (also when
+ * P = 0).  x and the map as in router_expert_matmul.
+ *
+ * grad_out [P, N] dtype, grad_weight [E, N, D] out_dtype.
+ */
+MR_API int router_expert_matmul_bwd_weight(const void* grad_out, mr_dtype dtype, const void* x,
+                                           const int32_t* expert_first_token_offset,
+                                           const int32_t* permuted_to_unpermuted, int T, int P,
+                                           int E, int N, int D, void* grad_weight,
+                                           mr_dtype out_dtype, mr_stream_t stream);
+
+/*
+ * router_expert_matmul_w4 — router_expert_matmul on 4-bit weights, for
+ * decoding (bf16 activations; made for a few rows per expert, right for any):
+ *   out[p, n] = sum_g scales[e, n, g] *
+ *               sum_{d in group g} (q[e, n, d] - z[e, n, g]) x[row(p), d]
+ * The integers enter the products exactly and each group's fp32 sum is scaled
+ * in fp32: no weight is rounded.
+ *
+ * x        [T, D] or [P, D] bf16 (map as in router_expert_matmul)
+ * qweight  [E, N, D / 2] bytes: element d in the low half of byte d / 2 when
+ *          d is even, in the high half when odd
+ * scales   [E, N, D / group_size] bf16
+ * zeros    [E, N, D / group_size] bytes, the low four bits count, or NULL: 8
+ * out      [P, N] out_dtype
+ * MR_ERR_INVALID: D % group_size != 0, x or qweight not 16-byte aligned.
+ * MR_ERR_UNSUPPORTED: group_size other than 32, 64 or 128.
+ */
+MR_API int router_expert_matmul_w4(const void* x, const uint8_t* qweight, const void* scales,
+                                   const uint8_t* zeros, int group_size,
+                                   const int32_t* expert_first_token_offset,
+                                   const int32_t* permuted_to_unpermuted, int T, int P, int E,
+                                   int N, int D, void* out, mr_dtype out_dtype,
+                                   mr_stream_t stream);
+
+/*
+ * router_combine_fwd — each token's sum over its K experts' outputs:
+ *   out[t] = sum_k topk_weights[t, k] expert_out[unpermuted_to_permuted[t + k T]]
+ * k ascending, in fp32.  topk_weights NULL: plain sums.  A choice whose map
+ * entry is -1 (router_expert_maps skipped it) or outside [0, T K) adds
+ * nothing; a token without choices gets zeros.
+ *
+ * expert_out   [T K, D] dtype (only the rows the map names are read)
+ * topk_weights [T, ld_weights] float, the first K columns, or NULL
+ * out          [T, D] dtype
+ * MR_ERR_INVALID also for T K > INT_MAX or ld_weights < K with weights.
+ */
+MR_API int router_combine_fwd(const void* expert_out, mr_dtype dtype,
+                              const int32_t* unpermuted_to_permuted, const float* topk_weights,
+                              int ld_weights, int T, int K, int D, void* out, mr_stream_t stream);
+
+/*
+ * router_combine_bwd — its gradients:
+ *   grad_expert_out[p(t, k)] = topk_weights[t, k] grad_out[t]   (1 without weights)
+ *   grad_weights[t, k]       = grad_out[t] . expert_out[p(t, k)]
+ * Rows of grad_expert_out that no choice names are left as they were; the
+ * grad_weights of a skipped choice is 0.  grad_weights may be NULL, and
+ * expert_out is then not read.  A map that names a row twice leaves that row
+ * of grad_expert_out unspecified.
+ *
+ * grad_out [T, D] dtype, grad_expert_out [T K, D] dtype, grad_weights [T, K]
+ * float (dense).  Errors: as router_combine_fwd; grad_weights without
+ * expert_out is MR_ERR_INVALID.
+ */
+MR_API int router_combine_bwd(const void* grad_out, mr_dtype dtype,
+                              const int32_t* unpermuted_to_permuted, const void* expert_out,
+                              const float* topk_weights, int ld_weights, int T, int K, int D,
+                              void* grad_expert_out, float* grad_weights, mr_stream_t stream);
 
 /* Static English text for a status code (never NULL). */
 MR_API const char* moe_router_strerror(int code);

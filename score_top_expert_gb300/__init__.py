@@ -10,6 +10,9 @@ _ROUTER_NAMES = ("router_topk_fwd", "router_topk_fwd_compact", "router_topk_fwd_
                  "router_expert_maps", "router_topk_bwd",
                  "router_aux_scores_fwd", "router_aux_scores_bwd", "router_aux_loss_fwd", "router_aux_loss_fwd_noalloc",
                  "router_aux_loss_bwd",
+                 "router_expert_matmul", "router_expert_matmul_bwd_input",
+                 "router_expert_matmul_bwd_weight", "router_expert_matmul_w4",
+                 "router_combine_fwd", "router_combine_bwd",
                  "force_path", "force_fwd_lanes", "device_status", "selftest_bounded_wait",
                  "RouterError", "lib", "library_path")
 

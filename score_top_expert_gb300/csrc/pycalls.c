@@ -93,6 +93,40 @@ static PyObject* call_aux_scores_bwd(PyObject* self, PyObject* const* args, Py_s
   return PyLong_FromLong(rc);
 }
 
+static PyObject* call_expert_matmul(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t x, w, off, p2u, o, stream;
+  int dt, T, P, E, N, D, odt;
+  void* out[] = {&x, &dt, &w, &off, &p2u, &T, &P, &E, &N, &D, &o, &odt, &stream};
+  if (convert(args, nargs, "pipppiiiiipip", out) != 0) return NULL;
+  const int rc = router_expert_matmul((const void*)x, (mr_dtype)dt, (const void*)w,
+                                      (const int32_t*)off, (const int32_t*)p2u, T, P, E, N, D,
+                                      (void*)o, (mr_dtype)odt, (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
+static PyObject* call_expert_matmul_w4(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t x, q, sc, z, off, p2u, o, stream;
+  int group, T, P, E, N, D, odt;
+  void* out[] = {&x, &q, &sc, &z, &group, &off, &p2u, &T, &P, &E, &N, &D, &o, &odt, &stream};
+  if (convert(args, nargs, "ppppippiiiiipip", out) != 0) return NULL;
+  const int rc = router_expert_matmul_w4(
+      (const void*)x, (const uint8_t*)q, (const void*)sc, (const uint8_t*)z, group,
+      (const int32_t*)off, (const int32_t*)p2u, T, P, E, N, D, (void*)o, (mr_dtype)odt,
+      (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
+static PyObject* call_combine_fwd(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t z, u2p, w, o, stream;
+  int dt, ld, T, K, D;
+  void* out[] = {&z, &dt, &u2p, &w, &ld, &T, &K, &D, &o, &stream};
+  if (convert(args, nargs, "pippiiiipp", out) != 0) return NULL;
+  const int rc =
+      router_combine_fwd((const void*)z, (mr_dtype)dt, (const int32_t*)u2p, (const float*)w, ld,
+                         T, K, D, (void*)o, (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
 static PyMethodDef kMethods[] = {
     {"router_topk_fwd", (PyCFunction)(void (*)(void))call_topk_fwd, METH_FASTCALL,
      "router_topk_fwd(logits, dtype, T, E, K, score_func, num_groups, group_topk, "
@@ -105,6 +139,16 @@ static PyMethodDef kMethods[] = {
      "intermediate, stream) -> status"},
     {"router_aux_scores_bwd", (PyCFunction)(void (*)(void))call_aux_scores_bwd, METH_FASTCALL,
      "router_aux_scores_bwd(grad_scores, saved, dtype, T, E, K, score_func, grad_logits, "
+     "stream) -> status"},
+    {"router_expert_matmul", (PyCFunction)(void (*)(void))call_expert_matmul, METH_FASTCALL,
+     "router_expert_matmul(x, dtype, weight, offsets, p2u, T, P, E, N, D, out, out_dtype, "
+     "stream) -> status"},
+    {"router_expert_matmul_w4", (PyCFunction)(void (*)(void))call_expert_matmul_w4,
+     METH_FASTCALL,
+     "router_expert_matmul_w4(x, qweight, scales, zeros, group_size, offsets, p2u, T, P, E, N, "
+     "D, out, out_dtype, stream) -> status"},
+    {"router_combine_fwd", (PyCFunction)(void (*)(void))call_combine_fwd, METH_FASTCALL,
+     "router_combine_fwd(expert_out, dtype, u2p, topk_weights, ld_weights, T, K, D, out, "
      "stream) -> status"},
     {NULL, NULL, 0, NULL}};
 

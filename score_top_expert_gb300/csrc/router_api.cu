@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "moe_router.h"
+#include "router_experts.cuh"
 #include "router_launch.cuh"
 
 using namespace moe_router;
@@ -91,6 +92,11 @@ bool device_info(DeviceInfo* out) {
 int* moe_router::device_status_word() {
   DeviceInfo di{};
   return device_info(&di) ? di.status : nullptr;
+}
+
+int moe_router::device_sm_count() {
+  DeviceInfo di{};
+  return device_info(&di) ? di.sms : 0;
 }
 
 namespace {

@@ -81,6 +81,16 @@ def lib() -> ctypes.CDLL:
         L.router_aux_loss_fwd_noalloc.restype = ctypes.c_int
         L.router_aux_loss_bwd.argtypes = [vp, vp, i, i, i, f, vp, vp]
         L.router_aux_loss_bwd.restype = ctypes.c_int
+        L.router_expert_matmul.argtypes = [vp, i, vp, vp, vp, i, i, i, i, i, vp, i, vp]
+        L.router_expert_matmul_bwd_input.argtypes = [vp, i, vp, vp, i, i, i, i, vp, i, vp]
+        L.router_expert_matmul_bwd_weight.argtypes = [vp, i, vp, vp, vp, i, i, i, i, i, vp, i, vp]
+        L.router_expert_matmul_w4.argtypes = [vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, vp, i, vp]
+        L.router_combine_fwd.argtypes = [vp, i, vp, vp, i, i, i, i, vp, vp]
+        L.router_combine_bwd.argtypes = [vp, i, vp, vp, vp, i, i, i, i, vp, vp, vp]
+        for fn in ("router_expert_matmul", "router_expert_matmul_bwd_input",
+                   "router_expert_matmul_bwd_weight", "router_expert_matmul_w4",
+                   "router_combine_fwd", "router_combine_bwd"):
+            getattr(L, fn).restype = ctypes.c_int
         L.moe_router_selftest_bounded_wait.restype = ctypes.c_int
         L.moe_router_strerror.argtypes = [i]
         L.moe_router_strerror.restype = ctypes.c_char_p
@@ -98,6 +108,9 @@ class _CtypesCalls:
         self.router_topk_bwd = L.router_topk_bwd
         self.router_aux_scores_fwd = L.router_aux_scores_fwd
         self.router_aux_scores_bwd = L.router_aux_scores_bwd
+        self.router_expert_matmul = L.router_expert_matmul
+        self.router_expert_matmul_w4 = L.router_expert_matmul_w4
+        self.router_combine_fwd = L.router_combine_fwd
 
 
 def _load_fast():
@@ -550,3 +563,228 @@ def router_aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor
                                        float(coeff), _ptr(grad_aux_scores), _stream(dev))
     _check("router_aux_loss_bwd", rc)
     return grad_aux_scores
+
+
+# ---- the experts' products and the combination ------------------------------
+def _same_device(t: torch.Tensor, name: str, index: int, dtypes, dim: int) -> torch.Tensor:
+    """``t`` checked (device, dtype, number of dimensions)."""
+    if t.get_device() != index or t.dtype not in dtypes or t.dim() != dim:
+        raise ValueError(f"{name} must be a {dim}-dimensional tensor of {dtypes} on cuda:{index}")
+    return t
+
+
+def _map_input(t: torch.Tensor, name: str, index: int, numel: int | None = None) -> torch.Tensor:
+    if t.get_device() != index or t.dtype != torch.int32 or t.dim() != 1 \
+            or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{name} must be a 1-dimensional int32 tensor"
+                         f"{'' if numel is None else f' of {numel} elements'} on cuda:{index}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _weight_input(t: torch.Tensor, name: str, index: int, dtypes) -> torch.Tensor:
+    _same_device(t, name, index, dtypes, 3)
+    if not t.is_contiguous():  # a copy at each call would cost more than the product
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _expert_rows(x, weight_dim, offsets, p2u, E):
+    """Checked (x, offsets, p2u) of a product; and T, P."""
+    dev = x.get_device()
+    offsets = _map_input(offsets, "expert_first_token_offset", dev, E + 1)
+    if x.shape[1] != weight_dim:
+        raise ValueError(f"x must have {weight_dim} columns")
+    if p2u is None:
+        return x, offsets, None, 0, x.shape[0]
+    p2u = _map_input(p2u, "permuted_to_unpermuted", dev)
+    return x, offsets, p2u, x.shape[0], p2u.numel()
+
+
+def router_expert_matmul(x: torch.Tensor, weight: torch.Tensor,
+                         expert_first_token_offset: torch.Tensor,
+                         permuted_to_unpermuted: torch.Tensor | None = None, *, out=None,
+                         out_dtype: torch.dtype | None = None):
+    """Product of each expert's weight [E, N, D] with its rows.  Returns out
+    [P, N] in ``out_dtype`` (default: x's): out[p] = weight[e] x[row(p)] for the
+    permuted rows p of expert e.  With ``permuted_to_unpermuted`` (from
+    router_expert_maps) x is the tokens [T, D], read through the map; without
+    it x is the permuted rows [P, D].  Rows that no expert owns are left as
+    they were in ``out``."""
+    x = _as_input(x, "x", _DTYPE)
+    dev = x.device
+    weight = _weight_input(weight, "weight", dev.index, (x.dtype,))
+    E, N, D = weight.shape
+    x, offsets, p2u, T, P = _expert_rows(x, D, expert_first_token_offset,
+                                         permuted_to_unpermuted, E)
+    odt = x.dtype if out_dtype is None else out_dtype
+    if odt not in _DTYPE:
+        raise ValueError(f"out_dtype must be one of {list(_DTYPE)}")
+    out = _out(out, (P, N), odt, dev, "out")
+    with _on(dev):
+        rc = _calls().router_expert_matmul(x.data_ptr(), _DTYPE[x.dtype], weight.data_ptr(),
+                                           offsets.data_ptr(), _ptr0(p2u), T, P, E, N, D,
+                                           out.data_ptr(), _DTYPE[odt], _stream(dev))
+    _check("router_expert_matmul", rc)
+    return out
+
+
+def router_expert_matmul_bwd_input(grad_out: torch.Tensor, weight: torch.Tensor,
+                                   expert_first_token_offset: torch.Tensor, *, grad_x=None,
+                                   out_dtype: torch.dtype | None = None):
+    """Gradient of router_expert_matmul by its rows: grad_x [P, D] on permuted
+    rows (``out_dtype``, default grad_out's).  For tokens read through the map,
+    router_combine_fwd without weights sums a token's rows."""
+    grad_out = _as_input(grad_out, "grad_out", _DTYPE)
+    dev = grad_out.device
+    weight = _weight_input(weight, "weight", dev.index, (grad_out.dtype,))
+    E, N, D = weight.shape
+    offsets = _map_input(expert_first_token_offset, "expert_first_token_offset", dev.index, E + 1)
+    if grad_out.shape[1] != N:
+        raise ValueError(f"grad_out must have {N} columns")
+    P = grad_out.shape[0]
+    odt = grad_out.dtype if out_dtype is None else out_dtype
+    if odt not in _DTYPE:
+        raise ValueError(f"out_dtype must be one of {list(_DTYPE)}")
+    grad_x = _out(grad_x, (P, D), odt, dev, "grad_x")
+    with _on(dev):
+        rc = lib().router_expert_matmul_bwd_input(
+            _ptr(grad_out), _DTYPE[grad_out.dtype], _ptr(weight), _ptr(offsets), P, E, N, D,
+            _ptr(grad_x), _DTYPE[odt], _stream(dev))
+    _check("router_expert_matmul_bwd_input", rc)
+    return grad_x
+
+
+def router_expert_matmul_bwd_weight(grad_out: torch.Tensor, x: torch.Tensor,
+                                    expert_first_token_offset: torch.Tensor,
+                                    permuted_to_unpermuted: torch.Tensor | None = None, *,
+                                    grad_weight=None, out_dtype: torch.dtype | None = None):
+    """Gradient of router_expert_matmul by its weights: grad_weight [E, N, D] in
+    ``out_dtype`` (default: x's); experts without rows get zeros.  x and the
+    map as in the forward."""
+    grad_out = _as_input(grad_out, "grad_out", _DTYPE)
+    x = _as_input(x, "x", (grad_out.dtype,))
+    dev = grad_out.device
+    if x.get_device() != dev.index:
+        raise ValueError("x must be on grad_out's device")
+    E = expert_first_token_offset.numel() - 1
+    N, D = grad_out.shape[1], x.shape[1]
+    x, offsets, p2u, T, P = _expert_rows(x, D, expert_first_token_offset,
+                                         permuted_to_unpermuted, E)
+    if grad_out.shape[0] != P:
+        raise ValueError(f"grad_out must have {P} rows")
+    odt = x.dtype if out_dtype is None else out_dtype
+    if odt not in _DTYPE:
+        raise ValueError(f"out_dtype must be one of {list(_DTYPE)}")
+    grad_weight = _out(grad_weight, (E, N, D), odt, dev, "grad_weight")
+    with _on(dev):
+        rc = lib().router_expert_matmul_bwd_weight(
+            _ptr(grad_out), _DTYPE[x.dtype], _ptr(x), _ptr(offsets), _ptr(p2u), T, P, E, N, D,
+            _ptr(grad_weight), _DTYPE[odt], _stream(dev))
+    _check("router_expert_matmul_bwd_weight", rc)
+    return grad_weight
+
+
+def router_expert_matmul_w4(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Tensor,
+                            expert_first_token_offset: torch.Tensor,
+                            permuted_to_unpermuted: torch.Tensor | None = None, *,
+                            zeros: torch.Tensor | None = None, out=None,
+                            out_dtype: torch.dtype | None = None):
+    """router_expert_matmul on 4-bit weights (decode batches).  x bf16; qweight
+    [E, N, D / 2] uint8, two elements a byte, the even one in the low half;
+    scales [E, N, D / group] bf16, zeros the same in uint8 (0..15) or None for
+    8; group 32, 64 or 128.  Returns out [P, N] in ``out_dtype`` (default
+    bf16)."""
+    x = _as_input(x, "x", (torch.bfloat16,))
+    dev = x.device
+    qweight = _weight_input(qweight, "qweight", dev.index, (torch.uint8,))
+    scales = _weight_input(scales, "scales", dev.index, (torch.bfloat16,))
+    E, N, half = qweight.shape
+    D, groups = 2 * half, scales.shape[2]
+    if scales.shape[:2] != (E, N) or groups < 1 or D % groups != 0:
+        raise ValueError("scales must be [E, N, D / group]")
+    if zeros is not None:
+        zeros = _weight_input(zeros, "zeros", dev.index, (torch.uint8,))
+        if zeros.shape != scales.shape:
+            raise ValueError("zeros must have the shape of scales")
+    x, offsets, p2u, T, P = _expert_rows(x, D, expert_first_token_offset,
+                                         permuted_to_unpermuted, E)
+    if x.data_ptr() & 15:
+        x = x.clone()
+    odt = torch.bfloat16 if out_dtype is None else out_dtype
+    if odt not in _DTYPE:
+        raise ValueError(f"out_dtype must be one of {list(_DTYPE)}")
+    out = _out(out, (P, N), odt, dev, "out")
+    with _on(dev):
+        rc = _calls().router_expert_matmul_w4(
+            x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), _ptr0(zeros), D // groups,
+            offsets.data_ptr(), _ptr0(p2u), T, P, E, N, D, out.data_ptr(), _DTYPE[odt],
+            _stream(dev))
+    _check("router_expert_matmul_w4", rc)
+    return out
+
+
+def _combine_weights(topk_weights, T, K, dev):
+    """Checked weights and their row stride (a column view of a wider buffer is read in place)."""
+    if topk_weights is None:
+        return None, 0
+    if topk_weights.dtype != torch.float32 or topk_weights.shape != (T, K) \
+            or topk_weights.get_device() != dev:
+        raise ValueError(f"topk_weights must be a float32 [{T}, {K}] tensor on cuda:{dev}")
+    if T == 0:
+        return topk_weights, K
+    if topk_weights.stride(1) != 1 or topk_weights.stride(0) < K:
+        topk_weights = topk_weights.contiguous()
+    return topk_weights, (topk_weights.stride(0) if T > 1 else K)
+
+
+def router_combine_fwd(expert_out: torch.Tensor, unpermuted_to_permuted: torch.Tensor, K: int,
+                       topk_weights: torch.Tensor | None = None, *, out=None):
+    """Each token's sum of its K experts' outputs, weighted by ``topk_weights``
+    [T, K] (None: plain sums).  expert_out [T K, D] in the maps' order; the map
+    is router_expert_maps's.  Returns out [T, D] in expert_out's dtype; a choice
+    with map entry -1 adds nothing."""
+    expert_out = _as_input(expert_out, "expert_out", _DTYPE)
+    dev = expert_out.device
+    K = int(K)
+    P, D = expert_out.shape
+    u2p = _map_input(unpermuted_to_permuted, "unpermuted_to_permuted", dev.index, P)
+    if K < 1 or P % K != 0:
+        raise ValueError("expert_out must have T K rows")
+    T = P // K
+    weights, ld = _combine_weights(topk_weights, T, K, dev.index)
+    out = _out(out, (T, D), expert_out.dtype, dev, "out")
+    with _on(dev):
+        rc = _calls().router_combine_fwd(expert_out.data_ptr(), _DTYPE[expert_out.dtype],
+                                         u2p.data_ptr(), _ptr0(weights), ld, T, K, D,
+                                         out.data_ptr(), _stream(dev))
+    _check("router_combine_fwd", rc)
+    return out
+
+
+def router_combine_bwd(grad_out: torch.Tensor, unpermuted_to_permuted: torch.Tensor, K: int,
+                       expert_out: torch.Tensor | None = None,
+                       topk_weights: torch.Tensor | None = None, *, grad_expert_out=None,
+                       grad_weights=None):
+    """Gradients of router_combine_fwd: (grad_expert_out [T K, D] in grad_out's
+    dtype, grad_weights [T, K] float32, or None when ``expert_out`` is None).
+    Rows of grad_expert_out that no choice names are left as they were."""
+    grad_out = _as_input(grad_out, "grad_out", _DTYPE)
+    dev = grad_out.device
+    K = int(K)
+    T, D = grad_out.shape
+    u2p = _map_input(unpermuted_to_permuted, "unpermuted_to_permuted", dev.index, T * K)
+    weights, ld = _combine_weights(topk_weights, T, K, dev.index)
+    if expert_out is not None:
+        expert_out = _as_input(expert_out, "expert_out", (grad_out.dtype,))
+        if expert_out.shape != (T * K, D) or expert_out.get_device() != dev.index:
+            raise ValueError(f"expert_out must be [{T * K}, {D}] on grad_out's device")
+        grad_weights = _out(grad_weights, (T, K), torch.float32, dev, "grad_weights")
+    elif grad_weights is not None:
+        raise ValueError("grad_weights needs expert_out")
+    grad_expert_out = _out(grad_expert_out, (T * K, D), grad_out.dtype, dev, "grad_expert_out")
+    with _on(dev):
+        rc = lib().router_combine_bwd(_ptr(grad_out), _DTYPE[grad_out.dtype], _ptr(u2p),
+                                      _ptr(expert_out), _ptr(weights), ld, T, K, D,
+                                      _ptr(grad_expert_out), _ptr(grad_weights), _stream(dev))
+    _check("router_combine_bwd", rc)
+    return grad_expert_out, grad_weights

@@ -21,7 +21,9 @@ int check_product(int T, int P, int E, int N, int D, bool mapped) {
 }
 
 int run_product(int form, const ExpertArgs& a, mr_stream_t stream) {
-  return launch_expert_matmul_vector(form, a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return expert_matmul_tc_ok(form, a) ? launch_expert_matmul_tc(form, a, st)
+                                      : launch_expert_matmul_vector(form, a, st);
 }
 
 }  // namespace

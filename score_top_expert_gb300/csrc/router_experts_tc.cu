@@ -1,0 +1,501 @@
+// Products grouped by expert on the tensor cores (bf16 operands, fp32 sums).
+//
+// The ragged dimension is the number of an expert's rows.  The tensor cores
+// take 128 or 256 values of one dimension at a time and any multiple of 16 of
+// the other, so the expert's weight rows (forward) or columns (input gradient)
+// go to the first and its ragged rows to the second: out^T = W x^T.  An expert
+// with n rows takes ceil(n / most) near-equal tiles, each rounded up to 16 (32
+// for a pair of CTAs), and one with two rows costs a product of 16.
+//
+//   forward       A = W[e] rows n, K-major (d);       B = x rows p, K-major (d)
+//   input grad    A = W[e] columns d, MN-major (n);   B = grad_out rows p, K-major (n)
+//   weight grad   A = grad_out columns n, MN-major;   B = x columns d, MN-major; both
+//                 over the expert's rows p, in slices of 64 from its first one
+//
+// Rows are brought in by gathering copies of four rows, each with its own
+// row index: a token's row through the expert map, and for indices behind the
+// expert's last row one past the tensor, which reads as zero.  So no row of
+// another expert enters a product, and the weight gradient's last slice needs
+// no mask.
+//
+// Block: 8 warps.  Warp 0 loads (6 stages of 64 contraction indices, 16 KB of
+// A and up to 16 KB of B each), one thread of warp 1 issues the products,
+// warp 2 owns the tensor memory, warps 4-7 store finished tiles while the next
+// one is computed into the other half of the accumulator columns.  CG = 2: two
+// CTAs share a tile of 256 x (up to 256), each holding half of A and of B, which
+// halves the shared-memory and L2 traffic per product.  The grid is
+// persistent; tile i goes to CTA (pair) i mod the grid.
+#include <atomic>
+
+#include "router_common.cuh"
+#include "router_experts.cuh"
+#include "router_tcgen.cuh"
+
+namespace moe_router {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kStages = 6;
+constexpr int kDeep = 64;                 // contraction indices per stage: 128 bytes
+constexpr int kRowsA = 128;               // values of A's dimension per CTA
+constexpr int kRowsB = 128;               // most values of B's dimension per CTA
+constexpr int kBytesA = kRowsA * 128;
+constexpr int kBytesB = kRowsB * 128;
+constexpr int kStageBytes = kBytesA + kBytesB;
+constexpr int kSmemBytes = kStages * kStageBytes + 1024;  // stages start on 1024 bytes
+
+struct TcArgs {
+  const int32_t* offsets;
+  const int32_t* p2u;
+  void* out;
+  int* status;
+  int T, P, E, N, D;
+  int x_rows;  // rows of the gathered x
+  int out_f32;
+};
+
+struct Tile {
+  int e;
+  int start, cnt;  // ragged rows (weight grad: the expert's)
+  int a0, b0;      // first value of A's dimension; weight grad: of B's
+};
+
+template <int FORM, int CG>
+struct Shape {
+  static constexpr int kTileA = kRowsA * CG;
+  static constexpr int kTileB = kRowsB * CG;
+  static constexpr int kRound = 16 * CG;
+  static constexpr uint32_t kColumns = 2 * kTileB;  // two accumulators
+};
+
+template <int FORM, int CG>
+__device__ __forceinline__ Tile find_tile(const TcArgs& g, const int* prefix, int tile) {
+  using S = Shape<FORM, CG>;
+  Tile t;
+  if constexpr (FORM == EX_WGRAD) {
+    const int ta = (g.N + S::kTileA - 1) / S::kTileA, tb = (g.D + S::kTileB - 1) / S::kTileB;
+    t.e = tile / (ta * tb);
+    const int r = tile - t.e * ta * tb;
+    t.a0 = r / tb * S::kTileA;
+    t.b0 = r % tb * S::kTileB;
+    int hi;
+    expert_rows(g.offsets, t.e, g.P, &t.start, &hi);
+    t.cnt = hi - t.start;
+  } else {
+    const int ta = ((FORM == EX_FWD ? g.N : g.D) + S::kTileA - 1) / S::kTileA;
+    t.e = expert_of_tile(prefix, g.E, tile / ta);
+    const int first = prefix[t.e], tiles = prefix[t.e + 1] - first;
+    const int r = tile - first * ta;
+    const int a = r / tiles;  // one slice of the weight, all row tiles, then the next
+    int lo, hi;
+    expert_rows(g.offsets, t.e, g.P, &lo, &hi);
+    const int each = ((hi - lo + tiles - 1) / tiles + S::kRound - 1) / S::kRound * S::kRound;
+    t.a0 = a * S::kTileA;
+    t.start = lo + (r - a * tiles) * each;
+    t.cnt = min(each, hi - t.start);
+    t.b0 = 0;
+  }
+  return t;
+}
+
+// Waits that give up set the CTA's flag and the device's status word.
+struct Waiter {
+  int* gave_up;
+  int* status;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    if (mbar_wait_bounded(bar, parity)) return true;
+    *reinterpret_cast<volatile int*>(gave_up) = 1;
+    atomicExch(status, kDeviceWaitTimeout);
+    return false;
+  }
+};
+
+template <int FORM, int CG>
+__global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
+    const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+    const TcArgs g) {
+  using S = Shape<FORM, CG>;
+  extern __shared__ uint8_t dynamic_smem[];
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done[2], drained[2];
+  __shared__ uint32_t tmem_at;
+  __shared__ int gave_up;
+  __shared__ int tmp[33];
+  __shared__ int prefix[FORM == EX_WGRAD ? 1 : MR_MAX_EXPERTS + 1];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const uint32_t stages_at = (smem_addr(dynamic_smem) + 1023u) & ~1023u;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&done[i], 1);
+      mbar_init(&drained[i], 4 * CG);  // one arrival per storing warp
+    }
+    gave_up = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc<CG>(&tmem_at, S::kColumns);
+  pdl_enter();
+  int tiles;
+  if constexpr (FORM == EX_WGRAD) {
+    tiles = g.E * ((g.N + S::kTileA - 1) / S::kTileA) * ((g.D + S::kTileB - 1) / S::kTileB);
+  } else {
+    tiles = expert_tile_prefix(g.offsets, g.E, g.P, S::kTileB, prefix, tmp) *
+            (((FORM == EX_FWD ? g.N : g.D) + S::kTileA - 1) / S::kTileA);
+  }
+  tc_fence_before();
+  if constexpr (CG == 2) cluster_sync(); else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  const Waiter wait{&gave_up, g.status};
+  const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
+  // contraction slices of a tile
+  const int fixed_slices = ((FORM == EX_FWD ? g.D : g.N) + kDeep - 1) / kDeep;
+
+  if (warp == 0) {
+    // ---- loads -----------------------------------------------------------------
+    int stage = 0;
+    uint32_t parity = 1;  // the first pass finds the stages empty
+    bool ok = true;
+    for (int i = first; i < tiles && ok; i += step) {
+      const Tile t = find_tile<FORM, CG>(g, prefix, i);
+      const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
+      // this CTA's rows of B: 4 per lane
+      const int rows = FORM == EX_WGRAD
+                           ? kRowsB
+                           : (t.cnt + S::kRound - 1) / S::kRound * S::kRound / CG;
+      int r[4];
+      if constexpr (FORM != EX_WGRAD) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int b = static_cast<int>(rank) * rows + 4 * lane + j;
+          r[j] = (4 * lane < rows && b < t.cnt) ? source_row(g.p2u, g.T, t.start + b) : g.x_rows;
+          if (r[j] < 0) r[j] = g.x_rows;
+        }
+      }
+      for (int s = 0; s < slices; ++s) {
+        // weight grad: lanes 0-15 load the first 64 columns, 16-31 the next; 4 rows each
+        int p[4];
+        if constexpr (FORM == EX_WGRAD) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int b = s * kDeep + 4 * (lane & 15) + j;
+            p[j] = b < t.cnt ? t.start + b : g.P;
+            r[j] = b < t.cnt ? source_row(g.p2u, g.T, t.start + b) : g.x_rows;
+            if (r[j] < 0) {
+              r[j] = g.x_rows;
+              p[j] = g.P;
+            }
+          }
+        }
+        ok = __all_sync(0xffffffffu, wait(&empty[stage], parity));
+        if (!ok) break;
+        const uint32_t at = stages_at + stage * kStageBytes;
+        const uint32_t bar =
+            CG == 2 ? map_to_rank(smem_addr(&full[stage]), 0) : smem_addr(&full[stage]);
+        if (lane == 0 && rank == 0) mbar_expect_tx(&full[stage], CG * (kBytesA + rows * 128));
+        __syncwarp();
+        const int a0 = t.a0 + static_cast<int>(rank) * kRowsA;
+        if constexpr (FORM == EX_FWD) {
+          if (lane == 0) tma_load_3d<CG>(at, &map_a, s * kDeep, a0, t.e, bar);
+        } else if constexpr (FORM == EX_DGRAD) {
+          if (lane < 2)
+            tma_load_3d<CG>(at + lane * 8192, &map_a, a0 + 64 * lane, s * kDeep, t.e, bar);
+        } else {
+          tma_gather4<CG>(at + lane * 512, &map_a, a0 + 64 * (lane >> 4), p[0], p[1], p[2], p[3],
+                          bar);
+        }
+        if constexpr (FORM == EX_WGRAD) {
+          tma_gather4<CG>(at + kBytesA + lane * 512, &map_b,
+                          t.b0 + static_cast<int>(rank) * kRowsB + 64 * (lane >> 4), r[0], r[1],
+                          r[2], r[3], bar);
+        } else {
+          if (4 * lane < rows)
+            tma_gather4<CG>(at + kBytesA + lane * 512, &map_b, s * kDeep, r[0], r[1], r[2], r[3],
+                            bar);
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---- products ----------------------------------------------------------------
+    int stage = 0, n = 0;  // n: tiles computed
+    uint32_t parity = 0;
+    bool ok = true;
+    for (int i = first; i < tiles && ok; i += step) {
+      const Tile t = find_tile<FORM, CG>(g, prefix, i);
+      const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
+      if (slices == 0) continue;
+      const int cols = FORM == EX_WGRAD ? S::kTileB
+                                        : (t.cnt + S::kRound - 1) / S::kRound * S::kRound;
+      const uint32_t desc =
+          product_desc(S::kTileA, cols, FORM != EX_FWD, FORM == EX_WGRAD);
+      const int buf = n & 1;
+      ok = wait(&drained[buf], ((n >> 1) & 1) ^ 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * S::kTileB;
+      for (int s = 0; s < slices; ++s) {
+        ok = wait(&full[stage], parity);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = stages_at + stage * kStageBytes;
+        // 16 contraction indices are 32 bytes of a K-major row, 16 rows of an
+        // MN-major slice
+        const uint64_t da = FORM == EX_FWD ? operand_desc(at, 0, 1024)
+                                           : operand_desc(at, 8192, 1024);
+        const uint64_t db = FORM == EX_WGRAD ? operand_desc(at + kBytesA, 8192, 1024)
+                                             : operand_desc(at + kBytesA, 0, 1024);
+        constexpr uint64_t ka = FORM == EX_FWD ? 2 : 128, kb = FORM == EX_WGRAD ? 128 : 2;
+#pragma unroll
+        for (int k = 0; k < kDeep / 16; ++k)
+          tc_product<CG>(d, da + k * ka, db + k * kb, desc, s > 0 || k > 0);
+        tc_commit<CG>(&empty[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
+        }
+      }
+      if (ok) tc_commit<CG>(&done[buf]);
+      ++n;
+    }
+  } else if (warp >= 4) {
+    // ---- stores --------------------------------------------------------------------
+    const int quad = warp - 4;
+    int n = 0;
+    bool ok = true;
+    for (int i = first; i < tiles && ok; i += step) {
+      const Tile t = find_tile<FORM, CG>(g, prefix, i);
+      const bool none = FORM == EX_WGRAD && t.cnt == 0;  // an expert without rows: zeros
+      const int buf = n & 1;
+      if (!none) {
+        ok = __all_sync(0xffffffffu, wait(&done[buf], (n >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const int row = t.a0 + static_cast<int>(rank) * kRowsA + quad * 32 + lane;  // of A's dimension
+      const int cols = FORM == EX_WGRAD ? min(S::kTileB, g.D - t.b0) : t.cnt;
+      const int rows = FORM == EX_DGRAD ? g.D : g.N;
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t v[32];
+        if (!none) {
+          tmem_load_32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * S::kTileB + c, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0u;
+        }
+        if (row < rows) {
+          if constexpr (FORM == EX_WGRAD) {
+            // a thread holds 32 neighbours of one output row
+            const size_t o = (static_cast<size_t>(t.e) * g.N + row) * g.D + t.b0 + c;
+            if (g.out_f32) {
+              float* out = static_cast<float*>(g.out) + o;
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                if (c + j < cols)
+                  __stcs(reinterpret_cast<uint4*>(out + j),
+                         make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+            } else {
+              unsigned short* out = static_cast<unsigned short*>(g.out) + o;
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  w[u] = f32_to_bf16_bits(__uint_as_float(v[j + 2 * u])) |
+                         (f32_to_bf16_bits(__uint_as_float(v[j + 2 * u + 1])) << 16);
+                if (c + j < cols)
+                  __stcs(reinterpret_cast<uint4*>(out + j), make_uint4(w[0], w[1], w[2], w[3]));
+              }
+            }
+          } else {
+            // a warp holds 32 neighbours of 32 output rows
+            const size_t o = static_cast<size_t>(t.start + c) * rows + row;
+            if (g.out_f32) {
+              float* out = static_cast<float*>(g.out) + o;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (c + j < cols) out[static_cast<size_t>(j) * rows] = __uint_as_float(v[j]);
+            } else {
+              unsigned short* out = static_cast<unsigned short*>(g.out) + o;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (c + j < cols)
+                  out[static_cast<size_t>(j) * rows] =
+                      static_cast<unsigned short>(f32_to_bf16_bits(__uint_as_float(v[j])));
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (!none) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+          mbar_arrive_cluster(CG == 2 ? map_to_rank(smem_addr(&drained[buf]), 0)
+                                      : smem_addr(&drained[buf]));
+        ++n;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  // After a wait that gave up: leave copies and products in flight another
+  // millisecond before the shared and tensor memory is given back.
+  if (*reinterpret_cast<volatile int*>(&gave_up))
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  if constexpr (CG == 2) cluster_sync(); else __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc<CG>(tmem, S::kColumns);
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up through the runtime.
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiled>(nullptr);
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// bf16 tensor of `rank` dimensions, innermost first, dense; 64-column boxes,
+// 128-byte swizzle, zeros outside.
+bool make_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+              const cuuint32_t* box) {
+  const EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
+  cuuint64_t strides[2];
+  strides[0] = dims[0] * 2;
+  if (rank == 3) strides[1] = strides[0] * dims[1];
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank),
+            const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool rows_map(CUtensorMap* map, const void* base, int rows, int cols) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint32_t box[2] = {64, 1};
+  return make_map(map, base, 2, dims, box);
+}
+
+bool weight_map(CUtensorMap* map, const void* base, const ExpertArgs& a, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.N),
+                              static_cast<cuuint64_t>(a.E)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  return make_map(map, base, 3, dims, box);
+}
+
+// Clusters of the kernel that run at once, asked once per device and kernel.
+constexpr int kDevices = 64;
+template <typename Kern>
+int resident_clusters(Kern kern, int cg, std::atomic<int>* known) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) !=
+      cudaSuccess)
+    return 0;
+  n = device_sm_count();
+  if (cg == 2) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  }
+  if (n > 0) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int FORM, int CG>
+int launch_typed(const ExpertArgs& a, cudaStream_t st) {
+  using S = Shape<FORM, CG>;
+  static std::atomic<int> known[kDevices];
+  const auto kern = expert_matmul_tc_kernel<FORM, CG>;
+  const int resident = resident_clusters(kern, CG, known);
+  TcArgs g{a.offsets, a.p2u, a.out, device_status_word(), a.T, a.P, a.E, a.N, a.D,
+           FORM == EX_DGRAD || a.p2u == nullptr ? a.P : a.T, a.out_dtype == DT_F32};
+  if (resident <= 0 || g.status == nullptr) return MR_ERR_CUDA;
+  CUtensorMap ma, mb;
+  const bool maps =
+      FORM == EX_FWD
+          ? weight_map(&ma, a.b, a, kRowsA) && rows_map(&mb, a.a, g.x_rows, a.D)
+          : FORM == EX_DGRAD
+                ? weight_map(&ma, a.b, a, kDeep) && rows_map(&mb, a.a, a.P, a.N)
+                : rows_map(&ma, a.a, a.P, a.N) && rows_map(&mb, a.b, g.x_rows, a.D);
+  if (!maps) return MR_ERR_CUDA;
+  const long long ta = ((FORM == EX_DGRAD ? a.D : a.N) + S::kTileA - 1) / S::kTileA;
+  const long long tb = FORM == EX_WGRAD
+                           ? static_cast<long long>(a.E) * ((a.D + S::kTileB - 1) / S::kTileB)
+                           : static_cast<long long>(a.E < a.P ? a.E : a.P) + a.P / S::kTileB;
+  const long long clusters = ta * tb < resident ? ta * tb : resident;
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, g) == cudaSuccess ? MR_OK : MR_ERR_CUDA;
+}
+
+template <int FORM>
+int launch_form(const ExpertArgs& a, cudaStream_t st) {
+  const bool pair = FORM == EX_WGRAD ? a.N > kRowsA : a.P >= 48ll * a.E;
+  return pair ? launch_typed<FORM, 2>(a, st) : launch_typed<FORM, 1>(a, st);
+}
+
+}  // namespace
+
+bool expert_matmul_tc_ok(int form, const ExpertArgs& a) {
+  const auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  if (a.dtype != DT_BF16 || a.P < 1 || !aligned(a.a) || !aligned(a.b) || !aligned(a.out))
+    return false;
+  if (a.D % 8 != 0) return false;
+  return form == EX_FWD || a.N % 8 == 0;
+}
+
+int launch_expert_matmul_tc(int form, const ExpertArgs& a, cudaStream_t st) {
+  return form == EX_FWD     ? launch_form<EX_FWD>(a, st)
+         : form == EX_DGRAD ? launch_form<EX_DGRAD>(a, st)
+                            : launch_form<EX_WGRAD>(a, st);
+}
+
+}  // namespace moe_router

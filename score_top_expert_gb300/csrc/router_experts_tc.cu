@@ -12,19 +12,26 @@
 //   weight grad   A = grad_out columns n, MN-major;   B = x columns d, MN-major; both
 //                 over the expert's rows p, in slices of 64 from its first one
 //
-// Rows are brought in by gathering copies of four rows, each with its own
-// row index: a token's row through the expert map, and for indices behind the
-// expert's last row one past the tensor, which reads as zero.  So no row of
-// another expert enters a product, and the weight gradient's last slice needs
-// no mask.
+// Rows that lie in order come in boxes of 16 rows.  Rows of x behind the expert
+// map, and the last rows of an expert in the weight gradient, come by gathering
+// copies of four rows, each with its own index; an index behind the expert's
+// last row points one past the tensor, which reads as zero.  So no row of
+// another expert enters a product (the boxes of the forward and the input
+// gradient may hold some: they fill columns that are not stored).
 //
-// Block: 8 warps.  Warp 0 loads (6 stages of 64 contraction indices, 16 KB of
-// A and up to 16 KB of B each), one thread of warp 1 issues the products,
+// Block: 16 warps.  Warp 0 loads A, warps 8-15 load B, 16 rows (weight grad:
+// of A and B, 16 rows x 64 columns) each, since a warp takes about 95 cycles to
+// issue one copy: one warp that issued 32 gathering copies a stage ran the
+// 8192 x 2048 x 2048 forward (64 experts, 4 choices) at 430 TFLOP/s, two at
+// 630, four at 910, eight at 1060.  One thread of warp 1 issues the products,
 // warp 2 owns the tensor memory, warps 4-7 store finished tiles while the next
-// one is computed into the other half of the accumulator columns.  CG = 2: two
-// CTAs share a tile of 256 x (up to 256), each holding half of A and of B, which
-// halves the shared-memory and L2 traffic per product.  The grid is
-// persistent; tile i goes to CTA (pair) i mod the grid.
+// one is computed into the other half of the accumulator columns.  A stage
+// holds 64 contraction indices: 16 KB of A and up to 16 KB of B.  Every loading
+// warp arrives on a stage's barrier even with nothing to load, so none falls
+// behind by a phase.  CG = 2: two CTAs share a tile of 256 x (up to 256), each
+// holding half of A and of B, which halves the shared-memory and L2 traffic
+// per product.  The grid is persistent; tile i goes to CTA (pair) i mod the
+// grid.
 #include <atomic>
 
 #include "router_common.cuh"
@@ -34,7 +41,8 @@
 namespace moe_router {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kLoaders = 8;               // warps that load B (weight grad: A and B)
+constexpr int kThreads = 256 + 32 * kLoaders;
 constexpr int kStages = 6;
 constexpr int kDeep = 64;                 // contraction indices per stage: 128 bytes
 constexpr int kRowsA = 128;               // values of A's dimension per CTA
@@ -110,9 +118,22 @@ struct Waiter {
   }
 };
 
+// Source rows of x behind rows b0 + 4 l .. + 3 of a tile, l = lane mod 4; one
+// past x behind the tile's last row.
+__device__ __forceinline__ void gather_rows(const TcArgs& g, const Tile& t, int b0, int lane,
+                                            int (&r)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int b = b0 + 4 * (lane & 3) + j;
+    r[j] = b < t.cnt ? source_row(g.p2u, g.T, t.start + b) : g.x_rows;
+    if (r[j] < 0) r[j] = g.x_rows;
+  }
+}
+
 template <int FORM, int CG>
 __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
     const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+    const __grid_constant__ CUtensorMap box_a, const __grid_constant__ CUtensorMap box_b,
     const TcArgs g) {
   using S = Shape<FORM, CG>;
   extern __shared__ uint8_t dynamic_smem[];
@@ -127,7 +148,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
   const uint32_t stages_at = (smem_addr(dynamic_smem) + 1023u) & ~1023u;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], CG * (FORM == EX_WGRAD ? kLoaders : kLoaders + 1));
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -155,67 +176,85 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
   // contraction slices of a tile
   const int fixed_slices = ((FORM == EX_FWD ? g.D : g.N) + kDeep - 1) / kDeep;
 
-  if (warp == 0) {
+  if (warp >= 8 || (warp == 0 && FORM != EX_WGRAD)) {
     // ---- loads -----------------------------------------------------------------
+    const int w = warp - 8;  // -1: the warp that loads A
     int stage = 0;
     uint32_t parity = 1;  // the first pass finds the stages empty
     bool ok = true;
     for (int i = first; i < tiles && ok; i += step) {
       const Tile t = find_tile<FORM, CG>(g, prefix, i);
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
-      // this CTA's rows of B: 4 per lane
-      const int rows = FORM == EX_WGRAD
-                           ? kRowsB
-                           : (t.cnt + S::kRound - 1) / S::kRound * S::kRound / CG;
-      int r[4];
+      // this CTA's rows of B
+      const int rows =
+          FORM == EX_WGRAD ? kRowsB : (t.cnt + S::kRound - 1) / S::kRound * S::kRound / CG;
+      const int b0 = static_cast<int>(rank) * rows + 16 * w;  // this warp's first row in the tile
+      const int a0 = t.a0 + static_cast<int>(rank) * kRowsA;
+      int r[4];  // lanes 0-3: four source rows each
       if constexpr (FORM != EX_WGRAD) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int b = static_cast<int>(rank) * rows + 4 * lane + j;
-          r[j] = (4 * lane < rows && b < t.cnt) ? source_row(g.p2u, g.T, t.start + b) : g.x_rows;
-          if (r[j] < 0) r[j] = g.x_rows;
-        }
+        if (w >= 0 && g.p2u != nullptr) gather_rows(g, t, b0, lane, r);
       }
       for (int s = 0; s < slices; ++s) {
-        // weight grad: lanes 0-15 load the first 64 columns, 16-31 the next; 4 rows each
-        int p[4];
+        int p[4], group = 0;
+        bool mapped = false, whole = true;
+        uint32_t bytes;
         if constexpr (FORM == EX_WGRAD) {
+          // warp: 16 rows x 64 columns of both operands
+          group = s * kDeep + 16 * (w >> 1);
+          whole = group + 16 <= t.cnt;
+          mapped = g.p2u != nullptr || !whole;
+          bytes = group < t.cnt ? 4096 : 0;
+          if (mapped && bytes > 0) {
+            gather_rows(g, t, group, lane, r);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int b = s * kDeep + 4 * (lane & 15) + j;
-            p[j] = b < t.cnt ? t.start + b : g.P;
-            r[j] = b < t.cnt ? source_row(g.p2u, g.T, t.start + b) : g.x_rows;
-            if (r[j] < 0) {
-              r[j] = g.x_rows;
-              p[j] = g.P;
+            for (int j = 0; j < 4; ++j) {
+              const int b = group + 4 * (lane & 3) + j;
+              p[j] = b < t.cnt && r[j] != g.x_rows ? t.start + b : g.P;
             }
+            // a row without a source counts in neither operand
+            whole = __all_sync(0xffffffffu, p[0] != g.P && p[1] != g.P && p[2] != g.P && p[3] != g.P);
           }
+        } else {
+          mapped = g.p2u != nullptr;
+          bytes = w < 0 ? kBytesA : 16 * w < rows ? 2048 : 0;
         }
         ok = __all_sync(0xffffffffu, wait(&empty[stage], parity));
         if (!ok) break;
         const uint32_t at = stages_at + stage * kStageBytes;
         const uint32_t bar =
             CG == 2 ? map_to_rank(smem_addr(&full[stage]), 0) : smem_addr(&full[stage]);
-        if (lane == 0 && rank == 0) mbar_expect_tx(&full[stage], CG * (kBytesA + rows * 128));
+        if (lane == 0) mbar_expect_tx_cluster(bar, bytes);
         __syncwarp();
-        const int a0 = t.a0 + static_cast<int>(rank) * kRowsA;
-        if constexpr (FORM == EX_FWD) {
-          if (lane == 0) tma_load_3d<CG>(at, &map_a, s * kDeep, a0, t.e, bar);
-        } else if constexpr (FORM == EX_DGRAD) {
-          if (lane < 2)
-            tma_load_3d<CG>(at + lane * 8192, &map_a, a0 + 64 * lane, s * kDeep, t.e, bar);
-        } else {
-          tma_gather4<CG>(at + lane * 512, &map_a, a0 + 64 * (lane >> 4), p[0], p[1], p[2], p[3],
-                          bar);
-        }
-        if constexpr (FORM == EX_WGRAD) {
-          tma_gather4<CG>(at + kBytesA + lane * 512, &map_b,
-                          t.b0 + static_cast<int>(rank) * kRowsB + 64 * (lane >> 4), r[0], r[1],
-                          r[2], r[3], bar);
-        } else {
-          if (4 * lane < rows)
-            tma_gather4<CG>(at + kBytesA + lane * 512, &map_b, s * kDeep, r[0], r[1], r[2], r[3],
-                            bar);
+        if (w < 0) {
+          if constexpr (FORM == EX_FWD) {
+            if (lane == 0) tma_load_3d<CG>(at, &map_a, s * kDeep, a0, t.e, bar);
+          } else if constexpr (FORM == EX_DGRAD) {
+            if (lane < 2)
+              tma_load_3d<CG>(at + lane * 8192, &map_a, a0 + 64 * lane, s * kDeep, t.e, bar);
+          }
+        } else if (bytes > 0) {
+          if constexpr (FORM == EX_WGRAD) {
+            const uint32_t piece = at + (w & 1) * 8192 + (w >> 1) * 2048;
+            const int ca = a0 + 64 * (w & 1);
+            const int cb = t.b0 + static_cast<int>(rank) * kRowsB + 64 * (w & 1);
+            if (whole) {
+              if (lane == 4) tma_load_2d<CG>(piece, &box_a, ca, t.start + group, bar);
+            } else if (lane < 4) {
+              tma_gather4<CG>(piece + lane * 512, &map_a, ca, p[0], p[1], p[2], p[3], bar);
+            }
+            if (!mapped) {
+              if (lane == 5) tma_load_2d<CG>(piece + kBytesA, &box_b, cb, t.start + group, bar);
+            } else if (lane < 4) {
+              tma_gather4<CG>(piece + kBytesA + lane * 512, &map_b, cb, r[0], r[1], r[2], r[3], bar);
+            }
+          } else {
+            const uint32_t piece = at + kBytesA + w * 2048;
+            if (!mapped) {
+              if (lane == 0) tma_load_2d<CG>(piece, &box_b, s * kDeep, t.start + b0, bar);
+            } else if (lane < 4) {
+              tma_gather4<CG>(piece + lane * 512, &map_b, s * kDeep, r[0], r[1], r[2], r[3], bar);
+            }
+          }
         }
         if (++stage == kStages) {
           stage = 0;
@@ -253,9 +292,10 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
         const uint64_t db = FORM == EX_WGRAD ? operand_desc(at + kBytesA, 8192, 1024)
                                              : operand_desc(at + kBytesA, 0, 1024);
         constexpr uint64_t ka = FORM == EX_FWD ? 2 : 128, kb = FORM == EX_WGRAD ? 128 : 2;
+        const int depth = FORM == EX_WGRAD ? min(kDeep, t.cnt - s * kDeep) : kDeep;
 #pragma unroll
         for (int k = 0; k < kDeep / 16; ++k)
-          tc_product<CG>(d, da + k * ka, db + k * kb, desc, s > 0 || k > 0);
+          if (16 * k < depth) tc_product<CG>(d, da + k * ka, db + k * kb, desc, s > 0 || k > 0);
         tc_commit<CG>(&empty[stage]);
         if (++stage == kStages) {
           stage = 0;
@@ -265,7 +305,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
       if (ok) tc_commit<CG>(&done[buf]);
       ++n;
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     // ---- stores --------------------------------------------------------------------
     const int quad = warp - 4;
     int n = 0;
@@ -393,9 +433,9 @@ bool make_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* di
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool rows_map(CUtensorMap* map, const void* base, int rows, int cols) {
+bool rows_map(CUtensorMap* map, const void* base, int rows, int cols, cuuint32_t high) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint32_t box[2] = {64, 1};
+  const cuuint32_t box[2] = {64, high};
   return make_map(map, base, 2, dims, box);
 }
 
@@ -445,13 +485,18 @@ int launch_typed(const ExpertArgs& a, cudaStream_t st) {
   TcArgs g{a.offsets, a.p2u, a.out, device_status_word(), a.T, a.P, a.E, a.N, a.D,
            FORM == EX_DGRAD || a.p2u == nullptr ? a.P : a.T, a.out_dtype == DT_F32};
   if (resident <= 0 || g.status == nullptr) return MR_ERR_CUDA;
-  CUtensorMap ma, mb;
-  const bool maps =
-      FORM == EX_FWD
-          ? weight_map(&ma, a.b, a, kRowsA) && rows_map(&mb, a.a, g.x_rows, a.D)
-          : FORM == EX_DGRAD
-                ? weight_map(&ma, a.b, a, kDeep) && rows_map(&mb, a.a, a.P, a.N)
-                : rows_map(&ma, a.a, a.P, a.N) && rows_map(&mb, a.b, g.x_rows, a.D);
+  // a and b: weights, or single rows for gathering; the boxes: 16 rows in order
+  CUtensorMap ma, mb, ba, bb;
+  bool maps;
+  if (FORM == EX_WGRAD) {
+    maps = rows_map(&ma, a.a, a.P, a.N, 1) && rows_map(&ba, a.a, a.P, a.N, 16) &&
+           rows_map(&mb, a.b, g.x_rows, a.D, 1) && rows_map(&bb, a.b, g.x_rows, a.D, 16);
+  } else {
+    const int cols = FORM == EX_FWD ? a.D : a.N;
+    maps = weight_map(&ma, a.b, a, FORM == EX_FWD ? kRowsA : kDeep) &&
+           rows_map(&mb, a.a, g.x_rows, cols, 1) && rows_map(&bb, a.a, g.x_rows, cols, 16);
+    ba = ma;
+  }
   if (!maps) return MR_ERR_CUDA;
   const long long ta = ((FORM == EX_DGRAD ? a.D : a.N) + S::kTileA - 1) / S::kTileA;
   const long long tb = FORM == EX_WGRAD
@@ -473,7 +518,7 @@ int launch_typed(const ExpertArgs& a, cudaStream_t st) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, g) == cudaSuccess ? MR_OK : MR_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, ba, bb, g) == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }
 
 template <int FORM>

@@ -20,18 +20,22 @@
 // gradient may hold some: they fill columns that are not stored).
 //
 // Block: 16 warps.  Warp 0 loads A, warps 8-15 load B, 16 rows (weight grad:
-// of A and B, 16 rows x 64 columns) each, since a warp takes about 95 cycles to
-// issue one copy: one warp that issued 32 gathering copies a stage ran the
-// 8192 x 2048 x 2048 forward (64 experts, 4 choices) at 430 TFLOP/s, two at
-// 630, four at 910, eight at 1060.  One thread of warp 1 issues the products,
-// warp 2 owns the tensor memory, warps 4-7 store finished tiles while the next
-// one is computed into the other half of the accumulator columns.  A stage
-// holds 64 contraction indices: 16 KB of A and up to 16 KB of B.  Every loading
-// warp arrives on a stage's barrier even with nothing to load, so none falls
-// behind by a phase.  CG = 2: two CTAs share a tile of 256 x (up to 256), each
-// holding half of A and of B, which halves the shared-memory and L2 traffic
-// per product.  The grid is persistent; tile i goes to CTA (pair) i mod the
-// grid.
+// of A and B, 16 rows x 64 columns) each.  One elected thread of warp 1 issues
+// the products, warp 2 owns the tensor memory, warps 4-7 store finished tiles
+// while the next one is computed into the other half of the accumulator
+// columns.  A stage holds 64 contraction indices: 16 KB of A and up to 16 KB of
+// B.  Every loading warp arrives on a stage's barrier even with nothing to
+// load, so none falls behind by a phase.  CG = 2: two CTAs share a tile of
+// 256 x (up to 256), each holding half of A and of B, which halves the
+// shared-memory and L2 traffic per product.  The grid is persistent; tile i
+// goes to CTA (pair) i mod the grid.
+//
+// What bounded it on the way (forward, 8192 tokens, 64 experts, 4 choices,
+// 2048 x 2048): the issue of copies and products.  Under a lane test each cost
+// 60 to 100 cycles; 32 gathers a stage from one warp ran at 430 TFLOP/s, from
+// eight warps at 1060, and with operands in uniform registers (elect_one) the
+// kernel runs at 1250 through the map and 1310 in order; 4096 x 4096 over 8
+// experts at 1590 and 1740 (input gradient).
 #include <atomic>
 
 #include "router_common.cuh"
@@ -43,18 +47,19 @@ namespace {
 
 constexpr int kLoaders = 8;               // warps that load B (weight grad: A and B)
 constexpr int kThreads = 256 + 32 * kLoaders;
-constexpr int kStages = 6;
+constexpr int kMaxStages = 6;
 constexpr int kDeep = 64;                 // contraction indices per stage: 128 bytes
 constexpr int kRowsA = 128;               // values of A's dimension per CTA
 constexpr int kRowsB = 128;               // most values of B's dimension per CTA
 constexpr int kBytesA = kRowsA * 128;
 constexpr int kBytesB = kRowsB * 128;
 constexpr int kStageBytes = kBytesA + kBytesB;
-constexpr int kStoreBytes = 4 * 2 * 4096;  // weight grad: two 32 x 128-byte boxes per storing warp
+constexpr int kBoxes = 4;  // weight grad: 32 x 128-byte boxes per storing warp
 
-// Dynamic shared memory; stages and boxes start on 1024 bytes.
+// Stages, and dynamic shared memory: stages and boxes start on 1024 bytes.
+constexpr int stages_of(int form) { return form == EX_WGRAD ? 5 : kMaxStages; }
 constexpr int smem_bytes(int form) {
-  return kStages * kStageBytes + (form == EX_WGRAD ? kStoreBytes : 0) + 1024;
+  return stages_of(form) * kStageBytes + (form == EX_WGRAD ? 4 * kBoxes * 4096 : 0) + 1024;
 }
 
 struct TcArgs {
@@ -64,6 +69,7 @@ struct TcArgs {
   int* status;
   int T, P, E, N, D;
   int x_rows;  // rows of the gathered x
+  uint32_t inv_T;  // floor(2^32 / T), at most 2^32 - 1
   int out_f32;
 };
 
@@ -78,6 +84,7 @@ struct Shape {
   static constexpr int kTileA = kRowsA * CG;
   static constexpr int kTileB = kRowsB * CG;
   static constexpr int kRound = 16 * CG;
+  static constexpr int kStages = stages_of(FORM);
   static constexpr uint32_t kColumns = 2 * kTileB;  // two accumulators
 };
 
@@ -123,24 +130,65 @@ struct Waiter {
   }
 };
 
-// Source rows of x behind rows b0 + 4 l .. + 3 of a tile, l = lane mod 4; one
-// past x behind the tile's last row.
-__device__ __forceinline__ void gather_rows(const TcArgs& g, const Tile& t, int b0, int lane,
-                                            int (&r)[4]) {
+// Tile *i, or the first one after it in this CTA's sequence that has products
+// (weight grad: an expert without rows has none).
+template <int FORM, int CG>
+__device__ __forceinline__ Tile next_tile(const TcArgs& g, const int* prefix, int tiles, int step,
+                                          int* i) {
+  Tile t{};
+  while (*i < tiles) {
+    t = find_tile<FORM, CG>(g, prefix, *i);
+    if (FORM != EX_WGRAD || t.cnt > 0) break;
+    *i += step;
+  }
+  return t;
+}
+
+// First row, within tile t, that loading warp w brings for slice s.
+template <int FORM, int CG>
+__device__ __forceinline__ int loader_row(const Tile& t, uint32_t rank, int w, int s) {
+  if (FORM == EX_WGRAD) return s * kDeep + 16 * (w >> 1);
+  constexpr int round = Shape<FORM, CG>::kRound;
+  return static_cast<int>(rank) * ((t.cnt + round - 1) / round * round / CG) + 16 * w;
+}
+
+// Map entries of tile rows b0 + 4 l .. + 3, l = lane mod 4 (the loads are
+// issued here and used a slice later).
+__device__ __forceinline__ void fetch_rows(const TcArgs& g, const Tile& t, int b0, int lane,
+                                           int (&u)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int b = b0 + 4 * (lane & 3) + j;
-    r[j] = b < t.cnt ? source_row(g.p2u, g.T, t.start + b) : g.x_rows;
-    if (r[j] < 0) r[j] = g.x_rows;
+    u[j] = b >= t.cnt ? -1 : g.p2u == nullptr ? t.start + b : g.p2u[t.start + b];
   }
 }
 
-__device__ __forceinline__ void load_or_zero(bool zero, uint32_t addr, uint32_t (&v)[32]) {
-  if (!zero) {
-    tmem_load_32(addr, v);
-  } else {
+// u mod T.  u inv_T / 2^32 is below u / T by less than 1, so its floor is the
+// quotient or one less.
+__device__ __forceinline__ int token_of(const TcArgs& g, int u) {
+  const int r = u - static_cast<int>(__umulhi(static_cast<uint32_t>(u), g.inv_T)) * g.T;
+  return r >= g.T ? r - g.T : r;
+}
+
+// Their rows of x: `none` for rows behind the tile's last.
+__device__ __forceinline__ void source_rows(const TcArgs& g, const int (&u)[4], int none,
+                                            int (&r)[4]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = 0u;
+  for (int j = 0; j < 4; ++j) r[j] = u[j] < 0 ? none : g.p2u == nullptr ? u[j] : token_of(g, u[j]);
+}
+
+// 16 rows of 64 columns: lanes 0-3 hold four row indices each.
+template <int CG>
+__device__ __forceinline__ void issue_gather(uint32_t dst, const CUtensorMap* map, int col,
+                                             const int (&r)[4], bool one, uint32_t bar) {
+  int q[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) q[j] = __shfl_sync(0xffffffffu, r[j & 3], j >> 2);
+  if (one) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      tma_gather4<CG>(dst + j * 512, map, col, q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3],
+                      bar);
   }
 }
 
@@ -157,18 +205,20 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
     const __grid_constant__ CUtensorMap map_out, const TcArgs g) {
   using S = Shape<FORM, CG>;
   extern __shared__ uint8_t dynamic_smem[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done[2], drained[2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], done[2], drained[2];
   __shared__ uint32_t tmem_at;
   __shared__ int gave_up;
   __shared__ int tmp[33];
   __shared__ int prefix[FORM == EX_WGRAD ? 1 : MR_MAX_EXPERTS + 1];
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same value in all lanes, and known to be
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const uint32_t stages_at = (smem_addr(dynamic_smem) + 1023u) & ~1023u;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], CG * (FORM == EX_WGRAD ? kLoaders : kLoaders + 1));
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(&full[i], CG * (kLoaders + 1));
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -196,112 +246,124 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
   // contraction slices of a tile
   const int fixed_slices = ((FORM == EX_FWD ? g.D : g.N) + kDeep - 1) / kDeep;
 
-  if (warp >= 8 || (warp == 0 && FORM != EX_WGRAD)) {
+  if (warp >= 8 || warp == 0) {
     // ---- loads -----------------------------------------------------------------
+    // The next slice's tile and map entries are fetched before the present
+    // slice's copies are issued, so their latency passes behind the issue.
     const int w = warp - 8;  // -1: the warp that loads A
+    const bool mapped = w >= 0 && (FORM == EX_WGRAD || g.p2u != nullptr);
     int stage = 0;
     uint32_t parity = 1;  // the first pass finds the stages empty
-    bool ok = true;
-    for (int i = first; i < tiles && ok; i += step) {
-      const Tile t = find_tile<FORM, CG>(g, prefix, i);
+    int i = first, s = 0;
+    Tile t = next_tile<FORM, CG>(g, prefix, tiles, step, &i);
+    int u[4];
+    if (mapped) fetch_rows(g, t, loader_row<FORM, CG>(t, rank, w, s), lane, u);
+    int r[4];
+    while (i < tiles) {
+      if (mapped && (FORM == EX_WGRAD || s == 0)) source_rows(g, u, g.x_rows, r);
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
-      // this CTA's rows of B
-      const int rows =
-          FORM == EX_WGRAD ? kRowsB : (t.cnt + S::kRound - 1) / S::kRound * S::kRound / CG;
-      const int b0 = static_cast<int>(rank) * rows + 16 * w;  // this warp's first row in the tile
+      int ni = i, ns = s + 1;
+      Tile nt = t;
+      int nu[4] = {u[0], u[1], u[2], u[3]};
+      if (ns == slices) {
+        ni += step;
+        nt = next_tile<FORM, CG>(g, prefix, tiles, step, &ni);
+        ns = 0;
+      }
+      if (mapped && ni < tiles && (FORM == EX_WGRAD || ns == 0))
+        fetch_rows(g, nt, loader_row<FORM, CG>(nt, rank, w, ns), lane, nu);
+
+      const int row = loader_row<FORM, CG>(t, rank, w, s);
       const int a0 = t.a0 + static_cast<int>(rank) * kRowsA;
-      int r[4];  // lanes 0-3: four source rows each
-      if constexpr (FORM != EX_WGRAD) {
-        if (w >= 0 && g.p2u != nullptr) gather_rows(g, t, b0, lane, r);
+      // weight grad: a slice inside the expert comes as whole boxes of A; the
+      // last one in pieces by the warps that load B
+      const bool all_a = FORM != EX_WGRAD || s * kDeep + kDeep <= t.cnt;
+      const bool whole = row + 16 <= t.cnt;
+      uint32_t bytes;
+      if (w < 0) {
+        bytes = all_a ? kBytesA : 0;
+      } else if (FORM == EX_WGRAD) {
+        bytes = row < t.cnt ? (all_a ? 2048 : 4096) : 0;
+      } else {
+        const int rows = (t.cnt + S::kRound - 1) / S::kRound * S::kRound / CG;
+        bytes = 16 * w < rows ? 2048 : 0;
       }
-      for (int s = 0; s < slices; ++s) {
-        int p[4], group = 0;
-        bool mapped = false, whole = true;
-        uint32_t bytes;
-        if constexpr (FORM == EX_WGRAD) {
-          // warp: 16 rows x 64 columns of both operands
-          group = s * kDeep + 16 * (w >> 1);
-          whole = group + 16 <= t.cnt;
-          mapped = g.p2u != nullptr || !whole;
-          bytes = group < t.cnt ? 4096 : 0;
-          if (mapped && bytes > 0) {
-            gather_rows(g, t, group, lane, r);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int b = group + 4 * (lane & 3) + j;
-              p[j] = b < t.cnt && r[j] != g.x_rows ? t.start + b : g.P;
-            }
-            // a row without a source counts in neither operand
-            whole = __all_sync(0xffffffffu, p[0] != g.P && p[1] != g.P && p[2] != g.P && p[3] != g.P);
-          }
-        } else {
-          mapped = g.p2u != nullptr;
-          bytes = w < 0 ? kBytesA : 16 * w < rows ? 2048 : 0;
-        }
-        ok = __all_sync(0xffffffffu, wait(&empty[stage], parity));
-        if (!ok) break;
-        const uint32_t at = stages_at + stage * kStageBytes;
-        const uint32_t bar =
-            CG == 2 ? map_to_rank(smem_addr(&full[stage]), 0) : smem_addr(&full[stage]);
-        if (lane == 0) mbar_expect_tx_cluster(bar, bytes);
-        __syncwarp();
-        if (w < 0) {
+      if (!__all_sync(0xffffffffu, wait(&empty[stage], parity))) break;
+      const uint32_t at = stages_at + stage * kStageBytes;
+      const uint32_t bar =
+          CG == 2 ? map_to_rank(smem_addr(&full[stage]), 0) : smem_addr(&full[stage]);
+      const bool one = elect_one();
+      if (one) mbar_expect_tx_cluster(bar, bytes);
+      if (bytes == 0) {
+      } else if (w < 0) {
+        if (one) {
           if constexpr (FORM == EX_FWD) {
-            if (lane == 0) tma_load_3d<CG>(at, &map_a, s * kDeep, a0, t.e, bar);
+            tma_load_3d<CG>(at, &map_a, s * kDeep, a0, t.e, bar);
           } else if constexpr (FORM == EX_DGRAD) {
-            if (lane < 2)
-              tma_load_3d<CG>(at + lane * 8192, &map_a, a0 + 64 * lane, s * kDeep, t.e, bar);
-          }
-        } else if (bytes > 0) {
-          if constexpr (FORM == EX_WGRAD) {
-            const uint32_t piece = at + (w & 1) * 8192 + (w >> 1) * 2048;
-            const int ca = a0 + 64 * (w & 1);
-            const int cb = t.b0 + static_cast<int>(rank) * kRowsB + 64 * (w & 1);
-            if (whole) {
-              if (lane == 4) tma_load_2d<CG>(piece, &box_a, ca, t.start + group, bar);
-            } else if (lane < 4) {
-              tma_gather4<CG>(piece + lane * 512, &map_a, ca, p[0], p[1], p[2], p[3], bar);
-            }
-            if (!mapped) {
-              if (lane == 5) tma_load_2d<CG>(piece + kBytesA, &box_b, cb, t.start + group, bar);
-            } else if (lane < 4) {
-              tma_gather4<CG>(piece + kBytesA + lane * 512, &map_b, cb, r[0], r[1], r[2], r[3], bar);
-            }
+            tma_load_3d<CG>(at, &map_a, a0, s * kDeep, t.e, bar);
+            tma_load_3d<CG>(at + 8192, &map_a, a0 + 64, s * kDeep, t.e, bar);
           } else {
-            const uint32_t piece = at + kBytesA + w * 2048;
-            if (!mapped) {
-              if (lane == 0) tma_load_2d<CG>(piece, &box_b, s * kDeep, t.start + b0, bar);
-            } else if (lane < 4) {
-              tma_gather4<CG>(piece + lane * 512, &map_b, s * kDeep, r[0], r[1], r[2], r[3], bar);
-            }
+            tma_load_2d<CG>(at, &box_a, a0, t.start + s * kDeep, bar);
+            tma_load_2d<CG>(at + 8192, &box_a, a0 + 64, t.start + s * kDeep, bar);
           }
         }
-        if (++stage == kStages) {
-          stage = 0;
-          parity ^= 1;
+      } else if constexpr (FORM == EX_WGRAD) {
+        const uint32_t piece = at + (w & 1) * 8192 + (w >> 1) * 2048;
+        const int cb = t.b0 + static_cast<int>(rank) * kRowsB + 64 * (w & 1);
+        if (g.p2u != nullptr || !whole) {
+          issue_gather<CG>(piece + kBytesA, &map_b, cb, r, one, bar);
+        } else if (one) {
+          tma_load_2d<CG>(piece + kBytesA, &box_b, cb, t.start + row, bar);
+        }
+        if (!all_a) {
+          int p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int b = row + 4 * (lane & 3) + j;
+            p[j] = b < t.cnt ? t.start + b : g.P;
+          }
+          issue_gather<CG>(piece, &map_a, a0 + 64 * (w & 1), p, one, bar);
+        }
+      } else {
+        const uint32_t piece = at + kBytesA + w * 2048;
+        if (mapped) {
+          issue_gather<CG>(piece, &map_b, s * kDeep, r, one, bar);
+        } else if (one) {
+          tma_load_2d<CG>(piece, &box_b, s * kDeep, t.start + row, bar);
         }
       }
+      if (++stage == S::kStages) {
+        stage = 0;
+        parity ^= 1;
+      }
+      i = ni;
+      t = nt;
+      s = ns;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = nu[j];
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---- products ----------------------------------------------------------------
     int stage = 0, n = 0;  // n: tiles computed
     uint32_t parity = 0;
     bool ok = true;
-    for (int i = first; i < tiles && ok; i += step) {
-      const Tile t = find_tile<FORM, CG>(g, prefix, i);
+    int i = first;
+    Tile t = next_tile<FORM, CG>(g, prefix, tiles, step, &i);
+    while (i < tiles && ok) {
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
-      if (slices == 0) continue;
       const int cols = FORM == EX_WGRAD ? S::kTileB
                                         : (t.cnt + S::kRound - 1) / S::kRound * S::kRound;
       const uint32_t desc =
           product_desc(S::kTileA, cols, FORM != EX_FWD, FORM == EX_WGRAD);
       const int buf = n & 1;
-      ok = wait(&drained[buf], ((n >> 1) & 1) ^ 1);
+      int ni = i + step;
+      Tile nt = t;
+      ok = __all_sync(0xffffffffu, wait(&drained[buf], ((n >> 1) & 1) ^ 1));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + buf * S::kTileB;
       for (int s = 0; s < slices; ++s) {
-        ok = wait(&full[stage], parity);
+        ok = __all_sync(0xffffffffu, wait(&full[stage], parity));
         if (!ok) break;
         tc_fence_after();
         const uint32_t at = stages_at + stage * kStageBytes;
@@ -313,22 +375,30 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
                                              : operand_desc(at + kBytesA, 0, 1024);
         constexpr uint64_t ka = FORM == EX_FWD ? 2 : 128, kb = FORM == EX_WGRAD ? 128 : 2;
         const int depth = FORM == EX_WGRAD ? min(kDeep, t.cnt - s * kDeep) : kDeep;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kDeep / 16; ++k)
-          if (16 * k < depth) tc_product<CG>(d, da + k * ka, db + k * kb, desc, s > 0 || k > 0);
-        tc_commit<CG>(&empty[stage]);
-        if (++stage == kStages) {
+          for (int k = 0; k < kDeep / 16; ++k)
+            if (16 * k < depth)
+              tc_product<CG>(d, da + k * ka, db + k * kb, desc, s > 0 || k > 0);
+          tc_commit<CG>(&empty[stage]);
+          if (s == slices - 1) tc_commit<CG>(&done[buf]);
+        }
+        __syncwarp();
+        if (++stage == S::kStages) {
           stage = 0;
           parity ^= 1;
         }
+        // the next tile is looked up while this slice is computed
+        if (s == 0) nt = next_tile<FORM, CG>(g, prefix, tiles, step, &ni);
       }
-      if (ok) tc_commit<CG>(&done[buf]);
       ++n;
+      i = ni;
+      t = nt;
     }
   } else if (warp >= 4 && warp < 8) {
     // ---- stores --------------------------------------------------------------------
     const int quad = warp - 4;
-    [[maybe_unused]] const uint32_t boxes_at = stages_at + kStages * kStageBytes + quad * 8192;
+    [[maybe_unused]] const uint32_t boxes_at = stages_at + S::kStages * kStageBytes + quad * (kBoxes * 4096);
     [[maybe_unused]] int chunk = 0;
     int n = 0;
     bool ok = true;
@@ -351,17 +421,30 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
         // piece directly touched 32 lines per instruction and ran at 2.9 TB/s.
         const int wide = g.out_f32 ? 32 : 64;
         const int cols = row0 < g.N ? min(S::kTileB, g.D - t.b0) : 0;
-        for (int c = 0; c < cols; c += wide) {
-          const uint32_t box = boxes_at + (chunk++ & 1) * 4096;
+        if (none && cols > 0) {  // one box of zeros for the whole tile
+          const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
+          if (lane == 0) bulk_wait_read<kBoxes - 1>();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) st_shared_v4(box + (j * 32 + lane) * 16, 0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            for (int c = 0; c < cols; c += wide) tma_store_3d(&map_out, box, t.b0 + c, row0, t.e);
+            bulk_commit();
+          }
+        }
+        for (int c = 0; c < cols && !none; c += wide) {
+          const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
           uint32_t v[32];
-          if (lane == 0) bulk_wait_read<1>();
+          if (lane == 0) bulk_wait_read<kBoxes - 1>();
           __syncwarp();
           if (g.out_f32) {
-            load_or_zero(none, acc + c, v);
+            tmem_load_32(acc + c, v);
           } else {
             uint32_t lo[32], hi[32];
-            load_or_zero(none, acc + c, lo);
-            load_or_zero(none, acc + c + 32, hi);
+            tmem_load_32(acc + c, lo);
+            tmem_load_32(acc + c + 32, hi);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               v[j] = f32_to_bf16_bits(__uint_as_float(lo[2 * j])) |
@@ -519,13 +602,15 @@ int launch_typed(const ExpertArgs& a, cudaStream_t st) {
   const auto kern = expert_matmul_tc_kernel<FORM, CG>;
   const int resident = resident_clusters(kern, CG, smem_bytes(FORM), known);
   TcArgs g{a.offsets, a.p2u, a.out, device_status_word(), a.T, a.P, a.E, a.N, a.D,
-           FORM == EX_DGRAD || a.p2u == nullptr ? a.P : a.T, a.out_dtype == DT_F32};
+           FORM == EX_DGRAD || a.p2u == nullptr ? a.P : a.T,
+           a.T > 1 ? static_cast<uint32_t>((1ull << 32) / a.T) : 0xffffffffu,
+           a.out_dtype == DT_F32};
   if (resident <= 0 || g.status == nullptr) return MR_ERR_CUDA;
   // a and b: weights, or single rows for gathering; the boxes: 16 rows in order
   CUtensorMap ma, mb, ba, bb, out;
   bool maps;
   if (FORM == EX_WGRAD) {
-    maps = rows_map(&ma, a.a, a.P, a.N, 1) && rows_map(&ba, a.a, a.P, a.N, 16) &&
+    maps = rows_map(&ma, a.a, a.P, a.N, 1) && rows_map(&ba, a.a, a.P, a.N, kDeep) &&
            rows_map(&mb, a.b, g.x_rows, a.D, 1) && rows_map(&bb, a.b, g.x_rows, a.D, 16) &&
            weight_map(&out, a.out, a, 32, g.out_f32 != 0);
   } else {

@@ -19,6 +19,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// True in one lane of a converged warp.  Copies and products take their
+// operands from the warp's uniform registers: issued by an elected lane of a
+// warp whose operands are the same in all lanes they cost a few instructions,
+// issued under a lane test some sixty to a hundred cycles each.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Every thread of both CTAs.
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();

@@ -192,6 +192,12 @@ __device__ __forceinline__ void issue_gather(uint32_t dst, const CUtensorMap* ma
   }
 }
 
+// Two values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
                                              uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
@@ -400,10 +406,15 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
     const int quad = warp - 4;
     [[maybe_unused]] const uint32_t boxes_at = stages_at + S::kStages * kStageBytes + quad * (kBoxes * 4096);
     [[maybe_unused]] int chunk = 0;
+    // the lane that issues copies: their groups are its own to wait for
+    [[maybe_unused]] const bool one = elect_one();
     int n = 0;
     bool ok = true;
+    Tile nt{};
+    if (first < tiles) nt = find_tile<FORM, CG>(g, prefix, first);
     for (int i = first; i < tiles && ok; i += step) {
-      const Tile t = find_tile<FORM, CG>(g, prefix, i);
+      const Tile t = nt;
+      if (i + step < tiles) nt = find_tile<FORM, CG>(g, prefix, i + step);
       const bool none = FORM == EX_WGRAD && t.cnt == 0;  // an expert without rows: zeros
       const int buf = n & 1;
       if (!none) {
@@ -423,13 +434,13 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
         const int cols = row0 < g.N ? min(S::kTileB, g.D - t.b0) : 0;
         if (none && cols > 0) {  // one box of zeros for the whole tile
           const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
-          if (lane == 0) bulk_wait_read<kBoxes - 1>();
+          if (one) bulk_wait_read<kBoxes - 1>();
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 8; ++j) st_shared_v4(box + (j * 32 + lane) * 16, 0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
+          if (one) {
             for (int c = 0; c < cols; c += wide) tma_store_3d(&map_out, box, t.b0 + c, row0, t.e);
             bulk_commit();
           }
@@ -437,21 +448,16 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
         for (int c = 0; c < cols && !none; c += wide) {
           const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
           uint32_t v[32];
-          if (lane == 0) bulk_wait_read<kBoxes - 1>();
+          if (one) bulk_wait_read<kBoxes - 1>();
           __syncwarp();
           if (g.out_f32) {
             tmem_load_32(acc + c, v);
           } else {
-            uint32_t lo[32], hi[32];
-            tmem_load_32(acc + c, lo);
-            tmem_load_32(acc + c + 32, hi);
+            uint32_t u[64];
+            tmem_load_64(acc + c, u);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              v[j] = f32_to_bf16_bits(__uint_as_float(lo[2 * j])) |
-                     (f32_to_bf16_bits(__uint_as_float(lo[2 * j + 1])) << 16);
-              v[j + 16] = f32_to_bf16_bits(__uint_as_float(hi[2 * j])) |
-                          (f32_to_bf16_bits(__uint_as_float(hi[2 * j + 1])) << 16);
-            }
+            for (int j = 0; j < 32; ++j)
+              v[j] = bf16_pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -459,7 +465,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
                          v[4 * j + 2], v[4 * j + 3]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
+          if (one) {
             tma_store_3d(&map_out, box, t.b0 + c, row0, t.e);
             bulk_commit();
           }
@@ -499,7 +505,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
         ++n;
       }
     }
-    if (FORM == EX_WGRAD && lane == 0) bulk_wait_all();
+    if (FORM == EX_WGRAD && one) bulk_wait_all();
   }
   __syncwarp();
   tc_fence_before();

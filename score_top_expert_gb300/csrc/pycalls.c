@@ -127,6 +127,17 @@ static PyObject* call_combine_fwd(PyObject* self, PyObject* const* args, Py_ssiz
   return PyLong_FromLong(rc);
 }
 
+static PyObject* call_combine_bwd(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t g, u2p, z, w, gz, gw, stream;
+  int dt, ld, T, K, D;
+  void* out[] = {&g, &dt, &u2p, &z, &w, &ld, &T, &K, &D, &gz, &gw, &stream};
+  if (convert(args, nargs, "pipppiiiippp", out) != 0) return NULL;
+  const int rc = router_combine_bwd((const void*)g, (mr_dtype)dt, (const int32_t*)u2p,
+                                    (const void*)z, (const float*)w, ld, T, K, D, (void*)gz,
+                                    (float*)gw, (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
 static PyMethodDef kMethods[] = {
     {"router_topk_fwd", (PyCFunction)(void (*)(void))call_topk_fwd, METH_FASTCALL,
      "router_topk_fwd(logits, dtype, T, E, K, score_func, num_groups, group_topk, "
@@ -150,6 +161,9 @@ static PyMethodDef kMethods[] = {
     {"router_combine_fwd", (PyCFunction)(void (*)(void))call_combine_fwd, METH_FASTCALL,
      "router_combine_fwd(expert_out, dtype, u2p, topk_weights, ld_weights, T, K, D, out, "
      "stream) -> status"},
+    {"router_combine_bwd", (PyCFunction)(void (*)(void))call_combine_bwd, METH_FASTCALL,
+     "router_combine_bwd(grad_out, dtype, u2p, expert_out, topk_weights, ld_weights, T, K, D, "
+     "grad_expert_out, grad_weights, stream) -> status"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pycalls",

@@ -30,6 +30,16 @@
 // shared-memory and L2 traffic per product.  The grid is persistent; tile i
 // goes to CTA (pair) i mod the grid.
 //
+// fp32 outputs.  The tensor cores add each 16-deep product to the accumulator
+// by truncation, so a sum of n of them is off by about n 2^-26 of its value
+// (measured: 4.7e-7 at n = 32), where a bf16 output's rounding is 2^-9.  A fp32
+// output's contraction is therefore cut into segments of at most 960: each is
+// an accumulator of its own and is added to the output, rounding to nearest, by
+// the threads (weight grad: the copy engine) that stored the one before, in
+// order, so results repeat bit for bit.  It costs 5 % of the 8192 x 2048 x 1024
+// forward over 256 experts and a quarter of the compute-bound one over 64
+// (205 to 268 us); adding through staged boxes took 285 us.
+//
 // What bounded it on the way (forward, 8192 tokens, 64 experts, 4 choices,
 // 2048 x 2048): the issue of copies and products.  Under a lane test each cost
 // 60 to 100 cycles; 32 gathers a stage from one warp ran at 430 TFLOP/s, from
@@ -49,6 +59,7 @@ constexpr int kLoaders = 8;               // warps that load B (weight grad: A a
 constexpr int kThreads = 256 + 32 * kLoaders;
 constexpr int kMaxStages = 6;
 constexpr int kDeep = 64;                 // contraction indices per stage: 128 bytes
+constexpr int kSegment = 15;              // most stages per accumulator of a fp32 output
 constexpr int kRowsA = 128;               // values of A's dimension per CTA
 constexpr int kRowsB = 128;               // most values of B's dimension per CTA
 constexpr int kBytesA = kRowsA * 128;
@@ -70,7 +81,6 @@ struct TcArgs {
   int T, P, E, N, D;
   int x_rows;  // rows of the gathered x
   uint32_t inv_T;  // floor(2^32 / T), at most 2^32 - 1
-  int out_f32;
 };
 
 struct Tile {
@@ -198,13 +208,27 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Adds v to *p without reading it back.
+__device__ __forceinline__ void red_add(float* p, float v) {
+  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
                                              uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
 
-template <int FORM, int CG>
+// Stages per accumulator of a tile: all of them, or for a fp32 output near-equal
+// shares of at most kSegment.
+template <bool F32>
+__device__ __forceinline__ int segment_of(int slices) {
+  if (!F32 || slices <= kSegment) return slices;
+  const int parts = (slices + kSegment - 1) / kSegment;
+  return (slices + parts - 1) / parts;
+}
+
+template <int FORM, int CG, bool F32>
 __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
     const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
     const __grid_constant__ CUtensorMap box_a, const __grid_constant__ CUtensorMap box_b,
@@ -350,7 +374,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
     }
   } else if (warp == 1 && rank == 0) {
     // ---- products ----------------------------------------------------------------
-    int stage = 0, n = 0;  // n: tiles computed
+    int stage = 0, n = 0;  // n: accumulators filled
     uint32_t parity = 0;
     bool ok = true;
     int i = first;
@@ -361,50 +385,57 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
                                         : (t.cnt + S::kRound - 1) / S::kRound * S::kRound;
       const uint32_t desc =
           product_desc(S::kTileA, cols, FORM != EX_FWD, FORM == EX_WGRAD);
-      const int buf = n & 1;
       int ni = i + step;
       Tile nt = t;
-      ok = __all_sync(0xffffffffu, wait(&drained[buf], ((n >> 1) & 1) ^ 1));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + buf * S::kTileB;
-      for (int s = 0; s < slices; ++s) {
-        ok = __all_sync(0xffffffffu, wait(&full[stage], parity));
+      const int segment = segment_of<F32>(slices);
+      for (int s0 = 0; s0 < slices && ok; s0 += segment) {
+        const int end = min(s0 + segment, slices);
+        const int buf = n & 1;
+        // an accumulator that the storing warps are done with
+        ok = __all_sync(0xffffffffu, wait(&drained[buf], ((n >> 1) & 1) ^ 1));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t at = stages_at + stage * kStageBytes;
-        // 16 contraction indices are 32 bytes of a K-major row, 16 rows of an
-        // MN-major slice
-        const uint64_t da = FORM == EX_FWD ? operand_desc(at, 0, 1024)
-                                           : operand_desc(at, 8192, 1024);
-        const uint64_t db = FORM == EX_WGRAD ? operand_desc(at + kBytesA, 8192, 1024)
-                                             : operand_desc(at + kBytesA, 0, 1024);
-        constexpr uint64_t ka = FORM == EX_FWD ? 2 : 128, kb = FORM == EX_WGRAD ? 128 : 2;
-        const int depth = FORM == EX_WGRAD ? min(kDeep, t.cnt - s * kDeep) : kDeep;
-        if (elect_one()) {
+        const uint32_t d = tmem + buf * S::kTileB;
+        for (int s = s0; s < end; ++s) {
+          ok = __all_sync(0xffffffffu, wait(&full[stage], parity));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = stages_at + stage * kStageBytes;
+          // 16 contraction indices are 32 bytes of a K-major row, 16 rows of an
+          // MN-major slice
+          const uint64_t da = FORM == EX_FWD ? operand_desc(at, 0, 1024)
+                                             : operand_desc(at, 8192, 1024);
+          const uint64_t db = FORM == EX_WGRAD ? operand_desc(at + kBytesA, 8192, 1024)
+                                               : operand_desc(at + kBytesA, 0, 1024);
+          constexpr uint64_t ka = FORM == EX_FWD ? 2 : 128, kb = FORM == EX_WGRAD ? 128 : 2;
+          const int depth = FORM == EX_WGRAD ? min(kDeep, t.cnt - s * kDeep) : kDeep;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kDeep / 16; ++k)
-            if (16 * k < depth)
-              tc_product<CG>(d, da + k * ka, db + k * kb, desc, s > 0 || k > 0);
-          tc_commit<CG>(&empty[stage]);
-          if (s == slices - 1) tc_commit<CG>(&done[buf]);
+            for (int k = 0; k < kDeep / 16; ++k)
+              if (16 * k < depth)
+                tc_product<CG>(d, da + k * ka, db + k * kb, desc, s > s0 || k > 0);
+            tc_commit<CG>(&empty[stage]);
+            if (s == end - 1) tc_commit<CG>(&done[buf]);
+          }
+          __syncwarp();
+          if (++stage == S::kStages) {
+            stage = 0;
+            parity ^= 1;
+          }
+          // the next tile is looked up while this slice is computed
+          if (s == 0) nt = next_tile<FORM, CG>(g, prefix, tiles, step, &ni);
         }
-        __syncwarp();
-        if (++stage == S::kStages) {
-          stage = 0;
-          parity ^= 1;
-        }
-        // the next tile is looked up while this slice is computed
-        if (s == 0) nt = next_tile<FORM, CG>(g, prefix, tiles, step, &ni);
+        ++n;
       }
-      ++n;
       i = ni;
       t = nt;
     }
   } else if (warp >= 4 && warp < 8) {
     // ---- stores --------------------------------------------------------------------
     const int quad = warp - 4;
-    [[maybe_unused]] const uint32_t boxes_at = stages_at + S::kStages * kStageBytes + quad * (kBoxes * 4096);
+    [[maybe_unused]] const uint32_t boxes_at =
+        stages_at + S::kStages * kStageBytes +
+        quad * (kBoxes * 4096);
     [[maybe_unused]] int chunk = 0;
     // the lane that issues copies: their groups are its own to wait for
     [[maybe_unused]] const bool one = elect_one();
@@ -416,93 +447,116 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
       const Tile t = nt;
       if (i + step < tiles) nt = find_tile<FORM, CG>(g, prefix, i + step);
       const bool none = FORM == EX_WGRAD && t.cnt == 0;  // an expert without rows: zeros
-      const int buf = n & 1;
-      if (!none) {
-        ok = __all_sync(0xffffffffu, wait(&done[buf], (n >> 1) & 1));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      const uint32_t acc =
-          tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * S::kTileB;
-      const int row0 = t.a0 + static_cast<int>(rank) * kRowsA + quad * 32;  // of A's dimension
-      if constexpr (FORM == EX_WGRAD) {
-        // a lane holds one row of the gradient: 128 bytes of it at a time go to
-        // shared memory (16-byte pieces swizzled, so that neither side meets a
-        // bank conflict) and leave as a box of 32 rows.  Storing each lane's
-        // piece directly touched 32 lines per instruction and ran at 2.9 TB/s.
-        const int wide = g.out_f32 ? 32 : 64;
-        const int cols = row0 < g.N ? min(S::kTileB, g.D - t.b0) : 0;
-        if (none && cols > 0) {  // one box of zeros for the whole tile
-          const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
-          if (one) bulk_wait_read<kBoxes - 1>();
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared_v4(box + (j * 32 + lane) * 16, 0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (one) {
-            for (int c = 0; c < cols; c += wide) tma_store_3d(&map_out, box, t.b0 + c, row0, t.e);
-            bulk_commit();
-          }
+      const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
+      // one accumulator after the other: the first is stored, the others added
+      const int segment = segment_of<F32>(slices);
+      for (int first_slice = 0; first_slice == 0 || first_slice < slices;) {
+        const bool add = first_slice > 0;
+        const int buf = n & 1;
+        if (!none) {
+          ok = __all_sync(0xffffffffu, wait(&done[buf], (n >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
         }
-        for (int c = 0; c < cols && !none; c += wide) {
-          const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
-          uint32_t v[32];
-          if (one) bulk_wait_read<kBoxes - 1>();
-          __syncwarp();
-          if (g.out_f32) {
-            tmem_load_32(acc + c, v);
-          } else {
-            uint32_t u[64];
-            tmem_load_64(acc + c, u);
+        const uint32_t acc =
+            tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * S::kTileB;
+        const int row0 = t.a0 + static_cast<int>(rank) * kRowsA + quad * 32;  // of A's dimension
+        if constexpr (FORM == EX_WGRAD) {
+          // a lane holds one row of the gradient: 128 bytes of it at a time go to
+          // shared memory (16-byte pieces swizzled, so that neither side meets a
+          // bank conflict) and leave as a box of 32 rows.  Storing each lane's
+          // piece directly touched 32 lines per instruction and ran at 2.9 TB/s.
+          constexpr int wide = F32 ? 32 : 64;
+          const int cols = row0 < g.N ? min(S::kTileB, g.D - t.b0) : 0;
+          if (none && cols > 0) {  // one box of zeros for the whole tile
+            const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
+            if (one) bulk_wait_read<kBoxes - 1>();
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = bf16_pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            st_shared_v4(box + lane * 128 + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1],
-                         v[4 * j + 2], v[4 * j + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (one) {
-            tma_store_3d(&map_out, box, t.b0 + c, row0, t.e);
-            bulk_commit();
-          }
-        }
-      } else {
-        const int row = row0 + lane;
-        const int rows = FORM == EX_DGRAD ? g.D : g.N;
-        for (int c = 0; c < t.cnt; c += 32) {
-          uint32_t v[32];
-          tmem_load_32(acc + c, v);
-          if (row < rows) {
-            // a warp holds 32 neighbours of 32 output rows
-            const size_t o = static_cast<size_t>(t.start + c) * rows + row;
-            if (g.out_f32) {
-              float* out = static_cast<float*>(g.out) + o;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c + j < t.cnt) out[static_cast<size_t>(j) * rows] = __uint_as_float(v[j]);
-            } else {
-              unsigned short* out = static_cast<unsigned short*>(g.out) + o;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (c + j < t.cnt)
-                  out[static_cast<size_t>(j) * rows] =
-                      static_cast<unsigned short>(f32_to_bf16_bits(__uint_as_float(v[j])));
+            for (int j = 0; j < 8; ++j) st_shared_v4(box + (j * 32 + lane) * 16, 0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (one) {
+              for (int c = 0; c < cols; c += wide) tma_store_3d(&map_out, box, t.b0 + c, row0, t.e);
+              bulk_commit();
             }
           }
-          __syncwarp();
+          if (add && one) bulk_wait_all();  // what it is added to has arrived
+          for (int c = 0; c < cols && !none; c += wide) {
+            const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
+            uint32_t v[32];
+            if (one) bulk_wait_read<kBoxes - 1>();
+            __syncwarp();
+            if constexpr (F32) {
+              tmem_load_32(acc + c, v);
+            } else {
+              uint32_t u[64];
+              tmem_load_64(acc + c, u);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                v[j] = bf16_pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(box + lane * 128 + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1],
+                           v[4 * j + 2], v[4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (one) {
+              if (add) tma_add_3d(&map_out, box, t.b0 + c, row0, t.e);
+              else tma_store_3d(&map_out, box, t.b0 + c, row0, t.e);
+              bulk_commit();
+            }
+          }
+        } else {
+          const int row = row0 + lane;
+          const int rows = FORM == EX_DGRAD ? g.D : g.N;
+          for (int c = 0; c < t.cnt; c += 32) {
+            uint32_t v[32];
+            tmem_load_32(acc + c, v);
+            // a warp holds 32 neighbours of 32 output rows
+            const size_t o = static_cast<size_t>(t.start + c) * rows + row;
+            if constexpr (F32) {
+              if (row < rows) {
+                float* out = static_cast<float*>(g.out) + o;
+                if (add) {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j, out += rows)
+                    if (c + j < t.cnt) red_add(out, __uint_as_float(v[j]));
+                } else if (c + 32 <= t.cnt) {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j, out += rows) *out = __uint_as_float(v[j]);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j, out += rows)
+                    if (c + j < t.cnt) *out = __uint_as_float(v[j]);
+                }
+              }
+            } else if (row < rows) {
+              unsigned short* out = static_cast<unsigned short*>(g.out) + o;
+              if (c + 32 <= t.cnt) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j, out += rows)
+                  *out = static_cast<unsigned short>(f32_to_bf16_bits(__uint_as_float(v[j])));
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j, out += rows)
+                  if (c + j < t.cnt)
+                    *out = static_cast<unsigned short>(f32_to_bf16_bits(__uint_as_float(v[j])));
+              }
+            }
+            __syncwarp();
+          }
         }
-      }
-      if (!none) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0)
-          mbar_arrive_cluster(CG == 2 ? map_to_rank(smem_addr(&drained[buf]), 0)
-                                      : smem_addr(&drained[buf]));
-        ++n;
+        if (!none) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0)
+            mbar_arrive_cluster(CG == 2 ? map_to_rank(smem_addr(&drained[buf]), 0)
+                                        : smem_addr(&drained[buf]));
+          ++n;
+        }
+        first_slice += max(segment, 1);
       }
     }
     if (FORM == EX_WGRAD && one) bulk_wait_all();
@@ -601,16 +655,15 @@ int resident_clusters(Kern kern, int cg, int smem, std::atomic<int>* known) {
   return n;
 }
 
-template <int FORM, int CG>
+template <int FORM, int CG, bool F32>
 int launch_typed(const ExpertArgs& a, cudaStream_t st) {
   using S = Shape<FORM, CG>;
   static std::atomic<int> known[kDevices];
-  const auto kern = expert_matmul_tc_kernel<FORM, CG>;
+  const auto kern = expert_matmul_tc_kernel<FORM, CG, F32>;
   const int resident = resident_clusters(kern, CG, smem_bytes(FORM), known);
   TcArgs g{a.offsets, a.p2u, a.out, device_status_word(), a.T, a.P, a.E, a.N, a.D,
            FORM == EX_DGRAD || a.p2u == nullptr ? a.P : a.T,
-           a.T > 1 ? static_cast<uint32_t>((1ull << 32) / a.T) : 0xffffffffu,
-           a.out_dtype == DT_F32};
+           a.T > 1 ? static_cast<uint32_t>((1ull << 32) / a.T) : 0xffffffffu};
   if (resident <= 0 || g.status == nullptr) return MR_ERR_CUDA;
   // a and b: weights, or single rows for gathering; the boxes: 16 rows in order
   CUtensorMap ma, mb, ba, bb, out;
@@ -618,7 +671,7 @@ int launch_typed(const ExpertArgs& a, cudaStream_t st) {
   if (FORM == EX_WGRAD) {
     maps = rows_map(&ma, a.a, a.P, a.N, 1) && rows_map(&ba, a.a, a.P, a.N, kDeep) &&
            rows_map(&mb, a.b, g.x_rows, a.D, 1) && rows_map(&bb, a.b, g.x_rows, a.D, 16) &&
-           weight_map(&out, a.out, a, 32, g.out_f32 != 0);
+           weight_map(&out, a.out, a, 32, F32);
   } else {
     const int cols = FORM == EX_FWD ? a.D : a.N;
     maps = weight_map(&ma, a.b, a, FORM == EX_FWD ? kRowsA : kDeep) &&
@@ -652,7 +705,9 @@ int launch_typed(const ExpertArgs& a, cudaStream_t st) {
 template <int FORM>
 int launch_form(const ExpertArgs& a, cudaStream_t st) {
   const bool pair = FORM == EX_WGRAD ? a.N > kRowsA : a.P >= 48ll * a.E;
-  return pair ? launch_typed<FORM, 2>(a, st) : launch_typed<FORM, 1>(a, st);
+  if (a.out_dtype == DT_F32)
+    return pair ? launch_typed<FORM, 2, true>(a, st) : launch_typed<FORM, 1, true>(a, st);
+  return pair ? launch_typed<FORM, 2, false>(a, st) : launch_typed<FORM, 1, false>(a, st);
 }
 
 }  // namespace

@@ -111,6 +111,7 @@ class _CtypesCalls:
         self.router_expert_matmul = L.router_expert_matmul
         self.router_expert_matmul_w4 = L.router_expert_matmul_w4
         self.router_combine_fwd = L.router_combine_fwd
+        self.router_combine_bwd = L.router_combine_bwd
 
 
 def _load_fast():
@@ -566,38 +567,41 @@ def router_aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor
 
 
 # ---- the experts' products and the combination ------------------------------
-def _same_device(t: torch.Tensor, name: str, index: int, dtypes, dim: int) -> torch.Tensor:
-    """``t`` checked (device, dtype, number of dimensions)."""
-    if t.get_device() != index or t.dtype not in dtypes or t.dim() != dim:
-        raise ValueError(f"{name} must be a {dim}-dimensional tensor of {dtypes} on cuda:{index}")
+# One token's calls take a few microseconds on the GPU, so the host's part is
+# written flat: every check reads tensor attributes directly, and the helpers
+# below run only to copy a strided input or to say what is wrong.
+_I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+_empty = torch.empty
+
+
+def _bad(name: str, what: str):
+    raise ValueError(f"{name} must be {what}")
+
+
+def _rows_2d(t: torch.Tensor, name: str, index: int | None, dtypes) -> torch.Tensor:
+    """Row input that did not pass the caller's quick test: copied if strided,
+    refused if wrong."""
+    t = _as_input(t, name, dtypes)
+    if index is not None and t.get_device() != index:
+        _bad(name, f"on cuda:{index}")
     return t
 
 
-def _map_input(t: torch.Tensor, name: str, index: int, numel: int | None = None) -> torch.Tensor:
-    if t.get_device() != index or t.dtype != torch.int32 or t.dim() != 1 \
+def _map_1d(t: torch.Tensor, name: str, index: int, numel: int | None) -> torch.Tensor:
+    """Expert map that did not pass the caller's quick test."""
+    if t.get_device() != index or t.dtype is not _I32 or t.dim() != 1 \
             or (numel is not None and t.numel() != numel):
-        raise ValueError(f"{name} must be a 1-dimensional int32 tensor"
-                         f"{'' if numel is None else f' of {numel} elements'} on cuda:{index}")
-    return t if t.is_contiguous() else t.contiguous()
+        _bad(name, f"a 1-dimensional int32 tensor"
+                   f"{'' if numel is None else f' of {numel} elements'} on cuda:{index}")
+    return t.contiguous()
 
 
-def _weight_input(t: torch.Tensor, name: str, index: int, dtypes) -> torch.Tensor:
-    _same_device(t, name, index, dtypes, 3)
-    if not t.is_contiguous():  # a copy at each call would cost more than the product
-        raise ValueError(f"{name} must be contiguous")
-    return t
-
-
-def _expert_rows(x, weight_dim, offsets, p2u, E):
-    """Checked (x, offsets, p2u) of a product; and T, P."""
-    dev = x.get_device()
-    offsets = _map_input(offsets, "expert_first_token_offset", dev, E + 1)
-    if x.shape[1] != weight_dim:
-        raise ValueError(f"x must have {weight_dim} columns")
-    if p2u is None:
-        return x, offsets, None, 0, x.shape[0]
-    p2u = _map_input(p2u, "permuted_to_unpermuted", dev)
-    return x, offsets, p2u, x.shape[0], p2u.numel()
+def _weight_3d(t: torch.Tensor, name: str, index: int, dtype):
+    """Refuse a weight that did not pass the caller's quick test (a copy at
+    each call would cost more than the product)."""
+    if t.get_device() != index or t.dtype is not dtype or t.dim() != 3:
+        _bad(name, f"a 3-dimensional {dtype} tensor on cuda:{index}")
+    _bad(name, "contiguous")
 
 
 def router_expert_matmul(x: torch.Tensor, weight: torch.Tensor,
@@ -610,21 +614,46 @@ def router_expert_matmul(x: torch.Tensor, weight: torch.Tensor,
     router_expert_maps) x is the tokens [T, D], read through the map; without
     it x is the permuted rows [P, D].  Rows that no expert owns are left as
     they were in ``out``."""
-    x = _as_input(x, "x", _DTYPE)
-    dev = x.device
-    weight = _weight_input(weight, "weight", dev.index, (x.dtype,))
+    dt = x.dtype
+    if not x.is_cuda or dt not in _DTYPE or x.dim() != 2 or not x.is_contiguous():
+        x = _rows_2d(x, "x", None, _DTYPE)
+    idx = x.get_device()
+    if weight.get_device() != idx or weight.dtype is not dt or weight.dim() != 3 \
+            or not weight.is_contiguous():
+        _weight_3d(weight, "weight", idx, dt)
     E, N, D = weight.shape
-    x, offsets, p2u, T, P = _expert_rows(x, D, expert_first_token_offset,
-                                         permuted_to_unpermuted, E)
-    odt = x.dtype if out_dtype is None else out_dtype
+    T, cols = x.shape
+    if cols != D:
+        _bad("x", f"[rows, {D}]")
+    off = expert_first_token_offset
+    if off.get_device() != idx or off.dtype is not _I32 or off.shape != (E + 1,) \
+            or not off.is_contiguous():
+        off = _map_1d(off, "expert_first_token_offset", idx, E + 1)
+    p2u = permuted_to_unpermuted
+    if p2u is None:
+        P, p2u_ptr = T, 0
+    else:
+        if p2u.get_device() != idx or p2u.dtype is not _I32 or p2u.dim() != 1 \
+                or not p2u.is_contiguous():
+            p2u = _map_1d(p2u, "permuted_to_unpermuted", idx, None)
+        P, p2u_ptr = p2u.numel(), p2u.data_ptr()
+    odt = dt if out_dtype is None else out_dtype
     if odt not in _DTYPE:
-        raise ValueError(f"out_dtype must be one of {list(_DTYPE)}")
-    out = _out(out, (P, N), odt, dev, "out")
-    with _on(dev):
-        rc = _calls().router_expert_matmul(x.data_ptr(), _DTYPE[x.dtype], weight.data_ptr(),
-                                           offsets.data_ptr(), _ptr0(p2u), T, P, E, N, D,
-                                           out.data_ptr(), _DTYPE[odt], _stream(dev))
-    _check("router_expert_matmul", rc)
+        _bad("out_dtype", f"one of {list(_DTYPE)}")
+    if out is None:
+        out = _empty((P, N), dtype=odt, device=x.device)
+    else:
+        out = _out(out, (P, N), odt, x.device, "out")
+    call = _calls().router_expert_matmul
+    args = (x.data_ptr(), _DTYPE[dt], weight.data_ptr(), off.data_ptr(), p2u_ptr, T, P, E, N, D,
+            out.data_ptr(), _DTYPE[odt], _raw_stream(idx))
+    if idx == _cur_dev():
+        rc = call(*args)
+    else:
+        with torch.cuda.device(idx):
+            rc = call(*args)
+    if rc != 0:
+        raise RouterError("router_expert_matmul", rc)
     return out
 
 
@@ -636,20 +665,23 @@ def router_expert_matmul_bwd_input(grad_out: torch.Tensor, weight: torch.Tensor,
     router_combine_fwd without weights sums a token's rows."""
     grad_out = _as_input(grad_out, "grad_out", _DTYPE)
     dev = grad_out.device
-    weight = _weight_input(weight, "weight", dev.index, (grad_out.dtype,))
+    idx, dt = dev.index, grad_out.dtype
+    if weight.get_device() != idx or weight.dtype is not dt or weight.dim() != 3 \
+            or not weight.is_contiguous():
+        _weight_3d(weight, "weight", idx, dt)
     E, N, D = weight.shape
-    offsets = _map_input(expert_first_token_offset, "expert_first_token_offset", dev.index, E + 1)
-    if grad_out.shape[1] != N:
-        raise ValueError(f"grad_out must have {N} columns")
+    off = _map_1d(expert_first_token_offset, "expert_first_token_offset", idx, E + 1)
     P = grad_out.shape[0]
-    odt = grad_out.dtype if out_dtype is None else out_dtype
+    if grad_out.shape[1] != N:
+        _bad("grad_out", f"[P, {N}]")
+    odt = dt if out_dtype is None else out_dtype
     if odt not in _DTYPE:
-        raise ValueError(f"out_dtype must be one of {list(_DTYPE)}")
+        _bad("out_dtype", f"one of {list(_DTYPE)}")
     grad_x = _out(grad_x, (P, D), odt, dev, "grad_x")
     with _on(dev):
         rc = lib().router_expert_matmul_bwd_input(
-            _ptr(grad_out), _DTYPE[grad_out.dtype], _ptr(weight), _ptr(offsets), P, E, N, D,
-            _ptr(grad_x), _DTYPE[odt], _stream(dev))
+            _ptr(grad_out), _DTYPE[dt], _ptr(weight), _ptr(off), P, E, N, D, _ptr(grad_x),
+            _DTYPE[odt], _stream(dev))
     _check("router_expert_matmul_bwd_input", rc)
     return grad_x
 
@@ -662,23 +694,25 @@ def router_expert_matmul_bwd_weight(grad_out: torch.Tensor, x: torch.Tensor,
     ``out_dtype`` (default: x's); experts without rows get zeros.  x and the
     map as in the forward."""
     grad_out = _as_input(grad_out, "grad_out", _DTYPE)
-    x = _as_input(x, "x", (grad_out.dtype,))
     dev = grad_out.device
-    if x.get_device() != dev.index:
-        raise ValueError("x must be on grad_out's device")
-    E = expert_first_token_offset.numel() - 1
-    N, D = grad_out.shape[1], x.shape[1]
-    x, offsets, p2u, T, P = _expert_rows(x, D, expert_first_token_offset,
-                                         permuted_to_unpermuted, E)
-    if grad_out.shape[0] != P:
-        raise ValueError(f"grad_out must have {P} rows")
-    odt = x.dtype if out_dtype is None else out_dtype
+    idx, dt = dev.index, grad_out.dtype
+    x = _rows_2d(x, "x", idx, (dt,))
+    off = _map_1d(expert_first_token_offset, "expert_first_token_offset", idx, None)
+    E = off.numel() - 1
+    T, D = x.shape
+    P, N = grad_out.shape
+    p2u = permuted_to_unpermuted
+    if p2u is not None:
+        p2u = _map_1d(p2u, "permuted_to_unpermuted", idx, P)
+    elif T != P:
+        _bad("x", f"[{P}, D] without a map")
+    odt = dt if out_dtype is None else out_dtype
     if odt not in _DTYPE:
-        raise ValueError(f"out_dtype must be one of {list(_DTYPE)}")
+        _bad("out_dtype", f"one of {list(_DTYPE)}")
     grad_weight = _out(grad_weight, (E, N, D), odt, dev, "grad_weight")
     with _on(dev):
         rc = lib().router_expert_matmul_bwd_weight(
-            _ptr(grad_out), _DTYPE[x.dtype], _ptr(x), _ptr(offsets), _ptr(p2u), T, P, E, N, D,
+            _ptr(grad_out), _DTYPE[dt], _ptr(x), _ptr(off), _ptr(p2u), T, P, E, N, D,
             _ptr(grad_weight), _DTYPE[odt], _stream(dev))
     _check("router_expert_matmul_bwd_weight", rc)
     return grad_weight
@@ -694,47 +728,76 @@ def router_expert_matmul_w4(x: torch.Tensor, qweight: torch.Tensor, scales: torc
     scales [E, N, D / group] bf16, zeros the same in uint8 (0..15) or None for
     8; group 32, 64 or 128.  Returns out [P, N] in ``out_dtype`` (default
     bf16)."""
-    x = _as_input(x, "x", (torch.bfloat16,))
-    dev = x.device
-    qweight = _weight_input(qweight, "qweight", dev.index, (torch.uint8,))
-    scales = _weight_input(scales, "scales", dev.index, (torch.bfloat16,))
-    E, N, half = qweight.shape
-    D, groups = 2 * half, scales.shape[2]
-    if scales.shape[:2] != (E, N) or groups < 1 or D % groups != 0:
-        raise ValueError("scales must be [E, N, D / group]")
-    if zeros is not None:
-        zeros = _weight_input(zeros, "zeros", dev.index, (torch.uint8,))
-        if zeros.shape != scales.shape:
-            raise ValueError("zeros must have the shape of scales")
-    x, offsets, p2u, T, P = _expert_rows(x, D, expert_first_token_offset,
-                                         permuted_to_unpermuted, E)
+    if not x.is_cuda or x.dtype is not _BF16 or x.dim() != 2 or not x.is_contiguous():
+        x = _rows_2d(x, "x", None, (_BF16,))
     if x.data_ptr() & 15:
         x = x.clone()
-    odt = torch.bfloat16 if out_dtype is None else out_dtype
+    idx = x.get_device()
+    if qweight.get_device() != idx or qweight.dtype is not _U8 or qweight.dim() != 3 \
+            or not qweight.is_contiguous():
+        _weight_3d(qweight, "qweight", idx, _U8)
+    if scales.get_device() != idx or scales.dtype is not _BF16 or scales.dim() != 3 \
+            or not scales.is_contiguous():
+        _weight_3d(scales, "scales", idx, _BF16)
+    E, N, half = qweight.shape
+    Es, Ns, groups = scales.shape
+    D = 2 * half
+    if Es != E or Ns != N or groups < 1 or D % groups != 0:
+        _bad("scales", "[E, N, D / group]")
+    z_ptr = 0
+    if zeros is not None:
+        if zeros.get_device() != idx or zeros.dtype is not _U8 or zeros.dim() != 3 \
+                or not zeros.is_contiguous():
+            _weight_3d(zeros, "zeros", idx, _U8)
+        if zeros.shape != scales.shape:
+            _bad("zeros", "of the shape of scales")
+        z_ptr = zeros.data_ptr()
+    T, cols = x.shape
+    if cols != D:
+        _bad("x", f"[rows, {D}]")
+    off = expert_first_token_offset
+    if off.get_device() != idx or off.dtype is not _I32 or off.shape != (E + 1,) \
+            or not off.is_contiguous():
+        off = _map_1d(off, "expert_first_token_offset", idx, E + 1)
+    p2u = permuted_to_unpermuted
+    if p2u is None:
+        P, p2u_ptr = T, 0
+    else:
+        if p2u.get_device() != idx or p2u.dtype is not _I32 or p2u.dim() != 1 \
+                or not p2u.is_contiguous():
+            p2u = _map_1d(p2u, "permuted_to_unpermuted", idx, None)
+        P, p2u_ptr = p2u.numel(), p2u.data_ptr()
+    odt = _BF16 if out_dtype is None else out_dtype
     if odt not in _DTYPE:
-        raise ValueError(f"out_dtype must be one of {list(_DTYPE)}")
-    out = _out(out, (P, N), odt, dev, "out")
-    with _on(dev):
-        rc = _calls().router_expert_matmul_w4(
-            x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), _ptr0(zeros), D // groups,
-            offsets.data_ptr(), _ptr0(p2u), T, P, E, N, D, out.data_ptr(), _DTYPE[odt],
-            _stream(dev))
-    _check("router_expert_matmul_w4", rc)
+        _bad("out_dtype", f"one of {list(_DTYPE)}")
+    if out is None:
+        out = _empty((P, N), dtype=odt, device=x.device)
+    else:
+        out = _out(out, (P, N), odt, x.device, "out")
+    call = _calls().router_expert_matmul_w4
+    args = (x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), z_ptr, D // groups,
+            off.data_ptr(), p2u_ptr, T, P, E, N, D, out.data_ptr(), _DTYPE[odt],
+            _raw_stream(idx))
+    if idx == _cur_dev():
+        rc = call(*args)
+    else:
+        with torch.cuda.device(idx):
+            rc = call(*args)
+    if rc != 0:
+        raise RouterError("router_expert_matmul_w4", rc)
     return out
 
 
-def _combine_weights(topk_weights, T, K, dev):
-    """Checked weights and their row stride (a column view of a wider buffer is read in place)."""
-    if topk_weights is None:
-        return None, 0
-    if topk_weights.dtype != torch.float32 or topk_weights.shape != (T, K) \
-            or topk_weights.get_device() != dev:
-        raise ValueError(f"topk_weights must be a float32 [{T}, {K}] tensor on cuda:{dev}")
-    if T == 0:
-        return topk_weights, K
-    if topk_weights.stride(1) != 1 or topk_weights.stride(0) < K:
-        topk_weights = topk_weights.contiguous()
-    return topk_weights, (topk_weights.stride(0) if T > 1 else K)
+def _combine_weights(w: torch.Tensor, T: int, K: int, idx: int):
+    """Checked combination weights and their row stride (a column view of a
+    wider buffer is read in place)."""
+    if w.dtype is not _F32 or w.shape != (T, K) or w.get_device() != idx:
+        _bad("topk_weights", f"a float32 [{T}, {K}] tensor on cuda:{idx}")
+    if w.is_contiguous():
+        return w, K
+    if w.stride(1) != 1 or w.stride(0) < K:
+        return w.contiguous(), K
+    return w, w.stride(0)
 
 
 def router_combine_fwd(expert_out: torch.Tensor, unpermuted_to_permuted: torch.Tensor, K: int,
@@ -743,21 +806,36 @@ def router_combine_fwd(expert_out: torch.Tensor, unpermuted_to_permuted: torch.T
     [T, K] (None: plain sums).  expert_out [T K, D] in the maps' order; the map
     is router_expert_maps's.  Returns out [T, D] in expert_out's dtype; a choice
     with map entry -1 adds nothing."""
-    expert_out = _as_input(expert_out, "expert_out", _DTYPE)
-    dev = expert_out.device
+    z, u2p = expert_out, unpermuted_to_permuted
+    if not z.is_cuda or z.dtype not in _DTYPE or z.dim() != 2 or not z.is_contiguous():
+        z = _rows_2d(z, "expert_out", None, _DTYPE)
+    idx, dt = z.get_device(), z.dtype
+    P, D = z.shape
+    if u2p.get_device() != idx or u2p.dtype is not _I32 or u2p.shape != (P,) \
+            or not u2p.is_contiguous():
+        u2p = _map_1d(u2p, "unpermuted_to_permuted", idx, P)
     K = int(K)
-    P, D = expert_out.shape
-    u2p = _map_input(unpermuted_to_permuted, "unpermuted_to_permuted", dev.index, P)
     if K < 1 or P % K != 0:
-        raise ValueError("expert_out must have T K rows")
+        _bad("expert_out", "[T K, D]")
     T = P // K
-    weights, ld = _combine_weights(topk_weights, T, K, dev.index)
-    out = _out(out, (T, D), expert_out.dtype, dev, "out")
-    with _on(dev):
-        rc = _calls().router_combine_fwd(expert_out.data_ptr(), _DTYPE[expert_out.dtype],
-                                         u2p.data_ptr(), _ptr0(weights), ld, T, K, D,
-                                         out.data_ptr(), _stream(dev))
-    _check("router_combine_fwd", rc)
+    w_ptr = ld = 0
+    if topk_weights is not None:
+        topk_weights, ld = _combine_weights(topk_weights, T, K, idx)
+        w_ptr = topk_weights.data_ptr()
+    if out is None:
+        out = _empty((T, D), dtype=dt, device=z.device)
+    else:
+        out = _out(out, (T, D), dt, z.device, "out")
+    call = _calls().router_combine_fwd
+    args = (z.data_ptr(), _DTYPE[dt], u2p.data_ptr(), w_ptr, ld, T, K, D, out.data_ptr(),
+            _raw_stream(idx))
+    if idx == _cur_dev():
+        rc = call(*args)
+    else:
+        with torch.cuda.device(idx):
+            rc = call(*args)
+    if rc != 0:
+        raise RouterError("router_combine_fwd", rc)
     return out
 
 
@@ -768,23 +846,49 @@ def router_combine_bwd(grad_out: torch.Tensor, unpermuted_to_permuted: torch.Ten
     """Gradients of router_combine_fwd: (grad_expert_out [T K, D] in grad_out's
     dtype, grad_weights [T, K] float32, or None when ``expert_out`` is None).
     Rows of grad_expert_out that no choice names are left as they were."""
-    grad_out = _as_input(grad_out, "grad_out", _DTYPE)
-    dev = grad_out.device
+    g, u2p, z = grad_out, unpermuted_to_permuted, expert_out
+    if not g.is_cuda or g.dtype not in _DTYPE or g.dim() != 2 or not g.is_contiguous():
+        g = _rows_2d(g, "grad_out", None, _DTYPE)
+    idx, dt = g.get_device(), g.dtype
+    dev = g.device
+    T, D = g.shape
     K = int(K)
-    T, D = grad_out.shape
-    u2p = _map_input(unpermuted_to_permuted, "unpermuted_to_permuted", dev.index, T * K)
-    weights, ld = _combine_weights(topk_weights, T, K, dev.index)
-    if expert_out is not None:
-        expert_out = _as_input(expert_out, "expert_out", (grad_out.dtype,))
-        if expert_out.shape != (T * K, D) or expert_out.get_device() != dev.index:
-            raise ValueError(f"expert_out must be [{T * K}, {D}] on grad_out's device")
-        grad_weights = _out(grad_weights, (T, K), torch.float32, dev, "grad_weights")
+    if K < 1:
+        _bad("K", "at least 1")
+    P = T * K
+    if u2p.get_device() != idx or u2p.dtype is not _I32 or u2p.shape != (P,) \
+            or not u2p.is_contiguous():
+        u2p = _map_1d(u2p, "unpermuted_to_permuted", idx, P)
+    w_ptr = ld = z_ptr = gw_ptr = 0
+    if topk_weights is not None:
+        topk_weights, ld = _combine_weights(topk_weights, T, K, idx)
+        w_ptr = topk_weights.data_ptr()
+    if z is not None:
+        if z.get_device() != idx or z.dtype is not dt or z.shape != (P, D) \
+                or not z.is_contiguous():
+            z = _rows_2d(z, "expert_out", idx, (dt,))
+            if z.shape != (P, D):
+                _bad("expert_out", f"[{P}, {D}]")
+        z_ptr = z.data_ptr()
+        if grad_weights is None:
+            grad_weights = _empty((T, K), dtype=_F32, device=dev)
+        else:
+            grad_weights = _out(grad_weights, (T, K), _F32, dev, "grad_weights")
+        gw_ptr = grad_weights.data_ptr()
     elif grad_weights is not None:
         raise ValueError("grad_weights needs expert_out")
-    grad_expert_out = _out(grad_expert_out, (T * K, D), grad_out.dtype, dev, "grad_expert_out")
-    with _on(dev):
-        rc = lib().router_combine_bwd(_ptr(grad_out), _DTYPE[grad_out.dtype], _ptr(u2p),
-                                      _ptr(expert_out), _ptr(weights), ld, T, K, D,
-                                      _ptr(grad_expert_out), _ptr(grad_weights), _stream(dev))
-    _check("router_combine_bwd", rc)
+    if grad_expert_out is None:
+        grad_expert_out = _empty((P, D), dtype=dt, device=dev)
+    else:
+        grad_expert_out = _out(grad_expert_out, (P, D), dt, dev, "grad_expert_out")
+    call = _calls().router_combine_bwd
+    args = (g.data_ptr(), _DTYPE[dt], u2p.data_ptr(), z_ptr, w_ptr, ld, T, K, D,
+            grad_expert_out.data_ptr(), gw_ptr, _raw_stream(idx))
+    if idx == _cur_dev():
+        rc = call(*args)
+    else:
+        with torch.cuda.device(idx):
+            rc = call(*args)
+    if rc != 0:
+        raise RouterError("router_combine_bwd", rc)
     return grad_expert_out, grad_weights

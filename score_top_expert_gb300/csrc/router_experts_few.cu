@@ -5,18 +5,20 @@
 //   4-bit: w[e, n, d] = s[e, n, g] (q[e, n, d] - z[e, n, g]),  d in group g
 //
 // The weights of the experts that have rows are the traffic and are read once
-// for up to 8 of an expert's rows.  A warp takes 16 weight rows at a time
-// through a ring of shared-memory stages of its own, 256 bytes of each row a
-// stage, filled by asynchronous copies three stages ahead, across tasks: no
-// warp waits for another, and 12 warps an SM keep about 147 KB in flight.  With
-// fewer tasks than warps the four warps of a block take a quarter of the
-// contraction each and add up in shared memory in a fixed order.
+// for up to 8 of an expert's rows.  A block's task is such a group of rows and a
+// span of the expert's weight rows: the rows of x are staged in shared memory in
+// the order the fragments want, then each of the 16 warps takes 16 weight rows
+// through two shared-memory stages of its own, 256 bytes of each row a stage,
+// filled by asynchronous copies a stage ahead, across tasks: 64 KB in flight on
+// an SM while the block changes its x.  With few tasks four
+// warps share 16 weight rows, a quarter of the contraction each, and add up in
+// shared memory in a fixed order.
 //
 // mma.sync m16n8k16 (16 weight rows, 8 permuted rows, fp32 sums) suits the
 // shape: a tcgen05 product would be 128 weight rows wide and needs the operand
 // pipeline that costs the latency here; neither is near its peak rate.  Which
 // columns of x meet which of w is free as long as both fragments agree, so a
-// thread takes 16 consecutive bytes of a row.
+// thread takes 16 consecutive bytes of a weight row.
 //
 // 4-bit arithmetic.  A nibble q becomes the bf16 128 + q by placing it in the
 // low mantissa bits of 128 (one and/or for two nibbles), and a bf16
@@ -28,6 +30,7 @@
 // words t V .. t V + V - 1 of each group (V = group / 32), so that a product's 16
 // columns lie in one group.
 #include <atomic>
+#include <climits>
 
 #include "router_common.cuh"
 #include "router_experts.cuh"
@@ -36,12 +39,15 @@
 namespace moe_router {
 namespace {
 
-constexpr int kRows = 16;         // weight rows per task
+constexpr int kRows = 16;         // weight rows per tile
 constexpr int kTokens = 8;        // permuted rows per task
-constexpr int kWarps = 4;         // per block
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kShare = 4;         // warps that share a tile when there are few
 constexpr int kChunk = 256;       // bytes of a weight row per stage
-constexpr int kStages = 4;
-constexpr int kBlocksPerSm = 3;
+constexpr int kStages = 2;
+constexpr int kStageBytes = kRows * kChunk;
+constexpr int kPanel = 4096;      // columns of x staged at a time
 
 // V: 32-bit words a thread takes of each step; 0: bf16 weights.
 template <int V>
@@ -55,18 +61,33 @@ struct Layout {
   static __device__ __forceinline__ int swizzle(int row) { return (row * kSwizzle) & 7; }
 };
 
-constexpr int kStageBytes = kRows * kChunk;
+// Bytes between staged rows of x: eight 16-byte reads of two neighbouring rows
+// fall into different banks.
+__host__ __device__ constexpr int x_pitch(int D) {
+  return ((D < kPanel ? D : kPanel) * 2 + 127) / 128 * 128 + 64;
+}
 
-// Dynamic shared memory: the rings, then the experts' prefix.
-constexpr int few_smem(int E) { return kWarps * kStages * kStageBytes + (E + 1) * 4; }
+// Dynamic shared memory: the rings, x, the experts' prefix.
+constexpr int few_smem(int E, int D) {
+  return kWarps * kStages * kStageBytes + kTokens * x_pitch(D) + (E + 1) * 4;
+}
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with sums that start at zero.
+__device__ __forceinline__ void mma_16816_from_zero(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                    uint32_t a2, uint32_t a3, uint32_t b0,
+                                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // nibbles i and i + 4 of w as the bf16 pair (q - z, q - z); zp = 128 + z twice
@@ -96,15 +117,18 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// V consecutive words of shared memory.
 template <int V>
-__device__ __forceinline__ void load_words(uint32_t at, uint32_t (&w)[V == 0 ? 4 : V]) {
-  if constexpr (V == 0 || V == 4)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
-  else if constexpr (V == 2)
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
-  else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+__device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[V]) {
+  if constexpr (V == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (V == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(at);
+  }
 }
 
 struct FewArgs {
@@ -118,228 +142,294 @@ struct FewArgs {
   int T, P, E, N, D, out_dtype;
 };
 
-// A task: up to 8 permuted rows of an expert and 16 of its weight rows.
+__device__ __forceinline__ void store_value(const FewArgs& g, size_t i, float v) {
+  if (g.out_dtype == DT_F32) static_cast<float*>(g.out)[i] = v;
+  else static_cast<unsigned short*>(g.out)[i] = static_cast<unsigned short>(f32_to_bf16_bits(v));
+}
+
+// The four warps of a team.
+__device__ __forceinline__ void team_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(32 * kShare) : "memory");
+}
+
+// A task: up to 8 permuted rows of an expert and a span of its weight tiles.
 struct Task {
-  int e, p0, cnt, n0;
+  int e, p0, cnt;
+  int first, last;  // weight tiles
 };
 
-__device__ __forceinline__ Task task_of(const FewArgs& g, const int* prefix, long long i,
-                                        int row_tiles) {
-  // an expert's 8-row groups follow one another for the same weight rows
+__device__ __forceinline__ Task task_of(const FewArgs& g, const int* prefix, int i, int spans,
+                                        int span, int row_tiles) {
+  // an expert's 8-row groups follow one another for the same weights
   Task t;
-  t.e = expert_of_tile(prefix, g.E, static_cast<int>(i / row_tiles));
+  t.e = expert_of_tile(prefix, g.E, i / spans);
   const int first = prefix[t.e], groups = prefix[t.e + 1] - first;
-  const int r = static_cast<int>(i - static_cast<long long>(first) * row_tiles);
-  t.n0 = r / groups * kRows;
+  const int r = i - first * spans;
+  const int s = groups == 1 ? r : r / groups;
+  t.first = s * span;
+  t.last = min(t.first + span, row_tiles);
   int lo, hi;
   expert_rows(g.offsets, t.e, g.P, &lo, &hi);
-  t.p0 = lo + (r % groups) * kTokens;
+  t.p0 = lo + (r - s * groups) * kTokens;
   t.cnt = min(kTokens, hi - t.p0);
   return t;
 }
 
-template <int V, bool ZEROS, bool SPLIT>
-__global__ __launch_bounds__(32 * kWarps, kBlocksPerSm) void expert_matmul_few_kernel(FewArgs g) {
+// Scales (low half) and zero points of one chunk of 16 weight rows: the quad's
+// lanes hold every fourth group of both of its rows and hand them round.
+template <int V>
+struct Meta {
+  static constexpr int kHeld = V == 0 ? 1 : (Layout<V>::kSteps + 3) / 4;
+  uint32_t a[kHeld], b[kHeld];
+
+  // ra, rb: the rows' first group
+  template <bool ZEROS>
+  __device__ __forceinline__ void load(const FewArgs& g, size_t ra, size_t rb, int c, int groups,
+                                       int t) {
+    if constexpr (V > 0) {
+      const unsigned short* scales = static_cast<const unsigned short*>(g.scales);
+      const int g0 = c * Layout<V>::kSteps + t;
+      const unsigned short *sa = scales + ra + g0, *sb = scales + rb + g0;
+      const uint8_t *za = g.zeros + ra + g0, *zb = g.zeros + rb + g0;
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) {
+        a[j] = b[j] = 0u;
+        if (g0 + 4 * j < groups) {
+          a[j] = sa[4 * j];
+          b[j] = sb[4 * j];
+          if (ZEROS) {
+            a[j] |= (za[4 * j] & 15u) << 16;
+            b[j] |= (zb[4 * j] & 15u) << 16;
+          }
+        }
+      }
+    }
+  }
+};
+
+template <int V, bool ZEROS, bool SHARED>
+__global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs g) {
   using L = Layout<V>;
-  extern __shared__ __align__(16) uint8_t ring[];
-  int* prefix = reinterpret_cast<int*>(ring + kWarps * kStages * kStageBytes);
+  constexpr int kTeams = SHARED ? kWarps / kShare : kWarps;  // of warps with a tile of their own
+  constexpr int span = kTeams;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* xs = smem + kWarps * kStages * kStageBytes;
+  const int pitch = x_pitch(g.D);
+  int* prefix = reinterpret_cast<int*>(xs + kTokens * pitch);
   __shared__ int tmp[33];
-  __shared__ float part[SPLIT ? kWarps : 1][kTokens][kRows + 1];
+  __shared__ float part[SHARED ? kWarps : 1][kTokens][kRows + 1];
 
   pdl_enter();
   const int row_tiles = (g.N + kRows - 1) / kRows;
-  const long long tasks =
-      static_cast<long long>(expert_tile_prefix(g.offsets, g.E, g.P, kTokens, prefix, tmp)) *
-      row_tiles;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int spans = (row_tiles + span - 1) / span;
+  const int tasks = expert_tile_prefix(g.offsets, g.E, g.P, kTokens, prefix, tmp) * spans;
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int team = SHARED ? warp / kShare : warp, member = SHARED ? warp % kShare : 0;
   const int gq = lane >> 2, t = lane & 3;  // fragment row (and token), place in the quad
-  const long long row_bytes = V == 0 ? 2ll * g.D : g.D / 2;
+  const int row_bytes = V == 0 ? 2 * g.D : g.D / 2;
   const int groups = V == 0 ? 0 : g.D / L::kStep;
   const int chunks = (g.D + L::kPerChunk - 1) / L::kPerChunk;
-  // this warp's chunks of each task
-  const int per = (chunks + kWarps - 1) / kWarps;
-  const int c0 = SPLIT ? min(warp * per, chunks) : 0;
-  const int c1 = SPLIT ? min(c0 + per, chunks) : chunks;
-  const long long first = SPLIT ? blockIdx.x : static_cast<long long>(blockIdx.x) * kWarps + warp;
-  const long long step = SPLIT ? gridDim.x : static_cast<long long>(gridDim.x) * kWarps;
-  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+  // this warp's chunks of each tile
+  const int per = SHARED ? (chunks + kShare - 1) / kShare : chunks;
+  const int c0 = min(member * per, chunks), c1 = min(c0 + per, chunks);
+  const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
                            warp * kStages * kStageBytes;
 
   // ---- copies: a cursor kStages - 1 stages ahead of the products -----------------
-  long long li = first;  // task and chunk the next copy belongs to
-  int lc = c0, lstage = 0;
-  const uint8_t* lsrc = nullptr;  // this lane's piece of the first row it copies
-  int lrows = 0;                  // weight rows of the task that exist
-  const int piece = (lane & 15) * 16, half = lane >> 4;  // 16 lanes copy a row, two rows at a time
-  auto begin_copies = [&]() {
-    if (li < tasks) {
-      const Task k = task_of(g, prefix, li, row_tiles);
-      lsrc = g.w + (static_cast<long long>(k.e) * g.N + k.n0 + half) * row_bytes + piece;
-      lrows = g.N - k.n0;
+  int li = blockIdx.x, ltile = 0, llast = 0, le = 0, lc = c0, lstage = 0;
+  const int half = lane >> 4;  // 16 lanes copy a row, two rows at a time
+  const int piece = (lane & 15) * 16;
+  const uint8_t* lsrc = nullptr;  // this lane's piece of the first row it copies, at chunk c0
+  auto next_tile = [&](bool fresh) {  // the cursor's tile: in its task, or the first of a later one
+    if (!fresh) ltile += kTeams;
+    while (li < tasks && (fresh || ltile >= llast)) {
+      if (!fresh) li += gridDim.x;
+      fresh = false;
+      if (li >= tasks) break;
+      const Task k = task_of(g, prefix, li, spans, span, row_tiles);
+      le = k.e;
+      ltile = k.first + team;
+      llast = k.last;
     }
+    lsrc = g.w + (static_cast<size_t>(le) * g.N + ltile * kRows + half) * row_bytes +
+           c0 * kChunk + piece;
   };
   auto copy_stage = [&]() {
-    if (li < tasks && c0 < c1) {
-      const long long col = static_cast<long long>(lc) * kChunk;
-      const bool inside = col + piece < row_bytes;
-      const uint32_t dst = ring_at + lstage * kStageBytes;
+    if (li < tasks) {
+      const uint32_t dst = ring_at + lstage * kStageBytes + half * kChunk;
+      if (ltile * kRows + kRows <= g.N && lc * kChunk + kChunk <= row_bytes) {
 #pragma unroll
-      for (int j = 0; j < kRows / 2; ++j) {
+        for (int j = 0; j < kRows / 2; ++j)
+          copy_16(dst + 2 * j * kChunk + (((lane & 15) ^ L::swizzle(2 * j + half)) << 4),
+                  lsrc + 2 * j * row_bytes, true);
+      } else {
         // rows past the last and columns past the row are filled with zeros
-        const int row = 2 * j + half;
-        const bool ok = inside && row < lrows;
-        copy_16(dst + row * kChunk + (((lane & 15) ^ L::swizzle(row)) << 4), ok ? lsrc + 2 * j * row_bytes + col : g.w, ok);
+        const bool inside = lc * kChunk + piece < row_bytes;
+#pragma unroll 1
+        for (int j = 0; j < kRows / 2; ++j) {
+          const bool ok = inside && ltile * kRows + half + 2 * j < g.N;
+          copy_16(dst + 2 * j * kChunk + (((lane & 15) ^ L::swizzle(2 * j + half)) << 4),
+                  ok ? lsrc + 2 * j * row_bytes : g.w, ok);
+        }
       }
+      lsrc += kChunk;
       if (++lc == c1) {
         lc = c0;
-        li += step;
-        begin_copies();
+        next_tile(false);
       }
     }
     if (++lstage == kStages) lstage = 0;
     copies_commit();
   };
-  begin_copies();
+  if (c0 < c1) next_tile(true);
+  else li = tasks;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) copy_stage();
 
   const unsigned short* __restrict__ x = static_cast<const unsigned short*>(g.x);
-  const unsigned short* __restrict__ scales = static_cast<const unsigned short*>(g.scales);
+  const uint8_t* const x_at = xs + gq * pitch + t * 16;
   int stage = 0;
-  for (long long i = first; i < tasks; i += step) {
-    const Task k = task_of(g, prefix, i, row_tiles);
-    // tokens past the last repeat it; their results are not stored
-    const int src = max(source_row(g.p2u, g.T, k.p0 + min(gq, k.cnt - 1)), 0);
-    const unsigned short* xr = x + static_cast<size_t>(src) * g.D;
-    const size_t ra = (static_cast<size_t>(k.e) * g.N + min(k.n0 + gq, g.N - 1)) * groups;
-    const size_t rb = (static_cast<size_t>(k.e) * g.N + min(k.n0 + gq + 8, g.N - 1)) * groups;
+  for (int i = blockIdx.x; i < tasks; i += gridDim.x) {
+    const Task k = task_of(g, prefix, i, spans, span, row_tiles);
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = c0; c < c1; ++c) {
-      copy_stage();
-      // Scales (low half) and zero points of this chunk: the quad's lanes hold
-      // every fourth group of both rows and hand them round.
-      constexpr int kHeld = V == 0 ? 1 : (L::kSteps + 3) / 4;
-      uint32_t ma[kHeld], mb[kHeld];
-      if constexpr (V > 0) {
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j) {
-          const int gi = c * L::kSteps + 4 * j + t;
-          ma[j] = mb[j] = 8u << 16;
-          if (gi < groups) {
-            const uint32_t za = ZEROS ? g.zeros[ra + gi] & 15u : 8u;
-            const uint32_t zb = ZEROS ? g.zeros[rb + gi] & 15u : 8u;
-            ma[j] = scales[ra + gi] | (za << 16);
-            mb[j] = scales[rb + gi] | (zb << 16);
-          }
+    Meta<V> meta, coming;
+    // this warp's tile: a span has one for each team, so that a tile's sums stay
+    // in registers over all panels of x
+    const int tile = k.first + team;
+    const size_t row = static_cast<size_t>(k.e) * g.N;
+    const size_t ra = (row + min(tile * kRows + gq, g.N - 1)) * groups;
+    const size_t rb = (row + min(tile * kRows + gq + 8, g.N - 1)) * groups;
+    if (tile < k.last && c0 < c1) meta.template load<ZEROS>(g, ra, rb, c0, groups, t);
+    for (int d0 = 0; d0 < g.D; d0 += kPanel) {
+      // ---- this panel of x ---------------------------------------------------------
+      const int cols = min(kPanel, g.D - d0);
+      const int pieces = (cols + 31) / 32 * 4;  // of 8 columns, whole steps of 32
+      __syncthreads();  // the panel before has been read
+      for (int q = threadIdx.x; q < k.cnt * pieces; q += kThreads) {
+        const int token = q / pieces, at = q - token * pieces;
+        const int src = source_row(g.p2u, g.T, k.p0 + token);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (src >= 0 && at * 8 < cols)
+          v = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(src) * g.D + d0 + at * 8);
+        int place = at;
+        if constexpr (V > 0) {
+          // word i of a step goes to thread i / V as its word i % V; columns
+          // (0, 4), (1, 5), (2, 6), (3, 7) of a word pair up as the nibbles do
+          constexpr int kWords = 4 * V;
+          const int step = at / kWords, w = at - step * kWords;
+          place = step * kWords + (w % V) * 4 + w / V;
+          v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                         __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
         }
+        *reinterpret_cast<uint4*>(xs + token * pitch + place * 16) = v;
       }
-      // This chunk's activations, all loads in flight before the wait for the
-      // weights: left to the steps, each waited for its own (the statements
-      // that read shared memory keep their order), 2.5 times the chunk's time.
-      const int col = c * L::kPerChunk;
-      constexpr int kLoads = L::kPerChunk / 32;
-      uint4 xs[kLoads];
+      __syncthreads();
+
+      // ---- products ------------------------------------------------------------------
+      const int b0 = max(c0, d0 / L::kPerChunk);
+      const int b1 = min(c1, (d0 + cols + L::kPerChunk - 1) / L::kPerChunk);
+      if (tile < k.last) {
+        for (int c = b0; c < b1; ++c) {
+          copy_stage();
+          if (c + 1 < c1) coming.template load<ZEROS>(g, ra, rb, c + 1, groups, t);
+          copies_wait<kStages - 1>();
+          __syncwarp();
+          const uint8_t* const at = smem + (warp * kStages + stage) * kStageBytes + gq * kChunk;
+          const int sw = L::swizzle(gq);  // and of row gq + 8
+          const int col = c * L::kPerChunk - d0;
+          const uint8_t* const xa = x_at + col * 2;
 #pragma unroll
-      for (int s = 0; s < L::kSteps; ++s)
+          for (int s = 0; s < L::kSteps; ++s) {
+            if (col + s * L::kStep >= cols) break;
+            if constexpr (V == 0) {
+              uint32_t wa[4], wb[4], xv[4];
+              const uint8_t* const from = at + (((4 * s + t) ^ sw) << 4);
+              load_words<4>(from, wa);
+              load_words<4>(from + 8 * kChunk, wb);
+              load_words<4>(xa + s * 64, xv);
+              mma_16816(acc, wa[0], wb[0], wa[1], wb[1], xv[0], xv[1]);
+              mma_16816(acc, wa[2], wb[2], wa[3], wb[3], xv[2], xv[3]);
+            } else {
+              uint32_t wa[V], wb[V];
+              const int byte = s * (16 * V) + t * (4 * V);
+              const uint8_t* const from = at + (((byte >> 4) ^ sw) << 4) + (byte & 15);
+              load_words<V>(from, wa);
+              load_words<V>(from + 8 * kChunk, wb);
+              const int holder = (lane & 28) | (s & 3);
+              const uint32_t a = __shfl_sync(0xffffffffu, meta.a[s >> 2], holder);
+              const uint32_t b = __shfl_sync(0xffffffffu, meta.b[s >> 2], holder);
+              const __nv_bfloat162 za = zero_pair(ZEROS ? a & 0xf0000u : 8u << 16);
+              const __nv_bfloat162 zb = zero_pair(ZEROS ? b & 0xf0000u : 8u << 16);
+              float p[4];
 #pragma unroll
-        for (int v = 0; v < kLoads / L::kSteps; ++v) {
-          const int d = col + s * L::kStep + (V == 0 ? t * 8 : t * (8 * V) + v * 8);
-          uint4& q = xs[s * (kLoads / L::kSteps) + v];
-          q = make_uint4(0u, 0u, 0u, 0u);
-          if (d < g.D) q = *reinterpret_cast<const uint4*>(xr + d);
+              for (int v = 0; v < V; ++v) {
+                uint32_t xv[4];
+                load_words<4>(xa + s * (64 * V) + v * 64, xv);
+                if (v == 0)
+                  mma_16816_from_zero(p, nibbles(wa[v], 0, za), nibbles(wb[v], 0, zb),
+                                      nibbles(wa[v], 1, za), nibbles(wb[v], 1, zb), xv[0], xv[1]);
+                else
+                  mma_16816(p, nibbles(wa[v], 0, za), nibbles(wb[v], 0, zb), nibbles(wa[v], 1, za),
+                            nibbles(wb[v], 1, zb), xv[0], xv[1]);
+                mma_16816(p, nibbles(wa[v], 2, za), nibbles(wb[v], 2, zb), nibbles(wa[v], 3, za),
+                          nibbles(wb[v], 3, zb), xv[2], xv[3]);
+              }
+              const float sa = __uint_as_float(a << 16), sb = __uint_as_float(b << 16);
+              acc[0] = fmaf(sa, p[0], acc[0]);
+              acc[1] = fmaf(sa, p[1], acc[1]);
+              acc[2] = fmaf(sb, p[2], acc[2]);
+              acc[3] = fmaf(sb, p[3], acc[3]);
+            }
+          }
+          __syncwarp();  // all lanes have read the stage before it is filled again
+          if (++stage == kStages) stage = 0;
+          meta = coming;
         }
-      copies_wait<kStages - 1>();
-      __syncwarp();
-      const uint32_t at = ring_at + stage * kStageBytes + gq * kChunk;
-      const int sw = L::swizzle(gq);  // and of row gq + 8
+        if (d0 + kPanel < g.D) continue;  // more panels: the sums go on
+        // fragment: weight rows gq and gq + 8, tokens 2 t and 2 t + 1
+        const int n0 = tile * kRows;
+        if constexpr (SHARED) {
+          float(*sums)[kTokens][kRows + 1] = part + team * kShare;
+          sums[member][2 * t][gq] = acc[0];
+          sums[member][2 * t + 1][gq] = acc[1];
+          sums[member][2 * t][gq + 8] = acc[2];
+          sums[member][2 * t + 1][gq + 8] = acc[3];
+          team_sync(team + 1);
+          const int token = member * 2 + (lane >> 4), n = lane & 15;
+          if (token < k.cnt && n0 + n < g.N) {
+            float v = sums[0][token][n];
 #pragma unroll
-      for (int s = 0; s < L::kSteps; ++s) {
-        const int d = col + s * L::kStep;
-        if (d >= g.D) break;
-        if constexpr (V == 0) {
-          uint32_t wa[4], wb[4];
-          const uint32_t from = at + (((4 * s + t) ^ sw) << 4);
-          load_words<V>(from, wa);
-          load_words<V>(from + 8 * kChunk, wb);
-          const uint4 xv = xs[s];
-          mma_16816(acc, wa[0], wb[0], wa[1], wb[1], xv.x, xv.y);
-          mma_16816(acc, wa[2], wb[2], wa[3], wb[3], xv.z, xv.w);
+            for (int w = 1; w < kShare; ++w) v += sums[w][token][n];
+            store_value(g, static_cast<size_t>(k.p0 + token) * g.N + n0 + n, v);
+          }
+          team_sync(team + 1);
         } else {
-          uint32_t wa[V], wb[V];
-          const int byte = s * (16 * V) + t * (4 * V);
-          const uint32_t from = at + (((byte >> 4) ^ sw) << 4) + (byte & 15);
-          load_words<V>(from, wa);
-          load_words<V>(from + 8 * kChunk, wb);
-          const int holder = (lane & 28) | (s & 3);
-          const uint32_t a = __shfl_sync(0xffffffffu, ma[s >> 2], holder);
-          const uint32_t b = __shfl_sync(0xffffffffu, mb[s >> 2], holder);
-          const __nv_bfloat162 za = zero_pair(a & 0xf0000u), zb = zero_pair(b & 0xf0000u);
-          float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const uint4 xv = xs[s * V + v];
-            // (x[0], x[4]), (x[1], x[5]), (x[2], x[6]), (x[3], x[7])
-            const uint32_t b0 = __byte_perm(xv.x, xv.z, 0x5410);
-            const uint32_t b1 = __byte_perm(xv.x, xv.z, 0x7632);
-            const uint32_t b2 = __byte_perm(xv.y, xv.w, 0x5410);
-            const uint32_t b3 = __byte_perm(xv.y, xv.w, 0x7632);
-            mma_16816(p, nibbles(wa[v], 0, za), nibbles(wb[v], 0, zb), nibbles(wa[v], 1, za),
-                      nibbles(wb[v], 1, zb), b0, b1);
-            mma_16816(p, nibbles(wa[v], 2, za), nibbles(wb[v], 2, zb), nibbles(wa[v], 3, za),
-                      nibbles(wb[v], 3, zb), b2, b3);
+          for (int j = 0; j < 4; ++j) {
+            const int token = 2 * t + (j & 1), n = n0 + gq + (j >> 1) * 8;
+            if (token < k.cnt && n < g.N)
+              store_value(g, static_cast<size_t>(k.p0 + token) * g.N + n, acc[j]);
           }
-          const float sa = __uint_as_float(a << 16), sb = __uint_as_float(b << 16);
-          acc[0] = fmaf(sa, p[0], acc[0]);
-          acc[1] = fmaf(sa, p[1], acc[1]);
-          acc[2] = fmaf(sb, p[2], acc[2]);
-          acc[3] = fmaf(sb, p[3], acc[3]);
-        }
-      }
-      __syncwarp();  // all lanes have read the stage before it is filled again
-      if (++stage == kStages) stage = 0;
-    }
-    // fragment: weight rows gq and gq + 8, tokens 2 t and 2 t + 1
-    if constexpr (SPLIT) {
-      part[warp][2 * t][gq] = acc[0];
-      part[warp][2 * t + 1][gq] = acc[1];
-      part[warp][2 * t][gq + 8] = acc[2];
-      part[warp][2 * t + 1][gq + 8] = acc[3];
-      __syncthreads();
-      const int token = threadIdx.x / kRows, n = threadIdx.x % kRows;
-      if (token < k.cnt && k.n0 + n < g.N) {
-        float s = part[0][token][n];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) s += part[w][token][n];
-        const size_t o = static_cast<size_t>(k.p0 + token) * g.N + k.n0 + n;
-        if (g.out_dtype == DT_F32) static_cast<float*>(g.out)[o] = s;
-        else static_cast<unsigned short*>(g.out)[o] = static_cast<unsigned short>(f32_to_bf16_bits(s));
-      }
-      __syncthreads();
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int token = 2 * t + (j & 1), n = k.n0 + gq + (j >> 1) * 8;
-        if (token < k.cnt && n < g.N) {
-          const size_t o = static_cast<size_t>(k.p0 + token) * g.N + n;
-          if (g.out_dtype == DT_F32) static_cast<float*>(g.out)[o] = acc[j];
-          else static_cast<unsigned short*>(g.out)[o] =
-              static_cast<unsigned short>(f32_to_bf16_bits(acc[j]));
         }
       }
     }
   }
 }
 
-template <int V, bool ZEROS, bool SPLIT>
-int launch_split(const FewArgs& a, long long tasks, int sms, cudaStream_t st) {
+template <int V, bool ZEROS, bool SHARED>
+int launch_shared(const FewArgs& a, long long groups, int sms, cudaStream_t st) {
+  constexpr int span = SHARED ? kWarps / kShare : kWarps;
   static std::atomic<int> granted[kSmemDevs];
-  const auto kern = expert_matmul_few_kernel<V, ZEROS, SPLIT>;
-  cudaError_t e = allow_smem(kern, few_smem(a.E), granted);
+  const auto kern = expert_matmul_few_kernel<V, ZEROS, SHARED>;
+  const int smem = few_smem(a.E, a.D);
+  cudaError_t e = allow_smem(kern, smem, granted);
   if (e != cudaSuccess) return MR_ERR_CUDA;
-  const long long blocks = SPLIT ? tasks : (tasks + kWarps - 1) / kWarps;
-  const long long most = static_cast<long long>(kBlocksPerSm) * sms;
-  e = launch_kernel(kern, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
-                    dim3(32 * kWarps), few_smem(a.E), st, a);
+  const int row_tiles = (a.N + kRows - 1) / kRows;
+  const long long tasks = groups * ((row_tiles + span - 1) / span);
+  if (tasks > INT_MAX) return MR_ERR_UNSUPPORTED;
+  e = launch_kernel(kern, dim3(static_cast<unsigned>(tasks < sms ? tasks : sms)), dim3(kThreads),
+                    smem, st, a);
   return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }
 
@@ -347,12 +437,13 @@ template <int V, bool ZEROS>
 int launch_typed(const FewArgs& a, cudaStream_t st) {
   const int sms = device_sm_count();
   if (sms <= 0) return MR_ERR_CUDA;
-  // tasks at most (the host does not know which experts have rows)
-  const long long tasks = (static_cast<long long>(a.E < a.P ? a.E : a.P) + a.P / kTokens) *
-                          ((a.N + kRows - 1) / kRows);
-  const bool split = tasks <= 2ll * kBlocksPerSm * sms * kWarps;
-  return split ? launch_split<V, ZEROS, true>(a, tasks, sms, st)
-               : launch_split<V, ZEROS, false>(a, tasks, sms, st);
+  // row groups at most (the host does not know which experts have rows)
+  const long long groups = static_cast<long long>(a.E < a.P ? a.E : a.P) + a.P / kTokens;
+  const int row_tiles = (a.N + kRows - 1) / kRows;
+  // Fewer tiles than twice the warps of the GPU: four warps to a tile.
+  if (groups * row_tiles <= 2ll * sms * kWarps)
+    return launch_shared<V, ZEROS, true>(a, groups, sms, st);
+  return launch_shared<V, ZEROS, false>(a, groups, sms, st);
 }
 
 }  // namespace

@@ -19,16 +19,18 @@
 // another expert enters a product (the boxes of the forward and the input
 // gradient may hold some: they fill columns that are not stored).
 //
-// Block: 16 warps.  Warp 0 loads A, warps 8-15 load B, 16 rows (weight grad:
-// of A and B, 16 rows x 64 columns) each.  One elected thread of warp 1 issues
-// the products, warp 2 owns the tensor memory, warps 4-7 store finished tiles
-// while the next one is computed into the other half of the accumulator
-// columns.  A stage holds 64 contraction indices: 16 KB of A and up to 16 KB of
-// B.  Every loading warp arrives on a stage's barrier even with nothing to
-// load, so none falls behind by a phase.  CG = 2: two CTAs share a tile of
-// 256 x (up to 256), each holding half of A and of B, which halves the
-// shared-memory and L2 traffic per product.  The grid is persistent; tile i
-// goes to CTA (pair) i mod the grid.
+// Block: 24 warps.  Warps 0 and 3 load A, warps 8-23 load B, 16 rows (weight
+// grad: of A and B, 16 rows x 64 columns) each: two groups of nine that take
+// alternate slices, since one warp needs 500 to 1200 cycles from one slice to the
+// next (four gathers are 400), and the products 350 to 500.  One elected thread
+// of warp 1 issues the products, warp 2 owns the tensor memory, warps 4-7 store
+// finished tiles while the next one is computed into the other half of the
+// accumulator columns.  A stage holds 64 contraction indices: 16 KB of A and up to
+// 16 KB of B.  Every loading warp arrives on its stages' barriers even with
+// nothing to load, so none falls behind by a phase.  CG = 2: two CTAs share a
+// tile of 256 x (up to 256), each holding half of A and of B, which halves the
+// shared-memory and L2 traffic per product.  The grid is persistent; tile i goes
+// to CTA (pair) i mod the grid.
 //
 // fp32 outputs.  The tensor cores add each 16-deep product to the accumulator
 // by truncation, so a sum of n of them is off by about n 2^-26 of its value
@@ -55,8 +57,8 @@
 namespace moe_router {
 namespace {
 
-constexpr int kLoaders = 8;               // warps that load B (weight grad: A and B)
-constexpr int kThreads = 256 + 32 * kLoaders;
+constexpr int kLoaders = 8;               // warps that load a slice of B (weight grad: A and B)
+constexpr int kThreads = 32 * (8 + 2 * kLoaders);
 constexpr int kMaxStages = 6;
 constexpr int kDeep = 64;                 // contraction indices per stage: 128 bytes
 constexpr int kSegment = 15;              // most stages per accumulator of a fp32 output
@@ -67,8 +69,9 @@ constexpr int kBytesB = kRowsB * 128;
 constexpr int kStageBytes = kBytesA + kBytesB;
 constexpr int kBoxes = 4;  // weight grad: 32 x 128-byte boxes per storing warp
 
-// Stages, and dynamic shared memory: stages and boxes start on 1024 bytes.
-constexpr int stages_of(int form) { return form == EX_WGRAD ? 5 : kMaxStages; }
+// Stages, and dynamic shared memory: stages and boxes start on 1024 bytes.  Stages
+// are even in number: each belongs to one of the two groups of loading warps.
+constexpr int stages_of(int form) { return form == EX_WGRAD ? 4 : kMaxStages; }
 constexpr int smem_bytes(int form) {
   return stages_of(form) * kStageBytes + (form == EX_WGRAD ? 4 * kBoxes * 4096 : 0) + 1024;
 }
@@ -99,7 +102,8 @@ struct Shape {
 };
 
 template <int FORM, int CG>
-__device__ __forceinline__ Tile find_tile(const TcArgs& g, const int* prefix, int tile) {
+__device__ __forceinline__ Tile find_tile(const TcArgs& g, const int* prefix, const int* offs,
+                                          int tile) {
   using S = Shape<FORM, CG>;
   Tile t;
   if constexpr (FORM == EX_WGRAD) {
@@ -108,17 +112,15 @@ __device__ __forceinline__ Tile find_tile(const TcArgs& g, const int* prefix, in
     const int r = tile - t.e * ta * tb;
     t.a0 = r / tb * S::kTileA;
     t.b0 = r % tb * S::kTileB;
-    int hi;
-    expert_rows(g.offsets, t.e, g.P, &t.start, &hi);
-    t.cnt = hi - t.start;
+    t.start = offs[t.e];
+    t.cnt = max(offs[t.e + 1] - t.start, 0);
   } else {
     const int ta = ((FORM == EX_FWD ? g.N : g.D) + S::kTileA - 1) / S::kTileA;
     t.e = expert_of_tile(prefix, g.E, tile / ta);
     const int first = prefix[t.e], tiles = prefix[t.e + 1] - first;
     const int r = tile - first * ta;
     const int a = r / tiles;  // one slice of the weight, all row tiles, then the next
-    int lo, hi;
-    expert_rows(g.offsets, t.e, g.P, &lo, &hi);
+    const int lo = offs[t.e], hi = max(offs[t.e + 1], lo);
     const int each = ((hi - lo + tiles - 1) / tiles + S::kRound - 1) / S::kRound * S::kRound;
     t.a0 = a * S::kTileA;
     t.start = lo + (r - a * tiles) * each;
@@ -143,11 +145,11 @@ struct Waiter {
 // Tile *i, or the first one after it in this CTA's sequence that has products
 // (weight grad: an expert without rows has none).
 template <int FORM, int CG>
-__device__ __forceinline__ Tile next_tile(const TcArgs& g, const int* prefix, int tiles, int step,
-                                          int* i) {
+__device__ __forceinline__ Tile next_tile(const TcArgs& g, const int* prefix, const int* offs,
+                                          int tiles, int step, int* i) {
   Tile t{};
   while (*i < tiles) {
-    t = find_tile<FORM, CG>(g, prefix, *i);
+    t = find_tile<FORM, CG>(g, prefix, offs, *i);
     if (FORM != EX_WGRAD || t.cnt > 0) break;
     *i += step;
   }
@@ -240,6 +242,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
   __shared__ int gave_up;
   __shared__ int tmp[33];
   __shared__ int prefix[FORM == EX_WGRAD ? 1 : MR_MAX_EXPERTS + 1];
+  __shared__ int offs[MR_MAX_EXPERTS + 1];  // the offsets, clamped to [0, P]
 
   // the same value in all lanes, and known to be
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -260,6 +263,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
   }
   if (warp == 2) tmem_alloc<CG>(&tmem_at, S::kColumns);
   pdl_enter();
+  for (int e = threadIdx.x; e <= g.E; e += blockDim.x) offs[e] = min(max(g.offsets[e], 0), g.P);
   int tiles;
   if constexpr (FORM == EX_WGRAD) {
     tiles = g.E * ((g.N + S::kTileA - 1) / S::kTileA) * ((g.D + S::kTileB - 1) / S::kTileB);
@@ -276,32 +280,39 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
   // contraction slices of a tile
   const int fixed_slices = ((FORM == EX_FWD ? g.D : g.N) + kDeep - 1) / kDeep;
 
-  if (warp >= 8 || warp == 0) {
+  if (warp >= 8 || warp == 0 || warp == 3) {
     // ---- loads -----------------------------------------------------------------
-    // The next slice's tile and map entries are fetched before the present
-    // slice's copies are issued, so their latency passes behind the issue.
-    const int w = warp - 8;  // -1: the warp that loads A
+    // Two groups of warps load alternate slices.  A group's next slice, its tile
+    // and its map entries are fetched before the present slice's copies are
+    // issued, so their latency passes behind the issue.
+    const int group = warp >= 8 ? (warp - 8) / kLoaders : warp == 3;
+    const int w = warp >= 8 ? (warp - 8) % kLoaders : -1;  // -1: the warps that load A
     const bool mapped = w >= 0 && (FORM == EX_WGRAD || g.p2u != nullptr);
-    int stage = 0;
+    int stage = group;
     uint32_t parity = 1;  // the first pass finds the stages empty
     int i = first, s = 0;
-    Tile t = next_tile<FORM, CG>(g, prefix, tiles, step, &i);
-    int u[4];
-    if (mapped) fetch_rows(g, t, loader_row<FORM, CG>(t, rank, w, s), lane, u);
-    int r[4];
-    while (i < tiles) {
-      if (mapped && (FORM == EX_WGRAD || s == 0)) source_rows(g, u, g.x_rows, r);
-      const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
-      int ni = i, ns = s + 1;
-      Tile nt = t;
-      int nu[4] = {u[0], u[1], u[2], u[3]};
-      if (ns == slices) {
-        ni += step;
-        nt = next_tile<FORM, CG>(g, prefix, tiles, step, &ni);
-        ns = 0;
+    Tile t = next_tile<FORM, CG>(g, prefix, offs, tiles, step, &i);
+    auto advance = [&](int* i, int* s, Tile* t) {
+      const int slices = FORM == EX_WGRAD ? (t->cnt + kDeep - 1) / kDeep : fixed_slices;
+      if (++*s == slices) {
+        *i += step;
+        *s = 0;
+        *t = next_tile<FORM, CG>(g, prefix, offs, tiles, step, i);
       }
-      if (mapped && ni < tiles && (FORM == EX_WGRAD || ns == 0))
-        fetch_rows(g, nt, loader_row<FORM, CG>(nt, rank, w, ns), lane, nu);
+    };
+    if (group == 1 && i < tiles) advance(&i, &s, &t);
+    int u[4], r[4];
+    bool fresh = true;  // the map entries in u are not yet rows in r
+    if (mapped && i < tiles) fetch_rows(g, t, loader_row<FORM, CG>(t, rank, w, s), lane, u);
+    while (i < tiles) {
+      if (mapped && (FORM == EX_WGRAD || fresh)) source_rows(g, u, g.x_rows, r);
+      int ni = i, ns = s;
+      Tile nt = t;
+      advance(&ni, &ns, &nt);
+      if (ni < tiles) advance(&ni, &ns, &nt);
+      fresh = ni != i;
+      if (mapped && ni < tiles && (FORM == EX_WGRAD || fresh))
+        fetch_rows(g, nt, loader_row<FORM, CG>(nt, rank, w, ns), lane, u);
 
       const int row = loader_row<FORM, CG>(t, rank, w, s);
       const int a0 = t.a0 + static_cast<int>(rank) * kRowsA;
@@ -362,15 +373,14 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
           tma_load_2d<CG>(piece, &box_b, s * kDeep, t.start + row, bar);
         }
       }
-      if (++stage == S::kStages) {
-        stage = 0;
+      stage += 2;
+      if (stage >= S::kStages) {
+        stage = group;
         parity ^= 1;
       }
       i = ni;
       t = nt;
       s = ns;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = nu[j];
     }
   } else if (warp == 1 && rank == 0) {
     // ---- products ----------------------------------------------------------------
@@ -378,7 +388,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
     uint32_t parity = 0;
     bool ok = true;
     int i = first;
-    Tile t = next_tile<FORM, CG>(g, prefix, tiles, step, &i);
+    Tile t = next_tile<FORM, CG>(g, prefix, offs, tiles, step, &i);
     while (i < tiles && ok) {
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
       const int cols = FORM == EX_WGRAD ? S::kTileB
@@ -423,29 +433,28 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
             parity ^= 1;
           }
           // the next tile is looked up while this slice is computed
-          if (s == 0) nt = next_tile<FORM, CG>(g, prefix, tiles, step, &ni);
+          if (s == 0) nt = next_tile<FORM, CG>(g, prefix, offs, tiles, step, &ni);
         }
         ++n;
       }
       i = ni;
       t = nt;
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4) {
     // ---- stores --------------------------------------------------------------------
     const int quad = warp - 4;
     [[maybe_unused]] const uint32_t boxes_at =
         stages_at + S::kStages * kStageBytes +
         quad * (kBoxes * 4096);
-    [[maybe_unused]] int chunk = 0;
     // the lane that issues copies: their groups are its own to wait for
     [[maybe_unused]] const bool one = elect_one();
     int n = 0;
     bool ok = true;
     Tile nt{};
-    if (first < tiles) nt = find_tile<FORM, CG>(g, prefix, first);
+    if (first < tiles) nt = find_tile<FORM, CG>(g, prefix, offs, first);
     for (int i = first; i < tiles && ok; i += step) {
       const Tile t = nt;
-      if (i + step < tiles) nt = find_tile<FORM, CG>(g, prefix, i + step);
+      if (i + step < tiles) nt = find_tile<FORM, CG>(g, prefix, offs, i + step);
       const bool none = FORM == EX_WGRAD && t.cnt == 0;  // an expert without rows: zeros
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
       // one accumulator after the other: the first is stored, the others added
@@ -469,8 +478,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
           constexpr int wide = F32 ? 32 : 64;
           const int cols = row0 < g.N ? min(S::kTileB, g.D - t.b0) : 0;
           if (none && cols > 0) {  // one box of zeros for the whole tile
-            const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
-            if (one) bulk_wait_read<kBoxes - 1>();
+            const uint32_t box = boxes_at;
+            if (one) bulk_wait_read<0>();
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j) st_shared_v4(box + (j * 32 + lane) * 16, 0u, 0u, 0u, 0u);
@@ -482,29 +491,40 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
             }
           }
           if (add && one) bulk_wait_all();  // what it is added to has arrived
-          for (int c = 0; c < cols && !none; c += wide) {
-            const uint32_t box = boxes_at + (chunk++ % kBoxes) * 4096;
-            uint32_t v[32];
-            if (one) bulk_wait_read<kBoxes - 1>();
+          for (int c0 = 0; c0 < cols && !none; c0 += kBoxes * wide) {
+            if (one) bulk_wait_read<0>();
             __syncwarp();
-            if constexpr (F32) {
-              tmem_load_32(acc + c, v);
-            } else {
-              uint32_t u[64];
-              tmem_load_64(acc + c, u);
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                v[j] = bf16_pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+            for (int q = 0; q < kBoxes; ++q) {
+              const int c = c0 + q * wide;
+              if (c >= cols) break;
+              const uint32_t box = boxes_at + q * 4096;
+              uint32_t v[32];
+              if constexpr (F32) {
+                tmem_load_32(acc + c, v);
+              } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint32_t u[32];
+                  tmem_load_32(acc + c + 32 * h, u);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    v[16 * h + j] =
+                        bf16_pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                st_shared_v4(box + lane * 128 + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1],
+                             v[4 * j + 2], v[4 * j + 3]);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              st_shared_v4(box + lane * 128 + ((j ^ (lane & 7)) << 4), v[4 * j], v[4 * j + 1],
-                           v[4 * j + 2], v[4 * j + 3]);
             fence_proxy_async_smem();
             __syncwarp();
             if (one) {
-              if (add) tma_add_3d(&map_out, box, t.b0 + c, row0, t.e);
-              else tma_store_3d(&map_out, box, t.b0 + c, row0, t.e);
+              for (int q = 0; q < kBoxes && c0 + q * wide < cols; ++q) {
+                if (add) tma_add_3d(&map_out, boxes_at + q * 4096, t.b0 + c0 + q * wide, row0, t.e);
+                else tma_store_3d(&map_out, boxes_at + q * 4096, t.b0 + c0 + q * wide, row0, t.e);
+              }
               bulk_commit();
             }
           }
@@ -704,7 +724,7 @@ int launch_typed(const ExpertArgs& a, cudaStream_t st) {
 
 template <int FORM>
 int launch_form(const ExpertArgs& a, cudaStream_t st) {
-  const bool pair = FORM == EX_WGRAD ? a.N > kRowsA : a.P >= 48ll * a.E;
+  const bool pair = FORM == EX_WGRAD ? a.N > kRowsA : a.P >= 40ll * a.E;
   if (a.out_dtype == DT_F32)
     return pair ? launch_typed<FORM, 2, true>(a, st) : launch_typed<FORM, 1, true>(a, st);
   return pair ? launch_typed<FORM, 2, false>(a, st) : launch_typed<FORM, 1, false>(a, st);

@@ -13,32 +13,48 @@
 namespace moe_router {
 namespace {
 
-// One 16-byte vector (VEC) or one element of a row, widened to fp32.
+// One 16-byte vector (VEC) or one element of a row, held as it was loaded (so
+// that rows in flight take four registers) and widened to fp32 when used.
 template <int DT, bool VEC>
 struct Piece {
   static constexpr int kN = !VEC ? 1 : DT == DT_F32 ? 4 : 8;
-  float v[kN];
+  static constexpr int kWords = VEC ? 4 : 1;
+  uint32_t w[kWords];
 
+  // STREAM: not kept in L1 (the forward's rows; it costs the backward 2 to 6 %)
+  template <bool STREAM>
   __device__ __forceinline__ void load(const void* base, size_t i) {
+    const uint8_t* at = static_cast<const uint8_t*>(base) + i * (DT == DT_F32 ? 4 : 2);
     if constexpr (!VEC) {
-      v[0] = DT == DT_F32 ? __ldcs(static_cast<const float*>(base) + i)
-                          : bf16_bits_to_f32(__ldcs(static_cast<const unsigned short*>(base) + i));
-    } else if constexpr (DT == DT_F32) {
-      const float4 t = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(base) + i));
-      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+      if (DT == DT_F32) w[0] = get<STREAM>(reinterpret_cast<const unsigned int*>(at));
+      else w[0] = get<STREAM>(reinterpret_cast<const unsigned short*>(at));
     } else {
-      const uint4 t =
-          __ldcs(reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(base) + i));
-      const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+      const uint4 t = get<STREAM>(reinterpret_cast<const uint4*>(at));
+      w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
+    }
+  }
+
+  template <bool STREAM, typename W>
+  __device__ __forceinline__ static W get(const W* p) {
+    return STREAM ? __ldcs(p) : __ldg(p);
+  }
+
+  __device__ __forceinline__ void widen(float (&v)[kN]) const {
+    if constexpr (DT == DT_F32) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kN; ++j) v[j] = __uint_as_float(w[j]);
+    } else if constexpr (!VEC) {
+      v[0] = bf16_bits_to_f32(w[0]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
         v[2 * j] = __uint_as_float(w[j] << 16);
         v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
       }
     }
   }
 
-  __device__ __forceinline__ void store(void* base, size_t i) const {
+  __device__ __forceinline__ static void store(void* base, size_t i, const float (&v)[kN]) {
     if constexpr (!VEC) {
       if (DT == DT_F32) __stcs(static_cast<float*>(base) + i, v[0]);
       else __stcs(static_cast<unsigned short*>(base) + i,
@@ -47,23 +63,28 @@ struct Piece {
       __stcs(reinterpret_cast<float4*>(static_cast<float*>(base) + i),
              make_float4(v[0], v[1], v[2], v[3]));
     } else {
-      uint32_t w[4];
+      uint32_t u[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = f32_to_bf16_bits(v[2 * j]) | (f32_to_bf16_bits(v[2 * j + 1]) << 16);
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        u[j] = *reinterpret_cast<const uint32_t*>(&p);
+      }
       __stcs(reinterpret_cast<uint4*>(static_cast<unsigned short*>(base) + i),
-             make_uint4(w[0], w[1], w[2], w[3]));
+             make_uint4(u[0], u[1], u[2], u[3]));
     }
   }
 };
 
-constexpr int kUnroll = 4;  // rows in flight per thread
+constexpr int kUnroll = 4;  // backward: rows in flight per thread
 
 // A warp sums one stretch of 32 pieces of one token's row: its lanes hold the
 // token's choices (two each for K > 32), handed round by shuffles, and load
-// kUnroll rows ahead of the sum.
-template <int DT, bool VEC>
-__global__ __launch_bounds__(256) void combine_fwd_kernel(CombineArgs a, int stretches) {
+// UNROLL rows ahead of the sum.
+// Eight rows in flight and four blocks an SM (8192 tokens, 8 choices, 2048 bf16:
+// 57 us, 61 with three blocks, 59 with four rows and five blocks), four rows for
+// K <= 4 (4096 columns: 72 us against 80).
+template <int DT, bool VEC, int UNROLL>
+__global__ __launch_bounds__(256, UNROLL == 8 ? 4 : 1) void combine_fwd_kernel(CombineArgs a, int stretches) {
   pdl_enter();
   constexpr int N = Piece<DT, VEC>::kN;
   const int lane = threadIdx.x & 31;
@@ -87,29 +108,27 @@ __global__ __launch_bounds__(256) void combine_fwd_kernel(CombineArgs a, int str
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-  for (int k0 = 0; k0 < a.K; k0 += kUnroll) {
-    int p[kUnroll];
-    float w[kUnroll];
-    Piece<DT, VEC> z[kUnroll];
+  for (int k0 = 0; k0 < a.K; k0 += UNROLL) {
+    int p[UNROLL];
+    float w[UNROLL];
+    Piece<DT, VEC> z[UNROLL];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < UNROLL; ++u) {
       const int k = k0 + u;  // the same for all lanes; past K the lane's own choice is empty
       p[u] = __shfl_sync(0xffffffffu, k < 32 ? p0 : p1, k & 31);
       w[u] = __shfl_sync(0xffffffffu, k < 32 ? w0 : w1, k & 31);
-      if (p[u] >= 0 && col < a.D) z[u].load(a.z, static_cast<size_t>(p[u]) * a.D + col);
+      if (p[u] >= 0 && col < a.D) z[u].template load<true>(a.z, static_cast<size_t>(p[u]) * a.D + col);
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (p[u] >= 0 && col < a.D)
+    for (int u = 0; u < UNROLL; ++u) {
+      if (p[u] < 0 || col >= a.D) continue;
+      float v[N];
+      z[u].widen(v);
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = fmaf(w[u], z[u].v[j], acc[j]);
+      for (int j = 0; j < N; ++j) acc[j] = fmaf(w[u], v[j], acc[j]);
+    }
   }
-  if (col < a.D) {
-    Piece<DT, VEC> y;
-#pragma unroll
-    for (int j = 0; j < N; ++j) y.v[j] = acc[j];
-    y.store(a.out, static_cast<size_t>(t) * a.D + col);
-  }
+  if (col < a.D) Piece<DT, VEC>::store(a.out, static_cast<size_t>(t) * a.D + col, acc);
 }
 
 // A block takes one token: kUnroll choices at a time, each thread its pieces
@@ -137,23 +156,26 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(CombineArgs a) {
       dot[u] = 0.0f;
     }
     for (int col = threadIdx.x * N; col < a.D; col += blockDim.x * N) {
-      Piece<DT, VEC> gy, z[kUnroll];
-      gy.load(a.gy, gy0 + col);
+      Piece<DT, VEC> g, z[kUnroll];
+      float gy[N];
+      g.template load<false>(a.gy, gy0 + col);
       if (dots) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          if (p[u] >= 0) z[u].load(a.z, static_cast<size_t>(p[u]) * a.D + col);
+          if (p[u] >= 0) z[u].template load<false>(a.z, static_cast<size_t>(p[u]) * a.D + col);
       }
+      g.widen(gy);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (p[u] < 0) continue;
-        Piece<DT, VEC> gz;
+        float gz[N], v[N];
+        if (dots) z[u].widen(v);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          if (dots) dot[u] = fmaf(gy.v[j], z[u].v[j], dot[u]);
-          gz.v[j] = w[u] * gy.v[j];
+          if (dots) dot[u] = fmaf(gy[j], v[j], dot[u]);
+          gz[j] = w[u] * gy[j];
         }
-        gz.store(a.out, static_cast<size_t>(p[u]) * a.D + col);
+        Piece<DT, VEC>::store(a.out, static_cast<size_t>(p[u]) * a.D + col, gz);
       }
     }
     if (dots) {
@@ -187,9 +209,10 @@ int fwd_typed(const CombineArgs& a, cudaStream_t st) {
   const int stretches = (a.D + 32 * N - 1) / (32 * N);
   const long long blocks = (static_cast<long long>(a.T) * stretches + 7) / 8;
   if (blocks > 0x7fffffffll) return MR_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(blocks));
   const cudaError_t e =
-      launch_kernel(combine_fwd_kernel<DT, VEC>, dim3(static_cast<unsigned>(blocks)), dim3(256),
-                    0, st, a, stretches);
+      a.K <= 4 ? launch_kernel(combine_fwd_kernel<DT, VEC, 4>, grid, dim3(256), 0, st, a, stretches)
+               : launch_kernel(combine_fwd_kernel<DT, VEC, 8>, grid, dim3(256), 0, st, a, stretches);
   return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }
 

@@ -64,7 +64,7 @@ bool expert_matmul_tc_ok(int form, const ExpertArgs& a);  // types and alignment
 int launch_expert_matmul_tc(int form, const ExpertArgs& a, cudaStream_t st);
 bool expert_matmul_few_ok(const ExpertArgs& a);
 int launch_expert_matmul_few(const ExpertArgs& a, cudaStream_t st);  // forward only
-int launch_expert_matmul_vector(int form, const ExpertArgs& a, cudaStream_t st);
+int launch_expert_matmul_split(int form, const ExpertArgs& a, cudaStream_t st);  // any operands
 int launch_expert_matmul_w4(const W4Args& a, cudaStream_t st);
 int launch_combine_fwd(const CombineArgs& a, cudaStream_t st);
 int launch_combine_bwd(const CombineArgs& a, cudaStream_t st);

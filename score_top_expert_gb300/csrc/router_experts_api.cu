@@ -30,7 +30,7 @@ int run_product(int form, const ExpertArgs& a, mr_stream_t stream) {
   if (form == EX_FWD && a.P <= kFewRows && expert_matmul_few_ok(a))
     return launch_expert_matmul_few(a, st);
   return expert_matmul_tc_ok(form, a) ? launch_expert_matmul_tc(form, a, st)
-                                      : launch_expert_matmul_vector(form, a, st);
+                                      : launch_expert_matmul_split(form, a, st);
 }
 
 }  // namespace

@@ -50,9 +50,7 @@
 // experts at 1590 and 1740 (input gradient).
 #include <atomic>
 
-#include "router_common.cuh"
-#include "router_experts.cuh"
-#include "router_tcgen.cuh"
+#include "router_experts_tiles.cuh"
 
 namespace moe_router {
 namespace {
@@ -60,8 +58,6 @@ namespace {
 constexpr int kLoaders = 8;               // warps that load a slice of B (weight grad: A and B)
 constexpr int kThreads = 32 * (8 + 2 * kLoaders);
 constexpr int kMaxStages = 6;
-constexpr int kDeep = 64;                 // contraction indices per stage: 128 bytes
-constexpr int kSegment = 15;              // most stages per accumulator of a fp32 output
 constexpr int kRowsA = 128;               // values of A's dimension per CTA
 constexpr int kRowsB = 128;               // most values of B's dimension per CTA
 constexpr int kBytesA = kRowsA * 128;
@@ -76,22 +72,6 @@ constexpr int smem_bytes(int form) {
   return stages_of(form) * kStageBytes + (form == EX_WGRAD ? 4 * kBoxes * 4096 : 0) + 1024;
 }
 
-struct TcArgs {
-  const int32_t* offsets;
-  const int32_t* p2u;
-  void* out;
-  int* status;
-  int T, P, E, N, D;
-  int x_rows;  // rows of the gathered x
-  uint32_t inv_T;  // floor(2^32 / T), at most 2^32 - 1
-};
-
-struct Tile {
-  int e;
-  int start, cnt;  // ragged rows (weight grad: the expert's)
-  int a0, b0;      // first value of A's dimension; weight grad: of B's
-};
-
 template <int FORM, int CG>
 struct Shape {
   static constexpr int kTileA = kRowsA * CG;
@@ -100,61 +80,6 @@ struct Shape {
   static constexpr int kStages = stages_of(FORM);
   static constexpr uint32_t kColumns = 2 * kTileB;  // two accumulators
 };
-
-template <int FORM, int CG>
-__device__ __forceinline__ Tile find_tile(const TcArgs& g, const int* prefix, const int* offs,
-                                          int tile) {
-  using S = Shape<FORM, CG>;
-  Tile t;
-  if constexpr (FORM == EX_WGRAD) {
-    const int ta = (g.N + S::kTileA - 1) / S::kTileA, tb = (g.D + S::kTileB - 1) / S::kTileB;
-    t.e = tile / (ta * tb);
-    const int r = tile - t.e * ta * tb;
-    t.a0 = r / tb * S::kTileA;
-    t.b0 = r % tb * S::kTileB;
-    t.start = offs[t.e];
-    t.cnt = max(offs[t.e + 1] - t.start, 0);
-  } else {
-    const int ta = ((FORM == EX_FWD ? g.N : g.D) + S::kTileA - 1) / S::kTileA;
-    t.e = expert_of_tile(prefix, g.E, tile / ta);
-    const int first = prefix[t.e], tiles = prefix[t.e + 1] - first;
-    const int r = tile - first * ta;
-    const int a = r / tiles;  // one slice of the weight, all row tiles, then the next
-    const int lo = offs[t.e], hi = max(offs[t.e + 1], lo);
-    const int each = ((hi - lo + tiles - 1) / tiles + S::kRound - 1) / S::kRound * S::kRound;
-    t.a0 = a * S::kTileA;
-    t.start = lo + (r - a * tiles) * each;
-    t.cnt = min(each, hi - t.start);
-    t.b0 = 0;
-  }
-  return t;
-}
-
-// Waits that give up set the CTA's flag and the device's status word.
-struct Waiter {
-  int* gave_up;
-  int* status;
-  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    if (mbar_wait_bounded(bar, parity)) return true;
-    *reinterpret_cast<volatile int*>(gave_up) = 1;
-    atomicExch(status, kDeviceWaitTimeout);
-    return false;
-  }
-};
-
-// Tile *i, or the first one after it in this CTA's sequence that has products
-// (weight grad: an expert without rows has none).
-template <int FORM, int CG>
-__device__ __forceinline__ Tile next_tile(const TcArgs& g, const int* prefix, const int* offs,
-                                          int tiles, int step, int* i) {
-  Tile t{};
-  while (*i < tiles) {
-    t = find_tile<FORM, CG>(g, prefix, offs, *i);
-    if (FORM != EX_WGRAD || t.cnt > 0) break;
-    *i += step;
-  }
-  return t;
-}
 
 // First row, within tile t, that loading warp w brings for slice s.
 template <int FORM, int CG>
@@ -173,13 +98,6 @@ __device__ __forceinline__ void fetch_rows(const TcArgs& g, const Tile& t, int b
     const int b = b0 + 4 * (lane & 3) + j;
     u[j] = b >= t.cnt ? -1 : g.p2u == nullptr ? t.start + b : g.p2u[t.start + b];
   }
-}
-
-// u mod T.  u inv_T / 2^32 is below u / T by less than 1, so its floor is the
-// quotient or one less.
-__device__ __forceinline__ int token_of(const TcArgs& g, int u) {
-  const int r = u - static_cast<int>(__umulhi(static_cast<uint32_t>(u), g.inv_T)) * g.T;
-  return r >= g.T ? r - g.T : r;
 }
 
 // Their rows of x: `none` for rows behind the tile's last.
@@ -204,30 +122,10 @@ __device__ __forceinline__ void issue_gather(uint32_t dst, const CUtensorMap* ma
   }
 }
 
-// Two values rounded to bf16, the first in the low half.
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Adds v to *p without reading it back.
-__device__ __forceinline__ void red_add(float* p, float v) {
-  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
-}
-
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
                                              uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
-}
-
-// Stages per accumulator of a tile: all of them, or for a fp32 output near-equal
-// shares of at most kSegment.
-template <bool F32>
-__device__ __forceinline__ int segment_of(int slices) {
-  if (!F32 || slices <= kSegment) return slices;
-  const int parts = (slices + kSegment - 1) / kSegment;
-  return (slices + parts - 1) / parts;
 }
 
 template <int FORM, int CG, bool F32>
@@ -291,13 +189,13 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
     int stage = group;
     uint32_t parity = 1;  // the first pass finds the stages empty
     int i = first, s = 0;
-    Tile t = next_tile<FORM, CG>(g, prefix, offs, tiles, step, &i);
+    Tile t = next_tile<FORM, S>(g, prefix, offs, tiles, step, &i);
     auto advance = [&](int* i, int* s, Tile* t) {
       const int slices = FORM == EX_WGRAD ? (t->cnt + kDeep - 1) / kDeep : fixed_slices;
       if (++*s == slices) {
         *i += step;
         *s = 0;
-        *t = next_tile<FORM, CG>(g, prefix, offs, tiles, step, i);
+        *t = next_tile<FORM, S>(g, prefix, offs, tiles, step, i);
       }
     };
     if (group == 1 && i < tiles) advance(&i, &s, &t);
@@ -388,7 +286,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
     uint32_t parity = 0;
     bool ok = true;
     int i = first;
-    Tile t = next_tile<FORM, CG>(g, prefix, offs, tiles, step, &i);
+    Tile t = next_tile<FORM, S>(g, prefix, offs, tiles, step, &i);
     while (i < tiles && ok) {
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
       const int cols = FORM == EX_WGRAD ? S::kTileB
@@ -433,7 +331,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
             parity ^= 1;
           }
           // the next tile is looked up while this slice is computed
-          if (s == 0) nt = next_tile<FORM, CG>(g, prefix, offs, tiles, step, &ni);
+          if (s == 0) nt = next_tile<FORM, S>(g, prefix, offs, tiles, step, &ni);
         }
         ++n;
       }
@@ -451,10 +349,10 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_tc_kernel(
     int n = 0;
     bool ok = true;
     Tile nt{};
-    if (first < tiles) nt = find_tile<FORM, CG>(g, prefix, offs, first);
+    if (first < tiles) nt = find_tile<FORM, S>(g, prefix, offs, first);
     for (int i = first; i < tiles && ok; i += step) {
       const Tile t = nt;
-      if (i + step < tiles) nt = find_tile<FORM, CG>(g, prefix, offs, i + step);
+      if (i + step < tiles) nt = find_tile<FORM, S>(g, prefix, offs, i + step);
       const bool none = FORM == EX_WGRAD && t.cnt == 0;  // an expert without rows: zeros
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
       // one accumulator after the other: the first is stored, the others added
@@ -683,7 +581,7 @@ int launch_typed(const ExpertArgs& a, cudaStream_t st) {
   const int resident = resident_clusters(kern, CG, smem_bytes(FORM), known);
   TcArgs g{a.offsets, a.p2u, a.out, device_status_word(), a.T, a.P, a.E, a.N, a.D,
            FORM == EX_DGRAD || a.p2u == nullptr ? a.P : a.T,
-           a.T > 1 ? static_cast<uint32_t>((1ull << 32) / a.T) : 0xffffffffu};
+           inverse_of(a.T)};
   if (resident <= 0 || g.status == nullptr) return MR_ERR_CUDA;
   // a and b: weights, or single rows for gathering; the boxes: 16 rows in order
   CUtensorMap ma, mb, ba, bb, out;

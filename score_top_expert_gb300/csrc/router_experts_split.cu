@@ -14,9 +14,9 @@
 // The tiles, their order and which operand is A are those of
 // router_experts_tc.cu with one CTA to a tile (128 x up to 128).  A stage holds 64
 // contraction indices of all parts.  Sixteen warps load: 64 neighbouring elements
-// of a row a warp at a time, two per lane, element loads at any alignment, all of
-// a stage's rows in flight before the wait for its space; the parts go to shared
-// memory in the layout that the tensor cores read.
+// of a row a warp at a time, two per lane, element loads at any alignment, the next
+// slice's rows of one operand in flight while the other's parts are stored; the
+// parts go to shared memory in the layout that the tensor cores read.
 //
 // Bound by the loading warps' instructions (about 16 for two elements): 517
 // tokens, 64 experts, 4 choices, 515 x 333 fp32.
@@ -57,29 +57,58 @@ struct SplitArgs {
   int out_f32;
 };
 
-// The upper halves of x0 and x1 as a bf16 pair; each value minus its half.
-__device__ __forceinline__ uint32_t take_part(uint32_t& x0, uint32_t& x1) {
-  const uint32_t pair = __byte_perm(x0, x1, 0x7632);
-  const float h0 = __uint_as_float(x0 & 0xffff0000u), h1 = __uint_as_float(x1 & 0xffff0000u);
-  // an infinity or NaN is its own first part and leaves nothing
-  x0 = (x0 & 0x7f800000u) == 0x7f800000u ? 0u : __float_as_uint(__uint_as_float(x0) - h0);
-  x1 = (x1 & 0x7f800000u) == 0x7f800000u ? 0u : __float_as_uint(__uint_as_float(x1) - h1);
-  return pair;
+// x minus its upper half; nothing of an infinity or NaN, which is its own first part.
+__device__ __forceinline__ uint32_t rest_of(uint32_t x) {
+  const float r = __uint_as_float(x) - __uint_as_float(x & 0xffff0000u);
+  return r == r ? __float_as_uint(r) : 0u;
+}
+
+__device__ __forceinline__ uint32_t rest_of_finite(uint32_t x) {
+  return __float_as_uint(__uint_as_float(x) - __uint_as_float(x & 0xffff0000u));
+}
+
+// The upper halves of x0 and x1 as a bf16 pair.
+__device__ __forceinline__ uint32_t upper_halves(uint32_t x0, uint32_t x1) {
+  return __byte_perm(x0, x1, 0x7632);
 }
 
 __device__ __forceinline__ void st_word(uint32_t at, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
-// Two elements of a row from column 2 * lane: as loaded, zero behind `cols`.
-__device__ __forceinline__ void load_two(const float* p, int cols, int lane, uint32_t (&v)[2]) {
-  v[0] = 2 * lane < cols ? __float_as_uint(__ldg(p + 2 * lane)) : 0u;
-  v[1] = 2 * lane + 1 < cols ? __float_as_uint(__ldg(p + 2 * lane + 1)) : 0u;
+// Element i as its bits, for bf16 in the low half.
+__device__ __forceinline__ uint32_t load_bits(const float* p) { return __float_as_uint(__ldg(p)); }
+__device__ __forceinline__ uint32_t load_bits(const unsigned short* p) { return __ldg(p); }
+
+// Two elements of a row from column 2 * lane, zero behind `cols`.
+template <typename TIn>
+__device__ __forceinline__ void load_two(const TIn* p, int cols, int lane, uint32_t (&v)[2]) {
+  v[0] = 2 * lane < cols ? load_bits(p + 2 * lane) : 0u;
+  v[1] = 2 * lane + 1 < cols ? load_bits(p + 2 * lane + 1) : 0u;
 }
-__device__ __forceinline__ void load_two(const unsigned short* p, int cols, int lane,
-                                         uint32_t (&v)[2]) {
-  v[0] = 2 * lane < cols ? __ldg(p + 2 * lane) : 0u;
-  v[1] = 2 * lane + 1 < cols ? __ldg(p + 2 * lane + 1) : 0u;
+
+// A warp's rows of a stage, row index w + 16 j.  Flat: rows of 64 columns, j = 0
+// .. 7.  Else 64 rows of 128 columns as two halves, j & 3 and j >> 2.  p: row w,
+// stride: 16 rows; `rows` of the 128 (64) and `cols` exist, the others are zero.
+template <bool FLAT, typename TIn>
+__device__ __forceinline__ void load_rows(const TIn* p, size_t stride, int rows, int cols, int w,
+                                          int lane, uint32_t (&v)[kOwn][2]) {
+  if (rows >= (FLAT ? 128 : 64) && cols >= (FLAT ? 64 : 128)) {
+    p += 2 * lane;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      const TIn* q = FLAT ? p + j * stride : p + (j & 3) * stride + (j >> 2) * 64;
+      v[j][0] = load_bits(q);
+      v[j][1] = load_bits(q + 1);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      const int r = w + 16 * (FLAT ? j : j & 3);
+      load_two(FLAT ? p + j * stride : p + (j & 3) * stride + (j >> 2) * 64,
+               r < rows ? cols - (FLAT ? 0 : (j >> 2) * 64) : 0, lane, v[j]);
+    }
+  }
 }
 
 // Row r of a part, two elements per lane, in the 128-byte swizzle.
@@ -89,8 +118,10 @@ __device__ __forceinline__ void store_parts(uint32_t at, int r, int lane, uint32
   if constexpr (Parts<TIn>::kN == 1) {
     st_word(to, v[0] | (v[1] << 16));
   } else {
-#pragma unroll
-    for (int p = 0; p < 3; ++p) st_word(to + p * kPartBytes, take_part(v[0], v[1]));
+    st_word(to, upper_halves(v[0], v[1]));
+    const uint32_t m0 = rest_of(v[0]), m1 = rest_of(v[1]);
+    st_word(to + kPartBytes, upper_halves(m0, m1));
+    st_word(to + 2 * kPartBytes, upper_halves(rest_of_finite(m0), rest_of_finite(m1)));
   }
 }
 
@@ -147,105 +178,96 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_split_kernel(const 
     const int w = warp - 8;
     const TIn* __restrict__ A = static_cast<const TIn*>(args.a);
     const TIn* __restrict__ B = static_cast<const TIn*>(args.b);
+    // Element loads of a slice's rows of one operand.  A's are in flight while B's
+    // parts of the slice before are stored and the other way round.
+    auto load_a = [&](const Tile& t, int s, uint32_t (&v)[kOwn][2]) {
+      const int k = s * kDeep;
+      if constexpr (FORM == EX_FWD)
+        load_rows<true>(A + (static_cast<size_t>(t.e) * g.N + t.a0 + w) * g.D + k,
+                        static_cast<size_t>(16) * g.D, g.N - t.a0, g.D - k, w, lane, v);
+      else if constexpr (FORM == EX_DGRAD)
+        load_rows<false>(A + (static_cast<size_t>(t.e) * g.N + k + w) * g.D + t.a0,
+                         static_cast<size_t>(16) * g.D, g.N - k, g.D - t.a0, w, lane, v);
+      else
+        load_rows<false>(A + static_cast<size_t>(t.start + k + w) * g.N + t.a0,
+                         static_cast<size_t>(16) * g.N, t.cnt - k, g.N - t.a0, w, lane, v);
+    };
+    [[maybe_unused]] const TIn* source[kOwn];  // forward: the tokens behind this warp's rows of B
+    auto load_b = [&](const Tile& t, int s, bool fresh, uint32_t (&v)[kOwn][2]) {
+      const int k = s * kDeep;
+      if constexpr (FORM == EX_FWD) {
+        if (fresh) {
+          int token[kOwn];
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            const int r = w + j * kLoaders;
+            token[j] = r < t.cnt ? (g.p2u == nullptr ? t.start + r : g.p2u[t.start + r]) : -1;
+          }
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            if (g.p2u != nullptr && token[j] >= 0) token[j] = token_of(g, token[j]);
+            source[j] = token[j] < 0 ? nullptr : B + static_cast<size_t>(token[j]) * g.D;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+          load_two(source[j] + k, source[j] == nullptr ? 0 : g.D - k, lane, v[j]);
+      } else if constexpr (FORM == EX_DGRAD) {
+        load_rows<true>(B + static_cast<size_t>(t.start + w) * g.N + k,
+                        static_cast<size_t>(16) * g.N, t.cnt, g.N - k, w, lane, v);
+      } else if (g.p2u == nullptr) {
+        load_rows<false>(B + static_cast<size_t>(t.start + k + w) * g.D + t.b0,
+                         static_cast<size_t>(16) * g.D, t.cnt - k, g.D - t.b0, w, lane, v);
+      } else {
+        int u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = k + w + 16 * j;
+          u[j] = r < t.cnt ? g.p2u[t.start + r] : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+          const int row = u[j & 3];
+          const TIn* p = B + static_cast<size_t>(row < 0 ? 0 : token_of(g, row)) * g.D + t.b0 +
+                         (j >> 2) * 64;
+          load_two(p, row < 0 ? 0 : g.D - t.b0 - (j >> 2) * 64, lane, v[j]);
+        }
+      }
+    };
     int stage = 0;
     uint32_t parity = 1;  // the first pass finds the stages empty
-    bool ok = true;
-    int i = first;
+    int i = first, s = 0;
     Tile t = next_tile<FORM, S>(g, prefix, offs, tiles, step, &i);
-    while (i < tiles && ok) {
+    uint32_t va[kOwn][2], vb[kOwn][2];
+    if (i < tiles) {
+      load_a(t, 0, va);
+      load_b(t, 0, true, vb);
+    }
+    while (i < tiles) {
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
       const int rows_b = FORM == EX_WGRAD ? kTileRows : (t.cnt + 15) / 16 * 16;
-      // forward: the tokens behind this warp's rows of B
-      [[maybe_unused]] int token[kOwn];
-      if constexpr (FORM == EX_FWD) {
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j) {
-          const int r = w + j * kLoaders;
-          token[j] = r < t.cnt ? (g.p2u == nullptr ? t.start + r : g.p2u[t.start + r]) : -1;
-        }
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j)
-          if (g.p2u != nullptr && token[j] >= 0) token[j] = token_of(g, token[j]);
+      if (++s == slices) {  // t and s: the slice after the one that is stored
+        s = 0;
+        i += step;
+        t = next_tile<FORM, S>(g, prefix, offs, tiles, step, &i);
       }
-      for (int s = 0; s < slices; ++s) {
-        uint32_t va[kOwn][2], vb[kOwn][2];
+      if (!__all_sync(0xffffffffu, wait(&empty[stage], parity))) break;
+      const uint32_t at = stages_at + stage * kStageBytes;
 #pragma unroll
-        for (int j = 0; j < kOwn; ++j) {
-          // row r of A: a value of A's dimension (forward), or an index of the
-          // contraction and half of the values
-          const int r = w + j * kLoaders;
-          const TIn* p = A;
-          int cols = 0;
-          if constexpr (FORM == EX_FWD) {
-            if (t.a0 + r < g.N) {
-              p = A + (static_cast<size_t>(t.e) * g.N + t.a0 + r) * g.D + s * kDeep;
-              cols = g.D - s * kDeep;
-            }
-          } else if constexpr (FORM == EX_DGRAD) {
-            const int k = s * kDeep + (r & 63), c = t.a0 + (r & 64);
-            if (k < g.N && c < g.D) {
-              p = A + (static_cast<size_t>(t.e) * g.N + k) * g.D + c;
-              cols = g.D - c;
-            }
-          } else {
-            const int k = s * kDeep + (r & 63), c = t.a0 + (r & 64);
-            if (k < t.cnt && c < g.N) {
-              p = A + static_cast<size_t>(t.start + k) * g.N + c;
-              cols = g.N - c;
-            }
-          }
-          load_two(p, cols, lane, va[j]);
-        }
+      for (int j = 0; j < kOwn; ++j) store_parts<TIn>(at, w + j * kLoaders, lane, va[j]);
+      if (i < tiles) load_a(t, s, va);
 #pragma unroll
-        for (int j = 0; j < kOwn; ++j) {
-          const int r = w + j * kLoaders;
-          const TIn* p = B;
-          int cols = 0;
-          if constexpr (FORM == EX_FWD) {
-            if (token[j] >= 0) {
-              p = B + static_cast<size_t>(token[j]) * g.D + s * kDeep;
-              cols = g.D - s * kDeep;
-            }
-          } else if constexpr (FORM == EX_DGRAD) {
-            if (r < t.cnt) {
-              p = B + static_cast<size_t>(t.start + r) * g.N + s * kDeep;
-              cols = g.N - s * kDeep;
-            }
-          } else {
-            const int k = s * kDeep + (r & 63), c = t.b0 + (r & 64);
-            if (k < t.cnt && c < g.D) {
-              int u = t.start + k;
-              if (g.p2u != nullptr) {
-                u = g.p2u[u];
-                u = u < 0 ? -1 : token_of(g, u);
-              }
-              if (u >= 0) {
-                p = B + static_cast<size_t>(u) * g.D + c;
-                cols = g.D - c;
-              }
-            }
-          }
-          load_two(p, cols, lane, vb[j]);
-        }
-        ok = __all_sync(0xffffffffu, wait(&empty[stage], parity));
-        if (!ok) break;
-        const uint32_t at = stages_at + stage * kStageBytes;
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j) store_parts<TIn>(at, w + j * kLoaders, lane, va[j]);
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j)
-          if (w + j * kLoaders < rows_b)
-            store_parts<TIn>(at + kN * kPartBytes, w + j * kLoaders, lane, vb[j]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          parity ^= 1;
-        }
+      for (int j = 0; j < kOwn; ++j)
+        if (w + j * kLoaders < rows_b)
+          store_parts<TIn>(at + kN * kPartBytes, w + j * kLoaders, lane, vb[j]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[stage]);
+      if (i < tiles) load_b(t, s, s == 0, vb);
+      if (++stage == kStages) {
+        stage = 0;
+        parity ^= 1;
       }
-      i += step;
-      t = next_tile<FORM, S>(g, prefix, offs, tiles, step, &i);
     }
   } else if (warp == 1) {
     // ---- products ----------------------------------------------------------------

@@ -437,7 +437,11 @@ MR_API int router_aux_loss_fwd_noalloc(const float* aux_scores, const uint8_t* r
  * weight  [E, N, D] dtype, input
  * out     [P, N] out_dtype, output
  * P = 0 is a no-op.  MR_ERR_INVALID also for a map with T = 0 and P > 0.
- * fp32 operands are multiplied in fp32 on the vector units.
+ * bf16 operands whose rows are 16-byte aligned (D, and for the gradients N, a
+ * multiple of 8) take the fastest kernels; any other alignment and fp32 operands
+ * are loaded element by element.  fp32 operands are multiplied as three bf16
+ * parts each (exact, but for terms below 2^-28 of a product), so that an
+ * infinite operand may give NaN where its product with a number is infinite.
  */
 MR_API int router_expert_matmul(const void* x, mr_dtype dtype, const void* weight,
                                 const int32_t* expert_first_token_offset,
@@ -488,7 +492,8 @@ MR_API int router_expert_matmul_bwd_weight(const void* grad_out, mr_dtype dtype,
  * zeros    [E, N, D / group_size] bytes, the low four bits count, or NULL: 8
  * out      [P, N] out_dtype
  * MR_ERR_INVALID: D % group_size != 0, x or qweight not 16-byte aligned.
- * MR_ERR_UNSUPPORTED: group_size other than 32, 64 or 128.
+ * MR_ERR_UNSUPPORTED: group_size other than 32, 64 or 128, or more than 2^31
+ * tasks of 8 rows and 48 weight rows.
  */
 MR_API int router_expert_matmul_w4(const void* x, const uint8_t* qweight, const void* scales,
                                    const uint8_t* zeros, int group_size,

@@ -20,14 +20,18 @@ int check_product(int T, int P, int E, int N, int D, bool mapped) {
   return MR_OK;
 }
 
-// Rows up to which the forward of bf16 operands takes the few-rows kernel.
+// Rows up to which, and columns from which, the forward of bf16 operands takes
+// the few-rows kernel.
 constexpr int kFewRows = 36;
+constexpr int kFewColumns = 512;
 
 int run_product(int form, const ExpertArgs& a, mr_stream_t stream) {
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // One token's rows: 4 experts of 1024 x 1024 take 10 us here and 13 us in the
-  // tensor-core pipeline, 64 rows of 47 experts of 1024 x 2048 53 and 51.
-  if (form == EX_FWD && a.P <= kFewRows && expert_matmul_few_ok(a))
+  // One token's rows: 4 experts of 1024 x 1024 take 10 us here and 14 us in the
+  // tensor-core pipeline, 2 of 4096 x 4096 22 and 29; 28 or more experts of 1024
+  // x 1024 the same in both.  Rows too short to pay for the staging of x take
+  // longer: 28 experts of 1736 x 88 22 us against 16.
+  if (form == EX_FWD && a.P <= kFewRows && a.D >= kFewColumns && expert_matmul_few_ok(a))
     return launch_expert_matmul_few(a, st);
   return expert_matmul_tc_ok(form, a) ? launch_expert_matmul_tc(form, a, st)
                                       : launch_expert_matmul_split(form, a, st);

@@ -614,10 +614,9 @@ def router_expert_matmul(x: torch.Tensor, weight: torch.Tensor,
     router_expert_maps) x is the tokens [T, D], read through the map; without
     it x is the permuted rows [P, D].  Rows that no expert owns are left as
     they were in ``out``."""
-    dt = x.dtype
-    if not x.is_cuda or dt not in _DTYPE or x.dim() != 2 or not x.is_contiguous():
+    dt, idx = x.dtype, x.get_device()
+    if idx < 0 or dt not in _DTYPE or x.dim() != 2 or not x.is_contiguous():
         x = _rows_2d(x, "x", None, _DTYPE)
-    idx = x.get_device()
     if weight.get_device() != idx or weight.dtype is not dt or weight.dim() != 3 \
             or not weight.is_contiguous():
         _weight_3d(weight, "weight", idx, dt)
@@ -626,8 +625,8 @@ def router_expert_matmul(x: torch.Tensor, weight: torch.Tensor,
     if cols != D:
         _bad("x", f"[rows, {D}]")
     off = expert_first_token_offset
-    if off.get_device() != idx or off.dtype is not _I32 or off.shape != (E + 1,) \
-            or not off.is_contiguous():
+    if off.get_device() != idx or off.dtype is not _I32 or off.numel() != E + 1 \
+            or off.dim() != 1 or not off.is_contiguous():
         off = _map_1d(off, "expert_first_token_offset", idx, E + 1)
     p2u = permuted_to_unpermuted
     if p2u is None:
@@ -644,14 +643,14 @@ def router_expert_matmul(x: torch.Tensor, weight: torch.Tensor,
         out = _empty((P, N), dtype=odt, device=x.device)
     else:
         out = _out(out, (P, N), odt, x.device, "out")
-    call = _calls().router_expert_matmul
-    args = (x.data_ptr(), _DTYPE[dt], weight.data_ptr(), off.data_ptr(), p2u_ptr, T, P, E, N, D,
-            out.data_ptr(), _DTYPE[odt], _raw_stream(idx))
+    call = (_fast or _calls()).router_expert_matmul
     if idx == _cur_dev():
-        rc = call(*args)
+        rc = call(x.data_ptr(), _DTYPE[dt], weight.data_ptr(), off.data_ptr(), p2u_ptr, T, P, E, N,
+                  D, out.data_ptr(), _DTYPE[odt], _raw_stream(idx))
     else:
         with torch.cuda.device(idx):
-            rc = call(*args)
+            rc = call(x.data_ptr(), _DTYPE[dt], weight.data_ptr(), off.data_ptr(), p2u_ptr, T, P, E,
+                      N, D, out.data_ptr(), _DTYPE[odt], _raw_stream(idx))
     if rc != 0:
         raise RouterError("router_expert_matmul", rc)
     return out
@@ -728,11 +727,11 @@ def router_expert_matmul_w4(x: torch.Tensor, qweight: torch.Tensor, scales: torc
     scales [E, N, D / group] bf16, zeros the same in uint8 (0..15) or None for
     8; group 32, 64 or 128.  Returns out [P, N] in ``out_dtype`` (default
     bf16)."""
-    if not x.is_cuda or x.dtype is not _BF16 or x.dim() != 2 or not x.is_contiguous():
+    idx = x.get_device()
+    if idx < 0 or x.dtype is not _BF16 or x.dim() != 2 or not x.is_contiguous():
         x = _rows_2d(x, "x", None, (_BF16,))
     if x.data_ptr() & 15:
         x = x.clone()
-    idx = x.get_device()
     if qweight.get_device() != idx or qweight.dtype is not _U8 or qweight.dim() != 3 \
             or not qweight.is_contiguous():
         _weight_3d(qweight, "qweight", idx, _U8)
@@ -756,8 +755,8 @@ def router_expert_matmul_w4(x: torch.Tensor, qweight: torch.Tensor, scales: torc
     if cols != D:
         _bad("x", f"[rows, {D}]")
     off = expert_first_token_offset
-    if off.get_device() != idx or off.dtype is not _I32 or off.shape != (E + 1,) \
-            or not off.is_contiguous():
+    if off.get_device() != idx or off.dtype is not _I32 or off.numel() != E + 1 \
+            or off.dim() != 1 or not off.is_contiguous():
         off = _map_1d(off, "expert_first_token_offset", idx, E + 1)
     p2u = permuted_to_unpermuted
     if p2u is None:
@@ -774,15 +773,16 @@ def router_expert_matmul_w4(x: torch.Tensor, qweight: torch.Tensor, scales: torc
         out = _empty((P, N), dtype=odt, device=x.device)
     else:
         out = _out(out, (P, N), odt, x.device, "out")
-    call = _calls().router_expert_matmul_w4
-    args = (x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), z_ptr, D // groups,
-            off.data_ptr(), p2u_ptr, T, P, E, N, D, out.data_ptr(), _DTYPE[odt],
-            _raw_stream(idx))
+    call = (_fast or _calls()).router_expert_matmul_w4
     if idx == _cur_dev():
-        rc = call(*args)
+        rc = call(x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), z_ptr, D // groups,
+                  off.data_ptr(), p2u_ptr, T, P, E, N, D, out.data_ptr(), _DTYPE[odt],
+                  _raw_stream(idx))
     else:
         with torch.cuda.device(idx):
-            rc = call(*args)
+            rc = call(x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), z_ptr, D // groups,
+                      off.data_ptr(), p2u_ptr, T, P, E, N, D, out.data_ptr(), _DTYPE[odt],
+                      _raw_stream(idx))
     if rc != 0:
         raise RouterError("router_expert_matmul_w4", rc)
     return out
@@ -807,12 +807,12 @@ def router_combine_fwd(expert_out: torch.Tensor, unpermuted_to_permuted: torch.T
     is router_expert_maps's.  Returns out [T, D] in expert_out's dtype; a choice
     with map entry -1 adds nothing."""
     z, u2p = expert_out, unpermuted_to_permuted
-    if not z.is_cuda or z.dtype not in _DTYPE or z.dim() != 2 or not z.is_contiguous():
-        z = _rows_2d(z, "expert_out", None, _DTYPE)
     idx, dt = z.get_device(), z.dtype
+    if idx < 0 or dt not in _DTYPE or z.dim() != 2 or not z.is_contiguous():
+        z = _rows_2d(z, "expert_out", None, _DTYPE)
     P, D = z.shape
-    if u2p.get_device() != idx or u2p.dtype is not _I32 or u2p.shape != (P,) \
-            or not u2p.is_contiguous():
+    if u2p.get_device() != idx or u2p.dtype is not _I32 or u2p.numel() != P \
+            or u2p.dim() != 1 or not u2p.is_contiguous():
         u2p = _map_1d(u2p, "unpermuted_to_permuted", idx, P)
     K = int(K)
     if K < 1 or P % K != 0:
@@ -826,14 +826,14 @@ def router_combine_fwd(expert_out: torch.Tensor, unpermuted_to_permuted: torch.T
         out = _empty((T, D), dtype=dt, device=z.device)
     else:
         out = _out(out, (T, D), dt, z.device, "out")
-    call = _calls().router_combine_fwd
-    args = (z.data_ptr(), _DTYPE[dt], u2p.data_ptr(), w_ptr, ld, T, K, D, out.data_ptr(),
-            _raw_stream(idx))
+    call = (_fast or _calls()).router_combine_fwd
     if idx == _cur_dev():
-        rc = call(*args)
+        rc = call(z.data_ptr(), _DTYPE[dt], u2p.data_ptr(), w_ptr, ld, T, K, D, out.data_ptr(),
+                  _raw_stream(idx))
     else:
         with torch.cuda.device(idx):
-            rc = call(*args)
+            rc = call(z.data_ptr(), _DTYPE[dt], u2p.data_ptr(), w_ptr, ld, T, K, D, out.data_ptr(),
+                      _raw_stream(idx))
     if rc != 0:
         raise RouterError("router_combine_fwd", rc)
     return out
@@ -847,17 +847,17 @@ def router_combine_bwd(grad_out: torch.Tensor, unpermuted_to_permuted: torch.Ten
     dtype, grad_weights [T, K] float32, or None when ``expert_out`` is None).
     Rows of grad_expert_out that no choice names are left as they were."""
     g, u2p, z = grad_out, unpermuted_to_permuted, expert_out
-    if not g.is_cuda or g.dtype not in _DTYPE or g.dim() != 2 or not g.is_contiguous():
-        g = _rows_2d(g, "grad_out", None, _DTYPE)
     idx, dt = g.get_device(), g.dtype
+    if idx < 0 or dt not in _DTYPE or g.dim() != 2 or not g.is_contiguous():
+        g = _rows_2d(g, "grad_out", None, _DTYPE)
     dev = g.device
     T, D = g.shape
     K = int(K)
     if K < 1:
         _bad("K", "at least 1")
     P = T * K
-    if u2p.get_device() != idx or u2p.dtype is not _I32 or u2p.shape != (P,) \
-            or not u2p.is_contiguous():
+    if u2p.get_device() != idx or u2p.dtype is not _I32 or u2p.numel() != P \
+            or u2p.dim() != 1 or not u2p.is_contiguous():
         u2p = _map_1d(u2p, "unpermuted_to_permuted", idx, P)
     w_ptr = ld = z_ptr = gw_ptr = 0
     if topk_weights is not None:
@@ -881,14 +881,14 @@ def router_combine_bwd(grad_out: torch.Tensor, unpermuted_to_permuted: torch.Ten
         grad_expert_out = _empty((P, D), dtype=dt, device=dev)
     else:
         grad_expert_out = _out(grad_expert_out, (P, D), dt, dev, "grad_expert_out")
-    call = _calls().router_combine_bwd
-    args = (g.data_ptr(), _DTYPE[dt], u2p.data_ptr(), z_ptr, w_ptr, ld, T, K, D,
-            grad_expert_out.data_ptr(), gw_ptr, _raw_stream(idx))
+    call = (_fast or _calls()).router_combine_bwd
     if idx == _cur_dev():
-        rc = call(*args)
+        rc = call(g.data_ptr(), _DTYPE[dt], u2p.data_ptr(), z_ptr, w_ptr, ld, T, K, D,
+                  grad_expert_out.data_ptr(), gw_ptr, _raw_stream(idx))
     else:
         with torch.cuda.device(idx):
-            rc = call(*args)
+            rc = call(g.data_ptr(), _DTYPE[dt], u2p.data_ptr(), z_ptr, w_ptr, ld, T, K, D,
+                      grad_expert_out.data_ptr(), gw_ptr, _raw_stream(idx))
     if rc != 0:
         raise RouterError("router_combine_bwd", rc)
     return grad_expert_out, grad_weights

@@ -83,6 +83,9 @@ PRODUCTS = [
     (900, 2, 1, 1000, 1608, "bf16", "f32", True), (20, 8, 2, 1600, 1608, "bf16", "f32", False),
     (1700, 1, 1, 264, 72, "bf16", "f32", True), (1700, 1, 1, 264, 72, "bf16", "bf16", True),
     (64, 8, 2, 128, 64, "f32", "f32", True), (37, 7, 3, 67, 129, "f32", "f32", True),
+    (20, 4, 2, 1100, 1301, "f32", "f32", True), (1100, 1, 1, 40, 33, "f32", "f32", True),
+    (30, 4, 2, 1003, 1201, "bf16", "f32", True), (260, 2, 1, 129, 130, "bf16", "bf16", False),
+    (3, 9, 4, 600, 776, "bf16", "bf16", True), (4, 9, 9, 40, 520, "bf16", "f32", False),
     (5, 3, 2, 33, 515, "f32", "bf16", False), (300, 2, 2, 100, 60, "f32", "f32", True),
 ]
 
@@ -227,6 +230,7 @@ def test_weights_past_32_bit_offsets(R):
     (4, 16, 3, 40, 96, 32, True, "f32", True), (7, 5, 5, 17, 320, 64, False, "f32", False),
     (33, 6, 2, 100, 256, 128, True, "bf16", True), (64, 3, 2, 130, 1056, 32, False, "f32", True),
     (9, 300, 6, 24, 64, 64, True, "f32", True), (200, 2, 1, 48, 640, 128, False, "bf16", True),
+    (3, 4, 2, 40, 8224, 32, True, "f32", True), (9, 3, 2, 20, 4480, 128, True, "bf16", False),
     (2, 2304, 36, 16, 2176, 128, True, "f32", True), (64, 2304, 36, 8, 32, 32, False, "bf16", True),
 ])
 def test_w4(R, T, E, K, N, D, group, zeros, out, gather):
@@ -258,6 +262,31 @@ def test_w4_with_empty_experts_and_skipped_choices(R):
     assert_within(down(y)[:placed][keep], ref[:placed][keep],
                   tolerance(ref, mag, 2 * D, "f32")[:placed][keep], "out")
     assert np.isnan(down(y)[:placed][~keep]).all()
+
+
+def test_w4_long_rows_over_many_tasks(R):
+    # more tiles than warps share, and activations longer than one staged panel
+    E, K, T, N, D, group = 8, 2, 8, 9984, 4224, 128
+    m = route(T, E, K, seed=7)
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    try:
+        q = torch.randint(0, 256, (E, N, D // 2), generator=gen, device=DEV, dtype=torch.uint8)
+        s = (torch.rand(E, N, D // group, generator=gen, device=DEV) * 0.01).bfloat16()
+        z = torch.randint(0, 16, (E, N, D // group), generator=gen, device=DEV, dtype=torch.uint8)
+        x = torch.randn(T, D, generator=gen, device=DEV).bfloat16()
+        y = R.router_expert_matmul_w4(x, q, s, up(m["off"]), up(m["p2u"]), zeros=z,
+                                      out_dtype=torch.float32)
+        for e in range(E):
+            a, b = int(m["off"][e]), int(m["off"][e + 1])
+            if a == b:
+                continue
+            w = torch.stack((q[e] & 15, q[e] >> 4), 2).view(N, D // group, group).double()
+            w = ((w - z[e].double()[..., None]) * s[e].double()[..., None]).view(N, D)
+            xe = x[torch.from_numpy(m["p2u"][a:b] % T).long().to(DEV)].double()
+            ref, mag = down(xe @ w.t()), down(xe.abs() @ w.abs().t())
+            assert_within(down(y[a:b]), ref, tolerance(ref, mag, 2 * D, "f32"), f"expert {e}")
+    finally:
+        torch.cuda.empty_cache()
 
 
 # ---- combination ---------------------------------------------------------------
@@ -432,12 +461,13 @@ def test_calls_repeat_bit_for_bit_and_replay_from_a_graph(R):
         assert all(torch.equal(a, b) for a, b in zip(outs, eager[i]))
 
 
-def test_two_streams_at_once(R):
-    T, E, K, N, D = 300, 16, 4, 264, 264
+@pytest.mark.parametrize("T,dtype", [(300, "bf16"), (300, "f32"), (6, "bf16")])
+def test_two_streams_at_once(R, T, dtype):
+    E, K, N, D = 16, 4, 264, 520
     m = route(T, E, K, seed=4)
     off, p2u = up(m["off"]), up(m["p2u"])
-    w = up(normals((E, N, D), 2, "bf16", 0.1), "bf16")
-    xs = [up(normals((T, D), s, "bf16"), "bf16") for s in (1, 2)]
+    w = up(normals((E, N, D), 2, dtype, 0.1), dtype)
+    xs = [up(normals((T, D), s, dtype), dtype) for s in (1, 2)]
     refs = [R.router_expert_matmul(x, w, off, p2u) for x in xs]
     streams = [torch.cuda.Stream() for _ in xs]
     outs = [[], []]

@@ -38,9 +38,9 @@
 // output's contraction is therefore cut into segments of at most 960: each is
 // an accumulator of its own and is added to the output, rounding to nearest, by
 // the threads (weight grad: the copy engine) that stored the one before, in
-// order, so results repeat bit for bit.  It costs 5 % of the 8192 x 2048 x 1024
-// forward over 256 experts and a quarter of the compute-bound one over 64
-// (205 to 268 us); adding through staged boxes took 285 us.
+// order, so results repeat bit for bit.  It costs a quarter of the compute-bound
+// forward (8192 tokens, 64 experts, 2048 x 2048: 205 to 268 us; adding through
+// staged boxes took 285 us).
 //
 // What bounded it on the way (forward, 8192 tokens, 64 experts, 4 choices,
 // 2048 x 2048): the issue of copies and products.  Under a lane test each cost

@@ -45,11 +45,6 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-               ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
-}
-
 // Arrive on a barrier given by its shared::cluster address and announce bytes.
 // Relaxed: the arriving warp publishes no writes of its own, and a release of
 // cluster scope at each stage costs more than the copies' issue.

@@ -152,6 +152,28 @@ def test_a_nan_stays_in_its_rows_and_expert(R):
     assert np.isfinite(gw).all()
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 136), ("bf16", 135), ("f32", 136)])
+def test_a_nan_among_rows_in_order_stays_there(R, dtype, D):
+    # rows in order are brought in whole boxes that may reach into the next expert
+    E, N = 3, 72
+    off = np.array([0, 40, 45, 100], np.int32)
+    x, w = normals((100, D), 1, dtype), normals((E, N, D), 2, dtype, 0.1)
+    g = normals((100, N), 3, dtype)
+    x[42] = np.nan
+    y = down(R.router_expert_matmul(up(x, dtype), up(w, dtype), up(off)))
+    bad = np.arange(100) == 42
+    assert np.isnan(y[bad]).all() and np.isfinite(y[~bad]).all()
+    gw = down(R.router_expert_matmul_bwd_weight(up(g, dtype), up(x, dtype), up(off)))
+    assert np.isnan(gw[1]).all() and np.isfinite(gw[[0, 2]]).all()
+    x = normals((100, D), 1, dtype)
+    g[44] = np.inf
+    gw = down(R.router_expert_matmul_bwd_weight(up(g, dtype), up(x, dtype), up(off)))
+    assert not np.isfinite(gw[1]).any() and np.isfinite(gw[[0, 2]]).all()
+    gx = down(R.router_expert_matmul_bwd_input(up(g, dtype), up(w, dtype), up(off)))
+    bad = np.arange(100) == 44
+    assert not np.isfinite(gx[bad]).any() and np.isfinite(gx[~bad]).all()
+
+
 def test_empty_batches(R):
     w = torch.randn(3, 8, 16, device=DEV).bfloat16()
     off = torch.zeros(4, dtype=torch.int32, device=DEV)

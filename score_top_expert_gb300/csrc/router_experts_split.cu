@@ -8,7 +8,9 @@
 // accumulator of its own and the seven small ones share another, so that the
 // truncation of the tensor cores' sums (see router_experts_tc.cu) acts on as few
 // additions of large terms as in a bf16 product; a contraction is cut into
-// segments the same way, and a segment's two sums are added in round-to-nearest.
+// segments of at most 512 the same way, and a segment's two sums are added in
+// round-to-nearest: 2.7e-7 of the value at 515 terms and 4.9e-7 at 3900, where
+// fp32 multiply-add loops leave 4e-7 and 1.1e-6.
 // An infinity times a value with an empty part is a NaN.
 //
 // The tiles, their order and which operand is A are those of
@@ -18,8 +20,12 @@
 // slice's rows of one operand in flight while the other's parts are stored; the
 // parts go to shared memory in the layout that the tensor cores read.
 //
-// Bound by the loading warps' instructions (about 16 for two elements): 517
-// tokens, 64 experts, 4 choices, 515 x 333 fp32.
+// Bound by shared memory, which the 32 instructions of a slice read 8 KB of
+// operands each from and the parts are written to, and by the loading warps'
+// instructions: 8192 tokens, 64 experts, 4 choices, 1024 x 1024 fp32 take 557 us
+// forward (123 TFLOP/s of fp32 products), 487 us and 645 us the gradients; the
+// vector units reach 75 at most.  With few tiles it is the latency of one slice
+// (about 1.3 us): 517 tokens of 515 x 333, 210 tiles of nine slices, 45 us.
 #include <atomic>
 
 #include "router_experts_tiles.cuh"
@@ -33,6 +39,8 @@ constexpr int kTileRows = 128;               // of A and (at most) of B
 constexpr int kPartBytes = kTileRows * 128;  // one part of one operand
 constexpr int kOwn = kTileRows / kLoaders;   // rows of each operand that a warp loads
 constexpr int kStages = 2;
+// Stages per accumulator of fp32 operands (15 left 9e-7 of the value at 3900 terms).
+constexpr int kSplitSegment = 8;
 constexpr int kPadded = 33;                  // weight grad: staging row, in words
 
 struct SplitShape {
@@ -280,7 +288,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_split_kernel(const 
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
       const int cols = FORM == EX_WGRAD ? kTileRows : (t.cnt + 15) / 16 * 16;
       const uint32_t desc = product_desc(kTileRows, cols, FORM != EX_FWD, FORM == EX_WGRAD);
-      const int segment = args.out_f32 ? segment_of<true>(slices) : slices;
+      const int segment = args.out_f32 ? segment_of<true>(slices, kN == 3 ? kSplitSegment : kSegment) : slices;
       int ni = i + step;
       Tile nt = t;
       for (int s0 = 0; s0 < slices && ok; s0 += segment) {
@@ -348,7 +356,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_split_kernel(const 
       if (i + step < tiles) nt = find_tile<FORM, S>(g, prefix, offs, i + step);
       const bool none = FORM == EX_WGRAD && t.cnt == 0;  // an expert without rows: zeros
       const int slices = FORM == EX_WGRAD ? (t.cnt + kDeep - 1) / kDeep : fixed_slices;
-      const int segment = args.out_f32 ? segment_of<true>(slices) : slices;
+      const int segment = args.out_f32 ? segment_of<true>(slices, kN == 3 ? kSplitSegment : kSegment) : slices;
       for (int first_slice = 0; first_slice == 0 || first_slice < slices;) {
         const bool add = first_slice > 0;  // fp32 only: to what this thread stored before
         const int buf = n & 1;

@@ -108,11 +108,11 @@ __device__ __forceinline__ void red_add(float* p, float v) {
 }
 
 // Stages per accumulator of a tile: all of them, or for a fp32 output near-equal
-// shares of at most kSegment.
+// shares of at most `most`.
 template <bool F32>
-__device__ __forceinline__ int segment_of(int slices) {
-  if (!F32 || slices <= kSegment) return slices;
-  const int parts = (slices + kSegment - 1) / kSegment;
+__device__ __forceinline__ int segment_of(int slices, int most = kSegment) {
+  if (!F32 || slices <= most) return slices;
+  const int parts = (slices + most - 1) / most;
   return (slices + parts - 1) / parts;
 }
 

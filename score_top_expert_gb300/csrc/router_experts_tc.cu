@@ -46,8 +46,10 @@
 // 2048 x 2048): the issue of copies and products.  Under a lane test each cost
 // 60 to 100 cycles; 32 gathers a stage from one warp ran at 430 TFLOP/s, from
 // eight warps at 1060, and with operands in uniform registers (elect_one) the
-// kernel runs at 1250 through the map and 1310 in order; 4096 x 4096 over 8
-// experts at 1590 and 1740 (input gradient).
+// kernel ran at 1250 through the map and 1310 in order, with two groups of loading
+// warps at 1400 and 1430; 4096 x 4096 over 8 experts at 1770 and 1800 (input
+// gradient).  What is left is the operands' way from L2: a slice takes 640 to 700
+// cycles (29 to 32 KB for each SM) at 172, 210 and 242 rows a tile alike.
 #include <atomic>
 
 #include "router_experts_tiles.cuh"

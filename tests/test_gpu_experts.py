@@ -79,6 +79,8 @@ PRODUCTS = [
     (70, 300, 6, 24, 40, "bf16", "f32", True), (50, 2304, 36, 16, 32, "bf16", "bf16", True),
     (515, 4, 2, 257, 255, "bf16", "bf16", True), (40, 6, 2, 64, 65, "bf16", "f32", True),
     (40, 6, 2, 65, 64, "bf16", "f32", True),
+    # many experts of unequal sizes, taken by size
+    (3000, 40, 3, 264, 72, "bf16", "f32", True), (9000, 150, 2, 72, 136, "bf16", "bf16", False),
     # contractions and experts longer than a fp32 output's segment
     (900, 2, 1, 1000, 1608, "bf16", "f32", True), (20, 8, 2, 1600, 1608, "bf16", "f32", False),
     (1700, 1, 1, 264, 72, "bf16", "f32", True), (1700, 1, 1, 264, 72, "bf16", "bf16", True),

@@ -492,7 +492,7 @@ MR_API int router_expert_matmul_bwd_weight(const void* grad_out, mr_dtype dtype,
  * zeros    [E, N, D / group_size] bytes, the low four bits count, or NULL: 8
  * out      [P, N] out_dtype
  * MR_ERR_INVALID: D % group_size != 0, x or qweight not 16-byte aligned.
- * MR_ERR_UNSUPPORTED: group_size other than 32, 64 or 128; more than 2^31 - 1
+ * MR_ERR_UNSUPPORTED: group_size other than 32, 64 or 128; more than 2^30
  * tasks (8 permuted rows by 64 weight rows each).
  */
 MR_API int router_expert_matmul_w4(const void* x, const uint8_t* qweight, const void* scales,

@@ -10,9 +10,14 @@
 // the order the fragments want, then each of the 16 warps takes 16 weight rows
 // through two shared-memory stages of its own, 256 bytes of each row a stage,
 // filled by asynchronous copies a stage ahead, across tasks: 64 KB in flight on
-// an SM while the block changes its x.  With few tasks four
-// warps share 16 weight rows, a quarter of the contraction each, and add up in
-// shared memory in a fixed order.
+// an SM while the block changes its x.  With few tasks four warps share 16 weight
+// rows, a quarter of the contraction each, and add up in shared memory in a fixed
+// order.
+//
+// What bounds it: the instructions that unpack the nibbles (11 for eight weights)
+// and their latency.  33 tokens, 512 experts, 22 choices, 1024 x 1024 in groups of
+// 128: 98 us with 8 warps, 78 with 12, 64 with 16 (2.5 TB/s of weights); groups of
+// 32 with zero points, a sixth of the traffic: 102 us at 1056 x 1000.
 //
 // mma.sync m16n8k16 (16 weight rows, 8 permuted rows, fp32 sums) suits the
 // shape: a tcgen05 product would be 128 weight rows wide and needs the operand
@@ -427,7 +432,7 @@ int launch_shared(const FewArgs& a, long long groups, int sms, cudaStream_t st) 
   if (e != cudaSuccess) return MR_ERR_CUDA;
   const int row_tiles = (a.N + kRows - 1) / kRows;
   const long long tasks = groups * ((row_tiles + span - 1) / span);
-  if (tasks > INT_MAX) return MR_ERR_UNSUPPORTED;
+  if (tasks > INT_MAX / 2) return MR_ERR_UNSUPPORTED;  // a block's next task stays an int
   e = launch_kernel(kern, dim3(static_cast<unsigned>(tasks < sms ? tasks : sms)), dim3(kThreads),
                     smem, st, a);
   return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;

@@ -138,6 +138,31 @@ static PyObject* call_combine_bwd(PyObject* self, PyObject* const* args, Py_ssiz
   return PyLong_FromLong(rc);
 }
 
+static PyObject* call_expert_matmul_bwd_input(PyObject* self, PyObject* const* args,
+                                              Py_ssize_t nargs) {
+  uintptr_t g, w, off, gx, stream;
+  int dt, P, E, N, D, odt;
+  void* out[] = {&g, &dt, &w, &off, &P, &E, &N, &D, &gx, &odt, &stream};
+  if (convert(args, nargs, "pippiiiipip", out) != 0) return NULL;
+  const int rc = router_expert_matmul_bwd_input((const void*)g, (mr_dtype)dt, (const void*)w,
+                                                (const int32_t*)off, P, E, N, D, (void*)gx,
+                                                (mr_dtype)odt, (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
+static PyObject* call_expert_matmul_bwd_weight(PyObject* self, PyObject* const* args,
+                                               Py_ssize_t nargs) {
+  uintptr_t g, x, off, p2u, gw, stream;
+  int dt, T, P, E, N, D, odt;
+  void* out[] = {&g, &dt, &x, &off, &p2u, &T, &P, &E, &N, &D, &gw, &odt, &stream};
+  if (convert(args, nargs, "pipppiiiiipip", out) != 0) return NULL;
+  const int rc = router_expert_matmul_bwd_weight((const void*)g, (mr_dtype)dt, (const void*)x,
+                                                 (const int32_t*)off, (const int32_t*)p2u, T, P,
+                                                 E, N, D, (void*)gw, (mr_dtype)odt,
+                                                 (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
 static PyMethodDef kMethods[] = {
     {"router_topk_fwd", (PyCFunction)(void (*)(void))call_topk_fwd, METH_FASTCALL,
      "router_topk_fwd(logits, dtype, T, E, K, score_func, num_groups, group_topk, "
@@ -164,6 +189,14 @@ static PyMethodDef kMethods[] = {
     {"router_combine_bwd", (PyCFunction)(void (*)(void))call_combine_bwd, METH_FASTCALL,
      "router_combine_bwd(grad_out, dtype, u2p, expert_out, topk_weights, ld_weights, T, K, D, "
      "grad_expert_out, grad_weights, stream) -> status"},
+    {"router_expert_matmul_bwd_input",
+     (PyCFunction)(void (*)(void))call_expert_matmul_bwd_input, METH_FASTCALL,
+     "router_expert_matmul_bwd_input(grad_out, dtype, weight, offsets, P, E, N, D, grad_x, "
+     "out_dtype, stream) -> status"},
+    {"router_expert_matmul_bwd_weight",
+     (PyCFunction)(void (*)(void))call_expert_matmul_bwd_weight, METH_FASTCALL,
+     "router_expert_matmul_bwd_weight(grad_out, dtype, x, offsets, p2u, T, P, E, N, D, "
+     "grad_weight, out_dtype, stream) -> status"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pycalls",

@@ -112,6 +112,8 @@ class _CtypesCalls:
         self.router_expert_matmul_w4 = L.router_expert_matmul_w4
         self.router_combine_fwd = L.router_combine_fwd
         self.router_combine_bwd = L.router_combine_bwd
+        self.router_expert_matmul_bwd_input = L.router_expert_matmul_bwd_input
+        self.router_expert_matmul_bwd_weight = L.router_expert_matmul_bwd_weight
 
 
 def _load_fast():
@@ -662,25 +664,32 @@ def router_expert_matmul_bwd_input(grad_out: torch.Tensor, weight: torch.Tensor,
     """Gradient of router_expert_matmul by its rows: grad_x [P, D] on permuted
     rows (``out_dtype``, default grad_out's).  For tokens read through the map,
     router_combine_fwd without weights sums a token's rows."""
-    grad_out = _as_input(grad_out, "grad_out", _DTYPE)
-    dev = grad_out.device
-    idx, dt = dev.index, grad_out.dtype
+    g = grad_out
+    idx, dt = g.get_device(), g.dtype
+    if idx < 0 or dt not in _DTYPE or g.dim() != 2 or not g.is_contiguous():
+        g = _rows_2d(g, "grad_out", None, _DTYPE)
     if weight.get_device() != idx or weight.dtype is not dt or weight.dim() != 3 \
             or not weight.is_contiguous():
         _weight_3d(weight, "weight", idx, dt)
     E, N, D = weight.shape
-    off = _map_1d(expert_first_token_offset, "expert_first_token_offset", idx, E + 1)
-    P = grad_out.shape[0]
-    if grad_out.shape[1] != N:
+    off = expert_first_token_offset
+    if off.get_device() != idx or off.dtype is not _I32 or off.numel() != E + 1 \
+            or off.dim() != 1 or not off.is_contiguous():
+        off = _map_1d(off, "expert_first_token_offset", idx, E + 1)
+    P, cols = g.shape
+    if cols != N:
         _bad("grad_out", f"[P, {N}]")
     odt = dt if out_dtype is None else out_dtype
     if odt not in _DTYPE:
         _bad("out_dtype", f"one of {list(_DTYPE)}")
-    grad_x = _out(grad_x, (P, D), odt, dev, "grad_x")
-    with _on(dev):
-        rc = lib().router_expert_matmul_bwd_input(
-            _ptr(grad_out), _DTYPE[dt], _ptr(weight), _ptr(off), P, E, N, D, _ptr(grad_x),
-            _DTYPE[odt], _stream(dev))
+    if grad_x is None:
+        grad_x = _empty((P, D), dtype=odt, device=g.device)
+    else:
+        grad_x = _out(grad_x, (P, D), odt, g.device, "grad_x")
+    with _on(idx):
+        rc = (_fast or _calls()).router_expert_matmul_bwd_input(
+            g.data_ptr(), _DTYPE[dt], weight.data_ptr(), off.data_ptr(), P, E, N, D,
+            grad_x.data_ptr(), _DTYPE[odt], _raw_stream(idx))
     _check("router_expert_matmul_bwd_input", rc)
     return grad_x
 
@@ -692,27 +701,40 @@ def router_expert_matmul_bwd_weight(grad_out: torch.Tensor, x: torch.Tensor,
     """Gradient of router_expert_matmul by its weights: grad_weight [E, N, D] in
     ``out_dtype`` (default: x's); experts without rows get zeros.  x and the
     map as in the forward."""
-    grad_out = _as_input(grad_out, "grad_out", _DTYPE)
-    dev = grad_out.device
-    idx, dt = dev.index, grad_out.dtype
-    x = _rows_2d(x, "x", idx, (dt,))
-    off = _map_1d(expert_first_token_offset, "expert_first_token_offset", idx, None)
+    g = grad_out
+    idx, dt = g.get_device(), g.dtype
+    if idx < 0 or dt not in _DTYPE or g.dim() != 2 or not g.is_contiguous():
+        g = _rows_2d(g, "grad_out", None, _DTYPE)
+    if x.get_device() != idx or x.dtype is not dt or x.dim() != 2 or not x.is_contiguous():
+        x = _rows_2d(x, "x", idx, (dt,))
+    off = expert_first_token_offset
+    if off.get_device() != idx or off.dtype is not _I32 or off.dim() != 1 \
+            or not off.is_contiguous():
+        off = _map_1d(off, "expert_first_token_offset", idx, None)
     E = off.numel() - 1
+    if E < 1:
+        _bad("expert_first_token_offset", "of at least two elements")
     T, D = x.shape
-    P, N = grad_out.shape
-    p2u = permuted_to_unpermuted
+    P, N = g.shape
+    p2u, p2u_ptr = permuted_to_unpermuted, 0
     if p2u is not None:
-        p2u = _map_1d(p2u, "permuted_to_unpermuted", idx, P)
+        if p2u.get_device() != idx or p2u.dtype is not _I32 or p2u.numel() != P \
+                or p2u.dim() != 1 or not p2u.is_contiguous():
+            p2u = _map_1d(p2u, "permuted_to_unpermuted", idx, P)
+        p2u_ptr = p2u.data_ptr()
     elif T != P:
         _bad("x", f"[{P}, D] without a map")
     odt = dt if out_dtype is None else out_dtype
     if odt not in _DTYPE:
         _bad("out_dtype", f"one of {list(_DTYPE)}")
-    grad_weight = _out(grad_weight, (E, N, D), odt, dev, "grad_weight")
-    with _on(dev):
-        rc = lib().router_expert_matmul_bwd_weight(
-            _ptr(grad_out), _DTYPE[dt], _ptr(x), _ptr(off), _ptr(p2u), T, P, E, N, D,
-            _ptr(grad_weight), _DTYPE[odt], _stream(dev))
+    if grad_weight is None:
+        grad_weight = _empty((E, N, D), dtype=odt, device=g.device)
+    else:
+        grad_weight = _out(grad_weight, (E, N, D), odt, g.device, "grad_weight")
+    with _on(idx):
+        rc = (_fast or _calls()).router_expert_matmul_bwd_weight(
+            g.data_ptr(), _DTYPE[dt], x.data_ptr(), off.data_ptr(), p2u_ptr, T, P, E, N, D,
+            grad_weight.data_ptr(), _DTYPE[odt], _raw_stream(idx))
     _check("router_expert_matmul_bwd_weight", rc)
     return grad_weight
 

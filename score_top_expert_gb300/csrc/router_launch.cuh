@@ -10,31 +10,9 @@
 #include "router_fwd.cuh"
 #include "router_fwd_reg.cuh"
 #include "router_fwd_staged.cuh"
+#include "router_smem.cuh"
 
 namespace moe_router {
-
-// Allow `kern` the dynamic shared memory `smem` (above the 48 KB default
-// only), once per device and size: `granted` is the calling launcher's own
-// record (one per kernel instantiation), the largest size set per device.
-constexpr int kSmemDevs = 64;
-template <typename Kern>
-cudaError_t allow_smem(Kern kern, size_t smem, std::atomic<int>* granted) {
-  if (smem <= 48 * 1024) return cudaSuccess;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  const bool cached = dev >= 0 && dev < kSmemDevs;
-  if (cached && granted[dev].load(std::memory_order_relaxed) >= static_cast<int>(smem))
-    return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e == cudaSuccess && cached) {
-    int cur = granted[dev].load(std::memory_order_relaxed);
-    while (cur < static_cast<int>(smem) &&
-           !granted[dev].compare_exchange_weak(cur, static_cast<int>(smem))) {
-    }
-  }
-  return e;
-}
 
 // Forward configuration chosen by the C ABI layer.
 struct FwdConfig {

@@ -19,6 +19,12 @@
 // 128: 98 us with 8 warps, 78 with 12, 64 with 16 (2.5 TB/s of weights); groups of
 // 32 with zero points, a sixth of the traffic: 102 us at 1056 x 1000.
 //
+// The tensor cores add the products of 16 columns to their accumulator by
+// truncation (see router_experts_tc.cu), so a sum starts from zero for each chunk
+// of 128 columns of bf16 weights, or each group of 4-bit weights, and is added to
+// the tile's in round-to-nearest: one sum over the whole row was off by 2.1e-6 of
+// its value at 8192 columns and 1.9e-5 at 65536.
+//
 // mma.sync m16n8k16 (16 weight rows, 8 permuted rows, fp32 sums) suits the
 // shape: a tcgen05 product would be 128 weight rows wide and needs the operand
 // pipeline that costs the latency here; neither is near its peak rate.  Which
@@ -344,6 +350,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
           const int sw = L::swizzle(gq);  // and of row gq + 8
           const int col = c * L::kPerChunk - d0;
           const uint8_t* const xa = x_at + col * 2;
+          [[maybe_unused]] float sum[4];  // bf16 weights: this chunk's
 #pragma unroll
           for (int s = 0; s < L::kSteps; ++s) {
             if (col + s * L::kStep >= cols) break;
@@ -353,8 +360,11 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
               load_words<4>(from, wa);
               load_words<4>(from + 8 * kChunk, wb);
               load_words<4>(xa + s * 64, xv);
-              mma_16816(acc, wa[0], wb[0], wa[1], wb[1], xv[0], xv[1]);
-              mma_16816(acc, wa[2], wb[2], wa[3], wb[3], xv[2], xv[3]);
+              if (s == 0)
+                mma_16816_from_zero(sum, wa[0], wb[0], wa[1], wb[1], xv[0], xv[1]);
+              else
+                mma_16816(sum, wa[0], wb[0], wa[1], wb[1], xv[0], xv[1]);
+              mma_16816(sum, wa[2], wb[2], wa[3], wb[3], xv[2], xv[3]);
             } else {
               uint32_t wa[V], wb[V];
               const int byte = s * (16 * V) + t * (4 * V);
@@ -386,6 +396,10 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
               acc[2] = fmaf(sb, p[2], acc[2]);
               acc[3] = fmaf(sb, p[3], acc[3]);
             }
+          }
+          if constexpr (V == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] += sum[j];
           }
           __syncwarp();  // all lanes have read the stage before it is filled again
           if (++stage == kStages) stage = 0;

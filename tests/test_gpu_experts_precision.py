@@ -1,0 +1,69 @@
+"""How far the expert products' fp32 outputs are from 64 bits, as a whole: relative
+2-norm errors, which see a loss of precision that element-wise bounds (the sum of
+the terms' magnitudes times their number) leave room for.
+
+The bound.  A tensor core adds 16 products to its accumulator by truncation, below
+the 24 bits of the sum: a chain of n additions loses at most n steps of 2^-25 of its
+value and n 2^-26 on average, all towards zero, so that a segment of n = 60 (960
+terms) is off by 60 2^-26 = 9.0e-7 of its value, as is a sum of segments whose signs
+differ.  Rounding to nearest at each segment's end, at most 2^-24 of the running sum
+and as often up as down, adds 2^-24 sqrt(k / 12) for k segments: 5.2e-8 at 9 of them,
+in square 3e-15 beside 8e-13.  Together below 1e-6.  A chain over 2000 terms without
+segments would be off by 1.9e-6.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+DEV = "cuda:0"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+BOUND = 1e-6
+
+
+@pytest.fixture(scope="module")
+def R():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from score_top_expert_gb300 import build
+    build.build()
+    import score_top_expert_gb300.router as r
+    r.lib()
+    return r
+
+
+def inputs(T, E, K, N, D, dtype, gather, seed=3):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def normals(*shape, scale=1.0):
+        return (torch.randn(*shape, generator=gen, device=DEV) * scale).to(DT[dtype])
+
+    P = T * K
+    expert = torch.randint(0, E, (P,), generator=gen, device=DEV).sort().values
+    off = torch.searchsorted(expert, torch.arange(E + 1, device=DEV)).int()
+    p2u = torch.randperm(P, generator=gen, device=DEV).int() if gather else None
+    x, w, g = normals(T if gather else P, D), normals(E, N, D, scale=D ** -0.5), normals(P, N)
+    rows = x if p2u is None else x[(p2u % T).long()]
+    return x, w, g, off, p2u, rows.double()
+
+
+def relative(got, ref):
+    assert torch.isfinite(got).all()
+    return float((got.double() - ref).norm() / ref.norm())
+
+
+def by_expert(a, off, m):
+    """[P, :] rows of each expert times m(e)."""
+    o = off.tolist()
+    return torch.cat([a[o[e]:o[e + 1]] @ m(e) for e in range(len(o) - 1)])
+
+
+# few rows: four warps to a tile (a quarter of the contraction each), and one
+@pytest.mark.parametrize("T,E,K,N,D", [
+    (6, 4, 4, 264, 520), (6, 4, 4, 264, 2000), (6, 4, 4, 264, 8000), (1, 1, 1, 40, 65536),
+    (36, 36, 1, 4096, 512), (36, 36, 1, 4096, 2008), (36, 36, 1, 2304, 8000)])
+def test_few_rows(R, T, E, K, N, D):
+    x, w, _, off, p2u, rows = inputs(T, E, K, N, D, "bf16", True)
+    y = R.router_expert_matmul(x, w, off, p2u, out_dtype=torch.float32)
+    ref = by_expert(rows, off, lambda e: w[e].double().t())
+    assert relative(y, ref) <= BOUND

@@ -440,8 +440,7 @@ MR_API int router_aux_loss_fwd_noalloc(const float* aux_scores, const uint8_t* r
  * bf16 operands whose rows are 16-byte aligned (D, and for the gradients N, a
  * multiple of 8) take the fastest kernels; any other alignment and fp32 operands
  * are loaded element by element.  fp32 operands are multiplied as three bf16
- * parts each (exact, but for terms below 2^-28 of a product), so that an
- * infinite operand may give NaN where its product with a number is infinite.
+ * parts each (exact, but for terms below 2^-28 of a product).
  */
 MR_API int router_expert_matmul(const void* x, mr_dtype dtype, const void* weight,
                                 const int32_t* expert_first_token_offset,

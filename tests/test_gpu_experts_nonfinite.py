@@ -77,3 +77,26 @@ def test_an_infinity_times_zero_is_a_nan(R):
     y = R.router_expert_matmul(x, w, off)
     same_specials(y, product(x, w.transpose(1, 2), OFF))
     assert y[3].isnan().sum() == 1
+
+
+@pytest.mark.parametrize("bits", [0x7f800001, 0x7f80ffff, -0x007fffff, 0x7fc00000, 0x7fffffff])
+def test_a_nan_of_any_bits_stays_a_nan(R, bits):
+    # 0x7f800001: nothing of its fraction is in the upper half
+    off = torch.tensor(OFF, device=DEV, dtype=torch.int32)
+    w, g = numbers((E, N, 130), 2, False), numbers((P, N), 3, False)
+
+    def with_nan(shape, seed, *at):
+        a = numbers(shape, seed, False)
+        a.view(torch.int32)[at] = bits
+        assert a[at].isnan()
+        return a
+
+    x = with_nan((P, 130), 1, 20, 100)
+    y = R.router_expert_matmul(x, w, off)
+    assert y[20].isnan().all() and y[:20].isfinite().all() and y[21:].isfinite().all()
+    gw = R.router_expert_matmul_bwd_weight(g, x, off)
+    assert gw[1, :, 100].isnan().all() and gw.isnan().sum() == N
+    y = R.router_expert_matmul(numbers((P, 130), 1, False), with_nan((E, N, 130), 2, 2, 5, 64), off)
+    assert y[21:, 5].isnan().all() and y.isnan().sum() == P - 21
+    gx = R.router_expert_matmul_bwd_input(with_nan((P, N), 3, 59, 1), w, off)
+    assert gx[59].isnan().all() and gx[:59].isfinite().all()

@@ -67,3 +67,53 @@ def test_few_rows(R, T, E, K, N, D):
     y = R.router_expert_matmul(x, w, off, p2u, out_dtype=torch.float32)
     ref = by_expert(rows, off, lambda e: w[e].double().t())
     assert relative(y, ref) <= BOUND
+
+
+# rows an expert: 25 take single CTAs on the tensor cores, 50 and more pairs; widths in
+# eights the copy engine, others and fp32 the element loads
+@pytest.mark.parametrize("length", [504, 2000, 8000])
+@pytest.mark.parametrize("dtype,odd,gather", [("bf16", 0, True), ("bf16", 0, False),
+                                              ("bf16", 1, True), ("f32", 0, True),
+                                              ("f32", 1, False)])
+@pytest.mark.parametrize("rows", [25, 50])
+def test_products_over_long_contractions(R, length, dtype, odd, gather, rows):
+    E, K = 8, 2
+    T, short, long = rows * E // K, 136 + odd, length + odd
+    x, w, _, off, p2u, xr = inputs(T, E, K, short, long, dtype, gather)
+    y = R.router_expert_matmul(x, w, off, p2u, out_dtype=torch.float32)
+    assert relative(y, by_expert(xr, off, lambda e: w[e].double().t())) <= BOUND
+    _, w, g, off, _, _ = inputs(T, E, K, long, short, dtype, gather, seed=4)
+    gx = R.router_expert_matmul_bwd_input(g, w, off, out_dtype=torch.float32)
+    assert relative(gx, by_expert(g.double(), off, lambda e: w[e].double())) <= BOUND
+
+
+# columns of grad_out: up to 128 single CTAs, more pairs
+@pytest.mark.parametrize("length", [500, 2000, 8000])
+@pytest.mark.parametrize("dtype,odd,gather", [("bf16", 0, True), ("bf16", 0, False),
+                                              ("bf16", 1, True), ("f32", 0, True),
+                                              ("f32", 1, False)])
+@pytest.mark.parametrize("N", [72, 264])
+def test_weight_gradient_over_many_rows(R, length, dtype, odd, gather, N):
+    # two experts of about `length` rows
+    x, _, g, off, p2u, xr = inputs(length, 2, 2, N + odd, 136 + odd, dtype, gather)
+    gw = R.router_expert_matmul_bwd_weight(g, x, off, p2u, out_dtype=torch.float32)
+    o = off.tolist()
+    ref = torch.stack([g[o[e]:o[e + 1]].double().t() @ xr[o[e]:o[e + 1]] for e in range(2)])
+    assert relative(gw, ref) <= BOUND
+
+
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("T,E,K,N", [(1, 4, 2, 264), (30, 40, 4, 1000)])
+def test_w4_over_long_rows(R, group, T, E, K, N):
+    D = 8192
+    x, _, _, off, p2u, xr = inputs(T, E, K, 8, D, "bf16", True)
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    q = torch.randint(0, 256, (E, N, D // 2), generator=gen, device=DEV, dtype=torch.uint8)
+    s = (torch.rand(E, N, D // group, generator=gen, device=DEV) + 0.5).bfloat16()
+    y = R.router_expert_matmul_w4(x, q, s, off, p2u, out_dtype=torch.float32)
+
+    def weight(e):
+        w = torch.stack((q[e] & 15, q[e] >> 4), 2).view(N, -1, group).double() - 8
+        return (w * s[e].double()[..., None]).view(N, D).t()
+
+    assert relative(y, by_expert(xr, off, weight)) <= BOUND

@@ -416,10 +416,22 @@ MR_API int router_aux_loss_fwd_noalloc(const float* aux_scores, const uint8_t* r
  * expert e owns rows [offset[e], offset[e + 1]) of expert_first_token_offset
  * [E + 1] (device memory, read by the kernels; values outside [0, P] or out of
  * order are clamped).  Rows of the [P, ...] outputs that no expert owns (at
- * and behind offset[E]) are left as they were.  Sums are fp32 whatever the
- * types, with one rounding at the store; repeated calls give the same bits.
- * Nothing is allocated and no workspace is needed.  A NaN or infinity stays
- * in the output rows (weight gradient: the experts) whose inputs hold it.
+ * and behind offset[E]) are left as they were.  Outputs must not overlap
+ * inputs or each other.  Nothing is allocated and no workspace is needed;
+ * repeated calls give the same bits.
+ *
+ * Sums are fp32 whatever the types.  In the products the tensor cores add 16
+ * terms at a time by truncation, each time about 2^-26 of the sum.  A fp32
+ * output is the round-to-nearest sum of segments of at most 960 terms (512 of
+ * fp32 operands; 128 in the bf16 forward of at most 36 rows and with 4-bit
+ * weights): for operands of random signs within 1e-6 of the exact one
+ * (relative 2-norm).  A bf16 output is one such sum at any length, off by about
+ * 2^-30 of its value for each term before it is rounded by up to 2^-8; take a
+ * fp32 output for gradients over several hundred thousand rows.  Adding a
+ * segment may leave zero for a result below 2^-126.  The combination adds in
+ * round-to-nearest.  A NaN or infinity stays in the output rows (weight
+ * gradient: the experts) whose inputs hold it.
+ *
  * MR_ERR_INVALID: a negative size, E, N, D or K < 1, unknown dtypes, a NULL
  * tensor that the call reads or writes.  MR_ERR_UNSUPPORTED: E >
  * MR_MAX_EXPERTS, K > MR_MAX_TOPK, N or D > MR_MAX_FEATURES.
@@ -440,7 +452,9 @@ MR_API int router_aux_loss_fwd_noalloc(const float* aux_scores, const uint8_t* r
  * bf16 operands whose rows are 16-byte aligned (D, and for the gradients N, a
  * multiple of 8) take the fastest kernels; any other alignment and fp32 operands
  * are loaded element by element.  fp32 operands are multiplied as three bf16
- * parts each (exact, but for terms below 2^-28 of a product).
+ * parts each: exact but for terms below 2^-28 of a product, and but for what
+ * of an operand lies below 2^-133, the smallest bf16 number (an operand below
+ * 2^-109 has bits there).
  */
 MR_API int router_expert_matmul(const void* x, mr_dtype dtype, const void* weight,
                                 const int32_t* expert_first_token_offset,
@@ -492,7 +506,7 @@ MR_API int router_expert_matmul_bwd_weight(const void* grad_out, mr_dtype dtype,
  * out      [P, N] out_dtype
  * MR_ERR_INVALID: D % group_size != 0, x or qweight not 16-byte aligned.
  * MR_ERR_UNSUPPORTED: group_size other than 32, 64 or 128; more than 2^30
- * tasks (8 permuted rows by 64 weight rows each).
+ * tasks (8 permuted rows by 256 weight rows each).
  */
 MR_API int router_expert_matmul_w4(const void* x, const uint8_t* qweight, const void* scales,
                                    const uint8_t* zeros, int group_size,

@@ -4,7 +4,8 @@
 // fp32.  A value's 24 significant bits are cut into three bf16 parts of 8,
 // x = h + m + l, exactly (each part is the upper half of what is left).  Of the
 // nine products of two values all but the smallest, l l, are computed, each exact
-// in fp32; what is left out is below 2^-28 of the product.  The first, h h, has an
+// in fp32; what is left out is below 2^-28 of the product, and what of a value lies
+// below 2^-133, the smallest bf16 number.  The first, h h, has an
 // accumulator of its own and the seven small ones share another, so that the
 // truncation of the tensor cores' sums (see router_experts_tc.cu) acts on as few
 // additions of large terms as in a bf16 product; a contraction is cut into

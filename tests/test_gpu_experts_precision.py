@@ -117,3 +117,43 @@ def test_w4_over_long_rows(R, group, T, E, K, N):
         return (w * s[e].double()[..., None]).view(N, D).t()
 
     assert relative(y, by_expert(xr, off, weight)) <= BOUND
+
+
+@pytest.mark.parametrize("exponent", [-100, -112, -120, -128, -136, -146])
+def test_tiny_fp32_operands_are_cut_at_2_to_the_minus_133(R, exponent):
+    # bf16 parts end at 2^-133: an operand counts as its multiple of that next to zero,
+    # so a product is off by at most 2^-133 times the other operand (at least 2^-133),
+    # and the sum of those is all that comes to the bound of ordinary operands
+    T, E, K, N, D = 40, 4, 2, 72, 130
+    x, w, g, off, p2u, _ = inputs(T, E, K, N, D, "f32", True)
+    x = (x.double() * 2.0 ** exponent).float()
+    w = w * 2.0 ** 100
+    y = R.router_expert_matmul(x, w, off, p2u).double()
+    xr = x[(p2u % T).long()].double()
+    ref = by_expert(xr, off, lambda e: w[e].double().t())
+    mag = by_expert(xr.abs(), off, lambda e: w[e].double().abs().t())
+    cut = by_expert(torch.ones_like(xr), off, lambda e: w[e].double().abs().t()) * 2.0 ** -133
+    assert ((y - ref).abs() <= (D + 2) * 2.0 ** -23 * (mag + cut) + cut).all()
+    # bf16 operands have no parts below it
+    xb, wb = x.bfloat16(), w.bfloat16()
+    y = R.router_expert_matmul(xb, wb, off, p2u, out_dtype=torch.float32).double()
+    xr = xb[(p2u % T).long()].double()
+    ref = by_expert(xr, off, lambda e: wb[e].double().t())
+    mag = by_expert(xr.abs(), off, lambda e: wb[e].double().abs().t())
+    assert ((y - ref).abs() <= (D + 2) * 2.0 ** -23 * mag).all()
+
+
+@pytest.mark.parametrize("dtype,odd,segment", [("bf16", 0, 960), ("bf16", 1, 960), ("f32", 0, 512)])
+def test_tiny_results_of_segmented_sums(R, dtype, odd, segment):
+    # adding a segment may leave zero for a result below 2^-126: at most that much for
+    # each addition, beside the bound of the sums (and the cut of fp32 operands)
+    T, E, K, N, D = 100, 4, 2, 72, 2000 + odd
+    x, w, g, off, p2u, _ = inputs(T, E, K, N, D, dtype, True)
+    x, w = x * 2.0 ** -66, w * 2.0 ** -62
+    y = R.router_expert_matmul(x, w, off, p2u, out_dtype=torch.float32).double()
+    xr = x[(p2u % T).long()].double()
+    ref = by_expert(xr, off, lambda e: w[e].double().t())
+    mag = by_expert(xr.abs(), off, lambda e: w[e].double().abs().t())
+    assert ref.abs().max() < 2.0 ** -125
+    steps = -(-D // segment)
+    assert ((y - ref).abs() <= (D + 2) * (2.0 ** -23 * mag + 2.0 ** -149) + steps * 2.0 ** -126).all()

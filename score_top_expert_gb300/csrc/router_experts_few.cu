@@ -14,10 +14,14 @@
 // rows, a quarter of the contraction each, and add up in shared memory in a fixed
 // order.
 //
-// What bounds it: the instructions that unpack the nibbles (11 for eight weights)
-// and their latency.  33 tokens, 512 experts, 22 choices, 1024 x 1024 in groups of
-// 128: 98 us with 8 warps, 78 with 12, 64 with 16 (2.5 TB/s of weights); groups of
-// 32 with zero points, a sixth of the traffic: 102 us at 1056 x 1000.
+// What bounds it (4 bits): latency at four warps a scheduler.  33 tokens, 512
+// experts, 22 choices, 1024 x 1024 in groups of 128: 98 us with 8 warps, 78 with 12,
+// 64 with 16 (2.5 TB/s of weights), a third of HBM and 55 % of the issue slots; a
+// warp waits 7.3 cycles from one instruction to the next, for the one before it, the
+// arithmetic pipe and its turn most, at the barriers around x and for memory a
+// quarter.  Eight weights of a lane take about 30 instructions, 11 of them to unpack
+// the nibbles.  Groups of 32 with zero points at 1056 x 1000: 103 us, with three
+// times the waits for global memory (scales).
 //
 // The tensor cores add the products of 16 columns to their accumulator by
 // truncation (see router_experts_tc.cu), so a sum starts from zero for each chunk

@@ -13,7 +13,7 @@
 // round-to-nearest: 2.7e-7 of the value at 515 terms and 4.9e-7 at 3900, where
 // fp32 multiply-add loops leave 4e-7 and 1.1e-6.
 // In the small products an infinity meets empty parts (NaN), so a first sum that
-// is not finite is the result by itself (557 to 563 us of the forward below).
+// is not finite is the result by itself (1 % of the kernel).
 //
 // The tiles, their order and which operand is A are those of
 // router_experts_tc.cu with one CTA to a tile (128 x up to 128).  A stage holds 64
@@ -22,12 +22,13 @@
 // slice's rows of one operand in flight while the other's parts are stored; the
 // parts go to shared memory in the layout that the tensor cores read.
 //
-// Bound by shared memory, which the 32 instructions of a slice read 8 KB of
-// operands each from and the parts are written to, and by the loading warps'
-// instructions: 8192 tokens, 64 experts, 4 choices, 1024 x 1024 fp32 take 557 us
-// forward (123 TFLOP/s of fp32 products), 487 us and 645 us the gradients; the
-// vector units reach 75 at most.  With few tiles it is the latency of one slice
-// (about 1.3 us): 517 tokens of 515 x 333, 210 tiles of nine slices, 45 us.
+// Bound by the slices, 1.9 to 2.3 us each whether a CTA has few or many: shared
+// memory, which the 32 instructions of a slice read 8 KB of operands each from and
+// the parts are written to, and the loading warps' instructions (issue slots at 56 to
+// 66 %, tensor pipe 30 to 42 %).  8192 tokens, 64 experts, 4 choices, 1024 x 1024 fp32
+// take 573 us forward (120 TFLOP/s of fp32 products), 500 us and 660 us the gradients;
+// the vector units reach 75 at most.  517 tokens of 515 x 333, two tiles of nine
+// slices on most SMs: 46 us.
 #include <atomic>
 
 #include "router_experts_tiles.cuh"
@@ -74,8 +75,8 @@ __device__ __forceinline__ uint32_t rest_of(uint32_t x) {
 }
 
 // x minus its rest, which is its upper half; of a NaN, whose bits may all lie in the
-// lower half, the NaN of any arithmetic (comparing and marking it instead took 17 %
-// of the kernel).
+// lower half, the NaN of any arithmetic (2 % of the kernel; comparing and marking it
+// instead took 17 %).
 __device__ __forceinline__ uint32_t without_rest(uint32_t x, uint32_t rest) {
   return __float_as_uint(__uint_as_float(x) - __uint_as_float(rest));
 }

@@ -34,7 +34,7 @@
 //
 // fp32 outputs.  The tensor cores add each 16-deep product to the accumulator
 // by truncation, so a sum of n of them is off by about n 2^-26 of its value
-// (measured: 4.7e-7 at n = 32), where a bf16 output's rounding is 2^-9.  A fp32
+// (measured: 4.7e-7 at n = 32), where a bf16 output's rounding is up to 2^-8.  A fp32
 // output's contraction is therefore cut into segments of at most 960: each is
 // an accumulator of its own and is added to the output, rounding to nearest, by
 // the threads (weight grad: the copy engine) that stored the one before, in
@@ -48,8 +48,9 @@
 // eight warps at 1060, and with operands in uniform registers (elect_one) the
 // kernel ran at 1250 through the map and 1310 in order, with two groups of loading
 // warps at 1400 and 1430; 4096 x 4096 over 8 experts at 1770 and 1800 (input
-// gradient).  What is left is the operands' way from L2: a slice takes 640 to 700
-// cycles (29 to 32 KB for each SM) at 172, 210 and 242 rows a tile alike.
+// gradient).  A slice takes 640 to 700 cycles (29 to 32 KB for each SM) at 172, 210
+// and 242 rows a tile alike, with L2 at 51 to 55 % of its rate and the tensor pipe at
+// 67 to 71 %; which part of its way sets that is not separated.
 #include <atomic>
 
 #include "router_experts_tiles.cuh"

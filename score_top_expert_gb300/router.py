@@ -571,7 +571,8 @@ def router_aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor
 # ---- the experts' products and the combination ------------------------------
 # One token's calls take a few microseconds on the GPU, so the host's part is
 # written flat: every check reads tensor attributes directly, and the helpers
-# below run only to copy a strided input or to say what is wrong.
+# below run only to copy a strided input or to say what is wrong.  The two
+# gradients of the products, which no single token calls, keep _on and _check.
 _I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
 _empty = torch.empty
 

@@ -89,6 +89,7 @@ typedef enum {
 #define MR_MAX_TOPK 36
 #define MR_MAX_GROUPS 32
 #define MR_MAX_FEATURES 65536 /* columns of the expert-side operators */
+#define MR_MAX_NORM_FEATURES 8192 /* columns of the norms around a block */
 
 /*
  * router_topk_fwd — score, select and emit the top-K experts of each token.
@@ -401,6 +402,57 @@ MR_API int router_aux_loss_fwd_noalloc(const float* aux_scores, const uint8_t* r
                                        int32_t* tokens_per_expert, mr_stream_t stream);
 
 /*
+ * The load-balancing loss sequence by sequence, from the logits and the router's
+ * compact choices: for packed batches of sequences, with padding, without [T, E]
+ * scores and maps between the calls (router_aux_loss_fwd is the loss of a whole
+ * batch from those).
+ *
+ * Sequence s owns the tokens [seq_offsets[s], seq_offsets[s + 1]), n_s of them
+ * (offsets in ascending order; values outside [0, T] are clamped); tokens of no
+ * sequence are padding: they count nowhere and their gradient is zero.
+ * seq_offsets NULL: one sequence of all T tokens (S = 1).  With q = softmax(x), or
+ * sigmoid(x) divided by its sum over the experts (as router_aux_scores_fwd),
+ *   c_se = choices of e by the tokens of s,  P_se = sum of q_te over them,
+ *   loss[0] = coeff / S sum_s E / (K n_s^2) sum_e c_se P_se
+ *   loss[1] = z_coeff / n sum_t (log sum_e exp x_te)^2,  n = sum_s n_s
+ * (a sequence without tokens adds zero; for one sequence of all tokens loss[0] is
+ * router_aux_loss_fwd's).  The counts carry no gradient:
+ *   grad_x_tj = grad_loss[0] coeff / S E / (K n_s^2) sum_e (c_se) dq_te/dx_tj
+ *             + grad_loss[1] z_coeff 2 lse_t / n softmax(x_t)_j
+ *
+ * logits            [T, E] dtype, input
+ * topk_indices      [T, ld_indices] int32, the first K columns, e.g. from
+ *                   router_topk_fwd_compact; an index outside [0, E) is skipped
+ * loss              [2] float, output
+ * tokens_per_expert [S, E] int32 c, output
+ * row_stats         [T, 2] float, output for the backward, 8-byte aligned (only the
+ *                   tokens of sequences are written)
+ * workspace         router_balance_loss_workspace_bytes(T, E, S) bytes, 16-byte
+ *                   aligned; needs no initialisation
+ * Two kernels; repeated calls give the same bits.  T = 0 writes zeros to the loss
+ * and the counts.  The backward takes the forward's logits, counts, row_stats and
+ * other arguments, and writes all T rows of grad_logits [T, E] dtype; it may not
+ * overlap the logits.
+ *
+ * MR_ERR_INVALID: T < 0, E < 1, K outside [1, E], S outside [1, max(T, 1)], S != 1
+ *   without seq_offsets, T E or T K > INT_MAX, an unknown dtype, a score_func
+ *   other than MR_SOFTMAX and MR_SIGMOID, ld_indices < K, a NULL tensor that the call
+ *   reads or writes, a small or misaligned workspace, misaligned row_stats.
+ * MR_ERR_UNSUPPORTED: E > MR_MAX_EXPERTS, K > MR_MAX_TOPK.
+ */
+MR_API size_t router_balance_loss_workspace_bytes(int T, int E, int S);
+MR_API int router_balance_loss_fwd(const void* logits, mr_dtype dtype, const int32_t* topk_indices,
+                                   int ld_indices, const int32_t* seq_offsets, int T, int E, int K,
+                                   int S, mr_score_func score_func, float coeff, float z_coeff,
+                                   float* loss, int32_t* tokens_per_expert, float* row_stats,
+                                   void* workspace, size_t workspace_bytes, mr_stream_t stream);
+MR_API int router_balance_loss_bwd(const float* grad_loss, const void* logits, mr_dtype dtype,
+                                   const int32_t* tokens_per_expert, const float* row_stats,
+                                   const int32_t* seq_offsets, int T, int E, int K, int S,
+                                   mr_score_func score_func, float coeff, float z_coeff,
+                                   void* grad_logits, mr_stream_t stream);
+
+/*
  * The expert-side operators: what runs on the rows that router_expert_maps
  * (or router_topk_fwd_maps) orders by expert.  A layer is
  *   router_topk_fwd_compact, router_expert_maps    weights, maps
@@ -516,6 +568,30 @@ MR_API int router_expert_matmul_w4(const void* x, const uint8_t* qweight, const 
                                    mr_stream_t stream);
 
 /*
+ * router_expert_matmul_w8 — router_expert_matmul on 8-bit integers with a scale for
+ * each row of x and each output channel (for serving; no gradients):
+ *   out[p, n] = x_scales[row(p)] weight_scales[e, n]
+ *               sum_d weight[e, n, d] x[row(p), d]
+ * Products are exact.  So are sums below 2^24 in any order, and with fp32 outputs
+ * segments of at most 960 terms, added up in round-to-nearest; a bf16 output is
+ * one sum, above 2^24 rounded as a bf16 product's.  (Up to four rows an expert on
+ * average: sums of 256 terms, whatever the output.)
+ *
+ * x              [T, D] or [P, D] int8 (map as in router_expert_matmul)
+ * x_scales       [T] or [P] float, of x's rows, e.g. from router_quantize_rows
+ * weight         [E, N, D] int8, any values
+ * weight_scales  [E, N] float
+ * out            [P, N] out_dtype
+ * Rows of 16-byte aligned int8 (D a multiple of 16) take the widest loads.
+ */
+MR_API int router_expert_matmul_w8(const int8_t* x, const float* x_scales, const int8_t* weight,
+                                   const float* weight_scales,
+                                   const int32_t* expert_first_token_offset,
+                                   const int32_t* permuted_to_unpermuted, int T, int P, int E,
+                                   int N, int D, void* out, mr_dtype out_dtype,
+                                   mr_stream_t stream);
+
+/*
  * router_combine_fwd — each token's sum over its K experts' outputs:
  *   out[t] = sum_k topk_weights[t, k] expert_out[unpermuted_to_permuted[t + k T]]
  * k ascending, in fp32.  topk_weights NULL: plain sums.  A choice whose map
@@ -548,6 +624,88 @@ MR_API int router_combine_bwd(const void* grad_out, mr_dtype dtype,
                               const int32_t* unpermuted_to_permuted, const void* expert_out,
                               const float* topk_weights, int ld_weights, int T, int K, int D,
                               void* grad_expert_out, float* grad_weights, mr_stream_t stream);
+
+/*
+ * router_quantize_rows — rows in 8-bit integers with a scale for each, the left
+ * operand of router_expert_matmul_w8:
+ *   scales[r] = max_d |x[r, d]| / 127 (fp32, correctly rounded; at least 2^-126
+ *               unless the row is all zeros: then 0)
+ *   q[r, d]   = x[r, d] / scales[r] rounded to the nearest integer, ties to even
+ *               (of the exact quotient), in [-127, 127]
+ * A row that holds an infinity or a NaN gets that for its scale, and zeros for its
+ * integers: what is multiplied by it stays NaN.
+ *
+ * x [R, D] dtype, q [R, D] int8, scales [R] float.  R = 0 is a no-op.
+ * MR_ERR_INVALID: R < 0, D < 1, an unknown dtype, a NULL tensor.
+ * MR_ERR_UNSUPPORTED: D > MR_MAX_FEATURES.
+ */
+MR_API int router_quantize_rows(const void* x, mr_dtype dtype, int R, int D, int8_t* q,
+                                float* scales, mr_stream_t stream);
+
+/*
+ * router_combine_norm_fwd — the end of an expert block and the beginning of the next
+ * one: the combination, the norm behind the block, its gate, the residual scale and
+ * sum, and the norm before the next block.  Per token t:
+ *   y = sum_k topk_weights[t, k] expert_out[unpermuted_to_permuted[t + k T]]
+ *       (as router_combine_fwd; without a map expert_out is [T, D], K is 1, there
+ *       are no topk_weights, and y is its row t)
+ *   h = y / sqrt(mean(y^2) + eps) post_weight      (y itself without post_weight)
+ *   x = residual + residual_scale gate h
+ *   n = x / sqrt(mean(x^2) + eps) pre_weight       (only with pre_weight)
+ * all in fp32; x and y are rounded once, where they are stored, and n is of the
+ * unrounded x.
+ *
+ * expert_out    [T K, D] (or [T, D]) dtype, residual [T, D] dtype
+ * post_weight, pre_weight  [D] float or NULL
+ * gate          NULL (MR_GATE_NONE), [T] float (MR_GATE_TOKEN) or [T, D] dtype
+ *               (MR_GATE_VALUE)
+ * sum           [T, D] dtype, output x
+ * normed        [T, D] dtype, output n (ignored without pre_weight)
+ * block_out     [T, D] dtype, output y, for the backward, or NULL
+ * rstd          [T, 2] float, output, for the backward, or NULL: the factors
+ *               1 / sqrt(..) of y and x, 1 where there is no norm; 8-byte aligned
+ * Outputs must not overlap inputs or each other.  One kernel, no workspace.
+ * T = 0 is a no-op.
+ * MR_ERR_INVALID: T < 0, K or D < 1, T K > INT_MAX, eps not above 0, an unknown dtype
+ *   or gate_kind, a gate that gate_kind does not name, ld_weights < K with weights,
+ *   K != 1 or weights without a map, a NULL tensor that the call reads or writes,
+ *   a misaligned rstd.
+ * MR_ERR_UNSUPPORTED: K > MR_MAX_TOPK, D > MR_MAX_NORM_FEATURES.
+ */
+typedef enum { MR_GATE_NONE = 0, MR_GATE_TOKEN = 1, MR_GATE_VALUE = 2 } mr_gate;
+MR_API int router_combine_norm_fwd(const void* expert_out, mr_dtype dtype,
+                                   const int32_t* unpermuted_to_permuted,
+                                   const float* topk_weights, int ld_weights, const void* residual,
+                                   const float* post_weight, const void* gate, mr_gate gate_kind,
+                                   float residual_scale, const float* pre_weight, float eps, int T,
+                                   int K, int D, void* sum, void* normed, void* block_out,
+                                   float* rstd, mr_stream_t stream);
+
+/*
+ * router_combine_norm_bwd — its gradients, from those of x (grad_sum) and n
+ * (grad_normed) to those of y, the residual, the gate and the weights; the grad_block
+ * [T, D] it writes is router_combine_bwd's grad_out.  block_out, sum and rstd are the
+ * forward's outputs (as they were rounded).
+ *
+ * grad_sum      [T, D] dtype, or NULL (zeros) with pre_weight
+ * grad_normed   [T, D] dtype, read with pre_weight only, as sum is
+ * block_out     read with post_weight or a gate only
+ * grad_block, grad_residual  [T, D] dtype, outputs
+ * grad_gate     like gate, output (ignored without one)
+ * grad_post_weight, grad_pre_weight  [D] float, outputs with the weight
+ * workspace     router_combine_norm_bwd_workspace_bytes(T, D) bytes, 16-byte aligned,
+ *               with either weight; needs no initialisation
+ * Two kernels with a weight, one without; repeated calls give the same bits.  T = 0
+ * writes zeros to the weights' gradients.  Errors: as the forward.
+ */
+MR_API size_t router_combine_norm_bwd_workspace_bytes(int T, int D);
+MR_API int router_combine_norm_bwd(const void* grad_sum, const void* grad_normed, mr_dtype dtype,
+                                   const void* block_out, const void* sum, const float* rstd,
+                                   const float* post_weight, const void* gate, mr_gate gate_kind,
+                                   float residual_scale, const float* pre_weight, int T, int D,
+                                   void* grad_block, void* grad_residual, void* grad_gate,
+                                   float* grad_post_weight, float* grad_pre_weight,
+                                   void* workspace, size_t workspace_bytes, mr_stream_t stream);
 
 /* Static English text for a status code (never NULL). */
 MR_API const char* moe_router_strerror(int code);

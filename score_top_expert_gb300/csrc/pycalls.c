@@ -163,6 +163,85 @@ static PyObject* call_expert_matmul_bwd_weight(PyObject* self, PyObject* const* 
   return PyLong_FromLong(rc);
 }
 
+static PyObject* call_expert_matmul_w8(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t x, xs, w, ws, off, p2u, o, stream;
+  int T, P, E, N, D, odt;
+  void* out[] = {&x, &xs, &w, &ws, &off, &p2u, &T, &P, &E, &N, &D, &o, &odt, &stream};
+  if (convert(args, nargs, "ppppppiiiiipip", out) != 0) return NULL;
+  const int rc = router_expert_matmul_w8(
+      (const int8_t*)x, (const float*)xs, (const int8_t*)w, (const float*)ws,
+      (const int32_t*)off, (const int32_t*)p2u, T, P, E, N, D, (void*)o, (mr_dtype)odt,
+      (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
+static PyObject* call_quantize_rows(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t x, q, s, stream;
+  int dt, R, D;
+  void* out[] = {&x, &dt, &R, &D, &q, &s, &stream};
+  if (convert(args, nargs, "piiippp", out) != 0) return NULL;
+  const int rc = router_quantize_rows((const void*)x, (mr_dtype)dt, R, D, (int8_t*)q, (float*)s,
+                                      (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
+static PyObject* call_combine_norm_fwd(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t z, u2p, w, res, post, gate, pre, sum, normed, block, rstd, stream;
+  int dt, ld, kind, T, K, D;
+  float scale, eps;
+  void* out[] = {&z,   &dt,  &u2p, &w, &ld, &res, &post, &gate,   &kind,  &scale,
+                 &pre, &eps, &T,   &K, &D,  &sum, &normed, &block, &rstd, &stream};
+  if (convert(args, nargs, "pippipppifpfiiippppp", out) != 0) return NULL;
+  const int rc = router_combine_norm_fwd(
+      (const void*)z, (mr_dtype)dt, (const int32_t*)u2p, (const float*)w, ld, (const void*)res,
+      (const float*)post, (const void*)gate, (mr_gate)kind, scale, (const float*)pre, eps, T, K,
+      D, (void*)sum, (void*)normed, (void*)block, (float*)rstd, (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
+static PyObject* call_combine_norm_bwd(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t gs, gn, block, sum, rstd, post, gate, pre, gb, gr, gg, gpost, gpre, ws, bytes, stream;
+  int dt, kind, T, D;
+  float scale;
+  void* out[] = {&gs, &gn, &dt, &block, &sum,   &rstd, &post, &gate,  &kind, &scale, &pre,
+                 &T,  &D,  &gb, &gr,    &gg,    &gpost, &gpre, &ws,   &bytes, &stream};
+  if (convert(args, nargs, "ppipppppifpiipppppppp", out) != 0) return NULL;
+  const int rc = router_combine_norm_bwd(
+      (const void*)gs, (const void*)gn, (mr_dtype)dt, (const void*)block, (const void*)sum,
+      (const float*)rstd, (const float*)post, (const void*)gate, (mr_gate)kind, scale,
+      (const float*)pre, T, D, (void*)gb, (void*)gr, (void*)gg, (float*)gpost, (float*)gpre,
+      (void*)ws, (size_t)bytes, (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
+static PyObject* call_balance_loss_fwd(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t x, idx, seq, loss, counts, stats, ws, bytes, stream;
+  int dt, ld, T, E, K, S, sf;
+  float coeff, z_coeff;
+  void* out[] = {&x,     &dt,      &idx,  &ld,     &seq,   &T,  &E,     &K,     &S,
+                 &sf,    &coeff,   &z_coeff, &loss, &counts, &stats, &ws, &bytes, &stream};
+  if (convert(args, nargs, "pipipiiiiiffpppppp", out) != 0) return NULL;
+  const int rc = router_balance_loss_fwd(
+      (const void*)x, (mr_dtype)dt, (const int32_t*)idx, ld, (const int32_t*)seq, T, E, K, S,
+      (mr_score_func)sf, coeff, z_coeff, (float*)loss, (int32_t*)counts, (float*)stats, (void*)ws,
+      (size_t)bytes, (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
+static PyObject* call_balance_loss_bwd(PyObject* self, PyObject* const* args, Py_ssize_t nargs) {
+  uintptr_t g, x, counts, stats, seq, gx, stream;
+  int dt, T, E, K, S, sf;
+  float coeff, z_coeff;
+  void* out[] = {&g, &x, &dt, &counts, &stats, &seq,     &T,  &E,
+                 &K, &S, &sf, &coeff,  &z_coeff, &gx, &stream};
+  if (convert(args, nargs, "ppipppiiiiiffpp", out) != 0) return NULL;
+  const int rc = router_balance_loss_bwd(
+      (const float*)g, (const void*)x, (mr_dtype)dt, (const int32_t*)counts, (const float*)stats,
+      (const int32_t*)seq, T, E, K, S, (mr_score_func)sf, coeff, z_coeff, (void*)gx,
+      (mr_stream_t)stream);
+  return PyLong_FromLong(rc);
+}
+
 static PyMethodDef kMethods[] = {
     {"router_topk_fwd", (PyCFunction)(void (*)(void))call_topk_fwd, METH_FASTCALL,
      "router_topk_fwd(logits, dtype, T, E, K, score_func, num_groups, group_topk, "
@@ -197,6 +276,31 @@ static PyMethodDef kMethods[] = {
      (PyCFunction)(void (*)(void))call_expert_matmul_bwd_weight, METH_FASTCALL,
      "router_expert_matmul_bwd_weight(grad_out, dtype, x, offsets, p2u, T, P, E, N, D, "
      "grad_weight, out_dtype, stream) -> status"},
+    {"router_expert_matmul_w8", (PyCFunction)(void (*)(void))call_expert_matmul_w8,
+     METH_FASTCALL,
+     "router_expert_matmul_w8(x, x_scales, weight, weight_scales, offsets, p2u, T, P, E, N, D, "
+     "out, out_dtype, stream) -> status"},
+    {"router_quantize_rows", (PyCFunction)(void (*)(void))call_quantize_rows, METH_FASTCALL,
+     "router_quantize_rows(x, dtype, R, D, q, scales, stream) -> status"},
+    {"router_combine_norm_fwd", (PyCFunction)(void (*)(void))call_combine_norm_fwd,
+     METH_FASTCALL,
+     "router_combine_norm_fwd(expert_out, dtype, u2p, topk_weights, ld_weights, residual, "
+     "post_weight, gate, gate_kind, residual_scale, pre_weight, eps, T, K, D, sum, normed, "
+     "block_out, rstd, stream) -> status"},
+    {"router_combine_norm_bwd", (PyCFunction)(void (*)(void))call_combine_norm_bwd,
+     METH_FASTCALL,
+     "router_combine_norm_bwd(grad_sum, grad_normed, dtype, block_out, sum, rstd, post_weight, "
+     "gate, gate_kind, residual_scale, pre_weight, T, D, grad_block, grad_residual, grad_gate, "
+     "grad_post_weight, grad_pre_weight, workspace, workspace_bytes, stream) -> status"},
+    {"router_balance_loss_fwd", (PyCFunction)(void (*)(void))call_balance_loss_fwd,
+     METH_FASTCALL,
+     "router_balance_loss_fwd(logits, dtype, topk_indices, ld_indices, seq_offsets, T, E, K, S, "
+     "score_func, coeff, z_coeff, loss, tokens_per_expert, row_stats, workspace, "
+     "workspace_bytes, stream) -> status"},
+    {"router_balance_loss_bwd", (PyCFunction)(void (*)(void))call_balance_loss_bwd,
+     METH_FASTCALL,
+     "router_balance_loss_bwd(grad_loss, logits, dtype, tokens_per_expert, row_stats, "
+     "seq_offsets, T, E, K, S, score_func, coeff, z_coeff, grad_logits, stream) -> status"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pycalls",

@@ -1,0 +1,723 @@
+// Load-balancing loss of each sequence of a packed batch, the tokens per expert, the
+// z loss, and the gradient of both by the logits.
+//
+//   sequence s owns tokens [o_s, o_{s+1}), n_s of them;  q = softmax(x) or
+//   sigma(x) / sum sigma(x);  c_se = choices of e in s;  P_se = sum_{t in s} q_te
+//   balance = coeff / S sum_s a_s sum_e c_se P_se,  a_s = E / (K n_s^2)
+//   z       = z_coeff / n sum_t lse(x_t)^2,         n = tokens of all sequences
+//   d/dx_tj = g0 coeff / S a_s w_tj (c_sj - sum_e c_se q_te)
+//             + g1 z_coeff 2 lse_t / n softmax(x_t)_j,
+//   w = q (softmax) or sigma (1 - sigma) / sum sigma (sigmoid)
+//
+// Bound by HBM: the forward reads the logits and the choices, the backward reads
+// the logits and writes the gradient; no [T, E] score, map or score gradient exists.
+//
+// Forward: a block takes a contiguous range of tokens, a team of 1 to 6 warps a row at a
+// time.  A lane holds up to 16 logits, the next row's loads in flight, and the column
+// sums of q of the rows that its team has seen; so a block leaves one row of column sums and
+// one of counts for each sequence that its range touches ("slot": block + sequence,
+// which rises by one or more from each to the next, so no two share one).  A
+// second kernel adds a sequence's slots up in order and ends the loss in 64 bits; the last block
+// to finish adds the blocks' shares.  No floating-point atomics: repeated calls
+// give the same bits.
+//
+// Backward: the same ranges; a team keeps its sequence's counts in registers.  They
+// enter as c_sj - K n_s / E: a constant less changes nothing, since q sums to one,
+// and leaves the difference c_sj - sum c q without the cancellation of two large numbers.
+#include <climits>
+
+#include "router_common.cuh"
+#include "router_experts.cuh"
+
+namespace moe_router {
+namespace {
+
+constexpr int kTeamWarps = 8;      // warps of a block whose rows take one warp each
+constexpr int kFinishThreads = 512;
+constexpr int kFinishGroups = kFinishThreads / 32;
+
+struct BalanceArgs {
+  const void* logits;
+  const int32_t* choices;     // [T, ld_choices]
+  const int32_t* seq;         // [S + 1] or NULL: one sequence of all T
+  float* loss;                // [2]
+  int32_t* counts;            // [S, E]
+  float2* stats;              // [T] softmax: max, sum exp; sigmoid: sum sigma, lse
+  float* slot_sums;           // [blocks + S, E]
+  int32_t* slot_counts;       // [blocks + S, E]
+  float* z_parts;             // [blocks]
+  double* parts;              // [finish blocks]
+  int* ticket;
+  const float* grad_loss;     // [2]
+  void* grad;                 // [T, E]
+  long long ld_choices;
+  int T, E, K, S;
+  int rows;                   // tokens of a block
+  int blocks;
+  float coeff, z_coeff;
+};
+
+// Tokens [lo, hi) of sequence s, kept within [0, T].
+__device__ __forceinline__ void sequence_range(const BalanceArgs& a, int s, int* lo, int* hi) {
+  if (a.seq == nullptr) {
+    *lo = 0;
+    *hi = a.T;
+    return;
+  }
+  *lo = min(max(a.seq[s], 0), a.T);
+  *hi = min(max(a.seq[s + 1], *lo), a.T);
+}
+
+// The first sequence that ends behind token t (S: none), by one warp: 32 ends at a
+// time.  Ends that are out of order give some sequence in [0, S].
+__device__ __forceinline__ int first_sequence(const BalanceArgs& a, int t) {
+  if (a.seq == nullptr) return 0;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = a.S;  // the answer is in [lo, hi]
+  while (hi > lo) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step + step - 1;  // the lane's last candidate
+    const bool before = at < hi && a.seq[at + 1] <= t;
+    const int n = __popc(__ballot_sync(0xffffffffu, before));
+    const int next = lo + n * step;
+    hi = min(hi, next + step - 1);
+    lo = min(next, hi);
+  }
+  return lo;
+}
+
+// Threads of a team of `warps` warps.
+__device__ __forceinline__ void team_sync(int team, int warps) {
+  if (warps > 1)
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
+}
+
+struct Team {
+  int warps, team, teams, warp, lane;
+  float* xch;  // [2][teams * warps][2]
+  int flip;
+
+  // Both values summed over the team's warps, in the same order in each.  Two
+  // sets of cells in turn, so that one barrier a row is enough.
+  __device__ __forceinline__ void sum2(float* x, float* y) {
+    if (warps == 1) return;
+    float* const mine = xch + (flip * teams + team) * warps * 2;
+    flip ^= 1;
+    if (lane == 0) {
+      mine[2 * warp] = *x;
+      mine[2 * warp + 1] = *y;
+    }
+    team_sync(team, warps);
+    float a = 0.0f, b = 0.0f;
+    for (int w = 0; w < warps; ++w) {
+      a += mine[2 * w];
+      b += mine[2 * w + 1];
+    }
+    *x = a;
+    *y = b;
+  }
+
+  // Maxima and sums of exponentials relative to them, of the team's warps, as one.
+  __device__ __forceinline__ void softmax_stats(float* m, float* s) {
+    if (warps == 1) return;
+    float* const mine = xch + (flip * teams + team) * warps * 2;
+    flip ^= 1;
+    if (lane == 0) {
+      mine[2 * warp] = *m;
+      mine[2 * warp + 1] = *s;
+    }
+    team_sync(team, warps);
+    float top = mine[0];
+    for (int w = 1; w < warps; ++w) top = fmaxf(top, mine[2 * w]);
+    float total = 0.0f;
+    for (int w = 0; w < warps; ++w)
+      total = fmaf(mine[2 * w + 1], ex2_approx((mine[2 * w] - top) * kLog2e), total);
+    *m = top;
+    *s = total;
+  }
+};
+
+__device__ __forceinline__ Team make_team(int warps, float* xch) {
+  Team t;
+  const int warp = threadIdx.x >> 5;
+  t.warps = warps;
+  t.team = warp / warps;
+  t.teams = blockDim.x / (32 * warps);
+  t.warp = warp - t.team * warps;
+  t.lane = threadIdx.x & 31;
+  t.xch = xch;
+  t.flip = 0;
+  return t;
+}
+
+// A lane's NV times four logits of a row: columns 4 (lane + 32 (warp + warps j)).
+template <int NV>
+struct Row {
+  float v[NV][4];
+};
+
+__device__ __forceinline__ int column_of(const Team& t, int j) {
+  return 4 * (t.lane + 32 * (t.warp + t.warps * j));
+}
+
+template <int DT, bool VEC, int NV>
+__device__ __forceinline__ void load_row(const BalanceArgs& a, const Team& t, int row,
+                                         Row<NV>* r) {
+  const size_t at = static_cast<size_t>(row) * a.E;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = column_of(t, j);
+    if (c < a.E) load4<DT, VEC>(a.logits, at, c, a.E, r->v[j]);
+  }
+}
+
+// Of the columns from c, is u one of the row's?
+template <bool VEC>
+__device__ __forceinline__ bool inside(int c, int u, int E) {
+  return VEC ? c < E : c + u < E;
+}
+
+template <int DT, bool VEC, int NV, int SF>
+__global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const BalanceArgs a,
+                                                                         int warps) {
+  extern __shared__ float dynamic[];  // teams > 1: [teams, E] column sums; then [E] counts
+  __shared__ float xch[2 * kTeamWarps * 2];
+  __shared__ float z_warp[kTeamWarps];
+  __shared__ int first_s;
+  pdl_enter();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+  Team t = make_team(warps, xch);
+  int* const hist = reinterpret_cast<int*>(dynamic + (t.teams > 1 ? t.teams * a.E : 0));
+  const int t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
+  if (threadIdx.x < 32) {
+    const int s = first_sequence(a, t0);
+    if (threadIdx.x == 0) first_s = s;
+  }
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  const bool want_lse = SF == SF_SOFTMAX || a.z_coeff != 0.0f;
+  float z = 0.0f;
+  for (int s = first_s, p = t0; s < a.S && p < t1; ++s) {
+    int lo, hi;
+    sequence_range(a, s, &lo, &hi);
+    lo = max(lo, p);
+    hi = min(hi, t1);
+    if (lo >= t1) break;
+    if (hi <= lo) continue;
+    p = hi;
+    // ---- counts: the choices of the range's tokens -----------------------------------
+    for (int i = threadIdx.x; i < (hi - lo) * a.K; i += blockDim.x) {
+      const int row = i / a.K;
+      const int e = a.choices[(lo + row) * a.ld_choices + (i - row * a.K)];
+      if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(hist + e, 1);
+    }
+    // ---- column sums of q --------------------------------------------------------------
+    Row<NV> sums{}, next;
+    int row = lo + t.team;
+    if (row < hi) load_row<DT, VEC>(a, t, row, &next);
+    for (; row < hi; row += t.teams) {
+      Row<NV> r = next;
+      if (row + t.teams < hi) load_row<DT, VEC>(a, t, row + t.teams, &next);
+      float top = -INFINITY, total = 0.0f, lse = 0.0f, factor;
+      if (want_lse) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (inside<VEC>(column_of(t, j), u, a.E)) top = fmaxf(top, r.v[j][u]);
+        top = seg_max<32>(top);
+      }
+      if constexpr (SF == SF_SOFTMAX) {
+        const float own = top;  // the warp's; a warp without columns adds zeros to the sum
+        const float shift = own == -INFINITY ? 0.0f : own * kLog2e;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const bool in = inside<VEC>(column_of(t, j), u, a.E);
+            r.v[j][u] = in ? exp_shifted(r.v[j][u], shift) : 0.0f;
+            total += r.v[j][u];
+          }
+        total = seg_sum<32>(total);
+        t.softmax_stats(&top, &total);
+        lse = top + logf(total);
+        factor = t.warps == 1 ? __fdiv_rn(1.0f, total)
+                              : __fdiv_rn(ex2_approx((own - top) * kLog2e), total);
+        if (t.warp == 0 && t.lane == 0) a.stats[row] = make_float2(top, total);
+      } else {
+        if (want_lse) {
+          const float shift = top == -INFINITY ? 0.0f : top * kLog2e;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (inside<VEC>(column_of(t, j), u, a.E)) total += exp_shifted(r.v[j][u], shift);
+          total = seg_sum<32>(total);
+          t.softmax_stats(&top, &total);
+          lse = top + logf(total);
+        }
+        float norm = 0.0f, unused = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const bool in = inside<VEC>(column_of(t, j), u, a.E);
+            r.v[j][u] = in ? sigmoid_f32(r.v[j][u]) : 0.0f;
+            norm += r.v[j][u];
+          }
+        norm = seg_sum<32>(norm);
+        t.sum2(&norm, &unused);
+        factor = __fdiv_rn(1.0f, norm);
+        if (t.warp == 0 && t.lane == 0) a.stats[row] = make_float2(norm, lse);
+      }
+      z = fmaf(lse, lse, z);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sums.v[j][u] = fmaf(r.v[j][u], factor, sums.v[j][u]);
+    }
+    // ---- the slot of this block and sequence ---------------------------------------------
+    const size_t slot = (static_cast<size_t>(blockIdx.x) + s) * a.E;
+    if (t.teams > 1) {
+      float* const mine = dynamic + t.team * a.E;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = column_of(t, j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c + u < a.E) mine[c + u] = sums.v[j][u];
+      }
+      __syncthreads();
+      for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        float v = dynamic[e];
+        for (int w = 1; w < t.teams; ++w) v += dynamic[w * a.E + e];
+        a.slot_sums[slot + e] = v;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = column_of(t, j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c + u < a.E) a.slot_sums[slot + c + u] = sums.v[j][u];
+      }
+      __syncthreads();
+    }
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+      a.slot_counts[slot + e] = hist[e];
+      hist[e] = 0;
+    }
+    __syncthreads();
+  }
+  // every lane of a team has its rows' z: the first of each counts
+  if (t.lane == 0) z_warp[threadIdx.x >> 5] = t.warp == 0 ? z : 0.0f;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float v = 0.0f;
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) v += z_warp[w];
+    a.z_parts[blockIdx.x] = v;
+  }
+}
+
+// Adds up each sequence's slots: 128 columns and one sequence at a time, 16 warps on
+// every 16th slot each; then counts times sums, and the last block the whole.
+__global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(const BalanceArgs a) {
+  __shared__ float sums[kFinishGroups][128];
+  __shared__ int counts[kFinishGroups][128];
+  __shared__ double shared[kFinishThreads / 32];
+  __shared__ int last;
+  pdl_enter();
+  const int tiles = (a.E + 127) / 128;
+  const long long items = static_cast<long long>(tiles) * a.S;
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const bool vec = (a.E & 3) == 0;
+  double share = 0.0;
+  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+    const int s = static_cast<int>(item / tiles);
+    const int c = static_cast<int>(item - static_cast<long long>(s) * tiles) * 128 + 4 * lane;
+    int lo, hi;
+    sequence_range(a, s, &lo, &hi);
+    const int b0 = lo / a.rows, b1 = hi > lo ? (hi - 1) / a.rows : b0 - 1;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int n[4] = {0, 0, 0, 0};
+    if (vec && c < a.E) {
+#pragma unroll 4
+      for (int b = b0 + group; b <= b1; b += kFinishGroups) {
+        const size_t at = (static_cast<size_t>(b) + s) * a.E + c;
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.slot_sums + at));
+        const int4 k = __ldcg(reinterpret_cast<const int4*>(a.slot_counts + at));
+        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+        n[0] += k.x; n[1] += k.y; n[2] += k.z; n[3] += k.w;
+      }
+    } else if (!vec) {
+      for (int b = b0 + group; b <= b1; b += kFinishGroups) {
+        const size_t at = (static_cast<size_t>(b) + s) * a.E + c;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c + u < a.E) {
+            v[u] += __ldcg(a.slot_sums + at + u);
+            n[u] += __ldcg(a.slot_counts + at + u);
+          }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      sums[group][4 * lane + u] = v[u];
+      counts[group][4 * lane + u] = n[u];
+    }
+    __syncthreads();
+    const int e = static_cast<int>(item - static_cast<long long>(s) * tiles) * 128 +
+                  static_cast<int>(threadIdx.x);
+    if (threadIdx.x < 128 && e < a.E) {
+      float p = 0.0f;
+      int k = 0;
+      const int groups = min(kFinishGroups, b1 - b0 + 1);
+      for (int g = 0; g < groups; ++g) {
+        p += sums[g][threadIdx.x];
+        k += counts[g][threadIdx.x];
+      }
+      a.counts[static_cast<size_t>(s) * a.E + e] = k;
+      const double tokens = hi - lo;
+      if (hi > lo)
+        share += static_cast<double>(k) * p * (a.E / (a.K * tokens * tokens));
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) share += __shfl_xor_sync(0xffffffffu, share, o);
+  if (lane == 0) shared[group] = share;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double v = 0.0;
+    for (int w = 0; w < 4; ++w) v += shared[w];  // threads 0 .. 127 have the shares
+    a.parts[blockIdx.x] = v;
+    __threadfence();
+    last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+  }
+  __syncthreads();
+  if (!last || threadIdx.x >= 32) return;
+  __threadfence();
+  double balance = 0.0, z = 0.0;
+  for (int b = lane; b < static_cast<int>(gridDim.x); b += 32) balance += __ldcg(a.parts + b);
+  for (int b = lane; b < a.blocks; b += 32) z += __ldcg(a.z_parts + b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    balance += __shfl_xor_sync(0xffffffffu, balance, o);
+    z += __shfl_xor_sync(0xffffffffu, z, o);
+  }
+  if (lane == 0) {
+    int lo, hi, unused;
+    sequence_range(a, 0, &lo, &unused);
+    sequence_range(a, a.S - 1, &unused, &hi);
+    a.loss[0] = static_cast<float>(balance * a.coeff / a.S);
+    a.loss[1] = a.z_coeff == 0.0f ? 0.0f : static_cast<float>(z * a.z_coeff / max(hi - lo, 1));
+  }
+}
+
+template <int DT, bool VEC, int NV, int SF>
+__global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_bwd_kernel(const BalanceArgs a,
+                                                                         int warps) {
+  __shared__ float xch[2 * kTeamWarps * 2];
+  __shared__ int first_s;
+  pdl_enter();
+  Team t = make_team(warps, xch);
+  const int t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
+  if (threadIdx.x < 32) {
+    const int s = first_sequence(a, t0);
+    if (threadIdx.x == 0) first_s = s;
+  }
+  __syncthreads();
+  int whole_lo, whole_hi, unused;
+  sequence_range(a, 0, &whole_lo, &unused);
+  sequence_range(a, a.S - 1, &unused, &whole_hi);
+  const float by_balance = a.grad_loss[0] * a.coeff / static_cast<float>(a.S);
+  const float by_z = a.z_coeff == 0.0f
+                         ? 0.0f
+                         : a.grad_loss[1] * a.z_coeff * 2.0f /
+                               static_cast<float>(max(whole_hi - whole_lo, 1));
+  // rows of no sequence: zeros
+  auto clear = [&](int from, int to) {
+    const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int row = from + t.team; row < to; row += t.teams)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = column_of(t, j);
+        if (c < a.E) store4<DT, VEC>(a.grad, static_cast<size_t>(row) * a.E, c, a.E, none);
+      }
+  };
+  int p = t0;
+  for (int s = first_s; s < a.S && p < t1; ++s) {
+    int lo, hi;
+    sequence_range(a, s, &lo, &hi);
+    const float tokens = static_cast<float>(hi - lo);
+    lo = max(lo, p);
+    hi = min(hi, t1);
+    if (lo >= t1) break;
+    if (hi <= lo) continue;
+    clear(p, lo);
+    p = hi;
+    const float scale = by_balance * (static_cast<float>(a.E) / a.K) / tokens / tokens;
+    const float mean = tokens * a.K / a.E;
+    Row<NV> c, next;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int col = column_of(t, j);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        c.v[j][u] = col + u < a.E
+                        ? static_cast<float>(a.counts[static_cast<size_t>(s) * a.E + col + u]) - mean
+                        : 0.0f;
+    }
+    int row = lo + t.team;
+    float2 st, next_st = make_float2(0.0f, 0.0f);
+    if (row < hi) {
+      load_row<DT, VEC>(a, t, row, &next);
+      next_st = a.stats[row];
+    }
+    for (; row < hi; row += t.teams) {
+      Row<NV> r = next;
+      st = next_st;
+      if (row + t.teams < hi) {
+        load_row<DT, VEC>(a, t, row + t.teams, &next);
+        next_st = a.stats[row + t.teams];
+      }
+      // r becomes q; sigmoid: t = sigma(-|x|) with the sign of x, so that sigma and
+      // 1 - sigma, t and 1 - t, are both without cancellation
+      const float inv = __fdiv_rn(1.0f, SF == SF_SOFTMAX ? st.y : st.x);
+      float dot = 0.0f, none = 0.0f, z = 0.0f;
+      Row<NV> x = r;
+      const float shift = (SF == SF_SOFTMAX ? st.x : st.y) * kLog2e;
+      if (SF == SF_SOFTMAX) z = by_z == 0.0f ? 0.0f : by_z * (st.x + logf(st.y));
+      else z = by_z * st.y;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const bool in = inside<VEC>(column_of(t, j), u, a.E);
+          if constexpr (SF == SF_SOFTMAX) {
+            r.v[j][u] = in ? exp_shifted(x.v[j][u], shift) * inv : 0.0f;
+            dot = fmaf(c.v[j][u], r.v[j][u], dot);
+          } else {
+            const float e = ex2_approx(-fabsf(x.v[j][u]) * kLog2e);
+            const float small = e * rcp_approx(1.0f + e);
+            r.v[j][u] = in ? copysignf(small, x.v[j][u]) : -0.0f;
+            dot = fmaf(c.v[j][u], signbit(r.v[j][u]) ? -r.v[j][u] : 1.0f - r.v[j][u], dot);
+          }
+        }
+      dot = seg_sum<32>(dot);
+      t.sum2(&dot, &none);
+      if (SF != SF_SOFTMAX) dot *= inv;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int col = column_of(t, j);
+        float g[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float d = scale * (c.v[j][u] - dot);
+          if (SF == SF_SOFTMAX) {
+            g[u] = r.v[j][u] * (d + z);
+          } else {
+            const float small = fabsf(r.v[j][u]);
+            g[u] = d * inv * small * (1.0f - small);
+            if (by_z != 0.0f) g[u] = fmaf(z, exp_shifted(x.v[j][u], shift), g[u]);
+          }
+        }
+        if (col < a.E) store4<DT, VEC>(a.grad, static_cast<size_t>(row) * a.E, col, a.E, g);
+      }
+    }
+  }
+  clear(p, t1);
+}
+
+// ---- host ------------------------------------------------------------------------
+// Warps of a row and times four columns of a lane: as few idle ones as possible, then
+// as few warps.  At most 6 warps of 3 for 2304 experts.
+struct Shape {
+  int warps, nv, teams;
+};
+
+Shape shape_of(int E) {
+  const int pieces = (E + 127) / 128;
+  Shape best{0, 0, 0};
+  int least = INT_MAX;
+  for (int nv = 4; nv >= 1; --nv) {
+    const int warps = (pieces + nv - 1) / nv;
+    if (warps > kTeamWarps) continue;
+    const int idle = warps * nv - pieces;
+    if (idle < least) {
+      least = idle;
+      best = Shape{warps, nv, kTeamWarps / warps};
+    }
+  }
+  return best;
+}
+
+// Tokens of a block: about `per_sm` blocks on each of 152 SMs, two rows a team at least.
+// A function of the sizes alone, so that sums have the same order on every GPU.
+int rows_of(int T, int teams, int per_sm) {
+  const int blocks = 152 * per_sm;
+  const int rows = (T + blocks - 1) / blocks;
+  return (rows < 2 * teams ? 2 * teams : (rows + teams - 1) / teams * teams);
+}
+
+constexpr int kBlocksPerSm = 3;
+constexpr int kFinishBlocks = 304;
+
+int blocks_of(int T, int rows) { return T == 0 ? 1 : (T + rows - 1) / rows; }
+
+struct Workspace {
+  size_t slots, z, parts, ticket, bytes;
+};
+
+Workspace workspace_of(int T, int E, int S) {
+  const Shape sh = shape_of(E);
+  const int blocks = blocks_of(T, rows_of(T, sh.teams, kBlocksPerSm));
+  const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  Workspace w;
+  w.slots = up((static_cast<size_t>(blocks) + S) * E * 4);
+  w.z = 2 * w.slots;
+  w.parts = w.z + up(static_cast<size_t>(blocks) * 4);
+  w.ticket = w.parts + kFinishBlocks * 8;
+  w.bytes = w.ticket + 256;
+  return w;
+}
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int check(int dtype, int T, int E, int K, int S, bool packed, int score_func) {
+  if (dtype != MR_F32 && dtype != MR_BF16) return MR_ERR_INVALID;
+  if (score_func != MR_SOFTMAX && score_func != MR_SIGMOID) return MR_ERR_INVALID;
+  if (T < 0 || E < 1 || K < 1 || K > E || S < 1) return MR_ERR_INVALID;
+  if (S > (T > 1 ? T : 1) || (!packed && S != 1)) return MR_ERR_INVALID;
+  if (static_cast<long long>(T) * E > INT_MAX || static_cast<long long>(T) * K > INT_MAX)
+    return MR_ERR_INVALID;
+  if (E > MR_MAX_EXPERTS || K > MR_MAX_TOPK) return MR_ERR_UNSUPPORTED;
+  return MR_OK;
+}
+
+template <int DT, bool VEC, int SF, bool FWD>
+cudaError_t launch_nv(const BalanceArgs& a, const Shape& sh, cudaStream_t st) {
+  const dim3 grid(a.blocks), block(32 * sh.warps * sh.teams);
+  const size_t smem = FWD ? static_cast<size_t>(sh.teams > 1 ? sh.teams + 1 : 1) * a.E * 4 : 0;
+  switch (sh.nv) {
+    case 1:
+      return launch_kernel(FWD ? balance_fwd_kernel<DT, VEC, 1, SF> : balance_bwd_kernel<DT, VEC, 1, SF>,
+                           grid, block, smem, st, a, sh.warps);
+    case 2:
+      return launch_kernel(FWD ? balance_fwd_kernel<DT, VEC, 2, SF> : balance_bwd_kernel<DT, VEC, 2, SF>,
+                           grid, block, smem, st, a, sh.warps);
+    case 3:
+      return launch_kernel(FWD ? balance_fwd_kernel<DT, VEC, 3, SF> : balance_bwd_kernel<DT, VEC, 3, SF>,
+                           grid, block, smem, st, a, sh.warps);
+    default:
+      return launch_kernel(FWD ? balance_fwd_kernel<DT, VEC, 4, SF> : balance_bwd_kernel<DT, VEC, 4, SF>,
+                           grid, block, smem, st, a, sh.warps);
+  }
+}
+
+template <bool FWD>
+cudaError_t launch_balance(const BalanceArgs& a, int dtype, int sf, bool vec, const Shape& sh,
+                           cudaStream_t st) {
+  if (dtype == MR_F32) {
+    if (sf == MR_SOFTMAX)
+      return vec ? launch_nv<DT_F32, true, SF_SOFTMAX, FWD>(a, sh, st)
+                 : launch_nv<DT_F32, false, SF_SOFTMAX, FWD>(a, sh, st);
+    return vec ? launch_nv<DT_F32, true, SF_SIGMOID, FWD>(a, sh, st)
+               : launch_nv<DT_F32, false, SF_SIGMOID, FWD>(a, sh, st);
+  }
+  if (sf == MR_SOFTMAX)
+    return vec ? launch_nv<DT_BF16, true, SF_SOFTMAX, FWD>(a, sh, st)
+               : launch_nv<DT_BF16, false, SF_SOFTMAX, FWD>(a, sh, st);
+  return vec ? launch_nv<DT_BF16, true, SF_SIGMOID, FWD>(a, sh, st)
+             : launch_nv<DT_BF16, false, SF_SIGMOID, FWD>(a, sh, st);
+}
+
+}  // namespace
+}  // namespace moe_router
+
+using namespace moe_router;
+
+extern "C" {
+
+size_t router_balance_loss_workspace_bytes(int T, int E, int S) {
+  if (T < 0 || E < 1 || E > MR_MAX_EXPERTS || S < 1) return 0;
+  return workspace_of(T, E, S).bytes;
+}
+
+int router_balance_loss_fwd(const void* logits, mr_dtype dtype, const int32_t* topk_indices,
+                            int ld_indices, const int32_t* seq_offsets, int T, int E, int K, int S,
+                            mr_score_func score_func, float coeff, float z_coeff, float* loss,
+                            int32_t* tokens_per_expert, float* row_stats, void* workspace,
+                            size_t workspace_bytes, mr_stream_t stream) {
+  const int rc = check(dtype, T, E, K, S, seq_offsets != nullptr, score_func);
+  if (rc != MR_OK) return rc;
+  if (ld_indices < K || loss == nullptr || tokens_per_expert == nullptr) return MR_ERR_INVALID;
+  if (T > 0 && (logits == nullptr || topk_indices == nullptr || row_stats == nullptr))
+    return MR_ERR_INVALID;
+  const Workspace w = workspace_of(T, E, S);
+  if (workspace == nullptr || workspace_bytes < w.bytes || !aligned(workspace, 16) ||
+      !aligned(row_stats, 8))
+    return MR_ERR_INVALID;
+  const Shape sh = shape_of(E);
+  uint8_t* const base = static_cast<uint8_t*>(workspace);
+  BalanceArgs a{};
+  a.logits = logits;
+  a.choices = topk_indices;
+  a.seq = seq_offsets;
+  a.loss = loss;
+  a.counts = tokens_per_expert;
+  a.stats = reinterpret_cast<float2*>(row_stats);
+  a.slot_sums = reinterpret_cast<float*>(base);
+  a.slot_counts = reinterpret_cast<int32_t*>(base + w.slots);
+  a.z_parts = reinterpret_cast<float*>(base + w.z);
+  a.parts = reinterpret_cast<double*>(base + w.parts);
+  a.ticket = reinterpret_cast<int*>(base + w.ticket);
+  a.ld_choices = ld_indices;
+  a.T = T; a.E = E; a.K = K; a.S = S;
+  a.rows = rows_of(T, sh.teams, kBlocksPerSm);
+  a.blocks = blocks_of(T, a.rows);
+  a.coeff = coeff;
+  a.z_coeff = z_coeff;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool vec = E % 4 == 0 && aligned(logits, dtype == MR_F32 ? 16 : 8);
+  if (launch_balance<true>(a, dtype, score_func, vec, sh, st) != cudaSuccess) return MR_ERR_CUDA;
+  const long long items = static_cast<long long>((E + 127) / 128) * S;
+  const dim3 grid(static_cast<unsigned>(items < kFinishBlocks ? items : kFinishBlocks));
+  return launch_kernel(balance_finish_kernel, grid, dim3(kFinishThreads), 0, st, a) == cudaSuccess
+             ? MR_OK
+             : MR_ERR_CUDA;
+}
+
+int router_balance_loss_bwd(const float* grad_loss, const void* logits, mr_dtype dtype,
+                            const int32_t* tokens_per_expert, const float* row_stats,
+                            const int32_t* seq_offsets, int T, int E, int K, int S,
+                            mr_score_func score_func, float coeff, float z_coeff,
+                            void* grad_logits, mr_stream_t stream) {
+  const int rc = check(dtype, T, E, K, S, seq_offsets != nullptr, score_func);
+  if (rc != MR_OK) return rc;
+  if (T == 0) return MR_OK;
+  if (grad_loss == nullptr || logits == nullptr || tokens_per_expert == nullptr ||
+      row_stats == nullptr || grad_logits == nullptr || !aligned(row_stats, 8))
+    return MR_ERR_INVALID;
+  const Shape sh = shape_of(E);
+  BalanceArgs a{};
+  a.logits = logits;
+  a.seq = seq_offsets;
+  a.counts = const_cast<int32_t*>(tokens_per_expert);
+  a.stats = reinterpret_cast<float2*>(const_cast<float*>(row_stats));
+  a.grad_loss = grad_loss;
+  a.grad = grad_logits;
+  a.T = T; a.E = E; a.K = K; a.S = S;
+  a.rows = rows_of(T, sh.teams, kBlocksPerSm);
+  a.blocks = blocks_of(T, a.rows);
+  a.coeff = coeff;
+  a.z_coeff = z_coeff;
+  const size_t piece = dtype == MR_F32 ? 16 : 8;
+  const bool vec = E % 4 == 0 && aligned(logits, piece) && aligned(grad_logits, piece);
+  return launch_balance<false>(a, dtype, score_func, vec, sh,
+                               reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MR_OK
+             : MR_ERR_CUDA;
+}
+
+}  // extern "C"

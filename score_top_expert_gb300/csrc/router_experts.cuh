@@ -44,6 +44,17 @@ struct W4Args {
   int T, P, E, N, D, group, out_dtype;
 };
 
+struct W8Args {
+  const int8_t* x;  // [T or P, D]
+  const float* x_scales;  // [T or P]
+  const int8_t* w;  // [E, N, D]
+  const float* w_scales;  // [E, N]
+  const int32_t* offsets;
+  const int32_t* p2u;
+  void* out;
+  int T, P, E, N, D, out_dtype;
+};
+
 struct CombineArgs {
   const void* z;         // expert outputs [T K, D]
   const void* gy;        // grad of the sums [T, D]
@@ -66,6 +77,9 @@ bool expert_matmul_few_ok(const ExpertArgs& a);
 int launch_expert_matmul_few(const ExpertArgs& a, cudaStream_t st);  // forward only
 int launch_expert_matmul_split(int form, const ExpertArgs& a, cudaStream_t st);  // any operands
 int launch_expert_matmul_w4(const W4Args& a, cudaStream_t st);
+int launch_expert_matmul_w8_tc(const W8Args& a, cudaStream_t st);  // any operands
+bool expert_matmul_w8_few_ok(const W8Args& a);
+int launch_expert_matmul_w8_few(const W8Args& a, cudaStream_t st);
 int launch_combine_fwd(const CombineArgs& a, cudaStream_t st);
 int launch_combine_bwd(const CombineArgs& a, cudaStream_t st);
 

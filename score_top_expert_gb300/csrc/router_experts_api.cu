@@ -25,6 +25,9 @@ int check_product(int T, int P, int E, int N, int D, bool mapped) {
 constexpr int kFewRows = 36;
 constexpr int kFewColumns = 512;
 
+// Rows an expert, on average, up to which 8-bit operands take the few-rows kernel.
+constexpr int kFewRowsW8 = 4;
+
 int run_product(int form, const ExpertArgs& a, mr_stream_t stream) {
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // One token's rows: 4 experts of 1024 x 1024 take 10 us here and 14 us in the
@@ -106,6 +109,25 @@ int router_expert_matmul_w4(const void* x, const uint8_t* qweight, const void* s
   const W4Args a{x, qweight, scales, zeros, expert_first_token_offset, permuted_to_unpermuted,
                  out, T, P, E, N, D, group_size, out_dtype};
   return launch_expert_matmul_w4(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int router_expert_matmul_w8(const int8_t* x, const float* x_scales, const int8_t* weight,
+                            const float* weight_scales, const int32_t* expert_first_token_offset,
+                            const int32_t* permuted_to_unpermuted, int T, int P, int E, int N,
+                            int D, void* out, mr_dtype out_dtype, mr_stream_t stream) {
+  if (!known_dtype(out_dtype)) return MR_ERR_INVALID;
+  const int rc = check_product(T, P, E, N, D, permuted_to_unpermuted != nullptr);
+  if (rc != MR_OK) return rc;
+  if (P == 0) return MR_OK;
+  if (x == nullptr || x_scales == nullptr || weight == nullptr || weight_scales == nullptr ||
+      expert_first_token_offset == nullptr || out == nullptr)
+    return MR_ERR_INVALID;
+  const W8Args a{x, x_scales, weight, weight_scales, expert_first_token_offset,
+                 permuted_to_unpermuted, out, T, P, E, N, D, out_dtype};
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return P <= kFewRowsW8 * static_cast<long long>(E) && expert_matmul_w8_few_ok(a)
+             ? launch_expert_matmul_w8_few(a, st)
+             : launch_expert_matmul_w8_tc(a, st);
 }
 
 // Sizes of the combination: every row index stays below 2^31.

@@ -50,6 +50,7 @@
 #include "router_common.cuh"
 #include "router_experts.cuh"
 #include "router_launch.cuh"
+#include "router_widen.cuh"
 
 namespace moe_router {
 namespace {
@@ -64,11 +65,15 @@ constexpr int kStages = 2;
 constexpr int kStageBytes = kRows * kChunk;
 constexpr int kPanel = 4096;      // columns of x staged at a time
 
-// V: 32-bit words a thread takes of each step; 0: bf16 weights.
+// V: 32-bit words a thread takes of each step; 0: bf16 weights, 8: 8-bit weights.
+template <int V>
+constexpr bool kFourBits = V == 1 || V == 2 || V == 4;
+
 template <int V>
 struct Layout {
-  static constexpr int kPerChunk = V == 0 ? kChunk / 2 : kChunk * 2;  // columns per stage
-  static constexpr int kStep = V == 0 ? 32 : 32 * V;                  // columns per step
+  // columns per stage, and per step
+  static constexpr int kPerChunk = V == 0 ? kChunk / 2 : V == 8 ? kChunk : kChunk * 2;
+  static constexpr int kStep = V == 0 ? 32 : V == 8 ? 64 : 32 * V;
   static constexpr int kSteps = kPerChunk / kStep;
   // Row r's 16-byte piece p lies at piece p ^ swizzle(r) of its 256 bytes, so
   // that the rows one load reads at the same column fall into different banks.
@@ -103,6 +108,15 @@ __device__ __forceinline__ void mma_16816_from_zero(float (&c)[4], uint32_t a0, 
       "{%8,%9}, {%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// fp16 operands.
+__device__ __forceinline__ void mma_16816_half(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // nibbles i and i + 4 of w as the bf16 pair (q - z, q - z); zp = 128 + z twice
@@ -148,6 +162,7 @@ __device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[V]) 
 
 struct FewArgs {
   const void* x;
+  const float* x_scales;  // 8 bits
   const uint8_t* w;
   const void* scales;
   const uint8_t* zeros;
@@ -190,18 +205,25 @@ __device__ __forceinline__ Task task_of(const FewArgs& g, const int* prefix, int
   return t;
 }
 
+// 8 bits: the scale of a permuted row times that of a weight row.
+__device__ __forceinline__ float scale_of(const FewArgs& g, const Task& k, int token, int n) {
+  const int src = source_row(g.p2u, g.T, k.p0 + token);
+  return (src >= 0 ? g.x_scales[src] : 0.0f) *
+         static_cast<const float*>(g.scales)[static_cast<size_t>(k.e) * g.N + n];
+}
+
 // Scales (low half) and zero points of one chunk of 16 weight rows: the quad's
 // lanes hold every fourth group of both of its rows and hand them round.
 template <int V>
 struct Meta {
-  static constexpr int kHeld = V == 0 ? 1 : (Layout<V>::kSteps + 3) / 4;
+  static constexpr int kHeld = !kFourBits<V> ? 1 : (Layout<V>::kSteps + 3) / 4;
   uint32_t a[kHeld], b[kHeld];
 
   // ra, rb: the rows' first group
   template <bool ZEROS>
   __device__ __forceinline__ void load(const FewArgs& g, size_t ra, size_t rb, int c, int groups,
                                        int t) {
-    if constexpr (V > 0) {
+    if constexpr (kFourBits<V>) {
       const unsigned short* scales = static_cast<const unsigned short*>(g.scales);
       const int g0 = c * Layout<V>::kSteps + t;
       const unsigned short *sa = scales + ra + g0, *sb = scales + rb + g0;
@@ -242,8 +264,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int team = SHARED ? warp / kShare : warp, member = SHARED ? warp % kShare : 0;
   const int gq = lane >> 2, t = lane & 3;  // fragment row (and token), place in the quad
-  const int row_bytes = V == 0 ? 2 * g.D : g.D / 2;
-  const int groups = V == 0 ? 0 : g.D / L::kStep;
+  const int row_bytes = V == 0 ? 2 * g.D : V == 8 ? g.D : g.D / 2;
+  const int groups = kFourBits<V> ? g.D / L::kStep : 0;
   const int chunks = (g.D + L::kPerChunk - 1) / L::kPerChunk;
   // this warp's chunks of each tile
   const int per = SHARED ? (chunks + kShare - 1) / kShare : chunks;
@@ -319,16 +341,28 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
     for (int d0 = 0; d0 < g.D; d0 += kPanel) {
       // ---- this panel of x ---------------------------------------------------------
       const int cols = min(kPanel, g.D - d0);
-      const int pieces = (cols + 31) / 32 * 4;  // of 8 columns, whole steps of 32
+      // of 8 columns, whole steps of 32 (8 bits: 64)
+      const int pieces = V == 8 ? (cols + 63) / 64 * 8 : (cols + 31) / 32 * 4;
       __syncthreads();  // the panel before has been read
       for (int q = threadIdx.x; q < k.cnt * pieces; q += kThreads) {
         const int token = q / pieces, at = q - token * pieces;
         const int src = source_row(g.p2u, g.T, k.p0 + token);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (V == 8) {
+          // piece q of a step's eight goes to thread q / 2 as its first or second
+          if (src >= 0 && at * 8 < cols) {
+            const uint2 b = *reinterpret_cast<const uint2*>(
+                static_cast<const int8_t*>(g.x) + static_cast<size_t>(src) * g.D + d0 + at * 8);
+            v = widen_eight(b.x, b.y);
+          }
+          *reinterpret_cast<uint4*>(
+              xs + token * pitch + ((at & ~7) + (at & 1) * 4 + ((at & 7) >> 1)) * 16) = v;
+          continue;
+        }
         if (src >= 0 && at * 8 < cols)
           v = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(src) * g.D + d0 + at * 8);
         int place = at;
-        if constexpr (V > 0) {
+        if constexpr (kFourBits<V>) {
           // word i of a step goes to thread i / V as its word i % V; columns
           // (0, 4), (1, 5), (2, 6), (3, 7) of a word pair up as the nibbles do
           constexpr int kWords = 4 * V;
@@ -354,7 +388,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
           const int sw = L::swizzle(gq);  // and of row gq + 8
           const int col = c * L::kPerChunk - d0;
           const uint8_t* const xa = x_at + col * 2;
-          [[maybe_unused]] float sum[4];  // bf16 weights: this chunk's
+          [[maybe_unused]] float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // 8 bits, bf16: this chunk's
 #pragma unroll
           for (int s = 0; s < L::kSteps; ++s) {
             if (col + s * L::kStep >= cols) break;
@@ -369,6 +403,23 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
               else
                 mma_16816(sum, wa[0], wb[0], wa[1], wb[1], xv[0], xv[1]);
               mma_16816(sum, wa[2], wb[2], wa[3], wb[3], xv[2], xv[3]);
+            } else if constexpr (V == 8) {
+              uint32_t wa[4], wb[4];
+              const uint8_t* const from = at + (((4 * s + t) ^ sw) << 4);
+              load_words<4>(from, wa);
+              load_words<4>(from + 8 * kChunk, wb);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t xv[4];
+                load_words<4>(xa + s * 128 + h * 64, xv);
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                  const uint32_t a = wa[2 * h + v] ^ 0x80808080u, b = wb[2 * h + v] ^ 0x80808080u;
+                  mma_16816_half(sum, widen_two(a, 0x4140), widen_two(b, 0x4140),
+                                 widen_two(a, 0x4342), widen_two(b, 0x4342), xv[2 * v],
+                                 xv[2 * v + 1]);
+                }
+              }
             } else {
               uint32_t wa[V], wb[V];
               const int byte = s * (16 * V) + t * (4 * V);
@@ -401,7 +452,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
               acc[3] = fmaf(sb, p[3], acc[3]);
             }
           }
-          if constexpr (V == 0) {
+          if constexpr (!kFourBits<V>) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[j] += sum[j];
           }
@@ -424,6 +475,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
             float v = sums[0][token][n];
 #pragma unroll
             for (int w = 1; w < kShare; ++w) v += sums[w][token][n];
+            if constexpr (V == 8) v *= scale_of(g, k, token, n0 + n);
             store_value(g, static_cast<size_t>(k.p0 + token) * g.N + n0 + n, v);
           }
           team_sync(team + 1);
@@ -431,8 +483,10 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int token = 2 * t + (j & 1), n = n0 + gq + (j >> 1) * 8;
-            if (token < k.cnt && n < g.N)
+            if (token < k.cnt && n < g.N) {
+              if constexpr (V == 8) acc[j] *= scale_of(g, k, token, n);
               store_value(g, static_cast<size_t>(k.p0 + token) * g.N + n, acc[j]);
+            }
           }
         }
       }
@@ -477,17 +531,28 @@ bool expert_matmul_few_ok(const ExpertArgs& a) {
 }
 
 int launch_expert_matmul_few(const ExpertArgs& a, cudaStream_t st) {
-  const FewArgs g{a.a, static_cast<const uint8_t*>(a.b), nullptr, nullptr, a.offsets, a.p2u,
+  const FewArgs g{a.a, nullptr, static_cast<const uint8_t*>(a.b), nullptr, nullptr, a.offsets, a.p2u,
                   a.out, a.T, a.P, a.E, a.N, a.D, a.out_dtype};
   return launch_typed<0, false>(g, st);
 }
 
 int launch_expert_matmul_w4(const W4Args& a, cudaStream_t st) {
-  const FewArgs g{a.x, a.q, a.scales, a.zeros, a.offsets, a.p2u, a.out, a.T, a.P, a.E, a.N, a.D,
+  const FewArgs g{a.x, nullptr, a.q, a.scales, a.zeros, a.offsets, a.p2u, a.out, a.T, a.P, a.E, a.N, a.D,
                   a.out_dtype};
   if (a.group == 32) return a.zeros ? launch_typed<1, true>(g, st) : launch_typed<1, false>(g, st);
   if (a.group == 64) return a.zeros ? launch_typed<2, true>(g, st) : launch_typed<2, false>(g, st);
   return a.zeros ? launch_typed<4, true>(g, st) : launch_typed<4, false>(g, st);
+}
+
+bool expert_matmul_w8_few_ok(const W8Args& a) {
+  const auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  return a.D % 16 == 0 && aligned(a.x) && aligned(a.w);
+}
+
+int launch_expert_matmul_w8_few(const W8Args& a, cudaStream_t st) {
+  const FewArgs g{a.x, a.x_scales, reinterpret_cast<const uint8_t*>(a.w), a.w_scales, nullptr,
+                  a.offsets, a.p2u, a.out, a.T, a.P, a.E, a.N, a.D, a.out_dtype};
+  return launch_typed<8, false>(g, st);
 }
 
 }  // namespace moe_router

@@ -1,0 +1,461 @@
+// Products grouped by expert on 8-bit integers with a scale for each row and each
+// output channel, on the tensor cores:
+//
+//   out[p, n] = x_scales[row(p)] weight_scales[e, n] sum_d weight[e, n, d] x[row(p), d]
+//
+// sm_103a's tcgen05 has no integer products.  An 8-bit integer is exact in fp16, a product
+// of two in fp32, and a sum of 960 of them stays below 2^24: so the operands are widened to
+// fp16 on their way to shared memory and multiplied at the 16-bit rate.  A fp32 output is
+// summed in segments of at most 960 terms, each exact; a bf16 output is one sum, exact
+// while it stays below 2^24 (and off by about 2^-30 of its value a term above that).
+//
+// The tiles and their order are those of router_experts_tc.cu's forward: 128 or 256 weight
+// rows by up to 128 or 256 of the expert's rows, one CTA or a pair.  Sixteen warps load: a
+// thread one 16-byte piece of a weight row and one of a row of x for each slice of 64
+// columns, kAhead slices ahead of the one that it widens and stores in the layout that the
+// tensor cores read.  In a pair each CTA's loading warps arrive on its own barrier and
+// one warp of the second CTA passes that on to the leader's: an arrival across the pair
+// costs the arriving warp hundreds of cycles.
+#include <atomic>
+
+#include "router_experts_tiles.cuh"
+#include "router_widen.cuh"
+
+namespace moe_router {
+namespace {
+
+constexpr int kLoaders = 16;
+constexpr int kThreads = 32 * (8 + kLoaders);
+constexpr int kStages = 6;
+constexpr int kAhead = 4;
+constexpr int kRowsA = 128;  // weight rows of a CTA
+constexpr int kRowsB = 128;  // most rows of x of a CTA
+constexpr int kBytesA = kRowsA * 128;
+constexpr int kBytesB = kRowsB * 128;
+constexpr int kStageBytes = kBytesA + kBytesB;
+constexpr int kSmem = kStages * kStageBytes + 1024;  // stages start on 1024 bytes
+
+template <int CG>
+struct Shape {
+  static constexpr int kTileA = kRowsA * CG;
+  static constexpr int kTileB = kRowsB * CG;
+  static constexpr int kRound = 16 * CG;
+  static constexpr uint32_t kColumns = 2 * kTileB;  // two accumulators
+};
+
+struct W8TcArgs {
+  TcArgs t;
+  const int8_t* x;
+  const int8_t* w;
+  const float* x_scales;
+  const float* w_scales;
+  int out_f32;
+};
+
+// 16 consecutive bytes of a row, VB bytes an access, of which `left` (a multiple of VB, or
+// more than 16) exist; zeros behind them.
+template <int VB>
+__device__ __forceinline__ uint4 load_piece(const int8_t* p, int left) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if constexpr (VB == 16) {
+    if (left > 0) v = __ldg(reinterpret_cast<const uint4*>(p));
+  } else if constexpr (VB == 8) {
+    if (left > 0) {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+      v.x = a.x;
+      v.y = a.y;
+    }
+    if (left > 8) {
+      const uint2 b = __ldg(reinterpret_cast<const uint2*>(p) + 1);
+      v.z = b.x;
+      v.w = b.y;
+    }
+  } else if constexpr (VB == 4) {
+    const unsigned* q = reinterpret_cast<const unsigned*>(p);
+    if (left > 0) v.x = __ldg(q);
+    if (left > 4) v.y = __ldg(q + 1);
+    if (left > 8) v.z = __ldg(q + 2);
+    if (left > 12) v.w = __ldg(q + 3);
+  } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    const uint8_t* q = reinterpret_cast<const uint8_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < left) w[i >> 2] |= static_cast<uint32_t>(__ldg(q + i)) << (8 * (i & 3));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return v;
+}
+
+// Eight bytes, widened, to one 16-byte piece of shared memory.
+__device__ __forceinline__ void store_wide(uint32_t at, uint32_t a, uint32_t b) {
+  const uint4 v = widen_eight(a, b);
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w) : "memory");
+}
+
+// Waits for data that the other CTA of the pair has published.
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ bool wait_cluster(const Waiter& w, uint64_t* bar, uint32_t parity) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const unsigned long long t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (try_wait_cluster(bar, parity)) return true;
+    if (global_timer_ns() - t0 > kWaitLimitNs) break;
+  }
+  *reinterpret_cast<volatile int*>(w.gave_up) = 1;
+  atomicExch(w.status, kDeviceWaitTimeout);
+  return false;
+}
+
+template <int CG, int VB, bool F32>
+__global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8TcArgs args) {
+  using S = Shape<CG>;
+  const TcArgs& g = args.t;
+  extern __shared__ uint8_t dynamic_smem[];
+  __shared__ __align__(8) uint64_t full[kStages], peer[kStages], empty[kStages], done[2], drained[2];
+  __shared__ uint32_t tmem_at;
+  __shared__ int gave_up;
+  __shared__ int tmp[33];
+  __shared__ int prefix[MR_MAX_EXPERTS + 1];
+  __shared__ int offs[MR_MAX_EXPERTS + 1];  // the offsets, clamped to [0, P]
+  __shared__ float row_scales[4][S::kTileB];  // of each storing warp
+
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const uint32_t stages_at = (smem_addr(dynamic_smem) + 1023u) & ~1023u;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], kLoaders);
+      mbar_init(&peer[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&done[i], 1);
+      mbar_init(&drained[i], 4 * CG);  // one arrival per storing warp
+    }
+    gave_up = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc<CG>(&tmem_at, S::kColumns);
+  pdl_enter();
+  for (int e = threadIdx.x; e <= g.E; e += blockDim.x) offs[e] = min(max(g.offsets[e], 0), g.P);
+  const int tiles = expert_tile_prefix(g.offsets, g.E, g.P, S::kTileB, prefix, tmp) *
+                    ((g.N + S::kTileA - 1) / S::kTileA);
+  tc_fence_before();
+  if constexpr (CG == 2) cluster_sync(); else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_at;
+  const Waiter wait{&gave_up, g.status};
+  const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
+  const int slices = (g.D + kDeep - 1) / kDeep;
+
+  if (warp >= 8) {
+    // ---- loads -----------------------------------------------------------------
+    const int row = (static_cast<int>(threadIdx.x) - 256) >> 2, quarter = threadIdx.x & 3;
+    // the load cursor, kAhead slices ahead of the stores
+    int li = first, ls = 0;
+    const int8_t *pa = nullptr, *pb = nullptr;
+    int left_a = 0, left_b = 0;  // bytes of the row from this thread's piece on
+    bool wanted = false;         // the tile has this row of x (rounded up)
+    auto enter = [&]() {         // tile li
+      const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, li);
+      const int n = t.a0 + static_cast<int>(rank) * kRowsA + row;
+      pa = args.w + (static_cast<size_t>(t.e) * g.N + n) * g.D + quarter * 16;
+      left_a = n < g.N ? g.D - quarter * 16 : 0;
+      const int half = (t.cnt + S::kRound - 1) / S::kRound * S::kRound / CG;
+      const int b = static_cast<int>(rank) * half + row;
+      wanted = row < half;
+      int source = -1;
+      if (wanted && b < t.cnt) {
+        source = g.p2u == nullptr ? t.start + b : g.p2u[t.start + b];
+        if (g.p2u != nullptr && source >= 0) source = token_of(g, source);
+      }
+      pb = args.x + static_cast<size_t>(max(source, 0)) * g.D + quarter * 16;
+      left_b = source >= 0 ? g.D - quarter * 16 : 0;
+    };
+    uint4 a[kAhead], b[kAhead];
+    uint32_t valid = 0, keep = 0;  // by slot: holds a slice; its row of x is stored
+    auto fetch = [&](int j) {
+      if (li >= tiles) {
+        valid &= ~(1u << j);
+        return;
+      }
+      valid |= 1u << j;
+      keep = wanted ? keep | (1u << j) : keep & ~(1u << j);
+      a[j] = load_piece<VB>(pa, left_a);
+      b[j] = load_piece<VB>(pb, left_b);
+      pa += kDeep;
+      pb += kDeep;
+      left_a -= kDeep;
+      left_b -= kDeep;
+      if (++ls == slices) {
+        ls = 0;
+        li += step;
+        if (li < tiles) enter();
+      }
+    };
+    if (li < tiles) enter();
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) fetch(j);
+    int stage = 0;
+    uint32_t parity = 1;  // the first pass finds the stages empty
+    // pieces 2 quarter and 2 quarter + 1 of the row's eight, in the 128-byte swizzle
+    const uint32_t to0 = row * 128 + (((2 * quarter) ^ (row & 7)) << 4);
+    const uint32_t to1 = row * 128 + (((2 * quarter + 1) ^ (row & 7)) << 4);
+    bool ok = true;
+    while (ok && valid != 0) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (!ok || !(valid >> j & 1u)) break;
+        ok = __all_sync(0xffffffffu, wait(&empty[stage], parity));
+        if (!ok) break;
+        const uint32_t at = stages_at + stage * kStageBytes;
+        store_wide(at + to0, a[j].x, a[j].y);
+        store_wide(at + to1, a[j].z, a[j].w);
+        if (keep >> j & 1u) {
+          store_wide(at + kBytesA + to0, b[j].x, b[j].y);
+          store_wide(at + kBytesA + to1, b[j].z, b[j].w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
+        }
+        fetch(j);
+      }
+    }
+  } else if (warp == 3 && CG == 2 && rank == 1) {
+    // ---- the second CTA's stages, announced to the leader ----------------------------
+    int stage = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+    for (int i = first; i < tiles && ok; i += step)
+      for (int s = 0; s < slices && ok; ++s) {
+        ok = __all_sync(0xffffffffu, wait(&full[stage], parity));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&peer[stage]), 0));
+        __syncwarp();
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
+        }
+      }
+  } else if (warp == 1 && rank == 0) {
+    // ---- products ----------------------------------------------------------------
+    int stage = 0, n = 0;  // n: accumulators filled
+    uint32_t parity = 0;
+    bool ok = true;
+    const int segment = segment_of<F32>(slices);
+    for (int i = first; i < tiles && ok; i += step) {
+      const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, i);
+      const int cols = (t.cnt + S::kRound - 1) / S::kRound * S::kRound;
+      const uint32_t desc = half_product_desc(S::kTileA, cols);
+      for (int s0 = 0; s0 < slices && ok; s0 += segment) {
+        const int end = min(s0 + segment, slices);
+        const int buf = n & 1;
+        // an accumulator that the storing warps are done with
+        ok = __all_sync(0xffffffffu, wait(&drained[buf], ((n >> 1) & 1) ^ 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * S::kTileB;
+        for (int s = s0; s < end; ++s) {
+          ok = __all_sync(0xffffffffu, wait(&full[stage], parity) &&
+                                           (CG == 1 || wait_cluster(wait, &peer[stage], parity)));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = stages_at + stage * kStageBytes;
+          const uint64_t da = operand_desc(at, 0, 1024);
+          const uint64_t db = operand_desc(at + kBytesA, 0, 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kDeep / 16; ++k)
+              tc_product<CG>(d, da + 2 * k, db + 2 * k, desc, s > s0 || k > 0);
+            tc_commit<CG>(&empty[stage]);
+            if (s == end - 1) tc_commit<CG>(&done[buf]);
+          }
+          __syncwarp();
+          if (++stage == kStages) {
+            stage = 0;
+            parity ^= 1;
+          }
+        }
+        ++n;
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---- stores --------------------------------------------------------------------
+    const int quad = warp - 4;
+    int n = 0;
+    bool ok = true;
+    const int segment = segment_of<F32>(slices);
+    for (int i = first; i < tiles && ok; i += step) {
+      const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, i);
+      // the rows' scales, while the tile is computed; each warp its own copy, so that one
+      // that gives up leaves none waiting
+      float* const by_row = row_scales[quad];
+      __syncwarp();
+      for (int b = lane; b < t.cnt; b += 32) {
+        int source = g.p2u == nullptr ? t.start + b : g.p2u[t.start + b];
+        if (g.p2u != nullptr && source >= 0) source = token_of(g, source);
+        by_row[b] = source >= 0 ? args.x_scales[source] : 0.0f;
+      }
+      const int row = t.a0 + static_cast<int>(rank) * kRowsA + quad * 32 + lane;
+      const float channel =
+          row < g.N ? args.w_scales[static_cast<size_t>(t.e) * g.N + row] : 0.0f;
+      __syncwarp();
+      for (int first_slice = 0; first_slice == 0 || first_slice < slices;) {
+        const bool add = first_slice > 0;  // fp32 only: to what this thread stored before
+        const int buf = n & 1;
+        ok = __all_sync(0xffffffffu, wait(&done[buf], (n >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t acc =
+            tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * S::kTileB;
+        for (int c = 0; c < t.cnt; c += 32) {
+          uint32_t v[32];
+          tmem_load_32(acc + c, v);
+          const size_t o = static_cast<size_t>(t.start + c) * g.N + row;
+          if (row < g.N) {
+            if constexpr (F32) {
+              float* out = static_cast<float*>(g.out) + o;
+#pragma unroll
+              for (int j = 0; j < 32; ++j, out += g.N)
+                if (c + j < t.cnt) {
+                  const float r = __uint_as_float(v[j]) * by_row[c + j] * channel;
+                  if (add) red_add(out, r);
+                  else *out = r;
+                }
+            } else {
+              unsigned short* out = static_cast<unsigned short*>(g.out) + o;
+#pragma unroll
+              for (int j = 0; j < 32; ++j, out += g.N)
+                if (c + j < t.cnt)
+                  *out = static_cast<unsigned short>(
+                      f32_to_bf16_bits(__uint_as_float(v[j]) * by_row[c + j] * channel));
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+          mbar_arrive_cluster(CG == 2 ? map_to_rank(smem_addr(&drained[buf]), 0)
+                                      : smem_addr(&drained[buf]));
+        ++n;
+        first_slice += max(segment, 1);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  // After a wait that gave up: leave products in flight another millisecond
+  // before the shared and tensor memory is given back.
+  if (*reinterpret_cast<volatile int*>(&gave_up))
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+  if constexpr (CG == 2) cluster_sync(); else __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc<CG>(tmem, S::kColumns);
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+// Clusters of the kernel that run at once, asked once per device and kernel.
+constexpr int kDevices = 64;
+template <typename Kern>
+int resident_clusters(Kern kern, int cg, std::atomic<int>* known) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+      cudaSuccess)
+    return 0;
+  n = device_sm_count();
+  if (cg == 2) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  }
+  if (n > 0) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int CG, int VB, bool F32>
+int launch_typed(const W8Args& a, cudaStream_t st) {
+  using S = Shape<CG>;
+  static std::atomic<int> known[kDevices];
+  const auto kern = expert_matmul_w8_kernel<CG, VB, F32>;
+  const int resident = resident_clusters(kern, CG, known);
+  W8TcArgs g{};
+  g.t = TcArgs{a.offsets, a.p2u, a.out, device_status_word(), a.T, a.P, a.E, a.N, a.D,
+               a.p2u == nullptr ? a.P : a.T, inverse_of(a.T)};
+  if (resident <= 0 || g.t.status == nullptr) return MR_ERR_CUDA;
+  g.x = a.x;
+  g.w = a.w;
+  g.x_scales = a.x_scales;
+  g.w_scales = a.w_scales;
+  const long long ta = (a.N + S::kTileA - 1) / S::kTileA;
+  const long long tb = static_cast<long long>(a.E < a.P ? a.E : a.P) + a.P / S::kTileB;
+  const long long clusters = ta * tb < resident ? ta * tb : resident;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, g) == cudaSuccess ? MR_OK : MR_ERR_CUDA;
+}
+
+template <int VB>
+int launch_width(const W8Args& a, cudaStream_t st) {
+  const bool pair = a.P >= 40ll * a.E;
+  if (a.out_dtype == DT_F32)
+    return pair ? launch_typed<2, VB, true>(a, st) : launch_typed<1, VB, true>(a, st);
+  return pair ? launch_typed<2, VB, false>(a, st) : launch_typed<1, VB, false>(a, st);
+}
+
+}  // namespace
+
+int launch_expert_matmul_w8_tc(const W8Args& a, cudaStream_t st) {
+  const uintptr_t all = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w) |
+                        static_cast<uintptr_t>(a.D);
+  return (all & 15u) == 0  ? launch_width<16>(a, st)
+         : (all & 7u) == 0 ? launch_width<8>(a, st)
+         : (all & 3u) == 0 ? launch_width<4>(a, st)
+                           : launch_width<1>(a, st);
+}
+
+}  // namespace moe_router

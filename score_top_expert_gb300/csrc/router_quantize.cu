@@ -1,0 +1,190 @@
+// Rows in 8 bits, with a scale for each:
+//
+//   scale = max |x| / 127,   q = x / scale to the nearest integer, ties to even
+//
+// Bound by HBM: a row is read once, held in the registers of the 1 to 16 warps of its
+// team (of more than 64 pieces a lane's later ones are read again), and written once.
+//
+// The quotient is the exact one's rounding.  x (1 / scale) is off by 2^-23 of itself, 1.6e-5
+// at 127; so only where it lies within 2e-5 of a half can its rounding be another one
+// (every row whose largest value is twice another has such a place: 63.5), and there the
+// remainder x - q scale decides, which one multiply-add gives exactly: a multiple of the
+// smaller operand's last bit and at most scale / 2.
+#include <climits>
+
+#include "router_common.cuh"
+#include "router_experts.cuh"
+#include "router_rows.cuh"
+
+namespace moe_router {
+namespace {
+
+constexpr int kMaxWarps = 16;
+constexpr int kBlockWarps = 8;
+constexpr float kMagic = 12582912.0f;     // 1.5 2^23: adding it rounds to an integer
+constexpr float kSmallest = 1.17549435e-38f;  // 2^-126
+
+// The integer q's low byte, of kMagic + q, put right where the quotient is next to a half.
+__device__ __noinline__ float decided(float x, float scale, float r) {
+  float q = r - kMagic;
+  const float d = fmaf(-q, scale, x);
+  const float twice = 2.0f * fabsf(d);
+  const bool odd = (__float_as_int(r) & 1) != 0;
+  if (twice > scale || (twice == scale && odd)) q += copysignf(1.0f, d);
+  return q + kMagic;
+}
+
+template <int N>
+__device__ __forceinline__ void quantize(const float (&x)[N], float scale, float inv,
+                                         uint32_t (&bytes)[N / 4]) {
+  float r[N], far = 0.0f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    r[j] = fmaf(x[j], inv, kMagic);
+    far = fmaxf(far, fabsf(fmaf(x[j], inv, kMagic - r[j])));
+  }
+  if (far > 0.49998f) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (fabsf(fmaf(x[j], inv, kMagic - r[j])) > 0.49998f) r[j] = decided(x[j], scale, r[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < N / 4; ++j) {
+    const uint32_t lo = __byte_perm(__float_as_uint(r[4 * j]), __float_as_uint(r[4 * j + 1]), 0x0040);
+    const uint32_t hi =
+        __byte_perm(__float_as_uint(r[4 * j + 2]), __float_as_uint(r[4 * j + 3]), 0x0040);
+    bytes[j] = __byte_perm(lo, hi, 0x5410);
+  }
+}
+
+template <typename P, int BYTES>
+__device__ __forceinline__ void store_bytes(int8_t* row, int col0, int lane, int D,
+                                            const uint32_t (&b)[P::kN / 4]) {
+  if constexpr (BYTES == 16) {
+    const int c = P::column(col0, 0, lane);
+    if (c >= D) return;
+    if constexpr (P::kN == 8) __stcs(reinterpret_cast<uint2*>(row + c), make_uint2(b[0], b[1]));
+    else __stcs(reinterpret_cast<unsigned int*>(row + c), b[0]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < P::kN; ++j) {
+      const int c = P::column(col0, j / P::kEach, lane) + j % P::kEach;
+      if (c < D) row[c] = static_cast<int8_t>(b[j >> 2] >> (8 * (j & 3)));
+    }
+  }
+}
+
+struct QuantizeArgs {
+  const void* x;
+  int8_t* q;
+  float* scales;
+  int R, D, warps;
+};
+
+template <int DT, int BYTES, int U>
+__global__ __launch_bounds__(32 * kMaxWarps) void quantize_kernel(const QuantizeArgs a) {
+  using P = Piece<DT, BYTES>;
+  __shared__ unsigned cells[kMaxWarps];
+  pdl_enter();
+  const int lane = threadIdx.x & 31, block_warp = threadIdx.x >> 5;
+  const int team = block_warp / a.warps, warp = block_warp - team * a.warps;
+  const int teams = (blockDim.x >> 5) / a.warps;
+  const long long row = static_cast<long long>(blockIdx.x) * teams + team;
+  if (row >= a.R) return;  // whole teams, with barriers of their own
+  const size_t at = static_cast<size_t>(row) * a.D;
+  const int stride = a.warps * 32 * P::kN;
+  P held[U];
+  unsigned top = 0;  // |x| as bits: a NaN is above an infinity, which is above all else
+  auto largest = [&](const P& p, int col) {
+    if (P::column(col, 0, lane) >= a.D) return;
+    float v[P::kN];
+    p.widen(v);
+#pragma unroll
+    for (int j = 0; j < P::kN; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+  };
+  const int col0 = warp * 32 * P::kN;
+#pragma unroll
+  for (int q = 0; q < U; ++q) held[q].template load<true>(a.x, at, col0 + q * stride, lane, a.D);
+#pragma unroll
+  for (int q = 0; q < U; ++q) largest(held[q], col0 + q * stride);
+  for (int col = col0 + U * stride; col < a.D; col += stride) {
+    P p;
+    p.template load<false>(a.x, at, col, lane, a.D);
+    largest(p, col);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (a.warps > 1) {
+    if (lane == 0) cells[block_warp] = top;
+    if (teams == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(a.warps * 32) : "memory");
+    for (int w = 0; w < a.warps; ++w) top = max(top, cells[team * a.warps + w]);
+  }
+  float scale = __fdiv_rn(__uint_as_float(top), 127.0f);
+  if (top != 0 && scale < kSmallest) scale = kSmallest;  // (whose inverse is a number)
+  const float inv = __fdiv_rn(1.0f, scale);
+  int8_t* const out = a.q + at;
+  auto finish = [&](const P& p, int col) {
+    if (P::column(col, 0, lane) >= a.D) return;
+    float v[P::kN];
+    p.widen(v);
+    uint32_t b[P::kN / 4];
+    // without a finite scale above zero all integers are zero
+    if (top - 1u < 0x7f7fffffu) {
+      quantize<P::kN>(v, scale, inv, b);
+    } else {
+#pragma unroll
+      for (int j = 0; j < P::kN / 4; ++j) b[j] = 0u;
+    }
+    store_bytes<P, BYTES>(out, col, lane, a.D, b);
+  };
+#pragma unroll
+  for (int q = 0; q < U; ++q) finish(held[q], col0 + q * stride);
+  for (int col = col0 + U * stride; col < a.D; col += stride) {
+    P p;
+    p.template load<false>(a.x, at, col, lane, a.D);
+    finish(p, col);
+  }
+  if (warp == 0 && lane == 0) a.scales[row] = scale;
+}
+
+template <int DT, int BYTES>
+int launch_typed(QuantizeArgs a, cudaStream_t st) {
+  constexpr int columns = 32 * Piece<DT, BYTES>::kN;
+  const int stretches = (a.D + columns - 1) / columns;
+  const int pieces = stretches <= kBlockWarps ? 1 : stretches <= 2 * kBlockWarps ? 2 : 4;
+  const int needed = (stretches + pieces - 1) / pieces;
+  a.warps = needed < kMaxWarps ? needed : kMaxWarps;
+  const int teams = a.warps >= kBlockWarps ? 1 : kBlockWarps / a.warps;
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(a.R) + teams - 1) / teams));
+  const dim3 block(32 * a.warps * teams);
+  const cudaError_t e =
+      pieces == 1   ? launch_kernel(quantize_kernel<DT, BYTES, 1>, grid, block, 0, st, a)
+      : pieces == 2 ? launch_kernel(quantize_kernel<DT, BYTES, 2>, grid, block, 0, st, a)
+                    : launch_kernel(quantize_kernel<DT, BYTES, 4>, grid, block, 0, st, a);
+  return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace moe_router
+
+using namespace moe_router;
+
+extern "C" int router_quantize_rows(const void* x, mr_dtype dtype, int R, int D, int8_t* q,
+                                    float* scales, mr_stream_t stream) {
+  if ((dtype != MR_F32 && dtype != MR_BF16) || R < 0 || D < 1) return MR_ERR_INVALID;
+  if (D > MR_MAX_FEATURES) return MR_ERR_UNSUPPORTED;
+  if (R == 0) return MR_OK;
+  if (x == nullptr || q == nullptr || scales == nullptr) return MR_ERR_INVALID;
+  const QuantizeArgs a{x, q, scales, R, D, 0};
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // wide accesses: rows of x in whole aligned 16 bytes, those of q as many values' bytes
+  const uintptr_t wide = reinterpret_cast<uintptr_t>(x) |
+                         static_cast<uintptr_t>(D) * (dtype == MR_F32 ? 4 : 2);
+  const bool aligned = (wide & 15u) == 0 &&
+                       (reinterpret_cast<uintptr_t>(q) & (dtype == MR_F32 ? 3u : 7u)) == 0;
+  if (dtype == MR_F32)
+    return aligned ? launch_typed<DT_F32, 16>(a, st) : launch_typed<DT_F32, 4>(a, st);
+  return aligned           ? launch_typed<DT_BF16, 16>(a, st)
+         : (wide & 3u) == 0 ? launch_typed<DT_BF16, 4>(a, st)
+                            : launch_typed<DT_BF16, 2>(a, st);
+}

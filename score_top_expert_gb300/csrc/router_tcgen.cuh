@@ -210,6 +210,11 @@ __device__ __forceinline__ uint32_t product_desc(int m, int n, bool a_mn_major, 
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// Instruction descriptor of fp16 x fp16 -> fp32, both K-major.
+__device__ __forceinline__ uint32_t half_product_desc(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
 // D (+)= A B over 16 contraction indices; one thread.
 template <int CG>
 __device__ __forceinline__ void tc_product(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,

@@ -1,0 +1,27 @@
+// 8-bit integers as fp16, for the products on the 16-bit tensor cores.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+namespace moe_router {
+
+// Two signed bytes of u (offset by 128) as fp16: 1024 + byte by placing it in the low
+// mantissa bits, then 1152 less; both exact.
+__device__ __forceinline__ uint32_t widen_two(uint32_t u, uint32_t select) {
+  const uint32_t v = __byte_perm(u, 0x64646464u, select);
+  const uint32_t offset = 0x64806480u;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v),
+                            *reinterpret_cast<const __half2*>(&offset));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// Eight signed bytes in order.
+__device__ __forceinline__ uint4 widen_eight(uint32_t a, uint32_t b) {
+  a ^= 0x80808080u;
+  b ^= 0x80808080u;
+  return make_uint4(widen_two(a, 0x4140), widen_two(a, 0x4342), widen_two(b, 0x4140),
+                    widen_two(b, 0x4342));
+}
+
+}  // namespace moe_router

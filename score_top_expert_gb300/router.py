@@ -87,9 +87,26 @@ def lib() -> ctypes.CDLL:
         L.router_expert_matmul_w4.argtypes = [vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, vp, i, vp]
         L.router_combine_fwd.argtypes = [vp, i, vp, vp, i, i, i, i, vp, vp]
         L.router_combine_bwd.argtypes = [vp, i, vp, vp, vp, i, i, i, i, vp, vp, vp]
+        sz = ctypes.c_size_t
+        L.router_expert_matmul_w8.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, i, vp]
+        L.router_quantize_rows.argtypes = [vp, i, i, i, vp, vp, vp]
+        L.router_combine_norm_fwd.argtypes = [vp, i, vp, vp, i, vp, vp, vp, i, f, vp, f, i, i, i,
+                                              vp, vp, vp, vp, vp]
+        L.router_combine_norm_bwd_workspace_bytes.argtypes = [i, i]
+        L.router_combine_norm_bwd_workspace_bytes.restype = sz
+        L.router_combine_norm_bwd.argtypes = [vp, vp, i, vp, vp, vp, vp, vp, i, f, vp, i, i, vp,
+                                              vp, vp, vp, vp, vp, sz, vp]
+        L.router_balance_loss_workspace_bytes.argtypes = [i, i, i]
+        L.router_balance_loss_workspace_bytes.restype = sz
+        L.router_balance_loss_fwd.argtypes = [vp, i, vp, i, vp, i, i, i, i, i, f, f, vp, vp, vp,
+                                              vp, sz, vp]
+        L.router_balance_loss_bwd.argtypes = [vp, vp, i, vp, vp, vp, i, i, i, i, i, f, f, vp, vp]
         for fn in ("router_expert_matmul", "router_expert_matmul_bwd_input",
                    "router_expert_matmul_bwd_weight", "router_expert_matmul_w4",
-                   "router_combine_fwd", "router_combine_bwd"):
+                   "router_expert_matmul_w8", "router_quantize_rows",
+                   "router_combine_fwd", "router_combine_bwd", "router_combine_norm_fwd",
+                   "router_combine_norm_bwd", "router_balance_loss_fwd",
+                   "router_balance_loss_bwd"):
             getattr(L, fn).restype = ctypes.c_int
         L.moe_router_selftest_bounded_wait.restype = ctypes.c_int
         L.moe_router_strerror.argtypes = [i]
@@ -114,6 +131,12 @@ class _CtypesCalls:
         self.router_combine_bwd = L.router_combine_bwd
         self.router_expert_matmul_bwd_input = L.router_expert_matmul_bwd_input
         self.router_expert_matmul_bwd_weight = L.router_expert_matmul_bwd_weight
+        self.router_expert_matmul_w8 = L.router_expert_matmul_w8
+        self.router_quantize_rows = L.router_quantize_rows
+        self.router_combine_norm_fwd = L.router_combine_norm_fwd
+        self.router_combine_norm_bwd = L.router_combine_norm_bwd
+        self.router_balance_loss_fwd = L.router_balance_loss_fwd
+        self.router_balance_loss_bwd = L.router_balance_loss_bwd
 
 
 def _load_fast():
@@ -568,12 +591,94 @@ def router_aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor
     return grad_aux_scores
 
 
+def _sequences(seq_offsets, dev) -> tuple[int, int]:
+    """(S, pointer) of a packed batch's sequence offsets [S + 1]; None: one sequence."""
+    if seq_offsets is None:
+        return 1, 0
+    if seq_offsets.get_device() != dev.index or seq_offsets.dtype != torch.int32 \
+            or seq_offsets.dim() != 1 or seq_offsets.numel() < 2 \
+            or not seq_offsets.is_contiguous():
+        raise ValueError("seq_offsets must be a contiguous int32 [S + 1] tensor on the logits' "
+                         "device")
+    return seq_offsets.numel() - 1, seq_offsets.data_ptr()
+
+
+def router_balance_loss_fwd(logits: torch.Tensor, topk_indices: torch.Tensor,
+                            score_func: str = "softmax", coeff: float = 1.0, z_coeff: float = 0.0,
+                            seq_offsets: torch.Tensor | None = None, *, loss=None,
+                            tokens_per_expert=None, row_stats=None, workspace=None):
+    """Load-balancing loss of each sequence of a packed batch, and the z loss, from the
+    logits [T, E] and the choices [T, K] int32 (router_topk_fwd_compact's; a column
+    view of a wider buffer is read in place).  ``seq_offsets`` [S + 1] int32: sequence s
+    is tokens seq_offsets[s] .. seq_offsets[s + 1] - 1, other tokens are padding; None:
+    all tokens are one.  Returns (loss [2] float32: balance and z loss,
+    tokens_per_expert [S, E] int32, row_stats [T, 2] float32 for the backward).  The
+    workspace (a uint8 CUDA tensor) is allocated here when not given."""
+    logits = _as_input(logits, "logits", _DTYPE)
+    T, E = logits.shape
+    dev = logits.device
+    idx = topk_indices
+    if idx.get_device() != dev.index or idx.dtype != torch.int32 or idx.dim() != 2 \
+            or idx.shape[0] != T or idx.shape[1] < 1:
+        raise ValueError(f"topk_indices must be an int32 [{T}, K] tensor on the logits' device")
+    K = idx.shape[1]
+    if not idx.is_contiguous() and (idx.stride(1) != 1 or idx.stride(0) < K):
+        idx = idx.contiguous()
+    ld = K if idx.is_contiguous() else idx.stride(0)
+    S, seq_ptr = _sequences(seq_offsets, dev)
+    loss = _out(loss, (2,), torch.float32, dev, "loss")
+    tokens_per_expert = _out(tokens_per_expert, (S, E), torch.int32, dev, "tokens_per_expert")
+    row_stats = _out(row_stats, (T, 2), torch.float32, dev, "row_stats")
+    if workspace is None:
+        nbytes = lib().router_balance_loss_workspace_bytes(T, E, S)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev.index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the logits' device")
+    with _on(dev):
+        rc = _calls().router_balance_loss_fwd(
+            logits.data_ptr(), _DTYPE[logits.dtype], idx.data_ptr(), ld, seq_ptr, T, E, K, S,
+            _score(score_func), float(coeff), float(z_coeff), loss.data_ptr(),
+            tokens_per_expert.data_ptr(), row_stats.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream(dev))
+    _check("router_balance_loss_fwd", rc)
+    return loss, tokens_per_expert, row_stats
+
+
+def router_balance_loss_bwd(grad_loss: torch.Tensor, logits: torch.Tensor,
+                            tokens_per_expert: torch.Tensor, row_stats: torch.Tensor, K: int,
+                            score_func: str = "softmax", coeff: float = 1.0, z_coeff: float = 0.0,
+                            seq_offsets: torch.Tensor | None = None, *, grad_logits=None):
+    """Gradient of both losses by the logits, [T, E] in the logits' dtype; padding gets
+    zeros.  ``grad_loss`` [2] float32; the other arguments are the forward's."""
+    logits = _as_input(logits, "logits", _DTYPE)
+    T, E = logits.shape
+    dev = logits.device
+    S, seq_ptr = _sequences(seq_offsets, dev)
+    for t, name, shape, dt in ((grad_loss, "grad_loss", (2,), torch.float32),
+                               (tokens_per_expert, "tokens_per_expert", (S, E), torch.int32),
+                               (row_stats, "row_stats", (T, 2), torch.float32)):
+        if t.get_device() != dev.index or t.dtype != dt or t.shape != shape:
+            raise ValueError(f"{name} must be a {dt} tensor of shape {shape} on {dev}")
+    grad_loss, row_stats = grad_loss.contiguous(), row_stats.contiguous()
+    tokens_per_expert = tokens_per_expert.contiguous()
+    grad_logits = _out(grad_logits, (T, E), logits.dtype, dev, "grad_logits")
+    with _on(dev):
+        rc = _calls().router_balance_loss_bwd(
+            grad_loss.data_ptr(), logits.data_ptr(), _DTYPE[logits.dtype],
+            tokens_per_expert.data_ptr(), row_stats.data_ptr(), seq_ptr, T, E, int(K), S,
+            _score(score_func), float(coeff), float(z_coeff), grad_logits.data_ptr(),
+            _stream(dev))
+    _check("router_balance_loss_bwd", rc)
+    return grad_logits
+
+
 # ---- the experts' products and the combination ------------------------------
 # One token's calls take a few microseconds on the GPU, so the host's part is
 # written flat: every check reads tensor attributes directly, and the helpers
 # below run only to copy a strided input or to say what is wrong.  The two
 # gradients of the products, which no single token calls, keep _on and _check.
 _I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+_I8 = torch.int8
 _empty = torch.empty
 
 
@@ -811,6 +916,91 @@ def router_expert_matmul_w4(x: torch.Tensor, qweight: torch.Tensor, scales: torc
     return out
 
 
+def _vector(t: torch.Tensor, name: str, idx: int, n: int) -> torch.Tensor:
+    """A contiguous float32 [n] tensor on the call's device."""
+    if t.get_device() != idx or t.dtype is not _F32 or t.dim() != 1 or t.shape[0] != n:
+        _bad(name, f"a float32 [{n}] tensor on cuda:{idx}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def router_quantize_rows(x: torch.Tensor, *, out=None, scales=None):
+    """Rows of x [R, D] in 8-bit integers with a scale for each.  Returns (q [R, D]
+    int8, scales [R] float32): scales = max |x| / 127 of the row, q = x / scales to the
+    nearest integer, ties to even."""
+    dt, idx = x.dtype, x.get_device()
+    if idx < 0 or dt not in _DTYPE or x.dim() != 2 or not x.is_contiguous():
+        x = _rows_2d(x, "x", None, _DTYPE)
+    R, D = x.shape
+    if out is None:
+        out = _empty((R, D), dtype=_I8, device=x.device)
+    else:
+        out = _out(out, (R, D), _I8, x.device, "out")
+    if scales is None:
+        scales = _empty((R,), dtype=_F32, device=x.device)
+    else:
+        scales = _out(scales, (R,), _F32, x.device, "scales")
+    call = (_fast or _calls()).router_quantize_rows
+    with _on(idx):
+        rc = call(x.data_ptr(), _DTYPE[dt], R, D, out.data_ptr(), scales.data_ptr(),
+                  _raw_stream(idx))
+    if rc != 0:
+        raise RouterError("router_quantize_rows", rc)
+    return out, scales
+
+
+def router_expert_matmul_w8(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.Tensor,
+                            weight_scales: torch.Tensor, expert_first_token_offset: torch.Tensor,
+                            permuted_to_unpermuted: torch.Tensor | None = None, *, out=None,
+                            out_dtype: torch.dtype | None = None):
+    """router_expert_matmul on 8-bit integers: x [T or P, D] int8 with a scale for
+    each row (router_quantize_rows), weight [E, N, D] int8 with weight_scales [E, N].
+    Returns out [P, N] in ``out_dtype`` (default bf16): the products' exact integers
+    times both scales.  The maps are as in router_expert_matmul."""
+    idx = x.get_device()
+    if idx < 0 or x.dtype is not _I8 or x.dim() != 2 or not x.is_contiguous():
+        x = _rows_2d(x, "x", None, (_I8,))
+    if weight.get_device() != idx or weight.dtype is not _I8 or weight.dim() != 3 \
+            or not weight.is_contiguous():
+        _weight_3d(weight, "weight", idx, _I8)
+    E, N, D = weight.shape
+    T, cols = x.shape
+    if cols != D:
+        _bad("x", f"[rows, {D}]")
+    if x_scales.get_device() != idx or x_scales.dtype is not _F32 or x_scales.shape != (T,) \
+            or not x_scales.is_contiguous():
+        x_scales = _vector(x_scales, "x_scales", idx, T)
+    if weight_scales.get_device() != idx or weight_scales.dtype is not _F32 \
+            or weight_scales.shape != (E, N) or not weight_scales.is_contiguous():
+        _bad("weight_scales", f"a contiguous float32 [{E}, {N}] tensor on cuda:{idx}")
+    off = expert_first_token_offset
+    if off.get_device() != idx or off.dtype is not _I32 or off.numel() != E + 1 \
+            or off.dim() != 1 or not off.is_contiguous():
+        off = _map_1d(off, "expert_first_token_offset", idx, E + 1)
+    p2u = permuted_to_unpermuted
+    if p2u is None:
+        P, p2u_ptr = T, 0
+    else:
+        if p2u.get_device() != idx or p2u.dtype is not _I32 or p2u.dim() != 1 \
+                or not p2u.is_contiguous():
+            p2u = _map_1d(p2u, "permuted_to_unpermuted", idx, None)
+        P, p2u_ptr = p2u.numel(), p2u.data_ptr()
+    odt = _BF16 if out_dtype is None else out_dtype
+    if odt not in _DTYPE:
+        _bad("out_dtype", f"one of {list(_DTYPE)}")
+    if out is None:
+        out = _empty((P, N), dtype=odt, device=x.device)
+    else:
+        out = _out(out, (P, N), odt, x.device, "out")
+    call = (_fast or _calls()).router_expert_matmul_w8
+    with _on(idx):
+        rc = call(x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(),
+                  off.data_ptr(), p2u_ptr, T, P, E, N, D, out.data_ptr(), _DTYPE[odt],
+                  _raw_stream(idx))
+    if rc != 0:
+        raise RouterError("router_expert_matmul_w8", rc)
+    return out
+
+
 def _combine_weights(w: torch.Tensor, T: int, K: int, idx: int):
     """Checked combination weights and their row stride (a column view of a
     wider buffer is read in place)."""
@@ -915,3 +1105,179 @@ def router_combine_bwd(grad_out: torch.Tensor, unpermuted_to_permuted: torch.Ten
     if rc != 0:
         raise RouterError("router_combine_bwd", rc)
     return grad_expert_out, grad_weights
+
+
+# ---- the norms around an expert block ------------------------------------------
+_GATE_NONE, _GATE_TOKEN, _GATE_VALUE = 0, 1, 2
+
+
+def _gate(gate, T: int, D: int, dt, idx: int):
+    """(tensor or None, kind) of a block's gate: [T] float32, or [T, D] of the rows'
+    type."""
+    if gate is None:
+        return None, _GATE_NONE
+    if gate.get_device() == idx:
+        if gate.shape == (T,) and gate.dtype is _F32:
+            return gate if gate.is_contiguous() else gate.contiguous(), _GATE_TOKEN
+        if gate.shape == (T, D) and gate.dtype is dt:
+            return gate if gate.is_contiguous() else gate.contiguous(), _GATE_VALUE
+    _bad("gate", f"a float32 [{T}] or a {dt} [{T}, {D}] tensor on cuda:{idx}")
+
+
+def _same_rows(t: torch.Tensor, name: str, T: int, D: int, dt, idx: int) -> torch.Tensor:
+    """A [T, D] tensor of the call's type and device."""
+    if t.get_device() != idx or t.dtype is not dt or t.shape != (T, D):
+        _bad(name, f"a {dt} [{T}, {D}] tensor on cuda:{idx}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def router_combine_norm_fwd(expert_out: torch.Tensor, residual: torch.Tensor,
+                            unpermuted_to_permuted: torch.Tensor | None = None,
+                            topk_weights: torch.Tensor | None = None, *,
+                            post_weight: torch.Tensor | None = None,
+                            gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                            pre_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                            save: bool = False, sum=None, normed=None, block_out=None, rstd=None):
+    """The end of an expert block in one call: y, each token's weighted sum of its
+    experts' outputs (as router_combine_fwd; without a map expert_out [T, D] itself), the
+    RMS norm behind the block (``post_weight`` [D] float32), its gate ([T] float32 or
+    [T, D]), x = residual + residual_scale gate norm(y), and the RMS norm of x before the
+    next block (``pre_weight``).  Returns (x [T, D], normed [T, D] or None, y [T, D] or
+    None, rstd [T, 2] float32 or None); the last two, for the backward, with
+    ``save=True`` or when given."""
+    res = residual
+    idx, dt = res.get_device(), res.dtype
+    if idx < 0 or dt not in _DTYPE or res.dim() != 2 or not res.is_contiguous():
+        res = _rows_2d(res, "residual", None, _DTYPE)
+    T, D = res.shape
+    dev = res.device
+    z, u2p = expert_out, unpermuted_to_permuted
+    if z.get_device() != idx or z.dtype is not dt or z.dim() != 2 or z.shape[1] != D \
+            or not z.is_contiguous():
+        z = _rows_2d(z, "expert_out", idx, (dt,))
+        if z.shape[1] != D:
+            _bad("expert_out", f"[T K, {D}]")
+    P = z.shape[0]
+    K, u2p_ptr, w_ptr, ld = 1, 0, 0, 0
+    if u2p is not None:
+        if T > 0:
+            K = P // T
+        if K < 1 or P != T * K:
+            _bad("expert_out", f"[{T} K, {D}]")
+        if u2p.get_device() != idx or u2p.dtype is not _I32 or u2p.numel() != P \
+                or u2p.dim() != 1 or not u2p.is_contiguous():
+            u2p = _map_1d(u2p, "unpermuted_to_permuted", idx, P)
+        u2p_ptr = u2p.data_ptr()
+        if topk_weights is not None and T > 0:
+            topk_weights, ld = _combine_weights(topk_weights, T, K, idx)
+            w_ptr = topk_weights.data_ptr()
+    else:
+        if topk_weights is not None:
+            raise ValueError("topk_weights needs unpermuted_to_permuted")
+        if P != T:
+            _bad("expert_out", f"[{T}, {D}] without a map")
+    post_ptr = pre_ptr = normed_ptr = 0
+    if post_weight is not None:
+        post_weight = _vector(post_weight, "post_weight", idx, D)
+        post_ptr = post_weight.data_ptr()
+    gate, kind = _gate(gate, T, D, dt, idx)
+    if pre_weight is not None:
+        pre_weight = _vector(pre_weight, "pre_weight", idx, D)
+        pre_ptr = pre_weight.data_ptr()
+        normed = _out(normed, (T, D), dt, dev, "normed")
+        normed_ptr = normed.data_ptr()
+    elif normed is not None:
+        raise ValueError("normed needs pre_weight")
+    sum = _out(sum, (T, D), dt, dev, "sum")
+    if save or block_out is not None:
+        block_out = _out(block_out, (T, D), dt, dev, "block_out")
+    if save or rstd is not None:
+        rstd = _out(rstd, (T, 2), _F32, dev, "rstd")
+    with _on(idx):
+        rc = (_fast or _calls()).router_combine_norm_fwd(
+            z.data_ptr(), _DTYPE[dt], u2p_ptr, w_ptr, ld, res.data_ptr(), post_ptr, _ptr0(gate),
+            kind, float(residual_scale), pre_ptr, float(eps), T, K, D, sum.data_ptr(), normed_ptr,
+            _ptr0(block_out), _ptr0(rstd), _raw_stream(idx))
+    _check("router_combine_norm_fwd", rc)
+    return sum, normed, block_out, rstd
+
+
+def router_combine_norm_bwd(grad_sum: torch.Tensor | None, grad_normed: torch.Tensor | None,
+                            block_out: torch.Tensor | None, sum: torch.Tensor | None,
+                            rstd: torch.Tensor | None, *,
+                            post_weight: torch.Tensor | None = None,
+                            gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                            pre_weight: torch.Tensor | None = None, grad_block=None,
+                            grad_residual=None, grad_gate=None, grad_post_weight=None,
+                            grad_pre_weight=None, workspace=None):
+    """Gradients of router_combine_norm_fwd from those of x and of the normed rows
+    (``grad_sum`` may be None with a pre_weight): (grad_block [T, D], the gradient of y
+    and router_combine_bwd's grad_out; grad_residual [T, D]; grad_gate like the gate;
+    grad_post_weight and grad_pre_weight [D] float32), None for what the forward did
+    not have.  ``block_out``, ``sum`` and ``rstd`` are the forward's; without a
+    pre_weight ``sum`` and ``grad_normed`` are not read and may be None, block_out
+    neither without a post_weight and a gate.  The workspace (a uint8 CUDA tensor) is
+    allocated here when not given."""
+    rows = grad_sum if grad_sum is not None else grad_normed
+    if rows is None:
+        raise ValueError("grad_sum or grad_normed must be given")
+    idx, dt = rows.get_device(), rows.dtype
+    if idx < 0 or dt not in _DTYPE or rows.dim() != 2:
+        rows = _rows_2d(rows, "grad_sum", None, _DTYPE)
+    T, D = rows.shape
+    dev = rows.device
+    pre, post = pre_weight is not None, post_weight is not None
+    if grad_sum is not None:
+        grad_sum = _same_rows(grad_sum, "grad_sum", T, D, dt, idx)
+    elif not pre:
+        raise ValueError("grad_sum must be given without a pre_weight")
+    if pre:
+        if grad_normed is None or sum is None:
+            raise ValueError("pre_weight needs grad_normed and sum")
+        grad_normed = _same_rows(grad_normed, "grad_normed", T, D, dt, idx)
+        sum = _same_rows(sum, "sum", T, D, dt, idx)
+        pre_weight = _vector(pre_weight, "pre_weight", idx, D)
+        grad_pre_weight = _out(grad_pre_weight, (D,), _F32, dev, "grad_pre_weight")
+    else:
+        grad_normed = sum = grad_pre_weight = None
+    gate, kind = _gate(gate, T, D, dt, idx)
+    if post or kind:
+        if block_out is None:
+            raise ValueError("post_weight and a gate need block_out")
+        block_out = _same_rows(block_out, "block_out", T, D, dt, idx)
+    else:
+        block_out = None
+    if post:
+        post_weight = _vector(post_weight, "post_weight", idx, D)
+        grad_post_weight = _out(grad_post_weight, (D,), _F32, dev, "grad_post_weight")
+    else:
+        grad_post_weight = None
+    nbytes = 0
+    if pre or post:
+        if rstd is None or rstd.get_device() != idx or rstd.dtype is not _F32 \
+                or rstd.shape != (T, 2):
+            _bad("rstd", f"a float32 [{T}, 2] tensor on cuda:{idx}")
+        rstd = rstd.contiguous()
+        nbytes = lib().router_combine_norm_bwd_workspace_bytes(T, D)
+        if workspace is None:
+            workspace = _empty((max(nbytes, 16),), dtype=_U8, device=dev)
+        elif workspace.get_device() != idx or not workspace.is_contiguous():
+            _bad("workspace", f"a contiguous tensor on cuda:{idx}")
+        nbytes = workspace.numel() * workspace.element_size()
+    else:
+        rstd = workspace = None
+    if kind:
+        grad_gate = _out(grad_gate, tuple(gate.shape), gate.dtype, dev, "grad_gate")
+    else:
+        grad_gate = None
+    grad_block = _out(grad_block, (T, D), dt, dev, "grad_block")
+    grad_residual = _out(grad_residual, (T, D), dt, dev, "grad_residual")
+    with _on(idx):
+        rc = (_fast or _calls()).router_combine_norm_bwd(
+            _ptr0(grad_sum), _ptr0(grad_normed), _DTYPE[dt], _ptr0(block_out), _ptr0(sum),
+            _ptr0(rstd), _ptr0(post_weight), _ptr0(gate), kind, float(residual_scale),
+            _ptr0(pre_weight), T, D, grad_block.data_ptr(), grad_residual.data_ptr(),
+            _ptr0(grad_gate), _ptr0(grad_post_weight), _ptr0(grad_pre_weight), _ptr0(workspace),
+            nbytes, _raw_stream(idx))
+    _check("router_combine_norm_bwd", rc)
+    return grad_block, grad_residual, grad_gate, grad_post_weight, grad_pre_weight

@@ -24,10 +24,10 @@
 namespace moe_router {
 namespace {
 
-constexpr int kLoaders = 16;
-constexpr int kThreads = 32 * (8 + kLoaders);
-constexpr int kStages = 6;
-constexpr int kAhead = 4;
+constexpr int kLoaders = 8;  // warps that load a slice; two groups of them take alternate slices
+constexpr int kThreads = 32 * (8 + 2 * kLoaders);
+constexpr int kStages = 6;   // even: each belongs to one of the groups
+constexpr int kAhead = 2;    // slices of its group that a thread holds
 constexpr int kRowsA = 128;  // weight rows of a CTA
 constexpr int kRowsB = 128;  // most rows of x of a CTA
 constexpr int kBytesA = kRowsA * 128;
@@ -94,6 +94,14 @@ __device__ __forceinline__ void store_wide(uint32_t at, uint32_t a, uint32_t b) 
                "r"(v.w) : "memory");
 }
 
+// One word to the other CTA of the pair, which completes four bytes on its barrier.  The
+// barrier's phase is ordered behind what this thread has seen, as by an arrival with
+// release semantics of cluster scope, but the thread goes on at once.
+__device__ __forceinline__ void announce(uint32_t word, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
+               ::"r"(word), "r"(1u), "r"(bar) : "memory");
+}
+
 // Waits for data that the other CTA of the pair has published.
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -125,7 +133,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
   const TcArgs& g = args.t;
   extern __shared__ uint8_t dynamic_smem[];
   __shared__ __align__(8) uint64_t full[kStages], peer[kStages], empty[kStages], done[2], drained[2];
-  __shared__ uint32_t tmem_at;
+  __shared__ uint32_t tmem_at, heard;
   __shared__ int gave_up;
   __shared__ int tmp[33];
   __shared__ int prefix[MR_MAX_EXPERTS + 1];
@@ -164,55 +172,75 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
 
   if (warp >= 8) {
     // ---- loads -----------------------------------------------------------------
-    const int row = (static_cast<int>(threadIdx.x) - 256) >> 2, quarter = threadIdx.x & 3;
-    // the load cursor, kAhead slices ahead of the stores
-    int li = first, ls = 0;
-    const int8_t *pa = nullptr, *pb = nullptr;
-    int left_a = 0, left_b = 0;  // bytes of the row from this thread's piece on
-    bool wanted = false;         // the tile has this row of x (rounded up)
-    auto enter = [&]() {         // tile li
+    const int group = (warp - 8) / kLoaders;
+    const int row = ((static_cast<int>(threadIdx.x) - 256) & (32 * kLoaders - 1)) >> 2;
+    const int quarter = threadIdx.x & 3;
+    // the load cursor, kAhead slices of the group ahead of the stores; rows `row` and
+    // row + 64 of both operands
+    int li = first, ls = group;
+    const int8_t *pa[2] = {}, *pb[2] = {};
+    int left_a[2] = {}, left_b[2] = {};  // bytes of the row from this thread's piece on
+    uint32_t wanted = 0;                 // by row: the tile has it (rounded up)
+    auto enter = [&]() {                 // tile li, slice ls
       const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, li);
-      const int n = t.a0 + static_cast<int>(rank) * kRowsA + row;
-      pa = args.w + (static_cast<size_t>(t.e) * g.N + n) * g.D + quarter * 16;
-      left_a = n < g.N ? g.D - quarter * 16 : 0;
       const int half = (t.cnt + S::kRound - 1) / S::kRound * S::kRound / CG;
-      const int b = static_cast<int>(rank) * half + row;
-      wanted = row < half;
-      int source = -1;
-      if (wanted && b < t.cnt) {
-        source = g.p2u == nullptr ? t.start + b : g.p2u[t.start + b];
-        if (g.p2u != nullptr && source >= 0) source = token_of(g, source);
+      const int at = quarter * 16 + ls * kDeep;
+      wanted = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = row + 64 * h;
+        const int n = t.a0 + static_cast<int>(rank) * kRowsA + r;
+        pa[h] = args.w + (static_cast<size_t>(t.e) * g.N + n) * g.D + at;
+        left_a[h] = n < g.N ? g.D - at : 0;
+        const int b = static_cast<int>(rank) * half + r;
+        int source = -1;
+        if (r < half) {
+          wanted |= 1u << h;
+          if (b < t.cnt) source = g.p2u == nullptr ? t.start + b : g.p2u[t.start + b];
+          if (g.p2u != nullptr && source >= 0) source = token_of(g, source);
+        }
+        pb[h] = args.x + static_cast<size_t>(max(source, 0)) * g.D + at;
+        left_b[h] = source >= 0 ? g.D - at : 0;
       }
-      pb = args.x + static_cast<size_t>(max(source, 0)) * g.D + quarter * 16;
-      left_b = source >= 0 ? g.D - quarter * 16 : 0;
     };
-    uint4 a[kAhead], b[kAhead];
-    uint32_t valid = 0, keep = 0;  // by slot: holds a slice; its row of x is stored
+    auto skip_tiles = [&]() {  // to the tile that holds slice ls
+      bool moved = false;
+      while (ls >= slices && li < tiles) {
+        ls -= slices;
+        li += step;
+        moved = true;
+      }
+      if (moved && li < tiles) enter();
+    };
+    uint4 a[kAhead][2], b[kAhead][2];
+    uint32_t valid = 0, keep = 0;  // by slot: holds a slice; its rows of x are stored
     auto fetch = [&](int j) {
       if (li >= tiles) {
         valid &= ~(1u << j);
         return;
       }
       valid |= 1u << j;
-      keep = wanted ? keep | (1u << j) : keep & ~(1u << j);
-      a[j] = load_piece<VB>(pa, left_a);
-      b[j] = load_piece<VB>(pb, left_b);
-      pa += kDeep;
-      pb += kDeep;
-      left_a -= kDeep;
-      left_b -= kDeep;
-      if (++ls == slices) {
-        ls = 0;
-        li += step;
-        if (li < tiles) enter();
+      keep = (keep & ~(3u << (2 * j))) | (wanted << (2 * j));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        a[j][h] = load_piece<VB>(pa[h], left_a[h]);
+        b[j][h] = load_piece<VB>(pb[h], left_b[h]);
+        pa[h] += 2 * kDeep;
+        pb[h] += 2 * kDeep;
+        left_a[h] -= 2 * kDeep;
+        left_b[h] -= 2 * kDeep;
       }
+      ls += 2;
+      if (ls >= slices) skip_tiles();
     };
-    if (li < tiles) enter();
+    if (ls >= slices) skip_tiles();
+    else if (li < tiles) enter();
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) fetch(j);
-    int stage = 0;
+    int stage = group;
     uint32_t parity = 1;  // the first pass finds the stages empty
     // pieces 2 quarter and 2 quarter + 1 of the row's eight, in the 128-byte swizzle
+    // (the same in row + 64)
     const uint32_t to0 = row * 128 + (((2 * quarter) ^ (row & 7)) << 4);
     const uint32_t to1 = row * 128 + (((2 * quarter + 1) ^ (row & 7)) << 4);
     bool ok = true;
@@ -223,17 +251,21 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
         ok = __all_sync(0xffffffffu, wait(&empty[stage], parity));
         if (!ok) break;
         const uint32_t at = stages_at + stage * kStageBytes;
-        store_wide(at + to0, a[j].x, a[j].y);
-        store_wide(at + to1, a[j].z, a[j].w);
-        if (keep >> j & 1u) {
-          store_wide(at + kBytesA + to0, b[j].x, b[j].y);
-          store_wide(at + kBytesA + to1, b[j].z, b[j].w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          store_wide(at + h * 8192 + to0, a[j][h].x, a[j][h].y);
+          store_wide(at + h * 8192 + to1, a[j][h].z, a[j][h].w);
+          if (keep >> (2 * j + h) & 1u) {
+            store_wide(at + kBytesA + h * 8192 + to0, b[j][h].x, b[j][h].y);
+            store_wide(at + kBytesA + h * 8192 + to1, b[j][h].z, b[j][h].w);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[stage]);
-        if (++stage == kStages) {
-          stage = 0;
+        stage += 2;
+        if (stage >= kStages) {
+          stage = group;
           parity ^= 1;
         }
         fetch(j);
@@ -248,7 +280,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
       for (int s = 0; s < slices && ok; ++s) {
         ok = __all_sync(0xffffffffu, wait(&full[stage], parity));
         if (!ok) break;
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&peer[stage]), 0));
+        if (lane == 0)
+          announce(map_to_rank(smem_addr(&heard), 0), map_to_rank(smem_addr(&peer[stage]), 0));
         __syncwarp();
         if (++stage == kStages) {
           stage = 0;
@@ -261,6 +294,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
     uint32_t parity = 0;
     bool ok = true;
     const int segment = segment_of<F32>(slices);
+    if (CG == 2 && lane == 0)
+      for (int i = 0; i < kStages; ++i) mbar_expect_tx_cluster(smem_addr(&peer[i]), 4);
     for (int i = first; i < tiles && ok; i += step) {
       const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, i);
       const int cols = (t.cnt + S::kRound - 1) / S::kRound * S::kRound;
@@ -285,6 +320,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
 #pragma unroll
             for (int k = 0; k < kDeep / 16; ++k)
               tc_product<CG>(d, da + 2 * k, db + 2 * k, desc, s > s0 || k > 0);
+            if (CG == 2) mbar_expect_tx_cluster(smem_addr(&peer[stage]), 4);  // of its next phase
             tc_commit<CG>(&empty[stage]);
             if (s == end - 1) tc_commit<CG>(&done[buf]);
           }

@@ -10,12 +10,14 @@
 // while it stays below 2^24 (and off by about 2^-30 of its value a term above that).
 //
 // The tiles and their order are those of router_experts_tc.cu's forward: 128 or 256 weight
-// rows by up to 128 or 256 of the expert's rows, one CTA or a pair.  Sixteen warps load: a
-// thread one 16-byte piece of a weight row and one of a row of x for each slice of 64
-// columns, kAhead slices ahead of the one that it widens and stores in the layout that the
-// tensor cores read.  In a pair each CTA's loading warps arrive on its own barrier and
-// one warp of the second CTA passes that on to the leader's: an arrival across the pair
-// costs the arriving warp hundreds of cycles.
+// rows by up to 128 or 256 of the expert's rows, one CTA or a pair.  Sixteen warps load
+// stages of 128 columns: eight lanes a row (whole lines: a request of 64-byte pieces took 11
+// wavefronts of the load pipe, the products' stages with it 1.4 times as long), two rows of
+// both operands a thread, kAhead stages ahead of the one that it widens and stores in the
+// layout that the tensor cores read.  In a pair each CTA's loading warps arrive on its own
+// barrier and one warp of the second CTA passes that on to the leader's by an
+// asynchronous store: an arrival with release semantics of cluster scope held it for about
+// 1500 cycles a stage.
 #include <atomic>
 
 #include "router_experts_tiles.cuh"
@@ -24,14 +26,17 @@
 namespace moe_router {
 namespace {
 
-constexpr int kLoaders = 8;  // warps that load a slice; two groups of them take alternate slices
-constexpr int kThreads = 32 * (8 + 2 * kLoaders);
-constexpr int kStages = 6;   // even: each belongs to one of the groups
-constexpr int kAhead = 2;    // slices of its group that a thread holds
+constexpr int kLoaders = 16;
+constexpr int kThreads = 32 * (8 + kLoaders);
+constexpr int kStages = 3;
+constexpr int kWide = 128;   // columns of a stage: two of the layout's 128-byte rows in fp16
+constexpr int kAhead = 2;    // stages that a thread holds
+constexpr int kMostStages = 7;  // of a fp32 output's sum
 constexpr int kRowsA = 128;  // weight rows of a CTA
 constexpr int kRowsB = 128;  // most rows of x of a CTA
-constexpr int kBytesA = kRowsA * 128;
-constexpr int kBytesB = kRowsB * 128;
+constexpr int kHalf = 128 * 128;  // 64 columns of an operand
+constexpr int kBytesA = 2 * kHalf;
+constexpr int kBytesB = 2 * kHalf;
 constexpr int kStageBytes = kBytesA + kBytesB;
 constexpr int kSmem = kStages * kStageBytes + 1024;  // stages start on 1024 bytes
 
@@ -168,23 +173,22 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
   const uint32_t tmem = tmem_at;
   const Waiter wait{&gave_up, g.status};
   const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
-  const int slices = (g.D + kDeep - 1) / kDeep;
+  const int slices = (g.D + kWide - 1) / kWide;
 
   if (warp >= 8) {
     // ---- loads -----------------------------------------------------------------
-    const int group = (warp - 8) / kLoaders;
-    const int row = ((static_cast<int>(threadIdx.x) - 256) & (32 * kLoaders - 1)) >> 2;
-    const int quarter = threadIdx.x & 3;
-    // the load cursor, kAhead slices of the group ahead of the stores; rows `row` and
-    // row + 64 of both operands
-    int li = first, ls = group;
+    const int row = (static_cast<int>(threadIdx.x) - 256) >> 3;
+    const int piece = threadIdx.x & 7;  // of the eight of a row and stage
+    // the load cursor, kAhead stages ahead of the stores; rows `row` and row + 64 of both
+    // operands
+    int li = first, ls = 0;
     const int8_t *pa[2] = {}, *pb[2] = {};
     int left_a[2] = {}, left_b[2] = {};  // bytes of the row from this thread's piece on
     uint32_t wanted = 0;                 // by row: the tile has it (rounded up)
-    auto enter = [&]() {                 // tile li, slice ls
+    auto enter = [&]() {                 // tile li
       const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, li);
       const int half = (t.cnt + S::kRound - 1) / S::kRound * S::kRound / CG;
-      const int at = quarter * 16 + ls * kDeep;
+      const int at = piece * 16;
       wanted = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -203,15 +207,6 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
         left_b[h] = source >= 0 ? g.D - at : 0;
       }
     };
-    auto skip_tiles = [&]() {  // to the tile that holds slice ls
-      bool moved = false;
-      while (ls >= slices && li < tiles) {
-        ls -= slices;
-        li += step;
-        moved = true;
-      }
-      if (moved && li < tiles) enter();
-    };
     uint4 a[kAhead][2], b[kAhead][2];
     uint32_t valid = 0, keep = 0;  // by slot: holds a slice; its rows of x are stored
     auto fetch = [&](int j) {
@@ -225,24 +220,34 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
       for (int h = 0; h < 2; ++h) {
         a[j][h] = load_piece<VB>(pa[h], left_a[h]);
         b[j][h] = load_piece<VB>(pb[h], left_b[h]);
-        pa[h] += 2 * kDeep;
-        pb[h] += 2 * kDeep;
-        left_a[h] -= 2 * kDeep;
-        left_b[h] -= 2 * kDeep;
+        pa[h] += kWide;
+        pb[h] += kWide;
+        left_a[h] -= kWide;
+        left_b[h] -= kWide;
       }
-      ls += 2;
-      if (ls >= slices) skip_tiles();
+      if (++ls == slices) {
+        ls = 0;
+        li += step;
+        if (li < tiles) enter();
+      }
     };
-    if (ls >= slices) skip_tiles();
-    else if (li < tiles) enter();
+    if (li < tiles) enter();
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) fetch(j);
-    int stage = group;
+    int stage = 0;
     uint32_t parity = 1;  // the first pass finds the stages empty
-    // pieces 2 quarter and 2 quarter + 1 of the row's eight, in the 128-byte swizzle
-    // (the same in row + 64)
-    const uint32_t to0 = row * 128 + (((2 * quarter) ^ (row & 7)) << 4);
-    const uint32_t to1 = row * 128 + (((2 * quarter + 1) ^ (row & 7)) << 4);
+    // The piece is two of the eight in a row of the 128-byte swizzle, row + 64 alike.  The
+    // lanes of a row's second half store the second first: the eight of a row then meet
+    // all banks.
+    const uint32_t half_at = row * 128 + (piece >> 2) * kHalf;
+    const uint32_t even = half_at + ((((2 * piece) & 7) ^ (row & 7)) << 4);
+    const uint32_t odd = half_at + ((((2 * piece + 1) & 7) ^ (row & 7)) << 4);
+    const bool swap = piece >= 4;
+    const uint32_t to0 = swap ? odd : even, to1 = swap ? even : odd;
+    auto store_piece = [&](uint32_t at, const uint4& v) {
+      store_wide(at + to0, swap ? v.z : v.x, swap ? v.w : v.y);
+      store_wide(at + to1, swap ? v.x : v.z, swap ? v.y : v.w);
+    };
     bool ok = true;
     while (ok && valid != 0) {
 #pragma unroll
@@ -253,19 +258,14 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
         const uint32_t at = stages_at + stage * kStageBytes;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          store_wide(at + h * 8192 + to0, a[j][h].x, a[j][h].y);
-          store_wide(at + h * 8192 + to1, a[j][h].z, a[j][h].w);
-          if (keep >> (2 * j + h) & 1u) {
-            store_wide(at + kBytesA + h * 8192 + to0, b[j][h].x, b[j][h].y);
-            store_wide(at + kBytesA + h * 8192 + to1, b[j][h].z, b[j][h].w);
-          }
+          store_piece(at + h * 8192, a[j][h]);
+          if (keep >> (2 * j + h) & 1u) store_piece(at + kBytesA + h * 8192, b[j][h]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[stage]);
-        stage += 2;
-        if (stage >= kStages) {
-          stage = group;
+        if (++stage == kStages) {
+          stage = 0;
           parity ^= 1;
         }
         fetch(j);
@@ -293,7 +293,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
     int stage = 0, n = 0;  // n: accumulators filled
     uint32_t parity = 0;
     bool ok = true;
-    const int segment = segment_of<F32>(slices);
+    const int segment = segment_of<F32>(slices, kMostStages);
     if (CG == 2 && lane == 0)
       for (int i = 0; i < kStages; ++i) mbar_expect_tx_cluster(smem_addr(&peer[i]), 4);
     for (int i = first; i < tiles && ok; i += step) {
@@ -318,8 +318,11 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
           const uint64_t db = operand_desc(at + kBytesA, 0, 1024);
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kDeep / 16; ++k)
-              tc_product<CG>(d, da + 2 * k, db + 2 * k, desc, s > s0 || k > 0);
+            for (int k = 0; k < kWide / 16; ++k) {
+              const uint64_t by = (k >> 2) * (kHalf >> 4) + (k & 3) * 2;
+              if (16 * k < g.D - s * kWide)
+                tc_product<CG>(d, da + by, db + by, desc, s > s0 || k > 0);
+            }
             if (CG == 2) mbar_expect_tx_cluster(smem_addr(&peer[stage]), 4);  // of its next phase
             tc_commit<CG>(&empty[stage]);
             if (s == end - 1) tc_commit<CG>(&done[buf]);
@@ -338,7 +341,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
     const int quad = warp - 4;
     int n = 0;
     bool ok = true;
-    const int segment = segment_of<F32>(slices);
+    const int segment = segment_of<F32>(slices, kMostStages);
     for (int i = first; i < tiles && ok; i += step) {
       const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, i);
       // the rows' scales, while the tile is computed; each warp its own copy, so that one

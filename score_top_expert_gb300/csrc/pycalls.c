@@ -242,6 +242,22 @@ static PyObject* call_balance_loss_bwd(PyObject* self, PyObject* const* args, Py
   return PyLong_FromLong(rc);
 }
 
+static PyObject* call_balance_loss_workspace(PyObject* self, PyObject* const* args,
+                                             Py_ssize_t nargs) {
+  int T, E, S;
+  void* out[] = {&T, &E, &S};
+  if (convert(args, nargs, "iii", out) != 0) return NULL;
+  return PyLong_FromSize_t(router_balance_loss_workspace_bytes(T, E, S));
+}
+
+static PyObject* call_combine_norm_bwd_workspace(PyObject* self, PyObject* const* args,
+                                                 Py_ssize_t nargs) {
+  int T, D;
+  void* out[] = {&T, &D};
+  if (convert(args, nargs, "ii", out) != 0) return NULL;
+  return PyLong_FromSize_t(router_combine_norm_bwd_workspace_bytes(T, D));
+}
+
 static PyMethodDef kMethods[] = {
     {"router_topk_fwd", (PyCFunction)(void (*)(void))call_topk_fwd, METH_FASTCALL,
      "router_topk_fwd(logits, dtype, T, E, K, score_func, num_groups, group_topk, "
@@ -301,6 +317,12 @@ static PyMethodDef kMethods[] = {
      METH_FASTCALL,
      "router_balance_loss_bwd(grad_loss, logits, dtype, tokens_per_expert, row_stats, "
      "seq_offsets, T, E, K, S, score_func, coeff, z_coeff, grad_logits, stream) -> status"},
+    {"router_balance_loss_workspace_bytes",
+     (PyCFunction)(void (*)(void))call_balance_loss_workspace, METH_FASTCALL,
+     "router_balance_loss_workspace_bytes(T, E, S) -> bytes"},
+    {"router_combine_norm_bwd_workspace_bytes",
+     (PyCFunction)(void (*)(void))call_combine_norm_bwd_workspace, METH_FASTCALL,
+     "router_combine_norm_bwd_workspace_bytes(T, D) -> bytes"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pycalls",

@@ -13,28 +13,36 @@
 // the logits and writes the gradient; no [T, E] score, map or score gradient exists.
 //
 // Forward: a block takes a contiguous range of tokens, a team of 1 to 6 warps a row at a
-// time.  A lane holds up to 16 logits, the next row's loads in flight, and the column
+// time.  A lane holds up to 16 logits, the next rows on their way, and the column
 // sums of q of the rows that its team has seen; so a block leaves one row of column sums and
 // one of counts for each sequence that its range touches ("slot": block + sequence,
 // which rises by one or more from each to the next, so no two share one).  A
-// second kernel adds a sequence's slots up in order and ends the loss in 64 bits; the last block
-// to finish adds the blocks' shares.  No floating-point atomics: repeated calls
+// second kernel adds a sequence's slots up in order; its last block to finish adds the
+// blocks' shares.  No floating-point atomics: repeated calls
 // give the same bits.
 //
 // Backward: the same ranges; a team keeps its sequence's counts in registers.  They
 // enter as c_sj - K n_s / E: a constant less changes nothing, since q sums to one,
 // and leaves the difference c_sj - sum c q without the cancellation of two large numbers.
+#include <atomic>
 #include <climits>
 
 #include "router_common.cuh"
 #include "router_experts.cuh"
+#include "router_launch.cuh"
+#include "router_rows.cuh"
 
 namespace moe_router {
 namespace {
 
 constexpr int kTeamWarps = 8;      // warps of a block whose rows take one warp each
-constexpr int kFinishThreads = 512;
-constexpr int kFinishGroups = kFinishThreads / 32;
+constexpr int kRing = 4;           // rows of a team under way
+constexpr int kFinishThreads = 1024;
+constexpr int kFinishGroups = kFinishThreads / 32;  // 32: a warp adds them up
+
+__host__ __device__ constexpr int ring_bytes(bool vec, int nv, int threads, int bytes) {
+  return vec ? kRing * nv * threads * bytes : 0;
+}
 
 struct BalanceArgs {
   const void* logits;
@@ -46,7 +54,7 @@ struct BalanceArgs {
   float* slot_sums;           // [blocks + S, E]
   int32_t* slot_counts;       // [blocks + S, E]
   float* z_parts;             // [blocks]
-  double* parts;              // [finish blocks]
+  float* parts;               // [finish blocks]
   int* ticket;
   const float* grad_loss;     // [2]
   void* grad;                 // [T, E]
@@ -86,6 +94,13 @@ __device__ __forceinline__ int first_sequence(const BalanceArgs& a, int t) {
   return lo;
 }
 
+// Largest of a warp's values, in one instruction.
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
 // Threads of a team of `warps` warps.
 __device__ __forceinline__ void team_sync(int team, int warps) {
   if (warps > 1)
@@ -97,24 +112,16 @@ struct Team {
   float* xch;  // [2][teams * warps][2]
   int flip;
 
-  // Both values summed over the team's warps, in the same order in each.  Two
+  // A value summed over the team's warps (at most eight), in the same order in each.  Two
   // sets of cells in turn, so that one barrier a row is enough.
-  __device__ __forceinline__ void sum2(float* x, float* y) {
-    if (warps == 1) return;
+  __device__ __forceinline__ float sum(float x) {
+    if (warps == 1) return x;
     float* const mine = xch + (flip * teams + team) * warps * 2;
     flip ^= 1;
-    if (lane == 0) {
-      mine[2 * warp] = *x;
-      mine[2 * warp + 1] = *y;
-    }
+    if (lane == 0) mine[warp] = x;
     team_sync(team, warps);
-    float a = 0.0f, b = 0.0f;
-    for (int w = 0; w < warps; ++w) {
-      a += mine[2 * w];
-      b += mine[2 * w + 1];
-    }
-    *x = a;
-    *y = b;
+    const int w = lane & 7;
+    return seg_sum<8>(w < warps ? mine[w] : 0.0f);
   }
 
   // Maxima and sums of exponentials relative to them, of the team's warps, as one.
@@ -127,13 +134,13 @@ struct Team {
       mine[2 * warp + 1] = *s;
     }
     team_sync(team, warps);
-    float top = mine[0];
-    for (int w = 1; w < warps; ++w) top = fmaxf(top, mine[2 * w]);
-    float total = 0.0f;
-    for (int w = 0; w < warps; ++w)
-      total = fmaf(mine[2 * w + 1], ex2_approx((mine[2 * w] - top) * kLog2e), total);
+    const int w = lane & 7;
+    const bool in = w < warps;
+    const float own = in ? mine[2 * w] : -INFINITY;
+    const float top = warp_max(own);
+    const float part = in ? mine[2 * w + 1] * ex2_approx((own - top) * kLog2e) : 0.0f;
     *m = top;
-    *s = total;
+    *s = seg_sum<8>(part);
   }
 };
 
@@ -171,22 +178,112 @@ __device__ __forceinline__ void load_row(const BalanceArgs& a, const Team& t, in
   }
 }
 
-// Of the columns from c, is u one of the row's?
-template <bool VEC>
-__device__ __forceinline__ bool inside(int c, int u, int E) {
-  return VEC ? c < E : c + u < E;
+// Columns outside the row as minus infinity: their exponentials and sigmoids are zero and
+// no maximum is theirs.
+template <bool VEC, int NV>
+__device__ __forceinline__ void blank_outside(const Team& t, int E, Row<NV>* r) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = column_of(t, j);
+    if (VEC ? c >= E : c + 4 > E) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (VEC || c + u >= E) r->v[j][u] = -INFINITY;
+    }
+  }
 }
+
+// The rows of a piece of the block's range on their way to the team, through places in
+// shared memory that belong to the thread: the thread waits for its own copies, no
+// barrier is needed, and kRing rows are under way where registers held one.  (Rows that are not
+// aligned are loaded when they are needed.)
+template <int DT, bool VEC, int NV>
+struct RowRing {
+  static constexpr int kBytes = DT == DT_F32 ? 16 : 8;  // of four logits
+  uint32_t base, end;     // the thread's first place, and behind its last row's
+  uint32_t taken, asked;  // places of the next row to take and to ask for
+  const uint8_t* from;    // the thread's first four logits of the latter
+  size_t stride;          // from one row of the team to the next, in bytes
+  int row, hi;            // the latter's number
+
+  __device__ __forceinline__ uint32_t width() const { return blockDim.x * kBytes; }
+
+  __device__ __forceinline__ void init(const BalanceArgs& a, const Team& t, void* smem) {
+    base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kBytes;
+    end = base + kRing * NV * width();
+    stride = static_cast<size_t>(t.teams) * a.E * (kBytes / 4);
+  }
+
+  __device__ __forceinline__ void request(const BalanceArgs& a, const Team& t) {
+    if constexpr (VEC) {
+      if (row < hi) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (column_of(t, j) < a.E)
+            copy_async<kBytes>(asked + j * width(), from + j * t.warps * (32 * kBytes));
+      }
+      row += t.teams;
+      from += stride;
+      asked += NV * width();
+      if (asked == end) asked = base;
+      copies_commit_group();
+    }
+  }
+
+  __device__ __forceinline__ void begin(const BalanceArgs& a, const Team& t, int lo, int stop) {
+    row = lo + t.team;
+    hi = stop;
+    from = static_cast<const uint8_t*>(a.logits) +
+           (static_cast<size_t>(row) * a.E + column_of(t, 0)) * (kBytes / 4);
+    taken = asked = base;
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) request(a, t);
+  }
+
+  // Row `at_row`, the next in the team's order.
+  __device__ __forceinline__ void take(const BalanceArgs& a, const Team& t, int at_row, Row<NV>* r) {
+    if constexpr (VEC) {
+      request(a, t);
+      copies_wait_group(kRing - 1);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t at = taken + j * width();
+        if constexpr (DT == DT_F32) {
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(r->v[j][0]), "=f"(r->v[j][1]), "=f"(r->v[j][2]), "=f"(r->v[j][3])
+                       : "r"(at) : "memory");
+        } else {
+          uint32_t x, y;
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(at) : "memory");
+          r->v[j][0] = __uint_as_float(x << 16);
+          r->v[j][1] = __uint_as_float(x & 0xffff0000u);
+          r->v[j][2] = __uint_as_float(y << 16);
+          r->v[j][3] = __uint_as_float(y & 0xffff0000u);
+        }
+      }
+      taken += NV * width();
+      if (taken == end) taken = base;
+    } else {
+      load_row<DT, false>(a, t, at_row, r);
+    }
+    blank_outside<VEC>(t, a.E, r);
+  }
+};
 
 template <int DT, bool VEC, int NV, int SF>
 __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const BalanceArgs a,
                                                                          int warps) {
-  extern __shared__ float dynamic[];  // teams > 1: [teams, E] column sums; then [E] counts
+  // the rows under way; teams > 1: [teams, E] column sums; then [E] counts
+  extern __shared__ __align__(16) float dynamic_smem[];
   __shared__ float xch[2 * kTeamWarps * 2];
   __shared__ float z_warp[kTeamWarps];
   __shared__ int first_s;
   pdl_enter();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   Team t = make_team(warps, xch);
+  RowRing<DT, VEC, NV> ring;
+  ring.init(a, t, dynamic_smem);
+  float* const dynamic = dynamic_smem + ring_bytes(VEC, NV, blockDim.x, ring.kBytes) / 4;
   int* const hist = reinterpret_cast<int*>(dynamic + (t.teams > 1 ? t.teams * a.E : 0));
   const int t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
   if (threadIdx.x < 32) {
@@ -195,7 +292,7 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const B
   }
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
   __syncthreads();
-  const bool want_lse = SF == SF_SOFTMAX || a.z_coeff != 0.0f;
+  const bool want_z = a.z_coeff != 0.0f;
   float z = 0.0f;
   for (int s = first_s, p = t0; s < a.S && p < t1; ++s) {
     int lo, hi;
@@ -205,72 +302,81 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const B
     if (lo >= t1) break;
     if (hi <= lo) continue;
     p = hi;
+    ring.begin(a, t, lo, hi);
     // ---- counts: the choices of the range's tokens -----------------------------------
-    for (int i = threadIdx.x; i < (hi - lo) * a.K; i += blockDim.x) {
-      const int row = i / a.K;
-      const int e = a.choices[(lo + row) * a.ld_choices + (i - row * a.K)];
-      if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(hist + e, 1);
+    const int32_t* const from = a.choices + lo * a.ld_choices;
+    const int n = (hi - lo) * a.K;
+    if (a.ld_choices == a.K) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int e = from[i];
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(hist + e, 1);
+      }
+    } else {
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int row = i / a.K;
+        const int e = from[row * a.ld_choices + (i - row * a.K)];
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(hist + e, 1);
+      }
     }
     // ---- column sums of q --------------------------------------------------------------
-    Row<NV> sums{}, next;
-    int row = lo + t.team;
-    if (row < hi) load_row<DT, VEC>(a, t, row, &next);
-    for (; row < hi; row += t.teams) {
-      Row<NV> r = next;
-      if (row + t.teams < hi) load_row<DT, VEC>(a, t, row + t.teams, &next);
-      float top = -INFINITY, total = 0.0f, lse = 0.0f, factor;
-      if (want_lse) {
+    Row<NV> sums{};
+    for (int row = lo + t.team; row < hi; row += t.teams) {
+      Row<NV> r;
+      ring.take(a, t, row, &r);
+      float top = -INFINITY, total = 0.0f, factor;
+      if (SF == SF_SOFTMAX || want_z) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (inside<VEC>(column_of(t, j), u, a.E)) top = fmaxf(top, r.v[j][u]);
-        top = seg_max<32>(top);
+          for (int u = 0; u < 4; ++u) top = fmaxf(top, r.v[j][u]);
+        top = warp_max(top);
       }
+      // (a warp without columns: its maximum is minus infinity, its sum zero)
+      const float own = top, shift = top == -INFINITY ? 0.0f : top * kLog2e;
       if constexpr (SF == SF_SOFTMAX) {
-        const float own = top;  // the warp's; a warp without columns adds zeros to the sum
-        const float shift = own == -INFINITY ? 0.0f : own * kLog2e;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const bool in = inside<VEC>(column_of(t, j), u, a.E);
-            r.v[j][u] = in ? exp_shifted(r.v[j][u], shift) : 0.0f;
+            r.v[j][u] = exp_shifted(r.v[j][u], shift);
             total += r.v[j][u];
           }
         total = seg_sum<32>(total);
         t.softmax_stats(&top, &total);
-        lse = top + logf(total);
-        factor = t.warps == 1 ? __fdiv_rn(1.0f, total)
-                              : __fdiv_rn(ex2_approx((own - top) * kLog2e), total);
-        if (t.warp == 0 && t.lane == 0) a.stats[row] = make_float2(top, total);
+        factor = rcp_approx(total);
+        if (t.warps > 1) factor *= ex2_approx((own - top) * kLog2e);
+        if (t.warp == 0) {
+          if (want_z) {
+            const float lse = top + logf(total);
+            z = fmaf(lse, lse, z);
+          }
+          if (t.lane == 0) a.stats[row] = make_float2(top, total);
+        }
       } else {
-        if (want_lse) {
-          const float shift = top == -INFINITY ? 0.0f : top * kLog2e;
+        float lse = 0.0f;
+        if (want_z) {
 #pragma unroll
           for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              if (inside<VEC>(column_of(t, j), u, a.E)) total += exp_shifted(r.v[j][u], shift);
+            for (int u = 0; u < 4; ++u) total += exp_shifted(r.v[j][u], shift);
           total = seg_sum<32>(total);
           t.softmax_stats(&top, &total);
           lse = top + logf(total);
+          z = fmaf(lse, lse, z);
         }
-        float norm = 0.0f, unused = 0.0f;
+        float norm = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const bool in = inside<VEC>(column_of(t, j), u, a.E);
-            r.v[j][u] = in ? sigmoid_f32(r.v[j][u]) : 0.0f;
+            r.v[j][u] = sigmoid_f32(r.v[j][u]);
             norm += r.v[j][u];
           }
-        norm = seg_sum<32>(norm);
-        t.sum2(&norm, &unused);
-        factor = __fdiv_rn(1.0f, norm);
+        norm = t.sum(seg_sum<32>(norm));
+        factor = rcp_approx(norm);
         if (t.warp == 0 && t.lane == 0) a.stats[row] = make_float2(norm, lse);
       }
-      z = fmaf(lse, lse, z);
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -324,14 +430,14 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const B
 __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(const BalanceArgs a) {
   __shared__ float sums[kFinishGroups][128];
   __shared__ int counts[kFinishGroups][128];
-  __shared__ double shared[kFinishThreads / 32];
+  __shared__ float shared[2][kFinishGroups];
   __shared__ int last;
   pdl_enter();
   const int tiles = (a.E + 127) / 128;
   const long long items = static_cast<long long>(tiles) * a.S;
   const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
   const bool vec = (a.E & 3) == 0;
-  double share = 0.0;
+  float share = 0.0f;
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
     const int s = static_cast<int>(item / tiles);
     const int c = static_cast<int>(item - static_cast<long long>(s) * tiles) * 128 + 4 * lane;
@@ -341,7 +447,7 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(const Ba
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int n[4] = {0, 0, 0, 0};
     if (vec && c < a.E) {
-#pragma unroll 4
+#pragma unroll 8
       for (int b = b0 + group; b <= b1; b += kFinishGroups) {
         const size_t at = (static_cast<size_t>(b) + s) * a.E + c;
         const float4 x = __ldcg(reinterpret_cast<const float4*>(a.slot_sums + at));
@@ -377,50 +483,59 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(const Ba
         k += counts[g][threadIdx.x];
       }
       a.counts[static_cast<size_t>(s) * a.E + e] = k;
-      const double tokens = hi - lo;
-      if (hi > lo)
-        share += static_cast<double>(k) * p * (a.E / (a.K * tokens * tokens));
+      // c_se P_se / n_s^2 (the factors that all share come last)
+      const float by_tokens = 1.0f / static_cast<float>(max(hi - lo, 1));
+      share = fmaf(static_cast<float>(k) * by_tokens, p * by_tokens, share);
     }
     __syncthreads();
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) share += __shfl_xor_sync(0xffffffffu, share, o);
-  if (lane == 0) shared[group] = share;
+  share = seg_sum<32>(share);
+  if (lane == 0) shared[0][group] = share;
   __syncthreads();
   if (threadIdx.x == 0) {
-    double v = 0.0;
-    for (int w = 0; w < 4; ++w) v += shared[w];  // threads 0 .. 127 have the shares
-    a.parts[blockIdx.x] = v;
+    // threads 0 .. 127 have the shares
+    a.parts[blockIdx.x] = (shared[0][0] + shared[0][1]) + (shared[0][2] + shared[0][3]);
     __threadfence();
     last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
   }
   __syncthreads();
-  if (!last || threadIdx.x >= 32) return;
+  if (!last) return;
   __threadfence();
-  double balance = 0.0, z = 0.0;
-  for (int b = lane; b < static_cast<int>(gridDim.x); b += 32) balance += __ldcg(a.parts + b);
-  for (int b = lane; b < a.blocks; b += 32) z += __ldcg(a.z_parts + b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    balance += __shfl_xor_sync(0xffffffffu, balance, o);
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-  }
+  // the blocks' shares and the ranges' z: each thread its own few, then in a fixed order
+  float balance = 0.0f, z = 0.0f;
+  for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += kFinishThreads)
+    balance += __ldcg(a.parts + b);
+  for (int b = threadIdx.x; b < a.blocks; b += kFinishThreads) z += __ldcg(a.z_parts + b);
+  balance = seg_sum<32>(balance);
+  z = seg_sum<32>(z);
   if (lane == 0) {
+    shared[0][group] = balance;
+    shared[1][group] = z;
+  }
+  __syncthreads();
+  if (group == 0) {
+    balance = seg_sum<32>(shared[0][lane]);
+    z = seg_sum<32>(shared[1][lane]);
     int lo, hi, unused;
     sequence_range(a, 0, &lo, &unused);
     sequence_range(a, a.S - 1, &unused, &hi);
-    a.loss[0] = static_cast<float>(balance * a.coeff / a.S);
-    a.loss[1] = a.z_coeff == 0.0f ? 0.0f : static_cast<float>(z * a.z_coeff / max(hi - lo, 1));
+    if (lane == 0) {
+      a.loss[0] = balance * (a.coeff * a.E / a.K / a.S);
+      a.loss[1] = a.z_coeff == 0.0f ? 0.0f : z * (a.z_coeff / max(hi - lo, 1));
+    }
   }
 }
 
 template <int DT, bool VEC, int NV, int SF>
 __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_bwd_kernel(const BalanceArgs a,
                                                                          int warps) {
+  extern __shared__ __align__(16) float dynamic_smem[];  // the rows under way
   __shared__ float xch[2 * kTeamWarps * 2];
   __shared__ int first_s;
   pdl_enter();
   Team t = make_team(warps, xch);
+  RowRing<DT, VEC, NV> ring;
+  ring.init(a, t, dynamic_smem);
   const int t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
   if (threadIdx.x < 32) {
     const int s = first_sequence(a, t0);
@@ -458,7 +573,8 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_bwd_kernel(const B
     p = hi;
     const float scale = by_balance * (static_cast<float>(a.E) / a.K) / tokens / tokens;
     const float mean = tokens * a.K / a.E;
-    Row<NV> c, next;
+    ring.begin(a, t, lo, hi);
+    Row<NV> c;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int col = column_of(t, j);
@@ -468,59 +584,47 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_bwd_kernel(const B
                         ? static_cast<float>(a.counts[static_cast<size_t>(s) * a.E + col + u]) - mean
                         : 0.0f;
     }
-    int row = lo + t.team;
-    float2 st, next_st = make_float2(0.0f, 0.0f);
-    if (row < hi) {
-      load_row<DT, VEC>(a, t, row, &next);
-      next_st = a.stats[row];
-    }
-    for (; row < hi; row += t.teams) {
-      Row<NV> r = next;
-      st = next_st;
-      if (row + t.teams < hi) {
-        load_row<DT, VEC>(a, t, row + t.teams, &next);
-        next_st = a.stats[row + t.teams];
-      }
-      // r becomes q; sigmoid: t = sigma(-|x|) with the sign of x, so that sigma and
-      // 1 - sigma, t and 1 - t, are both without cancellation
-      const float inv = __fdiv_rn(1.0f, SF == SF_SOFTMAX ? st.y : st.x);
-      float dot = 0.0f, none = 0.0f, z = 0.0f;
-      Row<NV> x = r;
+    float2 next_st = lo + t.team < hi ? a.stats[lo + t.team] : make_float2(0.0f, 1.0f);
+    for (int row = lo + t.team; row < hi; row += t.teams) {
+      const float2 st = next_st;
+      if (row + t.teams < hi) next_st = a.stats[row + t.teams];
+      Row<NV> r;
+      ring.take(a, t, row, &r);
+      const float inv = rcp_approx(SF == SF_SOFTMAX ? st.y : st.x);
       const float shift = (SF == SF_SOFTMAX ? st.x : st.y) * kLog2e;
-      if (SF == SF_SOFTMAX) z = by_z == 0.0f ? 0.0f : by_z * (st.x + logf(st.y));
-      else z = by_z * st.y;
+      float z = 0.0f;
+      if (by_z != 0.0f) z = by_z * (SF == SF_SOFTMAX ? st.x + logf(st.y) : st.y);
+      // r becomes exp(x - max), q times the row's sum; sigmoid: sigma(-|x|) with the sign of
+      // x, so that sigma and 1 - sigma are both without cancellation (x by itself for z)
+      Row<NV> x;
+      if (SF != SF_SOFTMAX) x = r;
+      float dot = 0.0f;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const bool in = inside<VEC>(column_of(t, j), u, a.E);
           if constexpr (SF == SF_SOFTMAX) {
-            r.v[j][u] = in ? exp_shifted(x.v[j][u], shift) * inv : 0.0f;
+            r.v[j][u] = exp_shifted(r.v[j][u], shift);
             dot = fmaf(c.v[j][u], r.v[j][u], dot);
           } else {
-            const float e = ex2_approx(-fabsf(x.v[j][u]) * kLog2e);
+            const float e = ex2_approx(-fabsf(r.v[j][u]) * kLog2e);
             const float small = e * rcp_approx(1.0f + e);
-            r.v[j][u] = in ? copysignf(small, x.v[j][u]) : -0.0f;
-            dot = fmaf(c.v[j][u], signbit(r.v[j][u]) ? -r.v[j][u] : 1.0f - r.v[j][u], dot);
+            dot = fmaf(c.v[j][u], r.v[j][u] < 0.0f ? small : 1.0f - small, dot);
+            r.v[j][u] = small;
           }
         }
-      dot = seg_sum<32>(dot);
-      t.sum2(&dot, &none);
-      if (SF != SF_SOFTMAX) dot *= inv;
+      dot = t.sum(seg_sum<32>(dot)) * inv;
+      // softmax: q (scale (c - dot) + z) = exp (by c + less); sigmoid alike, z apart
+      const float by = scale * inv, less = SF == SF_SOFTMAX ? inv * (z - scale * dot) : -by * dot;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int col = column_of(t, j);
         float g[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float d = scale * (c.v[j][u] - dot);
-          if (SF == SF_SOFTMAX) {
-            g[u] = r.v[j][u] * (d + z);
-          } else {
-            const float small = fabsf(r.v[j][u]);
-            g[u] = d * inv * small * (1.0f - small);
-            if (by_z != 0.0f) g[u] = fmaf(z, exp_shifted(x.v[j][u], shift), g[u]);
-          }
+          const float w = SF == SF_SOFTMAX ? r.v[j][u] : fmaf(-r.v[j][u], r.v[j][u], r.v[j][u]);
+          g[u] = w * fmaf(by, c.v[j][u], less);
+          if (SF != SF_SOFTMAX && by_z != 0.0f) g[u] = fmaf(z, exp_shifted(x.v[j][u], shift), g[u]);
         }
         if (col < a.E) store4<DT, VEC>(a.grad, static_cast<size_t>(row) * a.E, col, a.E, g);
       }
@@ -552,7 +656,23 @@ Shape shape_of(int E) {
   return best;
 }
 
-// Tokens of a block: about `per_sm` blocks on each of 152 SMs, two rows a team at least.
+size_t smem_of(int E, const Shape& sh, bool vec, int bytes, bool forward) {
+  return ring_bytes(vec, sh.nv, 32 * sh.warps * sh.teams, bytes) +
+         (forward ? static_cast<size_t>(sh.teams > 1 ? sh.teams + 1 : 1) * E * 4 : 0);
+}
+
+// Blocks that an SM holds (80 registers a thread, 227 KB), four at most: a block more than
+// that would run by itself behind the others.
+constexpr int kMostPerSm = 4;
+
+int blocks_per_sm(const Shape& sh, size_t smem) {
+  const int by_registers = 65536 / (80 * 32 * sh.warps * sh.teams);
+  const int by_memory = static_cast<int>(227 * 1024 / (smem + 2048));
+  const int n = by_registers < by_memory ? by_registers : by_memory;
+  return n < 1 ? 1 : n > kMostPerSm ? kMostPerSm : n;
+}
+
+// Tokens of a block: `per_sm` blocks on each of 152 SMs, two rows a team at least.
 // A function of the sizes alone, so that sums have the same order on every GPU.
 int rows_of(int T, int teams, int per_sm) {
   const int blocks = 152 * per_sm;
@@ -560,7 +680,6 @@ int rows_of(int T, int teams, int per_sm) {
   return (rows < 2 * teams ? 2 * teams : (rows + teams - 1) / teams * teams);
 }
 
-constexpr int kBlocksPerSm = 3;
 constexpr int kFinishBlocks = 304;
 
 int blocks_of(int T, int rows) { return T == 0 ? 1 : (T + rows - 1) / rows; }
@@ -571,7 +690,7 @@ struct Workspace {
 
 Workspace workspace_of(int T, int E, int S) {
   const Shape sh = shape_of(E);
-  const int blocks = blocks_of(T, rows_of(T, sh.teams, kBlocksPerSm));
+  const int blocks = blocks_of(T, rows_of(T, sh.teams, kMostPerSm));
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   Workspace w;
   w.slots = up((static_cast<size_t>(blocks) + S) * E * 4);
@@ -595,23 +714,26 @@ int check(int dtype, int T, int E, int K, int S, bool packed, int score_func) {
   return MR_OK;
 }
 
+template <int DT, bool VEC, int NV, int SF, bool FWD>
+cudaError_t launch_rows(const BalanceArgs& a, dim3 grid, dim3 block, size_t smem, int warps,
+                        cudaStream_t st) {
+  static std::atomic<int> granted[kSmemDevs];
+  const auto kern = FWD ? balance_fwd_kernel<DT, VEC, NV, SF> : balance_bwd_kernel<DT, VEC, NV, SF>;
+  // above 40 KB the kernel's own arrays may take it past the default of 48 KB
+  const size_t limit = smem > 40 * 1024 && smem <= 48 * 1024 ? 48 * 1024 + 16 : smem;
+  const cudaError_t e = allow_smem(kern, limit, granted);
+  return e == cudaSuccess ? launch_kernel(kern, grid, block, smem, st, a, warps) : e;
+}
+
 template <int DT, bool VEC, int SF, bool FWD>
 cudaError_t launch_nv(const BalanceArgs& a, const Shape& sh, cudaStream_t st) {
   const dim3 grid(a.blocks), block(32 * sh.warps * sh.teams);
-  const size_t smem = FWD ? static_cast<size_t>(sh.teams > 1 ? sh.teams + 1 : 1) * a.E * 4 : 0;
+  const size_t smem = smem_of(a.E, sh, VEC, DT == DT_F32 ? 16 : 8, FWD);
   switch (sh.nv) {
-    case 1:
-      return launch_kernel(FWD ? balance_fwd_kernel<DT, VEC, 1, SF> : balance_bwd_kernel<DT, VEC, 1, SF>,
-                           grid, block, smem, st, a, sh.warps);
-    case 2:
-      return launch_kernel(FWD ? balance_fwd_kernel<DT, VEC, 2, SF> : balance_bwd_kernel<DT, VEC, 2, SF>,
-                           grid, block, smem, st, a, sh.warps);
-    case 3:
-      return launch_kernel(FWD ? balance_fwd_kernel<DT, VEC, 3, SF> : balance_bwd_kernel<DT, VEC, 3, SF>,
-                           grid, block, smem, st, a, sh.warps);
-    default:
-      return launch_kernel(FWD ? balance_fwd_kernel<DT, VEC, 4, SF> : balance_bwd_kernel<DT, VEC, 4, SF>,
-                           grid, block, smem, st, a, sh.warps);
+    case 1: return launch_rows<DT, VEC, 1, SF, FWD>(a, grid, block, smem, sh.warps, st);
+    case 2: return launch_rows<DT, VEC, 2, SF, FWD>(a, grid, block, smem, sh.warps, st);
+    case 3: return launch_rows<DT, VEC, 3, SF, FWD>(a, grid, block, smem, sh.warps, st);
+    default: return launch_rows<DT, VEC, 4, SF, FWD>(a, grid, block, smem, sh.warps, st);
   }
 }
 
@@ -670,16 +792,17 @@ int router_balance_loss_fwd(const void* logits, mr_dtype dtype, const int32_t* t
   a.slot_sums = reinterpret_cast<float*>(base);
   a.slot_counts = reinterpret_cast<int32_t*>(base + w.slots);
   a.z_parts = reinterpret_cast<float*>(base + w.z);
-  a.parts = reinterpret_cast<double*>(base + w.parts);
+  a.parts = reinterpret_cast<float*>(base + w.parts);
   a.ticket = reinterpret_cast<int*>(base + w.ticket);
   a.ld_choices = ld_indices;
   a.T = T; a.E = E; a.K = K; a.S = S;
-  a.rows = rows_of(T, sh.teams, kBlocksPerSm);
+  const int piece = dtype == MR_F32 ? 16 : 8;
+  const bool vec = E % 4 == 0 && aligned(logits, piece);
+  a.rows = rows_of(T, sh.teams, blocks_per_sm(sh, smem_of(E, sh, vec, piece, true)));
   a.blocks = blocks_of(T, a.rows);
   a.coeff = coeff;
   a.z_coeff = z_coeff;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool vec = E % 4 == 0 && aligned(logits, dtype == MR_F32 ? 16 : 8);
   if (launch_balance<true>(a, dtype, score_func, vec, sh, st) != cudaSuccess) return MR_ERR_CUDA;
   const long long items = static_cast<long long>((E + 127) / 128) * S;
   const dim3 grid(static_cast<unsigned>(items < kFinishBlocks ? items : kFinishBlocks));
@@ -708,12 +831,12 @@ int router_balance_loss_bwd(const float* grad_loss, const void* logits, mr_dtype
   a.grad_loss = grad_loss;
   a.grad = grad_logits;
   a.T = T; a.E = E; a.K = K; a.S = S;
-  a.rows = rows_of(T, sh.teams, kBlocksPerSm);
+  const int piece = dtype == MR_F32 ? 16 : 8;
+  const bool vec = E % 4 == 0 && aligned(logits, piece) && aligned(grad_logits, piece);
+  a.rows = rows_of(T, sh.teams, blocks_per_sm(sh, smem_of(E, sh, vec, piece, false)));
   a.blocks = blocks_of(T, a.rows);
   a.coeff = coeff;
   a.z_coeff = z_coeff;
-  const size_t piece = dtype == MR_F32 ? 16 : 8;
-  const bool vec = E % 4 == 0 && aligned(logits, piece) && aligned(grad_logits, piece);
   return launch_balance<false>(a, dtype, score_func, vec, sh,
                                reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MR_OK

@@ -23,10 +23,12 @@
 // so all sums of a row are taken together behind one barrier.  A team keeps the
 // columns' sums for the weights' gradients of all its rows and leaves them as one row;
 // a second kernel adds those up in order: repeated calls give the same bits.
+#include <atomic>
 #include <climits>
 
 #include "router_common.cuh"
 #include "router_experts.cuh"
+#include "router_launch.cuh"
 #include "router_rows.cuh"
 
 namespace moe_router {
@@ -34,7 +36,16 @@ namespace {
 
 constexpr int kMaxWarps = 16;     // of a row
 constexpr int kBlockWarps = 8;    // of a block whose rows take fewer
-constexpr int kAhead = 4;         // forward: rows of z in flight
+#ifndef FWD_AHEAD
+#define FWD_AHEAD 8
+#endif
+#ifndef FWD_ONEPIECE
+#define FWD_ONEPIECE 8
+#endif
+#ifndef FWD_MIN
+#define FWD_MIN(U) (U == 1 ? 4 : U == 2 ? 3 : 1)
+#endif
+constexpr int kFwdWarps = 8;      // most warps of a row whose lanes hold one or two pieces
 constexpr int kSumThreads = 512;
 
 enum { GATE_NONE = 0, GATE_TOKEN = 1, GATE_VALUE = 2 };
@@ -70,12 +81,13 @@ struct RowTeam {
   float* cells;  // [teams, warps, kSums]
 
   __device__ __forceinline__ void sync() const {
-    if (warps == static_cast<int>(blockDim.x >> 5)) __syncthreads();
+    if (teams == 1) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
   }
 
-  // N values summed over the team, the same in all its threads.  The cells must not
-  // be in use by an earlier call.
+  // N values summed over the team, the same in all its threads.  With two sets of cells in
+  // turn one barrier is enough: who writes a set has passed the barrier behind its last
+  // reading.
   template <int N>
   __device__ __forceinline__ void sum(float* cells_at, float (&v)[N]) const {
 #pragma unroll
@@ -154,35 +166,51 @@ __device__ __forceinline__ void load_wide(const void* base, int row, int col0, i
   }
 }
 
-template <int DT, int BYTES, int U>
-__global__ __launch_bounds__(32 * kMaxWarps, 1) void norm_fwd_kernel(const NormArgs a) {
+// ONE: a block is one team (and has one barrier: sixteen a block, which barriers of teams
+// take, leave room for four blocks on an SM).
+template <int DT, int BYTES, int U, bool ONE>
+__global__ __launch_bounds__(32 * (U == 4 ? kMaxWarps : kFwdWarps), FWD_MIN(U))
+    void norm_fwd_kernel(const NormArgs a) {
   using P = Piece<DT, BYTES>;
+  constexpr int kAhead = FWD_AHEAD / U;  // rows of z in flight
   __shared__ float cells[2][kMaxWarps];
   pdl_enter();
-  const RowTeam r = row_team(a.warps);
-  const int t = blockIdx.x * r.teams + r.team;
+  RowTeam r = row_team(a.warps);
+  if (ONE) {
+    r.team = 0;
+    r.teams = 1;
+  }
+  const int lane = r.lane, t = blockIdx.x * r.teams + r.team;
   if (t >= a.T) return;  // whole teams, with barriers of their own
-  const int lane = r.lane;
+  const size_t at = static_cast<size_t>(t) * a.D;
   int col[U];
 #pragma unroll
   for (int q = 0; q < U; ++q) col[q] = (r.warp + q * a.warps) * 32 * P::kN;
 
-  // ---- the block's output -----------------------------------------------------------
+  // ---- the block's output, the residual's row (and the gate's) on the way ---------------
   float y[U][P::kN];
+  P res[U], gates[U];
+  int p0 = -1, p1 = -1;  // the row's choices and their weights, two to a lane
+  float w0 = 1.0f, w1 = 1.0f;
   if (a.u2p != nullptr) {
     const unsigned rows = static_cast<unsigned>(a.T) * static_cast<unsigned>(a.K);
-    int p0 = -1, p1 = -1;
-    float w0 = 0.0f, w1 = 0.0f;
     if (lane < a.K) {
       p0 = a.u2p[t + static_cast<size_t>(lane) * a.T];
-      w0 = a.weights != nullptr ? a.weights[t * a.ld_w + lane] : 1.0f;
+      if (a.weights != nullptr) w0 = a.weights[t * a.ld_w + lane];
     }
     if (lane + 32 < a.K) {
       p1 = a.u2p[t + static_cast<size_t>(lane + 32) * a.T];
-      w1 = a.weights != nullptr ? a.weights[t * a.ld_w + lane + 32] : 1.0f;
+      if (a.weights != nullptr) w1 = a.weights[t * a.ld_w + lane + 32];
     }
     if (static_cast<unsigned>(p0) >= rows) p0 = -1;
     if (static_cast<unsigned>(p1) >= rows) p1 = -1;
+  }
+#pragma unroll
+  for (int q = 0; q < U; ++q) {
+    res[q].template load<true>(a.residual, at, col[q], lane, a.D);
+    if (a.gate_kind == GATE_VALUE) gates[q].template load<true>(a.gate, at, col[q], lane, a.D);
+  }
+  if (a.u2p != nullptr) {
 #pragma unroll
     for (int q = 0; q < U; ++q)
 #pragma unroll
@@ -220,199 +248,302 @@ __global__ __launch_bounds__(32 * kMaxWarps, 1) void norm_fwd_kernel(const NormA
   }
   if (a.block != nullptr) {
 #pragma unroll
-    for (int q = 0; q < U; ++q)
-      P::store(a.block, static_cast<size_t>(t) * a.D, col[q], lane, a.D, y[q]);
+    for (int q = 0; q < U; ++q) P::store(a.block, at, col[q], lane, a.D, y[q]);
   }
 
-  // ---- the norm behind the block, gate, residual ---------------------------------------
-  float x[U][P::kN];
-#pragma unroll
-  for (int q = 0; q < U; ++q) load_wide<P, true>(a.residual, t, col[q], lane, a.D, x[q]);
+  // ---- the norm behind the block, gate, residual (weights asked for before the barriers) --
   float r_post = 1.0f, r_pre = 1.0f;
+  float by = a.scale;
+  if (a.gate_kind == GATE_TOKEN) by *= static_cast<const float*>(a.gate)[t];
   if (a.post_weight != nullptr) {
     float s[1] = {0.0f};
 #pragma unroll
-    for (int q = 0; q < U; ++q)
-#pragma unroll
-      for (int j = 0; j < P::kN; ++j) s[0] = fmaf(y[q][j], y[q][j], s[0]);
-    r.sum(cells[0], s);
-    r_post = __frsqrt_rn(s[0] / a.D + a.eps);
-  }
-  float by = a.scale * r_post;
-  if (a.gate_kind == GATE_TOKEN) by *= static_cast<const float*>(a.gate)[t];
-#pragma unroll
-  for (int q = 0; q < U; ++q) {
-    if (a.post_weight != nullptr) {
+    for (int q = 0; q < U; ++q) {
       float w[P::kN];
       vector_at<P, BYTES>(a.post_weight, col[q], lane, a.D, w);
 #pragma unroll
-      for (int j = 0; j < P::kN; ++j) y[q][j] *= w[j];
+      for (int j = 0; j < P::kN; ++j) {
+        s[0] = fmaf(y[q][j], y[q][j], s[0]);
+        y[q][j] *= w[j];
+      }
+    }
+    r.sum(cells[0], s);
+    r_post = __frsqrt_rn(s[0] / a.D + a.eps);
+  }
+  by *= r_post;
+  float x[U][P::kN];
+#pragma unroll
+  for (int q = 0; q < U; ++q) {
+    if (!any_inside<P>(col[q], lane, a.D)) {
+#pragma unroll
+      for (int j = 0; j < P::kN; ++j) x[q][j] = 0.0f;
+      continue;
     }
     if (a.gate_kind == GATE_VALUE) {
       float g[P::kN];
-      load_wide<P, true>(a.gate, t, col[q], lane, a.D, g);
+      gates[q].widen(g);
 #pragma unroll
       for (int j = 0; j < P::kN; ++j) y[q][j] *= g[j];
     }
+    res[q].widen(x[q]);
 #pragma unroll
     for (int j = 0; j < P::kN; ++j) x[q][j] = fmaf(by, y[q][j], x[q][j]);
-    P::store(a.sum, static_cast<size_t>(t) * a.D, col[q], lane, a.D, x[q]);
+    P::store(a.sum, at, col[q], lane, a.D, x[q]);
   }
 
   // ---- the norm before the next block -----------------------------------------------------
   if (a.pre_weight != nullptr) {
     float s[1] = {0.0f};
 #pragma unroll
-    for (int q = 0; q < U; ++q)
-#pragma unroll
-      for (int j = 0; j < P::kN; ++j) s[0] = fmaf(x[q][j], x[q][j], s[0]);
-    r.sum(cells[1], s);
-    r_pre = __frsqrt_rn(s[0] / a.D + a.eps);
-#pragma unroll
     for (int q = 0; q < U; ++q) {
       float w[P::kN];
       vector_at<P, BYTES>(a.pre_weight, col[q], lane, a.D, w);
 #pragma unroll
-      for (int j = 0; j < P::kN; ++j) x[q][j] *= r_pre * w[j];
-      P::store(a.normed, static_cast<size_t>(t) * a.D, col[q], lane, a.D, x[q]);
+      for (int j = 0; j < P::kN; ++j) {
+        s[0] = fmaf(x[q][j], x[q][j], s[0]);
+        x[q][j] *= w[j];
+      }
+    }
+    r.sum(cells[1], s);
+    r_pre = __frsqrt_rn(s[0] / a.D + a.eps);
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+#pragma unroll
+      for (int j = 0; j < P::kN; ++j) x[q][j] *= r_pre;
+      P::store(a.normed, at, col[q], lane, a.D, x[q]);
     }
   }
   if (a.rstd != nullptr && r.warp == 0 && lane == 0) a.rstd[t] = make_float2(r_post, r_pre);
 }
 
-// The rows of a backward that a lane holds, as they were loaded.
-template <typename P, int U>
-struct Held {
-  P gs[U], gn[U], x[U], y[U], gate[U];
-  float2 rstd;
-  float token_gate;
+// The rows of a backward on their way through shared memory: a thread's pieces go to places
+// of its own, so that it waits for its own copies and no barrier is needed; each warp's
+// first lane brings the row's factors and gate.  Both weights lie behind the ring, in the order
+// in which a warp reads them (16-byte accesses only).
+enum { ROW_GS = 0, ROW_GN = 1, ROW_X = 2, ROW_Y = 3, ROW_GATE = 4 };
 
-  __device__ __forceinline__ void load(const NormArgs& a, int t, const int (&col)[U], int lane) {
-    const size_t at = static_cast<size_t>(t) * a.D;
+__host__ __device__ constexpr int stage_bytes(int threads, int pieces, bool value) {
+  return threads * 16 * pieces * (4 + value) + threads / 32 * 16;
+}
+
+template <typename P, int U, bool VALUE>
+struct Ring {
+  static constexpr int kQuads = P::kN / 4;  // of a piece's columns
+  uint32_t base, weights;
+  int threads, thread, lane, stage_size;
+  int team_threads, team_thread;
+
+  __device__ __forceinline__ uint32_t at(int stage, int array, int q) const {
+    return base + stage * stage_size + ((array * U + q) * threads + thread) * 16;
+  }
+  __device__ __forceinline__ uint32_t factors_at(int stage) const {
+    return base + (stage + 1) * stage_size - (threads / 32 - (thread >> 5)) * 16;
+  }
+  __device__ __forceinline__ uint32_t weight_at(int which, int q, int h) const {
+    return weights + (((which * U + q) * kQuads + h) * team_threads + team_thread) * 16;
+  }
+
+  __device__ __forceinline__ void load(const NormArgs& a, int t, int stage, const int (&col)[U]) const {
+    const size_t row = static_cast<size_t>(t) * a.D;
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      if (a.grad_sum != nullptr) gs[q].template load<true>(a.grad_sum, at, col[q], lane, a.D);
+      if (!any_inside<P>(col[q], lane, a.D)) continue;
+      if (a.grad_sum != nullptr) P::load_async(at(stage, ROW_GS, q), a.grad_sum, row, col[q], lane, a.D);
       if (a.pre_weight != nullptr) {
-        gn[q].template load<true>(a.grad_normed, at, col[q], lane, a.D);
-        x[q].template load<true>(a.sum, at, col[q], lane, a.D);
+        P::load_async(at(stage, ROW_GN, q), a.grad_normed, row, col[q], lane, a.D);
+        P::load_async(at(stage, ROW_X, q), a.sum, row, col[q], lane, a.D);
       }
-      if (a.block != nullptr) y[q].template load<true>(a.block, at, col[q], lane, a.D);
-      if (a.gate_kind == GATE_VALUE) gate[q].template load<true>(a.gate, at, col[q], lane, a.D);
+      if (a.block != nullptr) P::load_async(at(stage, ROW_Y, q), a.block, row, col[q], lane, a.D);
+      if constexpr (VALUE)
+        P::load_async(at(stage, ROW_GATE, q), a.gate, row, col[q], lane, a.D);
     }
-    rstd = a.rstd != nullptr ? a.rstd[t] : make_float2(1.0f, 1.0f);
-    token_gate = a.gate_kind == GATE_TOKEN ? static_cast<const float*>(a.gate)[t] : 1.0f;
+    if (lane == 0) {
+      if (a.rstd != nullptr) copy_async<8>(factors_at(stage), a.rstd + t);
+      if (a.gate_kind == GATE_TOKEN)
+        copy_async<4>(factors_at(stage) + 8, static_cast<const float*>(a.gate) + t);
+    }
+  }
+
+  __device__ __forceinline__ float factor(int stage, int i) const {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(factors_at(stage) + 4 * i) : "memory");
+    return v;
+  }
+
+  __device__ __forceinline__ void widened(int stage, int array, int q, float (&v)[P::kN]) const {
+    P p;
+    p.read(at(stage, array, q));
+    p.widen(v);
+  }
+
+  template <int BYTES>
+  __device__ __forceinline__ void weight(const float* w, int which, int q, int col, int D,
+                                         float (&v)[P::kN]) const {
+    if constexpr (BYTES == 16) {
+#pragma unroll
+      for (int h = 0; h < kQuads; ++h)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
+                     : "r"(weight_at(which, q, h)));
+    } else {
+      vector_at<P, BYTES>(w, col, lane, D, v);
+    }
   }
 };
 
-template <int DT, int BYTES, int U>
-__global__ __launch_bounds__(32 * kMaxWarps, 1) void norm_bwd_kernel(const NormArgs a) {
+// With raw rows x and y (xh = r_pre x, yh = r_post y), u = grad_normed pre_weight and
+// c = gate post_weight y, a lane's share of the row's sums is
+//   s0 = sum u x,  s1 = sum c (grad_sum + r_pre u),  s2 = sum c x,
+// and then, with m = r_pre^2 mean(u x) and f = scale gate_token r_post,
+//   g_x = grad_sum + r_pre u - r_pre m x,  g_y = (f g_x) gate post_weight - y r_post mean_v r_post,
+//   the weights' sums take (r_pre grad_normed) x and (f g_x gate) y.
+template <int DT, int BYTES, int U, bool VALUE, bool LONG>
+__global__ __launch_bounds__(32 * (LONG ? kMaxWarps : kBlockWarps), U <= 2 ? 2 : 1)
+    void norm_bwd_kernel(const NormArgs a, int stages) {
   using P = Piece<DT, BYTES>;
+  extern __shared__ __align__(16) uint8_t dynamic_smem[];
   __shared__ float cells[2][3 * kMaxWarps];
   pdl_enter();
   const RowTeam r = row_team(a.warps);
   const int first = blockIdx.x * r.teams + r.team, step = gridDim.x * r.teams;
   const int lane = r.lane;
+  const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(dynamic_smem));
+  const int stage_size = stage_bytes(blockDim.x, U, VALUE);
+  const Ring<P, U, VALUE> ring{smem, smem + stages * stage_size, static_cast<int>(blockDim.x),
+                               static_cast<int>(threadIdx.x), lane, stage_size, a.warps * 32,
+                               r.warp * 32 + lane};
   int col[U];
 #pragma unroll
   for (int q = 0; q < U; ++q) col[q] = (r.warp + q * a.warps) * 32 * P::kN;
   const bool pre = a.pre_weight != nullptr, post = a.post_weight != nullptr;
+  int ahead = first;  // the next row to ask for
+  for (int s = 0; s < stages - 1; ++s, ahead += step) {
+    if (ahead < a.T) ring.load(a, ahead, s, col);
+    copies_commit_group();
+  }
+  if constexpr (BYTES == 16) {
+    if (r.team == 0) {
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const float* const w = which == 0 ? a.post_weight : a.pre_weight;
+#pragma unroll
+        for (int q = 0; q < U; ++q) {
+          float v[P::kN];
+#pragma unroll
+          for (int j = 0; j < P::kN; ++j) v[j] = 1.0f;
+          if (w != nullptr) vector_at<P, BYTES>(w, col[q], lane, a.D, v);
+#pragma unroll
+          for (int h = 0; h < ring.kQuads; ++h)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(ring.weight_at(which, q, h)),
+                         "f"(v[4 * h]), "f"(v[4 * h + 1]), "f"(v[4 * h + 2]), "f"(v[4 * h + 3])
+                         : "memory");
+        }
+      }
+    }
+    __syncthreads();
+  }
   float by_post[U][P::kN], by_pre[U][P::kN];  // the weights' gradients
 #pragma unroll
   for (int q = 0; q < U; ++q)
 #pragma unroll
     for (int j = 0; j < P::kN; ++j) by_post[q][j] = by_pre[q][j] = 0.0f;
-  Held<P, U> next;
-  if (first < a.T) next.load(a, first, col, lane);
-  int flip = 0;
+  int stage = 0, flip = 0;
   for (int t = first; t < a.T; t += step, flip ^= 1) {
-    const Held<P, U> h = next;
-    if (t + step < a.T) next.load(a, t + step, col, lane);
-    const float r_post = h.rstd.x, r_pre = h.rstd.y;
-    // sum u xh;  sum c (grad_sum + r_pre u);  sum c xh   (c without the token's gate)
+    __syncwarp();  // the lanes have read the factors of the stage that is filled again
+    if (ahead < a.T) ring.load(a, ahead, stage == 0 ? stages - 1 : stage - 1, col);
+    ahead += step;
+    copies_commit_group();
+    copies_wait_group(stages - 1);
+    __syncwarp();
+    const float r_post = a.rstd != nullptr ? ring.factor(stage, 0) : 1.0f;
+    const float r_pre = a.rstd != nullptr ? ring.factor(stage, 1) : 1.0f;
     float s[3] = {0.0f, 0.0f, 0.0f};
-    float g[U][P::kN], xh[U][P::kN], yh[U][P::kN], c[U][P::kN];
+    float g[U][P::kN];  // grad_sum + r_pre u
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const bool in = any_inside<P>(col[q], lane, a.D);
+      if (!any_inside<P>(col[q], lane, a.D)) continue;
+      float x[P::kN], v[P::kN], w[P::kN];
 #pragma unroll
-      for (int j = 0; j < P::kN; ++j) g[q][j] = xh[q][j] = yh[q][j] = c[q][j] = 0.0f;
-      if (!in) continue;
-      if (a.grad_sum != nullptr) h.gs[q].widen(g[q]);
+      for (int j = 0; j < P::kN; ++j) g[q][j] = x[j] = 0.0f;
+      if (a.grad_sum != nullptr) ring.widened(stage, ROW_GS, q, g[q]);
       if (pre) {
-        float w[P::kN], gn[P::kN];
-        vector_at<P, BYTES>(a.pre_weight, col[q], lane, a.D, w);
-        h.gn[q].widen(gn);
-        h.x[q].widen(xh[q]);
+        ring.widened(stage, ROW_X, q, x);
+        ring.widened(stage, ROW_GN, q, v);
+        ring.template weight<BYTES>(a.pre_weight, 1, q, col[q], a.D, w);
 #pragma unroll
         for (int j = 0; j < P::kN; ++j) {
-          xh[q][j] *= r_pre;
-          by_pre[q][j] = fmaf(gn[j], xh[q][j], by_pre[q][j]);
-          const float u = gn[j] * w[j];
-          s[0] = fmaf(u, xh[q][j], s[0]);
-          g[q][j] = fmaf(r_pre, u, g[q][j]);
+          const float gn = r_pre * v[j];
+          by_pre[q][j] = fmaf(gn, x[j], by_pre[q][j]);
+          s[0] = fmaf(gn * w[j], x[j], s[0]);
+          g[q][j] = fmaf(gn, w[j], g[q][j]);
         }
       }
       if (a.block != nullptr) {
-        h.y[q].widen(yh[q]);
-        float w[P::kN];
-        if (post) {
-          vector_at<P, BYTES>(a.post_weight, col[q], lane, a.D, w);
-        } else {
+        ring.widened(stage, ROW_Y, q, v);
+        if constexpr (VALUE) {
+          ring.widened(stage, ROW_GATE, q, w);
 #pragma unroll
-          for (int j = 0; j < P::kN; ++j) w[j] = 1.0f;
+          for (int j = 0; j < P::kN; ++j) v[j] *= w[j];
         }
-        float gate[P::kN];
-        if (a.gate_kind == GATE_VALUE) {
-          h.gate[q].widen(gate);
-        } else {
+        if (post) {
+          ring.template weight<BYTES>(a.post_weight, 0, q, col[q], a.D, w);
 #pragma unroll
-          for (int j = 0; j < P::kN; ++j) gate[j] = 1.0f;
+          for (int j = 0; j < P::kN; ++j) v[j] *= w[j];
         }
 #pragma unroll
         for (int j = 0; j < P::kN; ++j) {
-          yh[q][j] *= r_post;
-          c[q][j] = gate[j] * w[j] * yh[q][j];
-          s[1] = fmaf(c[q][j], g[q][j], s[1]);
-          s[2] = fmaf(c[q][j], xh[q][j], s[2]);
+          s[1] = fmaf(v[j], g[q][j], s[1]);
+          s[2] = fmaf(v[j], x[j], s[2]);
         }
       }
     }
     if (pre || post || a.gate_kind == GATE_TOKEN) r.sum(cells[flip], s);
-    const float mean = pre ? s[0] / a.D : 0.0f;
-    const float whole = s[1] - r_pre * mean * s[2];  // sum c g_x
-    const float by = a.scale * h.token_gate;
-    const float mean_v = post ? by * whole / a.D : 0.0f;
+    // s[0] = r_pre sum u x;  g_x = g - k x
+    const float k = pre ? r_pre * r_pre * (s[0] / a.D) : 0.0f;
+    const float whole = r_post * fmaf(-k, s[2], s[1]);  // sum c g_x, of yh
+    const float by = a.gate_kind == GATE_TOKEN ? a.scale * ring.factor(stage, 2) : a.scale;
+    const float f = by * r_post;
+    const float back = post ? r_post * r_post * (by * whole / a.D) : 0.0f;
     if (a.gate_kind == GATE_TOKEN && r.warp == 0 && lane == 0)
       static_cast<float*>(a.grad_gate)[t] = a.scale * whole;
     const size_t at = static_cast<size_t>(t) * a.D;
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       if (!any_inside<P>(col[q], lane, a.D)) continue;
+      float v[P::kN], w[P::kN];
+      if (pre) {
+        ring.widened(stage, ROW_X, q, v);
 #pragma unroll
-      for (int j = 0; j < P::kN; ++j) g[q][j] = fmaf(-r_pre * mean, xh[q][j], g[q][j]);
+        for (int j = 0; j < P::kN; ++j) g[q][j] = fmaf(-k, v[j], g[q][j]);
+      }
       P::store(a.grad_residual, at, col[q], lane, a.D, g[q]);
-      float w[P::kN], gate[P::kN], v[P::kN];
+      if (a.block != nullptr) ring.widened(stage, ROW_Y, q, v);
+      if (post) ring.template weight<BYTES>(a.post_weight, 0, q, col[q], a.D, w);
+      if constexpr (VALUE) {
+        float gate[P::kN], gg[P::kN];
+        ring.widened(stage, ROW_GATE, q, gate);
 #pragma unroll
-      for (int j = 0; j < P::kN; ++j) w[j] = gate[j] = 1.0f;
-      if (post) vector_at<P, BYTES>(a.post_weight, col[q], lane, a.D, w);
-      if (a.gate_kind == GATE_VALUE) {
-        h.gate[q].widen(gate);
-#pragma unroll
-        for (int j = 0; j < P::kN; ++j) v[j] = a.scale * g[q][j] * w[j] * yh[q][j];
-        P::store(a.grad_gate, at, col[q], lane, a.D, v);
-      }
-#pragma unroll
-      for (int j = 0; j < P::kN; ++j) {
-        const float gh = by * gate[j] * g[q][j];
-        if (post) {
-          by_post[q][j] = fmaf(gh, yh[q][j], by_post[q][j]);
-          v[j] = r_post * (gh * w[j] - yh[q][j] * mean_v);
-        } else {
-          v[j] = gh;
+        for (int j = 0; j < P::kN; ++j) {
+          gg[j] = f * g[q][j] * v[j];
+          if (post) gg[j] *= w[j];
+          g[q][j] *= gate[j];
         }
+        P::store(a.grad_gate, at, col[q], lane, a.D, gg);
       }
-      P::store(a.grad_block, at, col[q], lane, a.D, v);
+      if (post) {
+#pragma unroll
+        for (int j = 0; j < P::kN; ++j) {
+          const float gh = f * g[q][j];
+          by_post[q][j] = fmaf(gh, v[j], by_post[q][j]);
+          g[q][j] = fmaf(gh, w[j], -back * v[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < P::kN; ++j) g[q][j] *= by;
+      }
+      P::store(a.grad_block, at, col[q], lane, a.D, g[q]);
     }
+    if (++stage == stages) stage = 0;
   }
   if (a.partial == nullptr) return;
   float* const mine = a.partial + static_cast<size_t>(first) * 2 * a.D;
@@ -473,25 +604,29 @@ int access_bytes(const NormArgs& a, int dtype) {
   return (all & 15u) == 0 ? 16 : (all & 3u) == 0 ? 4 : 2;
 }
 
-// Warps of a row and pieces of a lane: as few pieces as 16 warps allow.
+// Warps of a row and pieces of a lane.  Forward: one piece up to 8 warps, two up to 16
+// pieces, else four.  Backward: as few pieces as 16 warps allow.
 struct Split {
   int warps, pieces, teams;
 };
 
-Split split_of(int D, int columns) {
+Split split_of(int D, int columns, bool forward) {
   const int stretches = (D + columns - 1) / columns;
-  const int pieces = stretches <= kMaxWarps ? 1 : stretches <= 2 * kMaxWarps ? 2 : 4;
+  int pieces;
+  if (forward) pieces = stretches <= FWD_ONEPIECE ? 1 : stretches <= 2 * kFwdWarps ? 2 : 4;
+  else pieces = stretches == 1 ? 1 : stretches <= 2 * kBlockWarps ? 2 : 4;
   const int warps = (stretches + pieces - 1) / pieces;
   return Split{warps, pieces, warps >= kBlockWarps ? 1 : kBlockWarps / warps};
 }
 
-// Teams of a backward: eight rows each at least, and no more than about two blocks of
-// each SM hold.  From the sizes alone, so that sums have the same order on every GPU.
+// Blocks of a backward: what is resident, two on each SM for up to two pieces to a lane and one
+// for longer rows.  From the sizes alone, so that sums have the same order on every GPU.
 constexpr int kBwdBlocks = 2 * 152;
 
 int bwd_blocks(int T, const Split& s) {
   const int most = (T + s.teams - 1) / s.teams;
-  return most < kBwdBlocks ? most : kBwdBlocks;
+  const int resident = s.pieces > 2 ? kBwdBlocks / 2 : kBwdBlocks;
+  return most < resident ? most : resident;
 }
 
 // Rows of partial sums for any alignment (narrow accesses take more warps a row, so
@@ -501,28 +636,54 @@ size_t partial_rows(int T) {
   return static_cast<size_t>(T) + kBlockWarps < most ? static_cast<size_t>(T) + kBlockWarps : most;
 }
 
+template <int DT, int BYTES, int U>
+cudaError_t launch_fwd_pieces(const NormArgs& a, const Split& s, cudaStream_t st) {
+  const dim3 grid((a.T + s.teams - 1) / s.teams), block(32 * s.warps * s.teams);
+  return s.teams == 1 ? launch_kernel(norm_fwd_kernel<DT, BYTES, U, true>, grid, block, 0, st, a)
+                      : launch_kernel(norm_fwd_kernel<DT, BYTES, U, false>, grid, block, 0, st, a);
+}
+
 template <int DT, int BYTES>
 int launch_fwd(NormArgs a, cudaStream_t st) {
-  const Split s = split_of(a.D, 32 * Piece<DT, BYTES>::kN);
+  const Split s = split_of(a.D, 32 * Piece<DT, BYTES>::kN, true);
   a.warps = s.warps;
-  const dim3 grid((a.T + s.teams - 1) / s.teams), block(32 * s.warps * s.teams);
-  const cudaError_t e =
-      s.pieces == 1   ? launch_kernel(norm_fwd_kernel<DT, BYTES, 1>, grid, block, 0, st, a)
-      : s.pieces == 2 ? launch_kernel(norm_fwd_kernel<DT, BYTES, 2>, grid, block, 0, st, a)
-                      : launch_kernel(norm_fwd_kernel<DT, BYTES, 4>, grid, block, 0, st, a);
+  const cudaError_t e = s.pieces == 1   ? launch_fwd_pieces<DT, BYTES, 1>(a, s, st)
+                        : s.pieces == 2 ? launch_fwd_pieces<DT, BYTES, 2>(a, s, st)
+                                        : launch_fwd_pieces<DT, BYTES, 4>(a, s, st);
   return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
+}
+
+// Rows on their way: as many as the blocks' shares of shared memory hold, four at most.
+template <int DT, int BYTES, int U, bool VALUE, bool LONG>
+cudaError_t launch_bwd_pieces(const NormArgs& a, const Split& s, int blocks, cudaStream_t st) {
+  static std::atomic<int> granted[kSmemDevs];
+  const int threads = 32 * s.warps * s.teams;
+  const int size = stage_bytes(threads, U, VALUE);
+  const int weights = BYTES == 16 ? 2 * U * Piece<DT, BYTES>::kN * 4 * 32 * s.warps : 0;
+  int stages = ((U <= 2 ? 112 : 224) * 1024 - weights) / size;
+  stages = stages > 4 ? 4 : stages < 1 ? 1 : stages;
+  const size_t smem = static_cast<size_t>(stages) * size + weights;
+  const auto kern = norm_bwd_kernel<DT, BYTES, U, VALUE, LONG>;
+  const cudaError_t e = allow_smem(kern, smem > 40 * 1024 && smem <= 48 * 1024 ? 49168 : smem, granted);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(blocks), dim3(threads), smem, st, a, stages);
+}
+
+template <int DT, int BYTES, bool VALUE>
+cudaError_t launch_bwd_rows(const NormArgs& a, const Split& s, int blocks, cudaStream_t st) {
+  if (s.pieces == 1) return launch_bwd_pieces<DT, BYTES, 1, VALUE, false>(a, s, blocks, st);
+  if (s.pieces == 2) return launch_bwd_pieces<DT, BYTES, 2, VALUE, false>(a, s, blocks, st);
+  return s.warps <= kBlockWarps ? launch_bwd_pieces<DT, BYTES, 4, VALUE, false>(a, s, blocks, st)
+                                : launch_bwd_pieces<DT, BYTES, 4, VALUE, true>(a, s, blocks, st);
 }
 
 template <int DT, int BYTES>
 int launch_bwd(NormArgs a, cudaStream_t st) {
-  const Split s = split_of(a.D, 32 * Piece<DT, BYTES>::kN);
+  const Split s = split_of(a.D, 32 * Piece<DT, BYTES>::kN, false);
   a.warps = s.warps;
   const int blocks = bwd_blocks(a.T, s);
-  const dim3 grid(blocks), block(32 * s.warps * s.teams);
-  cudaError_t e =
-      s.pieces == 1   ? launch_kernel(norm_bwd_kernel<DT, BYTES, 1>, grid, block, 0, st, a)
-      : s.pieces == 2 ? launch_kernel(norm_bwd_kernel<DT, BYTES, 2>, grid, block, 0, st, a)
-                      : launch_kernel(norm_bwd_kernel<DT, BYTES, 4>, grid, block, 0, st, a);
+  cudaError_t e = a.gate_kind == GATE_VALUE ? launch_bwd_rows<DT, BYTES, true>(a, s, blocks, st)
+                                            : launch_bwd_rows<DT, BYTES, false>(a, s, blocks, st);
   if (e == cudaSuccess && a.partial != nullptr)
     e = launch_kernel(norm_sum_kernel, dim3((a.D + 31) / 32, 2), dim3(kSumThreads), 0, st,
                       static_cast<const float*>(a.partial), blocks * s.teams, a.D, a.grad_post,

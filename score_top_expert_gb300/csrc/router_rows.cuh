@@ -6,6 +6,30 @@
 
 namespace moe_router {
 
+// N bytes (4, 8 or 16) from global to the thread's own place in shared memory, on their way
+// until the thread waits for the group; zeros instead when not `valid`.
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool valid = true) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+                 "r"(valid ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(N),
+                 "r"(valid ? N : 0) : "memory");
+}
+
+__device__ __forceinline__ void copies_commit_group() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Until at most `pending` (0 to 3) of the thread's groups are on their way.
+__device__ __forceinline__ void copies_wait_group(int pending) {
+  if (pending >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // What a lane holds of a stretch of 32 kN columns of a row, as it was loaded (so
 // that rows in flight take few registers), widened to fp32 when used.  BYTES is
 // what one access takes: 16 where every row is 16-byte aligned, else 4 or 2, in
@@ -42,6 +66,32 @@ struct Piece {
         w[q] = get<STREAM>(reinterpret_cast<const unsigned short*>(at + c * kSize));
       }
     }
+  }
+
+  // The same 16 bytes of the lane, to its place in shared memory and back.  (Two-byte
+  // accesses have no asynchronous copy: they are stored there.)
+  __device__ __forceinline__ static void load_async(uint32_t to, const void* base, size_t row,
+                                                    int col0, int lane, int D) {
+    const uint8_t* at = static_cast<const uint8_t*>(base) + row * kSize;
+    if constexpr (BYTES == 16) {
+      copy_async<16>(to, at + column(col0, 0, lane) * kSize);
+    } else if constexpr (BYTES == 4) {
+#pragma unroll
+      for (int q = 0; q < kAccesses; ++q) {
+        const int c = column(col0, q, lane);
+        copy_async<4>(to + 4 * q, c < D ? at + c * kSize : at, c < D);
+      }
+    } else {
+      Piece p;
+      p.template load<true>(base, row, col0, lane, D);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(p.w[0]), "r"(p.w[1]),
+                   "r"(p.w[2]), "r"(p.w[3]) : "memory");
+    }
+  }
+
+  __device__ __forceinline__ void read(uint32_t from) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from) : "memory");
   }
 
   template <bool STREAM, typename W>

@@ -137,6 +137,8 @@ class _CtypesCalls:
         self.router_combine_norm_bwd = L.router_combine_norm_bwd
         self.router_balance_loss_fwd = L.router_balance_loss_fwd
         self.router_balance_loss_bwd = L.router_balance_loss_bwd
+        self.router_balance_loss_workspace_bytes = L.router_balance_loss_workspace_bytes
+        self.router_combine_norm_bwd_workspace_bytes = L.router_combine_norm_bwd_workspace_bytes
 
 
 def _load_fast():
@@ -591,87 +593,6 @@ def router_aux_loss_bwd(grad_loss: torch.Tensor, tokens_per_expert: torch.Tensor
     return grad_aux_scores
 
 
-def _sequences(seq_offsets, dev) -> tuple[int, int]:
-    """(S, pointer) of a packed batch's sequence offsets [S + 1]; None: one sequence."""
-    if seq_offsets is None:
-        return 1, 0
-    if seq_offsets.get_device() != dev.index or seq_offsets.dtype != torch.int32 \
-            or seq_offsets.dim() != 1 or seq_offsets.numel() < 2 \
-            or not seq_offsets.is_contiguous():
-        raise ValueError("seq_offsets must be a contiguous int32 [S + 1] tensor on the logits' "
-                         "device")
-    return seq_offsets.numel() - 1, seq_offsets.data_ptr()
-
-
-def router_balance_loss_fwd(logits: torch.Tensor, topk_indices: torch.Tensor,
-                            score_func: str = "softmax", coeff: float = 1.0, z_coeff: float = 0.0,
-                            seq_offsets: torch.Tensor | None = None, *, loss=None,
-                            tokens_per_expert=None, row_stats=None, workspace=None):
-    """Load-balancing loss of each sequence of a packed batch, and the z loss, from the
-    logits [T, E] and the choices [T, K] int32 (router_topk_fwd_compact's; a column
-    view of a wider buffer is read in place).  ``seq_offsets`` [S + 1] int32: sequence s
-    is tokens seq_offsets[s] .. seq_offsets[s + 1] - 1, other tokens are padding; None:
-    all tokens are one.  Returns (loss [2] float32: balance and z loss,
-    tokens_per_expert [S, E] int32, row_stats [T, 2] float32 for the backward).  The
-    workspace (a uint8 CUDA tensor) is allocated here when not given."""
-    logits = _as_input(logits, "logits", _DTYPE)
-    T, E = logits.shape
-    dev = logits.device
-    idx = topk_indices
-    if idx.get_device() != dev.index or idx.dtype != torch.int32 or idx.dim() != 2 \
-            or idx.shape[0] != T or idx.shape[1] < 1:
-        raise ValueError(f"topk_indices must be an int32 [{T}, K] tensor on the logits' device")
-    K = idx.shape[1]
-    if not idx.is_contiguous() and (idx.stride(1) != 1 or idx.stride(0) < K):
-        idx = idx.contiguous()
-    ld = K if idx.is_contiguous() else idx.stride(0)
-    S, seq_ptr = _sequences(seq_offsets, dev)
-    loss = _out(loss, (2,), torch.float32, dev, "loss")
-    tokens_per_expert = _out(tokens_per_expert, (S, E), torch.int32, dev, "tokens_per_expert")
-    row_stats = _out(row_stats, (T, 2), torch.float32, dev, "row_stats")
-    if workspace is None:
-        nbytes = lib().router_balance_loss_workspace_bytes(T, E, S)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    elif workspace.get_device() != dev.index or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the logits' device")
-    with _on(dev):
-        rc = _calls().router_balance_loss_fwd(
-            logits.data_ptr(), _DTYPE[logits.dtype], idx.data_ptr(), ld, seq_ptr, T, E, K, S,
-            _score(score_func), float(coeff), float(z_coeff), loss.data_ptr(),
-            tokens_per_expert.data_ptr(), row_stats.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(dev))
-    _check("router_balance_loss_fwd", rc)
-    return loss, tokens_per_expert, row_stats
-
-
-def router_balance_loss_bwd(grad_loss: torch.Tensor, logits: torch.Tensor,
-                            tokens_per_expert: torch.Tensor, row_stats: torch.Tensor, K: int,
-                            score_func: str = "softmax", coeff: float = 1.0, z_coeff: float = 0.0,
-                            seq_offsets: torch.Tensor | None = None, *, grad_logits=None):
-    """Gradient of both losses by the logits, [T, E] in the logits' dtype; padding gets
-    zeros.  ``grad_loss`` [2] float32; the other arguments are the forward's."""
-    logits = _as_input(logits, "logits", _DTYPE)
-    T, E = logits.shape
-    dev = logits.device
-    S, seq_ptr = _sequences(seq_offsets, dev)
-    for t, name, shape, dt in ((grad_loss, "grad_loss", (2,), torch.float32),
-                               (tokens_per_expert, "tokens_per_expert", (S, E), torch.int32),
-                               (row_stats, "row_stats", (T, 2), torch.float32)):
-        if t.get_device() != dev.index or t.dtype != dt or t.shape != shape:
-            raise ValueError(f"{name} must be a {dt} tensor of shape {shape} on {dev}")
-    grad_loss, row_stats = grad_loss.contiguous(), row_stats.contiguous()
-    tokens_per_expert = tokens_per_expert.contiguous()
-    grad_logits = _out(grad_logits, (T, E), logits.dtype, dev, "grad_logits")
-    with _on(dev):
-        rc = _calls().router_balance_loss_bwd(
-            grad_loss.data_ptr(), logits.data_ptr(), _DTYPE[logits.dtype],
-            tokens_per_expert.data_ptr(), row_stats.data_ptr(), seq_ptr, T, E, int(K), S,
-            _score(score_func), float(coeff), float(z_coeff), grad_logits.data_ptr(),
-            _stream(dev))
-    _check("router_balance_loss_bwd", rc)
-    return grad_logits
-
-
 # ---- the experts' products and the combination ------------------------------
 # One token's calls take a few microseconds on the GPU, so the host's part is
 # written flat: every check reads tensor attributes directly, and the helpers
@@ -940,9 +861,13 @@ def router_quantize_rows(x: torch.Tensor, *, out=None, scales=None):
     else:
         scales = _out(scales, (R,), _F32, x.device, "scales")
     call = (_fast or _calls()).router_quantize_rows
-    with _on(idx):
+    if idx == _cur_dev():
         rc = call(x.data_ptr(), _DTYPE[dt], R, D, out.data_ptr(), scales.data_ptr(),
                   _raw_stream(idx))
+    else:
+        with torch.cuda.device(idx):
+            rc = call(x.data_ptr(), _DTYPE[dt], R, D, out.data_ptr(), scales.data_ptr(),
+                      _raw_stream(idx))
     if rc != 0:
         raise RouterError("router_quantize_rows", rc)
     return out, scales
@@ -992,10 +917,15 @@ def router_expert_matmul_w8(x: torch.Tensor, x_scales: torch.Tensor, weight: tor
     else:
         out = _out(out, (P, N), odt, x.device, "out")
     call = (_fast or _calls()).router_expert_matmul_w8
-    with _on(idx):
+    if idx == _cur_dev():
         rc = call(x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(),
                   off.data_ptr(), p2u_ptr, T, P, E, N, D, out.data_ptr(), _DTYPE[odt],
                   _raw_stream(idx))
+    else:
+        with torch.cuda.device(idx):
+            rc = call(x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(),
+                      weight_scales.data_ptr(), off.data_ptr(), p2u_ptr, T, P, E, N, D,
+                      out.data_ptr(), _DTYPE[odt], _raw_stream(idx))
     if rc != 0:
         raise RouterError("router_expert_matmul_w8", rc)
     return out
@@ -1107,15 +1037,117 @@ def router_combine_bwd(grad_out: torch.Tensor, unpermuted_to_permuted: torch.Ten
     return grad_expert_out, grad_weights
 
 
+# ---- the balance loss of a packed batch -----------------------------------------
+def _sequences(seq_offsets, idx: int) -> tuple[int, int]:
+    """(S, pointer) of a packed batch's sequence offsets [S + 1]."""
+    n = seq_offsets.numel()
+    if seq_offsets.get_device() != idx or seq_offsets.dtype is not _I32 \
+            or seq_offsets.dim() != 1 or n < 2 or not seq_offsets.is_contiguous():
+        _bad("seq_offsets", f"a contiguous int32 [S + 1] tensor on cuda:{idx}")
+    return n - 1, seq_offsets.data_ptr()
+
+
+def router_balance_loss_fwd(logits: torch.Tensor, topk_indices: torch.Tensor,
+                            score_func: str = "softmax", coeff: float = 1.0, z_coeff: float = 0.0,
+                            seq_offsets: torch.Tensor | None = None, *, loss=None,
+                            tokens_per_expert=None, row_stats=None, workspace=None):
+    """Load-balancing loss of each sequence of a packed batch, and the z loss, from the
+    logits [T, E] and the choices [T, K] int32 (router_topk_fwd_compact's; a column
+    view of a wider buffer is read in place).  ``seq_offsets`` [S + 1] int32: sequence s
+    is tokens seq_offsets[s] .. seq_offsets[s + 1] - 1, other tokens are padding; None:
+    all tokens are one.  Returns (loss [2] float32: balance and z loss,
+    tokens_per_expert [S, E] int32, row_stats [T, 2] float32 for the backward).  The
+    workspace (a uint8 CUDA tensor) is allocated here when not given."""
+    x, dt, idx = logits, logits.dtype, logits.get_device()
+    if idx < 0 or dt not in _DTYPE or x.dim() != 2 or not x.is_contiguous():
+        x = _as_input(x, "logits", _DTYPE)
+    T, E = x.shape
+    dev = x.device
+    choices = topk_indices
+    if choices.get_device() != idx or choices.dtype is not _I32 or choices.dim() != 2 \
+            or choices.shape[0] != T or choices.shape[1] < 1:
+        _bad("topk_indices", f"an int32 [{T}, K] tensor on cuda:{idx}")
+    ld = K = choices.shape[1]
+    if not choices.is_contiguous():
+        if choices.stride(1) != 1 or choices.stride(0) < K:
+            choices = choices.contiguous()
+        else:
+            ld = choices.stride(0)
+    S, seq_ptr = (1, 0) if seq_offsets is None else _sequences(seq_offsets, idx)
+    loss = _empty((2,), dtype=_F32, device=dev) if loss is None \
+        else _out(loss, (2,), _F32, dev, "loss")
+    counts = _empty((S, E), dtype=_I32, device=dev) if tokens_per_expert is None \
+        else _out(tokens_per_expert, (S, E), _I32, dev, "tokens_per_expert")
+    stats = _empty((T, 2), dtype=_F32, device=dev) if row_stats is None \
+        else _out(row_stats, (T, 2), _F32, dev, "row_stats")
+    calls = _fast or _calls()
+    if workspace is None:
+        nbytes = calls.router_balance_loss_workspace_bytes(T, E, S) or 16
+        workspace = _empty((nbytes,), dtype=_U8, device=dev)
+    else:
+        if workspace.get_device() != idx or not workspace.is_contiguous():
+            _bad("workspace", f"a contiguous tensor on cuda:{idx}")
+        nbytes = workspace.numel() * workspace.element_size()
+    sf = _score(score_func)
+    if idx == _cur_dev():
+        rc = calls.router_balance_loss_fwd(
+            x.data_ptr(), _DTYPE[dt], choices.data_ptr(), ld, seq_ptr, T, E, K, S, sf, coeff,
+            z_coeff, loss.data_ptr(), counts.data_ptr(), stats.data_ptr(), workspace.data_ptr(),
+            nbytes, _raw_stream(idx))
+    else:
+        with torch.cuda.device(idx):
+            rc = calls.router_balance_loss_fwd(
+                x.data_ptr(), _DTYPE[dt], choices.data_ptr(), ld, seq_ptr, T, E, K, S, sf, coeff,
+                z_coeff, loss.data_ptr(), counts.data_ptr(), stats.data_ptr(),
+                workspace.data_ptr(), nbytes, _raw_stream(idx))
+    if rc != 0:
+        raise RouterError("router_balance_loss_fwd", rc)
+    return loss, counts, stats
+
+
+def router_balance_loss_bwd(grad_loss: torch.Tensor, logits: torch.Tensor,
+                            tokens_per_expert: torch.Tensor, row_stats: torch.Tensor, K: int,
+                            score_func: str = "softmax", coeff: float = 1.0, z_coeff: float = 0.0,
+                            seq_offsets: torch.Tensor | None = None, *, grad_logits=None):
+    """Gradient of both losses by the logits, [T, E] in the logits' dtype; padding gets
+    zeros.  ``grad_loss`` [2] float32; the other arguments are the forward's."""
+    x, dt, idx = logits, logits.dtype, logits.get_device()
+    if idx < 0 or dt not in _DTYPE or x.dim() != 2 or not x.is_contiguous():
+        x = _as_input(x, "logits", _DTYPE)
+    T, E = x.shape
+    S, seq_ptr = (1, 0) if seq_offsets is None else _sequences(seq_offsets, idx)
+    g, counts, stats = grad_loss, tokens_per_expert, row_stats
+    if g.get_device() != idx or g.dtype is not _F32 or g.shape != (2,) or not g.is_contiguous():
+        g = _vector(g, "grad_loss", idx, 2)
+    if counts.get_device() != idx or counts.dtype is not _I32 or counts.shape != (S, E) \
+            or not counts.is_contiguous():
+        _bad("tokens_per_expert", f"a contiguous int32 [{S}, {E}] tensor on cuda:{idx}")
+    if stats.get_device() != idx or stats.dtype is not _F32 or stats.shape != (T, 2) \
+            or not stats.is_contiguous():
+        _bad("row_stats", f"a contiguous float32 [{T}, 2] tensor on cuda:{idx}")
+    out = _empty((T, E), dtype=dt, device=x.device) if grad_logits is None \
+        else _out(grad_logits, (T, E), dt, x.device, "grad_logits")
+    sf = _score(score_func)
+    call = (_fast or _calls()).router_balance_loss_bwd
+    if idx == _cur_dev():
+        rc = call(g.data_ptr(), x.data_ptr(), _DTYPE[dt], counts.data_ptr(), stats.data_ptr(),
+                  seq_ptr, T, E, K, S, sf, coeff, z_coeff, out.data_ptr(), _raw_stream(idx))
+    else:
+        with torch.cuda.device(idx):
+            rc = call(g.data_ptr(), x.data_ptr(), _DTYPE[dt], counts.data_ptr(),
+                      stats.data_ptr(), seq_ptr, T, E, K, S, sf, coeff, z_coeff, out.data_ptr(),
+                      _raw_stream(idx))
+    if rc != 0:
+        raise RouterError("router_balance_loss_bwd", rc)
+    return out
+
+
 # ---- the norms around an expert block ------------------------------------------
-_GATE_NONE, _GATE_TOKEN, _GATE_VALUE = 0, 1, 2
+_GATE_TOKEN, _GATE_VALUE = 1, 2  # 0: none
 
 
 def _gate(gate, T: int, D: int, dt, idx: int):
-    """(tensor or None, kind) of a block's gate: [T] float32, or [T, D] of the rows'
-    type."""
-    if gate is None:
-        return None, _GATE_NONE
+    """(tensor, kind) of a block's gate: [T] float32, or [T, D] of the rows' type."""
     if gate.get_device() == idx:
         if gate.shape == (T,) and gate.dtype is _F32:
             return gate if gate.is_contiguous() else gate.contiguous(), _GATE_TOKEN
@@ -1124,10 +1156,10 @@ def _gate(gate, T: int, D: int, dt, idx: int):
     _bad("gate", f"a float32 [{T}] or a {dt} [{T}, {D}] tensor on cuda:{idx}")
 
 
-def _same_rows(t: torch.Tensor, name: str, T: int, D: int, dt, idx: int) -> torch.Tensor:
+def _same_rows(t: torch.Tensor, name: str, shape, dt, idx: int) -> torch.Tensor:
     """A [T, D] tensor of the call's type and device."""
-    if t.get_device() != idx or t.dtype is not dt or t.shape != (T, D):
-        _bad(name, f"a {dt} [{T}, {D}] tensor on cuda:{idx}")
+    if t.get_device() != idx or t.dtype is not dt or t.shape != shape:
+        _bad(name, f"a {dt} {list(shape)} tensor on cuda:{idx}")
     return t if t.is_contiguous() else t.contiguous()
 
 
@@ -1180,25 +1212,39 @@ def router_combine_norm_fwd(expert_out: torch.Tensor, residual: torch.Tensor,
     if post_weight is not None:
         post_weight = _vector(post_weight, "post_weight", idx, D)
         post_ptr = post_weight.data_ptr()
-    gate, kind = _gate(gate, T, D, dt, idx)
+    gate_ptr = kind = 0
+    if gate is not None:
+        gate, kind = _gate(gate, T, D, dt, idx)
+        gate_ptr = gate.data_ptr()
     if pre_weight is not None:
         pre_weight = _vector(pre_weight, "pre_weight", idx, D)
         pre_ptr = pre_weight.data_ptr()
-        normed = _out(normed, (T, D), dt, dev, "normed")
+        normed = _empty((T, D), dtype=dt, device=dev) if normed is None \
+            else _out(normed, (T, D), dt, dev, "normed")
         normed_ptr = normed.data_ptr()
     elif normed is not None:
         raise ValueError("normed needs pre_weight")
-    sum = _out(sum, (T, D), dt, dev, "sum")
+    sum = _empty((T, D), dtype=dt, device=dev) if sum is None \
+        else _out(sum, (T, D), dt, dev, "sum")
+    block_ptr = rstd_ptr = 0
     if save or block_out is not None:
         block_out = _out(block_out, (T, D), dt, dev, "block_out")
+        block_ptr = block_out.data_ptr()
     if save or rstd is not None:
         rstd = _out(rstd, (T, 2), _F32, dev, "rstd")
-    with _on(idx):
-        rc = (_fast or _calls()).router_combine_norm_fwd(
-            z.data_ptr(), _DTYPE[dt], u2p_ptr, w_ptr, ld, res.data_ptr(), post_ptr, _ptr0(gate),
-            kind, float(residual_scale), pre_ptr, float(eps), T, K, D, sum.data_ptr(), normed_ptr,
-            _ptr0(block_out), _ptr0(rstd), _raw_stream(idx))
-    _check("router_combine_norm_fwd", rc)
+        rstd_ptr = rstd.data_ptr()
+    call = (_fast or _calls()).router_combine_norm_fwd
+    if idx == _cur_dev():
+        rc = call(z.data_ptr(), _DTYPE[dt], u2p_ptr, w_ptr, ld, res.data_ptr(), post_ptr, gate_ptr,
+                  kind, residual_scale, pre_ptr, eps, T, K, D, sum.data_ptr(), normed_ptr,
+                  block_ptr, rstd_ptr, _raw_stream(idx))
+    else:
+        with torch.cuda.device(idx):
+            rc = call(z.data_ptr(), _DTYPE[dt], u2p_ptr, w_ptr, ld, res.data_ptr(), post_ptr,
+                      gate_ptr, kind, residual_scale, pre_ptr, eps, T, K, D, sum.data_ptr(),
+                      normed_ptr, block_ptr, rstd_ptr, _raw_stream(idx))
+    if rc != 0:
+        raise RouterError("router_combine_norm_fwd", rc)
     return sum, normed, block_out, rstd
 
 
@@ -1225,59 +1271,72 @@ def router_combine_norm_bwd(grad_sum: torch.Tensor | None, grad_normed: torch.Te
     if idx < 0 or dt not in _DTYPE or rows.dim() != 2:
         rows = _rows_2d(rows, "grad_sum", None, _DTYPE)
     T, D = rows.shape
-    dev = rows.device
+    shape, dev = (T, D), rows.device
+    gs_ptr = gn_ptr = x_ptr = y_ptr = rstd_ptr = 0
+    post_ptr = pre_ptr = gate_ptr = kind = gpost_ptr = gpre_ptr = ggate_ptr = ws_ptr = nbytes = 0
     pre, post = pre_weight is not None, post_weight is not None
     if grad_sum is not None:
-        grad_sum = _same_rows(grad_sum, "grad_sum", T, D, dt, idx)
+        grad_sum = _same_rows(grad_sum, "grad_sum", shape, dt, idx)
+        gs_ptr = grad_sum.data_ptr()
     elif not pre:
         raise ValueError("grad_sum must be given without a pre_weight")
     if pre:
         if grad_normed is None or sum is None:
             raise ValueError("pre_weight needs grad_normed and sum")
-        grad_normed = _same_rows(grad_normed, "grad_normed", T, D, dt, idx)
-        sum = _same_rows(sum, "sum", T, D, dt, idx)
+        grad_normed = _same_rows(grad_normed, "grad_normed", shape, dt, idx)
+        sum = _same_rows(sum, "sum", shape, dt, idx)
         pre_weight = _vector(pre_weight, "pre_weight", idx, D)
-        grad_pre_weight = _out(grad_pre_weight, (D,), _F32, dev, "grad_pre_weight")
+        grad_pre_weight = _empty((D,), dtype=_F32, device=dev) if grad_pre_weight is None \
+            else _out(grad_pre_weight, (D,), _F32, dev, "grad_pre_weight")
+        gn_ptr, x_ptr = grad_normed.data_ptr(), sum.data_ptr()
+        pre_ptr, gpre_ptr = pre_weight.data_ptr(), grad_pre_weight.data_ptr()
     else:
-        grad_normed = sum = grad_pre_weight = None
-    gate, kind = _gate(gate, T, D, dt, idx)
+        grad_pre_weight = None
+    if gate is not None:
+        gate, kind = _gate(gate, T, D, dt, idx)
+        grad_gate = _empty(gate.shape, dtype=gate.dtype, device=dev) if grad_gate is None \
+            else _out(grad_gate, tuple(gate.shape), gate.dtype, dev, "grad_gate")
+        gate_ptr, ggate_ptr = gate.data_ptr(), grad_gate.data_ptr()
+    else:
+        grad_gate = None
     if post or kind:
         if block_out is None:
             raise ValueError("post_weight and a gate need block_out")
-        block_out = _same_rows(block_out, "block_out", T, D, dt, idx)
-    else:
-        block_out = None
+        block_out = _same_rows(block_out, "block_out", shape, dt, idx)
+        y_ptr = block_out.data_ptr()
     if post:
         post_weight = _vector(post_weight, "post_weight", idx, D)
-        grad_post_weight = _out(grad_post_weight, (D,), _F32, dev, "grad_post_weight")
+        grad_post_weight = _empty((D,), dtype=_F32, device=dev) if grad_post_weight is None \
+            else _out(grad_post_weight, (D,), _F32, dev, "grad_post_weight")
+        post_ptr, gpost_ptr = post_weight.data_ptr(), grad_post_weight.data_ptr()
     else:
         grad_post_weight = None
-    nbytes = 0
+    calls = _fast or _calls()
     if pre or post:
         if rstd is None or rstd.get_device() != idx or rstd.dtype is not _F32 \
-                or rstd.shape != (T, 2):
-            _bad("rstd", f"a float32 [{T}, 2] tensor on cuda:{idx}")
-        rstd = rstd.contiguous()
-        nbytes = lib().router_combine_norm_bwd_workspace_bytes(T, D)
+                or rstd.shape != (T, 2) or not rstd.is_contiguous():
+            _bad("rstd", f"a contiguous float32 [{T}, 2] tensor on cuda:{idx}")
+        rstd_ptr = rstd.data_ptr()
         if workspace is None:
-            workspace = _empty((max(nbytes, 16),), dtype=_U8, device=dev)
-        elif workspace.get_device() != idx or not workspace.is_contiguous():
-            _bad("workspace", f"a contiguous tensor on cuda:{idx}")
-        nbytes = workspace.numel() * workspace.element_size()
+            nbytes = calls.router_combine_norm_bwd_workspace_bytes(T, D) or 16
+            workspace = _empty((nbytes,), dtype=_U8, device=dev)
+        else:
+            if workspace.get_device() != idx or not workspace.is_contiguous():
+                _bad("workspace", f"a contiguous tensor on cuda:{idx}")
+            nbytes = workspace.numel() * workspace.element_size()
+        ws_ptr = workspace.data_ptr()
+    grad_block = _empty(shape, dtype=dt, device=dev) if grad_block is None \
+        else _out(grad_block, shape, dt, dev, "grad_block")
+    grad_residual = _empty(shape, dtype=dt, device=dev) if grad_residual is None \
+        else _out(grad_residual, shape, dt, dev, "grad_residual")
+    args = (gs_ptr, gn_ptr, _DTYPE[dt], y_ptr, x_ptr, rstd_ptr, post_ptr, gate_ptr, kind,
+            residual_scale, pre_ptr, T, D, grad_block.data_ptr(), grad_residual.data_ptr(),
+            ggate_ptr, gpost_ptr, gpre_ptr, ws_ptr, nbytes)
+    if idx == _cur_dev():
+        rc = calls.router_combine_norm_bwd(*args, _raw_stream(idx))
     else:
-        rstd = workspace = None
-    if kind:
-        grad_gate = _out(grad_gate, tuple(gate.shape), gate.dtype, dev, "grad_gate")
-    else:
-        grad_gate = None
-    grad_block = _out(grad_block, (T, D), dt, dev, "grad_block")
-    grad_residual = _out(grad_residual, (T, D), dt, dev, "grad_residual")
-    with _on(idx):
-        rc = (_fast or _calls()).router_combine_norm_bwd(
-            _ptr0(grad_sum), _ptr0(grad_normed), _DTYPE[dt], _ptr0(block_out), _ptr0(sum),
-            _ptr0(rstd), _ptr0(post_weight), _ptr0(gate), kind, float(residual_scale),
-            _ptr0(pre_weight), T, D, grad_block.data_ptr(), grad_residual.data_ptr(),
-            _ptr0(grad_gate), _ptr0(grad_post_weight), _ptr0(grad_pre_weight), _ptr0(workspace),
-            nbytes, _raw_stream(idx))
-    _check("router_combine_norm_bwd", rc)
+        with torch.cuda.device(idx):
+            rc = calls.router_combine_norm_bwd(*args, _raw_stream(idx))
+    if rc != 0:
+        raise RouterError("router_combine_norm_bwd", rc)
     return grad_block, grad_residual, grad_gate, grad_post_weight, grad_pre_weight

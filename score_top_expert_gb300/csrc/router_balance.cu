@@ -12,14 +12,17 @@
 // Bound by HBM: the forward reads the logits and the choices, the backward reads
 // the logits and writes the gradient; no [T, E] score, map or score gradient exists.
 //
-// Forward: a block takes a contiguous range of tokens, a team of 1 to 6 warps a row at a
-// time.  A lane holds up to 16 logits, the next rows on their way, and the column
-// sums of q of the rows that its team has seen; so a block leaves one row of column sums and
-// one of counts for each sequence that its range touches ("slot": block + sequence,
+// Forward: a block takes a contiguous range of tokens, a warp a row at a time (two warps
+// above 1152 experts).  A lane holds up to 36 logits, the next rows on their way, and the
+// column sums of q of the rows that its team has seen; so a block leaves one row of column
+// sums and one of counts for each sequence that its range touches ("slot": block + sequence,
 // which rises by one or more from each to the next, so no two share one).  A
 // second kernel adds a sequence's slots up in order; its last block to finish adds the
-// blocks' shares.  No floating-point atomics: repeated calls
-// give the same bits.
+// blocks' shares.  No floating-point atomics: repeated calls give the same bits.
+//
+// Few warps to a row: what a row costs beside its values (two reductions, a barrier, its
+// copies' addresses) is paid once a warp.  8192 x 2304 with six warps a row and 12 logits to a
+// lane took 242 instructions a warp and row, 29 us.
 //
 // Backward: the same ranges; a team keeps its sequence's counts in registers.  They
 // enter as c_sj - K n_s / E: a constant less changes nothing, since q sums to one,
@@ -35,13 +38,24 @@
 namespace moe_router {
 namespace {
 
-constexpr int kTeamWarps = 8;      // warps of a block whose rows take one warp each
-constexpr int kRing = 4;           // rows of a team under way
-constexpr int kFinishThreads = 1024;
-constexpr int kFinishGroups = kFinishThreads / 32;  // 32: a warp adds them up
+constexpr int kMostWarps = 8;  // of a block
 
-__host__ __device__ constexpr int ring_bytes(bool vec, int nv, int threads, int bytes) {
-  return vec ? kRing * nv * threads * bytes : 0;
+// By a lane's four-column pieces: a block's threads; the rows of a team under way (about 8 KB a
+// warp, three rows at least: with one row ahead of 9 KB a team waited 2.4 us for each); registers a
+// thread, which fix the blocks of an SM.
+__host__ __device__ constexpr int threads_of(int nv) { return nv <= 6 ? 256 : 192; }
+__host__ __device__ constexpr int ring_rows(int nv, int bytes) {
+  const int n = 8192 / (nv * 32 * bytes);
+  return n < 3 ? 3 : n > 8 ? 8 : n;
+}
+constexpr int registers_of(int nv) { return nv <= 4 ? 80 : nv <= 6 ? 128 : 168; }
+
+// Shared memory of the rows and (8 bytes a thread) of the choices under way.
+__host__ __device__ constexpr int ring_bytes(bool vec, int nv, int bytes) {
+  return vec ? ring_rows(nv, bytes) * nv * threads_of(nv) * bytes : 0;
+}
+__host__ __device__ constexpr int choice_bytes(bool vec, int nv, int bytes) {
+  return vec ? ring_rows(nv, bytes) * threads_of(nv) * 8 : 0;
 }
 
 struct BalanceArgs {
@@ -109,7 +123,7 @@ __device__ __forceinline__ void team_sync(int team, int warps) {
 
 struct Team {
   int warps, team, teams, warp, lane;
-  float* xch;  // [2][teams * warps][2]
+  float* xch;  // [2][teams, warps][2]
   int flip;
 
   // A value summed over the team's warps (at most eight), in the same order in each.  Two
@@ -193,26 +207,24 @@ __device__ __forceinline__ void blank_outside(const Team& t, int E, Row<NV>* r) 
   }
 }
 
-// The rows of a piece of the block's range on their way to the team, through places in
-// shared memory that belong to the thread: the thread waits for its own copies, no
-// barrier is needed, and kRing rows are under way where registers held one.  (Rows that are not
-// aligned are loaded when they are needed.)
-template <int DT, bool VEC, int NV>
+// The rows of the block's range on their way to the team, through places in shared memory
+// that belong to the thread: the thread waits for its own copies, no barrier is needed,
+// and several rows are under way where registers held one.  They are asked for before it
+// is known which sequences they belong to.  A row's choices come along, to the team's
+// first warp.  (Rows that are not aligned are loaded when they are needed.)
+template <int DT, bool VEC, int NV, bool CHOICES>
 struct RowRing {
   static constexpr int kBytes = DT == DT_F32 ? 16 : 8;  // of four logits
-  uint32_t base, end;     // the thread's first place, and behind its last row's
-  uint32_t taken, asked;  // places of the next row to take and to ask for
+  static constexpr int kRing = ring_rows(NV, kBytes);
+  [[maybe_unused]] static constexpr uint32_t kWidth = threads_of(NV) * kBytes;  // of a block's pieces j
+  [[maybe_unused]] static constexpr uint32_t kChoiceWidth = threads_of(NV) * 8;
+  uint32_t base;          // the thread's first place
+  int taken, asked;       // of the next row to take and to ask for, in rows
+  uint32_t choice_base;
   const uint8_t* from;    // the thread's first four logits of the latter
-  size_t stride;          // from one row of the team to the next, in bytes
+  const int32_t* choose;  // the lane's choice of the latter
+  size_t stride, choice_stride;  // from one row of the team to the next, in bytes and choices
   int row, hi;            // the latter's number
-
-  __device__ __forceinline__ uint32_t width() const { return blockDim.x * kBytes; }
-
-  __device__ __forceinline__ void init(const BalanceArgs& a, const Team& t, void* smem) {
-    base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kBytes;
-    end = base + kRing * NV * width();
-    stride = static_cast<size_t>(t.teams) * a.E * (kBytes / 4);
-  }
 
   __device__ __forceinline__ void request(const BalanceArgs& a, const Team& t) {
     if constexpr (VEC) {
@@ -220,34 +232,53 @@ struct RowRing {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (column_of(t, j) < a.E)
-            copy_async<kBytes>(asked + j * width(), from + j * t.warps * (32 * kBytes));
+            copy_async<kBytes>(base + (asked * NV + j) * kWidth, from + j * t.warps * (32 * kBytes));
+        if (CHOICES && t.warp == 0) {
+          const uint32_t to = choice_base + asked * kChoiceWidth;
+          if (t.lane < a.K) copy_async<4>(to, choose);
+          if (t.lane + 32 < a.K) copy_async<4>(to + 4, choose + 32);
+        }
       }
       row += t.teams;
       from += stride;
-      asked += NV * width();
-      if (asked == end) asked = base;
+      choose += choice_stride;
+      if (++asked == kRing) asked = 0;
       copies_commit_group();
     }
   }
 
-  __device__ __forceinline__ void begin(const BalanceArgs& a, const Team& t, int lo, int stop) {
+  __device__ __forceinline__ void begin(const BalanceArgs& a, const Team& t, void* smem, int lo,
+                                        int stop) {
+    base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kBytes;
+    choice_base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
+                  ring_bytes(VEC, NV, kBytes) + threadIdx.x * 8;
     row = lo + t.team;
     hi = stop;
+    stride = static_cast<size_t>(t.teams) * a.E * (kBytes / 4);
+    choice_stride = t.teams * a.ld_choices;
     from = static_cast<const uint8_t*>(a.logits) +
            (static_cast<size_t>(row) * a.E + column_of(t, 0)) * (kBytes / 4);
-    taken = asked = base;
+    choose = a.choices + row * a.ld_choices + t.lane;
+    taken = asked = 0;
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) request(a, t);
   }
 
-  // Row `at_row`, the next in the team's order.
-  __device__ __forceinline__ void take(const BalanceArgs& a, const Team& t, int at_row, Row<NV>* r) {
+  // The team's next row is one of padding.
+  __device__ __forceinline__ void skip(const BalanceArgs& a, const Team& t) {
+    request(a, t);
+    if (++taken == kRing) taken = 0;
+  }
+
+  // Row `at_row`, the team's next, and (first warp) its choices: -1 behind the last.
+  __device__ __forceinline__ void take(const BalanceArgs& a, const Team& t, int at_row, Row<NV>* r,
+                                       int* c0, int* c1) {
     if constexpr (VEC) {
       request(a, t);
-      copies_wait_group(kRing - 1);
+      copies_wait_group<kRing - 1>();
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const uint32_t at = taken + j * width();
+        const uint32_t at = base + (taken * NV + j) * kWidth;
         if constexpr (DT == DT_F32) {
           asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                        : "=f"(r->v[j][0]), "=f"(r->v[j][1]), "=f"(r->v[j][2]), "=f"(r->v[j][3])
@@ -261,31 +292,43 @@ struct RowRing {
           r->v[j][3] = __uint_as_float(y & 0xffff0000u);
         }
       }
-      taken += NV * width();
-      if (taken == end) taken = base;
+      if (CHOICES && t.warp == 0) {
+        int x, y;
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(x), "=r"(y) : "r"(choice_base + taken * kChoiceWidth) : "memory");
+        *c0 = t.lane < a.K ? x : -1;
+        *c1 = t.lane + 32 < a.K ? y : -1;
+      }
+      if (++taken == kRing) taken = 0;
     } else {
       load_row<DT, false>(a, t, at_row, r);
+      if (CHOICES && t.warp == 0) {
+        const int32_t* const c = a.choices + at_row * a.ld_choices + t.lane;
+        *c0 = t.lane < a.K ? c[0] : -1;
+        *c1 = t.lane + 32 < a.K ? c[32] : -1;
+      }
     }
-    blank_outside<VEC>(t, a.E, r);
+    if (a.E < 128 * NV * t.warps) blank_outside<VEC>(t, a.E, r);
   }
 };
 
 template <int DT, bool VEC, int NV, int SF>
-__global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const BalanceArgs a,
-                                                                         int warps) {
-  // the rows under way; teams > 1: [teams, E] column sums; then [E] counts
-  extern __shared__ __align__(16) float dynamic_smem[];
-  __shared__ float xch[2 * kTeamWarps * 2];
-  __shared__ float z_warp[kTeamWarps];
+__global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_fwd_kernel(
+    const BalanceArgs a, int warps) {
+  // the rows and choices under way; [E] column sums; [E] counts
+  extern __shared__ __align__(16) uint8_t dynamic_smem[];
+  __shared__ float xch[2 * kMostWarps * 2];
+  __shared__ float z_warp[kMostWarps];
   __shared__ int first_s;
   pdl_enter();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   Team t = make_team(warps, xch);
-  RowRing<DT, VEC, NV> ring;
-  ring.init(a, t, dynamic_smem);
-  float* const dynamic = dynamic_smem + ring_bytes(VEC, NV, blockDim.x, ring.kBytes) / 4;
-  int* const hist = reinterpret_cast<int*>(dynamic + (t.teams > 1 ? t.teams * a.E : 0));
   const int t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
+  RowRing<DT, VEC, NV, true> ring;
+  ring.begin(a, t, dynamic_smem, t0, t1);
+  float* const block_sums = reinterpret_cast<float*>(
+      dynamic_smem + ring_bytes(VEC, NV, ring.kBytes) + choice_bytes(VEC, NV, ring.kBytes));
+  int* const hist = reinterpret_cast<int*>(block_sums + a.E);
   if (threadIdx.x < 32) {
     const int s = first_sequence(a, t0);
     if (threadIdx.x == 0) first_s = s;
@@ -294,6 +337,7 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const B
   __syncthreads();
   const bool want_z = a.z_coeff != 0.0f;
   float z = 0.0f;
+  int row = t0 + t.team;  // the team's next
   for (int s = first_s, p = t0; s < a.S && p < t1; ++s) {
     int lo, hi;
     sequence_range(a, s, &lo, &hi);
@@ -302,28 +346,17 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const B
     if (lo >= t1) break;
     if (hi <= lo) continue;
     p = hi;
-    ring.begin(a, t, lo, hi);
-    // ---- counts: the choices of the range's tokens -----------------------------------
-    const int32_t* const from = a.choices + lo * a.ld_choices;
-    const int n = (hi - lo) * a.K;
-    if (a.ld_choices == a.K) {
-#pragma unroll 4
-      for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int e = from[i];
-        if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(hist + e, 1);
-      }
-    } else {
-      for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int row = i / a.K;
-        const int e = from[row * a.ld_choices + (i - row * a.K)];
-        if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(hist + e, 1);
-      }
-    }
-    // ---- column sums of q --------------------------------------------------------------
+    for (; row < lo; row += t.teams) ring.skip(a, t);
+    // ---- column sums of q, and counts ----------------------------------------------------
     Row<NV> sums{};
-    for (int row = lo + t.team; row < hi; row += t.teams) {
+    for (; row < hi; row += t.teams) {
       Row<NV> r;
-      ring.take(a, t, row, &r);
+      int c0 = -1, c1 = -1;
+      ring.take(a, t, row, &r, &c0, &c1);
+      if (t.warp == 0) {
+        if (static_cast<unsigned>(c0) < static_cast<unsigned>(a.E)) atomicAdd(hist + c0, 1);
+        if (static_cast<unsigned>(c1) < static_cast<unsigned>(a.E)) atomicAdd(hist + c1, 1);
+      }
       float top = -INFINITY, total = 0.0f, factor;
       if (SF == SF_SOFTMAX || want_z) {
 #pragma unroll
@@ -382,39 +415,38 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const B
 #pragma unroll
         for (int u = 0; u < 4; ++u) sums.v[j][u] = fmaf(r.v[j][u], factor, sums.v[j][u]);
     }
-    // ---- the slot of this block and sequence ---------------------------------------------
-    const size_t slot = (static_cast<size_t>(blockIdx.x) + s) * a.E;
-    if (t.teams > 1) {
-      float* const mine = dynamic + t.team * a.E;
+    // ---- the slot of this block and sequence: the teams' sums one after the other --------
+    for (int w = 0; w < t.teams; ++w) {
+      if (t.team == w) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = column_of(t, j);
+        for (int j = 0; j < NV; ++j) {
+          const int c = column_of(t, j);
+          if constexpr (VEC) {
+            float4* const to = reinterpret_cast<float4*>(block_sums + c);
+            if (c < a.E) {
+              const float4 v = w == 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *to;
+              *to = make_float4(v.x + sums.v[j][0], v.y + sums.v[j][1], v.z + sums.v[j][2],
+                                v.w + sums.v[j][3]);
+            }
+          } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (c + u < a.E) mine[c + u] = sums.v[j][u];
-      }
-      __syncthreads();
-      for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        float v = dynamic[e];
-        for (int w = 1; w < t.teams; ++w) v += dynamic[w * a.E + e];
-        a.slot_sums[slot + e] = v;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = column_of(t, j);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (c + u < a.E) a.slot_sums[slot + c + u] = sums.v[j][u];
+            for (int u = 0; u < 4; ++u)
+              if (c + u < a.E)
+                block_sums[c + u] = (w == 0 ? 0.0f : block_sums[c + u]) + sums.v[j][u];
+          }
+        }
       }
       __syncthreads();
     }
+    const size_t slot = (static_cast<size_t>(blockIdx.x) + s) * a.E;
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+      a.slot_sums[slot + e] = block_sums[e];
       a.slot_counts[slot + e] = hist[e];
       hist[e] = 0;
     }
     __syncthreads();
   }
+  copies_wait_group<0>();  // (rows of padding that nobody took)
   // every lane of a team has its rows' z: the first of each counts
   if (t.lane == 0) z_warp[threadIdx.x >> 5] = t.warp == 0 ? z : 0.0f;
   __syncthreads();
@@ -425,76 +457,97 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_fwd_kernel(const B
   }
 }
 
-// Adds up each sequence's slots: 128 columns and one sequence at a time, 16 warps on
-// every 16th slot each; then counts times sums, and the last block the whole.
-__global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(const BalanceArgs a) {
-  __shared__ float sums[kFinishGroups][128];
-  __shared__ int counts[kFinishGroups][128];
-  __shared__ float shared[2][kFinishGroups];
+// Adds up each sequence's slots, then counts times sums, and the last block the whole.  An item is
+// a sequence and 32 WIDE columns: GROUPS warps take every GROUPS-th slot each.  With few
+// slots to a sequence a warp takes an item by itself, 128 columns wide.
+template <int GROUPS, int WIDE, int WARPS>
+__global__ __launch_bounds__(32 * WARPS) void balance_finish_kernel(const BalanceArgs a) {
+  constexpr int kCols = 32 * WIDE, kItems = WARPS / GROUPS;
+  __shared__ float sums[GROUPS == 1 ? 1 : GROUPS][kCols];
+  __shared__ int counts[GROUPS == 1 ? 1 : GROUPS][kCols];
+  __shared__ float shared[2][WARPS];
   __shared__ int last;
   pdl_enter();
-  const int tiles = (a.E + 127) / 128;
+  const int tiles = (a.E + kCols - 1) / kCols;
   const long long items = static_cast<long long>(tiles) * a.S;
-  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5;
-  const bool vec = (a.E & 3) == 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp % GROUPS;
+  const bool vec = WIDE == 4 && (a.E & 3) == 0;
   float share = 0.0f;
-  for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+  for (long long item = static_cast<long long>(blockIdx.x) * kItems + warp / GROUPS; item < items;
+       item += static_cast<long long>(gridDim.x) * kItems) {
     const int s = static_cast<int>(item / tiles);
-    const int c = static_cast<int>(item - static_cast<long long>(s) * tiles) * 128 + 4 * lane;
+    const int c = static_cast<int>(item - static_cast<long long>(s) * tiles) * kCols + WIDE * lane;
     int lo, hi;
     sequence_range(a, s, &lo, &hi);
     const int b0 = lo / a.rows, b1 = hi > lo ? (hi - 1) / a.rows : b0 - 1;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int n[4] = {0, 0, 0, 0};
-    if (vec && c < a.E) {
-#pragma unroll 8
-      for (int b = b0 + group; b <= b1; b += kFinishGroups) {
-        const size_t at = (static_cast<size_t>(b) + s) * a.E + c;
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.slot_sums + at));
-        const int4 k = __ldcg(reinterpret_cast<const int4*>(a.slot_counts + at));
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        n[0] += k.x; n[1] += k.y; n[2] += k.z; n[3] += k.w;
+    float v[WIDE];
+    int n[WIDE];
+#pragma unroll
+    for (int u = 0; u < WIDE; ++u) {
+      v[u] = 0.0f;
+      n[u] = 0;
+    }
+    if (vec) {
+      if (c < a.E) {
+#pragma unroll 4
+        for (int b = b0 + group; b <= b1; b += GROUPS) {
+          const size_t at = (static_cast<size_t>(b) + s) * a.E + c;
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(a.slot_sums + at));
+          const int4 k = __ldcg(reinterpret_cast<const int4*>(a.slot_counts + at));
+          v[0] += x.x; n[0] += k.x;
+          if constexpr (WIDE == 4) {
+            v[1] += x.y; v[2] += x.z; v[3] += x.w;
+            n[1] += k.y; n[2] += k.z; n[3] += k.w;
+          }
+        }
       }
-    } else if (!vec) {
-      for (int b = b0 + group; b <= b1; b += kFinishGroups) {
+    } else {
+#pragma unroll 8
+      for (int b = b0 + group; b <= b1; b += GROUPS) {
         const size_t at = (static_cast<size_t>(b) + s) * a.E + c;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < WIDE; ++u)
           if (c + u < a.E) {
             v[u] += __ldcg(a.slot_sums + at + u);
             n[u] += __ldcg(a.slot_counts + at + u);
           }
       }
     }
+    const float by_tokens = 1.0f / static_cast<float>(max(hi - lo, 1));
+    if constexpr (GROUPS > 1) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      sums[group][4 * lane + u] = v[u];
-      counts[group][4 * lane + u] = n[u];
-    }
-    __syncthreads();
-    const int e = static_cast<int>(item - static_cast<long long>(s) * tiles) * 128 +
-                  static_cast<int>(threadIdx.x);
-    if (threadIdx.x < 128 && e < a.E) {
-      float p = 0.0f;
-      int k = 0;
-      const int groups = min(kFinishGroups, b1 - b0 + 1);
-      for (int g = 0; g < groups; ++g) {
-        p += sums[g][threadIdx.x];
-        k += counts[g][threadIdx.x];
+      for (int u = 0; u < WIDE; ++u) {
+        sums[group][WIDE * lane + u] = v[u];
+        counts[group][WIDE * lane + u] = n[u];
       }
-      a.counts[static_cast<size_t>(s) * a.E + e] = k;
-      // c_se P_se / n_s^2 (the factors that all share come last)
-      const float by_tokens = 1.0f / static_cast<float>(max(hi - lo, 1));
-      share = fmaf(static_cast<float>(k) * by_tokens, p * by_tokens, share);
+      __syncthreads();
+      if (warp == 0) {
+        const int groups = min(GROUPS, b1 - b0 + 1);
+        for (int g = 1; g < groups; ++g)
+#pragma unroll
+          for (int u = 0; u < WIDE; ++u) {
+            v[u] += sums[g][WIDE * lane + u];
+            n[u] += counts[g][WIDE * lane + u];
+          }
+      }
+      __syncthreads();
     }
-    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int u = 0; u < WIDE; ++u)
+        if (c + u < a.E) {
+          a.counts[static_cast<size_t>(s) * a.E + c + u] = n[u];
+          // c_se P_se / n_s^2 (the factors that all share come last)
+          share = fmaf(static_cast<float>(n[u]) * by_tokens, v[u] * by_tokens, share);
+        }
+    }
   }
   share = seg_sum<32>(share);
-  if (lane == 0) shared[0][group] = share;
+  if (lane == 0) shared[0][warp] = share;
   __syncthreads();
   if (threadIdx.x == 0) {
-    // threads 0 .. 127 have the shares
-    a.parts[blockIdx.x] = (shared[0][0] + shared[0][1]) + (shared[0][2] + shared[0][3]);
+    for (int w = GROUPS; w < WARPS; w += GROUPS) share += shared[0][w];
+    a.parts[blockIdx.x] = share;
     __threadfence();
     last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
   }
@@ -503,19 +556,20 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(const Ba
   __threadfence();
   // the blocks' shares and the ranges' z: each thread its own few, then in a fixed order
   float balance = 0.0f, z = 0.0f;
-  for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += kFinishThreads)
+  for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += 32 * WARPS)
     balance += __ldcg(a.parts + b);
-  for (int b = threadIdx.x; b < a.blocks; b += kFinishThreads) z += __ldcg(a.z_parts + b);
+  if (a.z_coeff != 0.0f)
+    for (int b = threadIdx.x; b < a.blocks; b += 32 * WARPS) z += __ldcg(a.z_parts + b);
   balance = seg_sum<32>(balance);
   z = seg_sum<32>(z);
   if (lane == 0) {
-    shared[0][group] = balance;
-    shared[1][group] = z;
+    shared[0][warp] = balance;
+    shared[1][warp] = z;
   }
   __syncthreads();
-  if (group == 0) {
-    balance = seg_sum<32>(shared[0][lane]);
-    z = seg_sum<32>(shared[1][lane]);
+  if (warp == 0) {
+    balance = seg_sum<32>(lane < WARPS ? shared[0][lane] : 0.0f);
+    z = seg_sum<32>(lane < WARPS ? shared[1][lane] : 0.0f);
     int lo, hi, unused;
     sequence_range(a, 0, &lo, &unused);
     sequence_range(a, a.S - 1, &unused, &hi);
@@ -527,16 +581,16 @@ __global__ __launch_bounds__(kFinishThreads) void balance_finish_kernel(const Ba
 }
 
 template <int DT, bool VEC, int NV, int SF>
-__global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_bwd_kernel(const BalanceArgs a,
-                                                                         int warps) {
-  extern __shared__ __align__(16) float dynamic_smem[];  // the rows under way
-  __shared__ float xch[2 * kTeamWarps * 2];
+__global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_bwd_kernel(
+    const BalanceArgs a, int warps) {
+  extern __shared__ __align__(16) uint8_t dynamic_smem[];  // the rows under way
+  __shared__ float xch[2 * kMostWarps * 2];
   __shared__ int first_s;
   pdl_enter();
   Team t = make_team(warps, xch);
-  RowRing<DT, VEC, NV> ring;
-  ring.init(a, t, dynamic_smem);
   const int t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
+  RowRing<DT, VEC, NV, false> ring;
+  ring.begin(a, t, dynamic_smem, t0, t1);
   if (threadIdx.x < 32) {
     const int s = first_sequence(a, t0);
     if (threadIdx.x == 0) first_s = s;
@@ -550,18 +604,20 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_bwd_kernel(const B
                          ? 0.0f
                          : a.grad_loss[1] * a.z_coeff * 2.0f /
                                static_cast<float>(max(whole_hi - whole_lo, 1));
+  int row = t0 + t.team;  // the team's next
   // rows of no sequence: zeros
-  auto clear = [&](int from, int to) {
+  auto clear = [&](int to) {
     const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int row = from + t.team; row < to; row += t.teams)
+    for (; row < to; row += t.teams) {
+      ring.skip(a, t);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = column_of(t, j);
         if (c < a.E) store4<DT, VEC>(a.grad, static_cast<size_t>(row) * a.E, c, a.E, none);
       }
+    }
   };
-  int p = t0;
-  for (int s = first_s; s < a.S && p < t1; ++s) {
+  for (int s = first_s, p = t0; s < a.S && p < t1; ++s) {
     int lo, hi;
     sequence_range(a, s, &lo, &hi);
     const float tokens = static_cast<float>(hi - lo);
@@ -569,11 +625,10 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_bwd_kernel(const B
     hi = min(hi, t1);
     if (lo >= t1) break;
     if (hi <= lo) continue;
-    clear(p, lo);
     p = hi;
+    clear(lo);
     const float scale = by_balance * (static_cast<float>(a.E) / a.K) / tokens / tokens;
     const float mean = tokens * a.K / a.E;
-    ring.begin(a, t, lo, hi);
     Row<NV> c;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -584,12 +639,13 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_bwd_kernel(const B
                         ? static_cast<float>(a.counts[static_cast<size_t>(s) * a.E + col + u]) - mean
                         : 0.0f;
     }
-    float2 next_st = lo + t.team < hi ? a.stats[lo + t.team] : make_float2(0.0f, 1.0f);
-    for (int row = lo + t.team; row < hi; row += t.teams) {
+    float2 next_st = row < hi ? a.stats[row] : make_float2(0.0f, 1.0f);
+    for (; row < hi; row += t.teams) {
       const float2 st = next_st;
       if (row + t.teams < hi) next_st = a.stats[row + t.teams];
       Row<NV> r;
-      ring.take(a, t, row, &r);
+      int none0, none1;
+      ring.take(a, t, row, &r, &none0, &none1);
       const float inv = rcp_approx(SF == SF_SOFTMAX ? st.y : st.x);
       const float shift = (SF == SF_SOFTMAX ? st.x : st.y) * kLog2e;
       float z = 0.0f;
@@ -630,43 +686,35 @@ __global__ __launch_bounds__(32 * kTeamWarps, 3) void balance_bwd_kernel(const B
       }
     }
   }
-  clear(p, t1);
+  clear(t1);
+  copies_wait_group<0>();
 }
 
 // ---- host ------------------------------------------------------------------------
-// Warps of a row and times four columns of a lane: as few idle ones as possible, then
-// as few warps.  At most 6 warps of 3 for 2304 experts.
+// Warps of a row and times four columns of a lane: the fewest warps, then the fewest pieces
+// that are built.
 struct Shape {
   int warps, nv, teams;
 };
 
 Shape shape_of(int E) {
-  const int pieces = (E + 127) / 128;
-  Shape best{0, 0, 0};
-  int least = INT_MAX;
-  for (int nv = 4; nv >= 1; --nv) {
-    const int warps = (pieces + nv - 1) / nv;
-    if (warps > kTeamWarps) continue;
-    const int idle = warps * nv - pieces;
-    if (idle < least) {
-      least = idle;
-      best = Shape{warps, nv, kTeamWarps / warps};
-    }
-  }
-  return best;
+  const int pieces = (E + 127) / 128;  // at most 18
+  const int warps = pieces <= 9 ? 1 : 2, least = (pieces + warps - 1) / warps;
+  const int nv = least <= 2 ? least : least <= 4 ? 4 : least <= 6 ? 6 : 9;
+  return Shape{warps, nv, threads_of(nv) / 32 / warps};
 }
 
 size_t smem_of(int E, const Shape& sh, bool vec, int bytes, bool forward) {
-  return ring_bytes(vec, sh.nv, 32 * sh.warps * sh.teams, bytes) +
-         (forward ? static_cast<size_t>(sh.teams > 1 ? sh.teams + 1 : 1) * E * 4 : 0);
+  const size_t ring = ring_bytes(vec, sh.nv, bytes);
+  return forward ? ring + choice_bytes(vec, sh.nv, bytes) + static_cast<size_t>(E) * 8 : ring;
 }
 
-// Blocks that an SM holds (80 registers a thread, 227 KB), four at most: a block more than
-// that would run by itself behind the others.
-constexpr int kMostPerSm = 4;
+// Blocks that an SM holds, by registers and shared memory: a block more than that would run
+// by itself behind the others.
+constexpr int kMostPerSm = 3;
 
 int blocks_per_sm(const Shape& sh, size_t smem) {
-  const int by_registers = 65536 / (80 * 32 * sh.warps * sh.teams);
+  const int by_registers = 65536 / (registers_of(sh.nv) * threads_of(sh.nv));
   const int by_memory = static_cast<int>(227 * 1024 / (smem + 2048));
   const int n = by_registers < by_memory ? by_registers : by_memory;
   return n < 1 ? 1 : n > kMostPerSm ? kMostPerSm : n;
@@ -680,7 +728,7 @@ int rows_of(int T, int teams, int per_sm) {
   return (rows < 2 * teams ? 2 * teams : (rows + teams - 1) / teams * teams);
 }
 
-constexpr int kFinishBlocks = 304;
+constexpr int kFinishBlocks = 608;
 
 int blocks_of(int T, int rows) { return T == 0 ? 1 : (T + rows - 1) / rows; }
 
@@ -696,7 +744,7 @@ Workspace workspace_of(int T, int E, int S) {
   w.slots = up((static_cast<size_t>(blocks) + S) * E * 4);
   w.z = 2 * w.slots;
   w.parts = w.z + up(static_cast<size_t>(blocks) * 4);
-  w.ticket = w.parts + kFinishBlocks * 8;
+  w.ticket = w.parts + up(kFinishBlocks * 4);
   w.bytes = w.ticket + 256;
   return w;
 }
@@ -727,14 +775,33 @@ cudaError_t launch_rows(const BalanceArgs& a, dim3 grid, dim3 block, size_t smem
 
 template <int DT, bool VEC, int SF, bool FWD>
 cudaError_t launch_nv(const BalanceArgs& a, const Shape& sh, cudaStream_t st) {
-  const dim3 grid(a.blocks), block(32 * sh.warps * sh.teams);
+  const dim3 grid(a.blocks), block(threads_of(sh.nv));
   const size_t smem = smem_of(a.E, sh, VEC, DT == DT_F32 ? 16 : 8, FWD);
   switch (sh.nv) {
     case 1: return launch_rows<DT, VEC, 1, SF, FWD>(a, grid, block, smem, sh.warps, st);
     case 2: return launch_rows<DT, VEC, 2, SF, FWD>(a, grid, block, smem, sh.warps, st);
-    case 3: return launch_rows<DT, VEC, 3, SF, FWD>(a, grid, block, smem, sh.warps, st);
-    default: return launch_rows<DT, VEC, 4, SF, FWD>(a, grid, block, smem, sh.warps, st);
+    case 4: return launch_rows<DT, VEC, 4, SF, FWD>(a, grid, block, smem, sh.warps, st);
+    case 6: return launch_rows<DT, VEC, 6, SF, FWD>(a, grid, block, smem, sh.warps, st);
+    default: return launch_rows<DT, VEC, 9, SF, FWD>(a, grid, block, smem, sh.warps, st);
   }
+}
+
+// Slots to a sequence up to which a warp adds them up by itself (512 sequences of 16 tokens, 2304
+// experts: 32 warps to each took 100 us).
+constexpr int kFewSlots = 8;
+
+cudaError_t launch_finish(const BalanceArgs& a, cudaStream_t st) {
+  const auto grid = [](long long items, int each, int most) {
+    const long long n = (items + each - 1) / each;
+    return dim3(static_cast<unsigned>(n < most ? n : most));
+  };
+  if (a.blocks / a.S + 1 <= kFewSlots)
+    return launch_kernel(balance_finish_kernel<1, 4, 8>,
+                         grid(static_cast<long long>((a.E + 127) / 128) * a.S, 8, kFinishBlocks),
+                         dim3(256), 0, st, a);
+  return launch_kernel(balance_finish_kernel<32, 1, 32>,
+                       grid(static_cast<long long>((a.E + 31) / 32) * a.S, 1, kFinishBlocks),
+                       dim3(1024), 0, st, a);
 }
 
 template <bool FWD>
@@ -804,11 +871,7 @@ int router_balance_loss_fwd(const void* logits, mr_dtype dtype, const int32_t* t
   a.z_coeff = z_coeff;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (launch_balance<true>(a, dtype, score_func, vec, sh, st) != cudaSuccess) return MR_ERR_CUDA;
-  const long long items = static_cast<long long>((E + 127) / 128) * S;
-  const dim3 grid(static_cast<unsigned>(items < kFinishBlocks ? items : kFinishBlocks));
-  return launch_kernel(balance_finish_kernel, grid, dim3(kFinishThreads), 0, st, a) == cudaSuccess
-             ? MR_OK
-             : MR_ERR_CUDA;
+  return launch_finish(a, st) == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }
 
 int router_balance_loss_bwd(const float* grad_loss, const void* logits, mr_dtype dtype,

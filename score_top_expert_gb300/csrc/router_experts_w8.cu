@@ -10,14 +10,19 @@
 // while it stays below 2^24 (and off by about 2^-30 of its value a term above that).
 //
 // The tiles and their order are those of router_experts_tc.cu's forward: 128 or 256 weight
-// rows by up to 128 or 256 of the expert's rows, one CTA or a pair.  Sixteen warps load
-// stages of 128 columns: eight lanes a row (whole lines: a request of 64-byte pieces took 11
-// wavefronts of the load pipe, the products' stages with it 1.4 times as long), two rows of
-// both operands a thread, kAhead stages ahead of the one that it widens and stores in the
-// layout that the tensor cores read.  In a pair each CTA's loading warps arrive on its own
-// barrier and one warp of the second CTA passes that on to the leader's by an
-// asynchronous store: an arrival with release semantics of cluster scope held it for about
-// 1500 cycles a stage.
+// rows by up to 128 or 256 of the expert's rows, one CTA or a pair.  Stages hold 128 columns;
+// two groups of eight warps load alternate ones: eight lanes a row (whole lines: a request of
+// 64-byte pieces took 11 wavefronts of the load pipe), four rows of both operands a thread, each
+// piece asked for two stages ahead in the registers that its predecessor has just left, widened
+// and stored in the layout that the tensor cores read.  One group's stores (half of the
+// shared memory's time) pass while the other fetches and waits: with all sixteen warps on
+// each stage, 8192 tokens, 8 experts, 4096 x 4096 took 390 us.
+//
+// In a pair each CTA's loading warps arrive on its own barrier and one warp of the second
+// CTA passes that on to the leader's by an asynchronous store: an arrival with release
+// semantics of cluster scope held it for about 1500 cycles a stage.  A tile's lookup and its
+// scales' loads are made a tile ahead: made where they were needed they took 5000 of the
+// 10400 cycles of a tile with 43 rows and four stages.
 #include <atomic>
 
 #include "router_experts_tiles.cuh"
@@ -26,11 +31,11 @@
 namespace moe_router {
 namespace {
 
-constexpr int kLoaders = 16;
-constexpr int kThreads = 32 * (8 + kLoaders);
+constexpr int kLoaders = 8;  // warps of each of the two groups
+constexpr int kThreads = 32 * (8 + 2 * kLoaders);
 constexpr int kStages = 3;
 constexpr int kWide = 128;   // columns of a stage: two of the layout's 128-byte rows in fp16
-constexpr int kAhead = 2;    // stages that a thread holds
+constexpr int kOwn = 4;      // rows of each operand that a thread loads, 32 apart
 constexpr int kMostStages = 7;  // of a fp32 output's sum
 constexpr int kRowsA = 128;  // weight rows of a CTA
 constexpr int kRowsB = 128;  // most rows of x of a CTA
@@ -54,7 +59,7 @@ struct W8TcArgs {
   const int8_t* w;
   const float* x_scales;
   const float* w_scales;
-  int out_f32;
+  uint32_t inv_a;  // inverse_of the weight's slices
 };
 
 // 16 consecutive bytes of a row, VB bytes an access, of which `left` (a multiple of VB, or
@@ -132,6 +137,49 @@ __device__ __forceinline__ bool wait_cluster(const Waiter& w, uint64_t* bar, uin
   return false;
 }
 
+// Arrives on a barrier of the pair's leader once the warp's tensor-memory loads are complete.
+// Relaxed: nothing else is published, and an arrival with release semantics waits for the
+// output's stores.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// find_tile by a whole warp: 32 probes at a time, and divisions only for an expert of
+// several row tiles.
+template <typename S>
+__device__ __forceinline__ Tile find_tile_by_warp(const TcArgs& g, const int* prefix,
+                                                  const int* offs, int tile, int slices_a,
+                                                  uint32_t inv_a) {
+  const int lane = threadIdx.x & 31;
+  int q = static_cast<int>(__umulhi(static_cast<uint32_t>(tile), inv_a));  // tile / slices_a, or one less
+  if (tile - q * slices_a >= slices_a) ++q;
+  int lo = 0, width = g.E;  // prefix[lo] <= q < prefix[lo + width]
+  while (width > 1) {
+    const int step = (width + 31) / 32;
+    const bool below = lane * step < width && prefix[lo + lane * step] <= q;
+    const int n = __popc(__ballot_sync(0xffffffffu, below)) - 1;
+    lo += n * step;
+    width = min(step, width - n * step);
+  }
+  Tile t;
+  t.e = lo;
+  t.b0 = 0;
+  const int first = prefix[lo], of = prefix[lo + 1] - first;
+  const int from = offs[lo], to = max(offs[lo + 1], from);
+  int a = tile - first * slices_a, r = 0, each = to - from;
+  if (of > 1) {
+    const int at = a;
+    a = at / of;  // one slice of the weight, all row tiles, then the next
+    r = at - a * of;
+    each = (each + of - 1) / of;
+  }
+  each = (each + S::kRound - 1) / S::kRound * S::kRound;
+  t.a0 = a * S::kTileA;
+  t.start = from + r * each;
+  t.cnt = min(each, to - t.start);
+  return t;
+}
+
 template <int CG, int VB, bool F32>
 __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8TcArgs args) {
   using S = Shape<CG>;
@@ -165,78 +213,82 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
   if (warp == 2) tmem_alloc<CG>(&tmem_at, S::kColumns);
   pdl_enter();
   for (int e = threadIdx.x; e <= g.E; e += blockDim.x) offs[e] = min(max(g.offsets[e], 0), g.P);
-  const int tiles = expert_tile_prefix(g.offsets, g.E, g.P, S::kTileB, prefix, tmp) *
-                    ((g.N + S::kTileA - 1) / S::kTileA);
+  const int slices_a = (g.N + S::kTileA - 1) / S::kTileA;
+  const int tiles = expert_tile_prefix(g.offsets, g.E, g.P, S::kTileB, prefix, tmp) * slices_a;
   tc_fence_before();
   if constexpr (CG == 2) cluster_sync(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_at;
   const Waiter wait{&gave_up, g.status};
   const int first = static_cast<int>(blockIdx.x) / CG, step = static_cast<int>(gridDim.x) / CG;
+  const auto find = [&](int tile) {
+    return find_tile_by_warp<S>(g, prefix, offs, tile, slices_a, args.inv_a);
+  };
   const int slices = (g.D + kWide - 1) / kWide;
 
   if (warp >= 8) {
     // ---- loads -----------------------------------------------------------------
-    const int row = (static_cast<int>(threadIdx.x) - 256) >> 3;
+    const int group = (warp - 8) / kLoaders;
+    const int row = ((static_cast<int>(threadIdx.x) - 256) & (32 * kLoaders - 1)) >> 3;
     const int piece = threadIdx.x & 7;  // of the eight of a row and stage
-    // the load cursor, kAhead stages ahead of the stores; rows `row` and row + 64 of both
-    // operands
-    int li = first, ls = 0;
-    const int8_t *pa[2] = {}, *pb[2] = {};
-    int left_a[2] = {}, left_b[2] = {};  // bytes of the row from this thread's piece on
-    uint32_t wanted = 0;                 // by row: the tile has it (rounded up)
-    auto enter = [&]() {                 // tile li
-      const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, li);
+    const size_t far = static_cast<size_t>(32) * g.D;
+    // the cursor: tile li, stage ls of it, this thread's rows row + 32 h of both operands
+    int li = first, ls = group;
+    const int8_t* pa = nullptr;
+    int source[kOwn];     // rows of x, -1: none
+    uint32_t has_a = 0, wanted = 0;  // by h: the weight has the row; the tile has (rounded up)
+    auto enter = [&]() {
+      const Tile t = find(li);
+      const int n = t.a0 + static_cast<int>(rank) * kRowsA + row;
+      pa = args.w + (static_cast<size_t>(t.e) * g.N + n) * g.D + piece * 16;
       const int half = (t.cnt + S::kRound - 1) / S::kRound * S::kRound / CG;
-      const int at = piece * 16;
-      wanted = 0;
+      has_a = wanted = 0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = row + 64 * h;
-        const int n = t.a0 + static_cast<int>(rank) * kRowsA + r;
-        pa[h] = args.w + (static_cast<size_t>(t.e) * g.N + n) * g.D + at;
-        left_a[h] = n < g.N ? g.D - at : 0;
-        const int b = static_cast<int>(rank) * half + r;
-        int source = -1;
+      for (int h = 0; h < kOwn; ++h) {
+        const int r = row + 32 * h, b = static_cast<int>(rank) * half + r;
+        if (n + 32 * h < g.N) has_a |= 1u << h;
+        source[h] = -1;
         if (r < half) {
           wanted |= 1u << h;
-          if (b < t.cnt) source = g.p2u == nullptr ? t.start + b : g.p2u[t.start + b];
-          if (g.p2u != nullptr && source >= 0) source = token_of(g, source);
+          if (b < t.cnt) source[h] = g.p2u == nullptr ? t.start + b : g.p2u[t.start + b];
         }
-        pb[h] = args.x + static_cast<size_t>(max(source, 0)) * g.D + at;
-        left_b[h] = source >= 0 ? g.D - at : 0;
+      }
+      if (g.p2u != nullptr) {
+#pragma unroll
+        for (int h = 0; h < kOwn; ++h)
+          if (source[h] >= 0) source[h] = token_of(g, source[h]);
       }
     };
-    uint4 a[kAhead][2], b[kAhead][2];
-    uint32_t valid = 0, keep = 0;  // by slot: holds a slice; its rows of x are stored
-    auto fetch = [&](int j) {
-      if (li >= tiles) {
-        valid &= ~(1u << j);
-        return;
-      }
-      valid |= 1u << j;
-      keep = (keep & ~(3u << (2 * j))) | (wanted << (2 * j));
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        a[j][h] = load_piece<VB>(pa[h], left_a[h]);
-        b[j][h] = load_piece<VB>(pb[h], left_b[h]);
-        pa[h] += kWide;
-        pb[h] += kWide;
-        left_a[h] -= kWide;
-        left_b[h] -= kWide;
-      }
-      if (++ls == slices) {
-        ls = 0;
+    auto settle = [&]() {  // the cursor behind its tile's last stage: on to the tile that has it
+      if (ls < slices) return;
+      do {
+        ls -= slices;
         li += step;
-        if (li < tiles) enter();
-      }
+      } while (ls >= slices && li < tiles);
+      if (li < tiles) enter();
     };
-    if (li < tiles) enter();
+    uint4 a[kOwn], b[kOwn];
+    auto load_a = [&](int h) {
+      const int at = ls * kWide;
+      a[h] = load_piece<VB>(pa + at + h * far, has_a >> h & 1u ? g.D - piece * 16 - at : 0);
+    };
+    auto load_b = [&](int h) {
+      const int at = piece * 16 + ls * kWide;
+      b[h] = load_piece<VB>(args.x + static_cast<size_t>(max(source[h], 0)) * g.D + at,
+                            source[h] >= 0 ? g.D - at : 0);
+    };
+    if (ls >= slices) settle();
+    else if (li < tiles) enter();
+    if (li < tiles) {
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) fetch(j);
-    int stage = 0;
+      for (int h = 0; h < kOwn; ++h) {
+        load_a(h);
+        load_b(h);
+      }
+    }
+    int stage = group;
     uint32_t parity = 1;  // the first pass finds the stages empty
-    // The piece is two of the eight in a row of the 128-byte swizzle, row + 64 alike.  The
+    // The piece is two of the eight in a row of the 128-byte swizzle, rows 32 apart alike.  The
     // lanes of a row's second half store the second first: the eight of a row then meet
     // all banks.
     const uint32_t half_at = row * 128 + (piece >> 2) * kHalf;
@@ -248,27 +300,32 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
       store_wide(at + to0, swap ? v.z : v.x, swap ? v.w : v.y);
       store_wide(at + to1, swap ? v.x : v.z, swap ? v.y : v.w);
     };
-    bool ok = true;
-    while (ok && valid != 0) {
+    while (li < tiles) {
+      const uint32_t keep = wanted;
+      ls += 2;
+      settle();
+      const bool more = li < tiles;
+      if (!__all_sync(0xffffffffu, wait(&empty[stage], parity))) break;
+      const uint32_t at = stages_at + stage * kStageBytes;
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (!ok || !(valid >> j & 1u)) break;
-        ok = __all_sync(0xffffffffu, wait(&empty[stage], parity));
-        if (!ok) break;
-        const uint32_t at = stages_at + stage * kStageBytes;
+      for (int h = 0; h < kOwn; ++h) {
+        store_piece(at + h * 4096, a[h]);
+        if (more) load_a(h);
+      }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          store_piece(at + h * 8192, a[j][h]);
-          if (keep >> (2 * j + h) & 1u) store_piece(at + kBytesA + h * 8192, b[j][h]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          parity ^= 1;
-        }
-        fetch(j);
+      for (int h = 0; h < kOwn; ++h) {
+        if (keep >> h & 1u) store_piece(at + kBytesA + h * 4096, b[h]);
+        if (more) load_b(h);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[stage]);
+      // Three stages, two groups: a group's next use of a stage lies two phases on, the other
+      // group's between them; its wait for the stage in between has seen the earlier phase end.
+      stage += 2;
+      if (stage >= kStages) {
+        stage -= kStages;
+        parity ^= 1;
       }
     }
   } else if (warp == 3 && CG == 2 && rank == 1) {
@@ -296,8 +353,10 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
     const int segment = segment_of<F32>(slices, kMostStages);
     if (CG == 2 && lane == 0)
       for (int i = 0; i < kStages; ++i) mbar_expect_tx_cluster(smem_addr(&peer[i]), 4);
+    Tile t{};
+    if (first < tiles) t = find(first);
     for (int i = first; i < tiles && ok; i += step) {
-      const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, i);
+      Tile nt = t;
       const int cols = (t.cnt + S::kRound - 1) / S::kRound * S::kRound;
       const uint32_t desc = half_product_desc(S::kTileA, cols);
       for (int s0 = 0; s0 < slices && ok; s0 += segment) {
@@ -332,9 +391,12 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
             stage = 0;
             parity ^= 1;
           }
+          // the next tile is looked up while this stage is computed
+          if (s == 0 && i + step < tiles) nt = find(i + step);
         }
         ++n;
       }
+      t = nt;
     }
   } else if (warp >= 4 && warp < 8) {
     // ---- stores --------------------------------------------------------------------
@@ -342,21 +404,37 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
     int n = 0;
     bool ok = true;
     const int segment = segment_of<F32>(slices, kMostStages);
-    for (int i = first; i < tiles && ok; i += step) {
-      const Tile t = find_tile<EX_FWD, S>(g, prefix, offs, i);
-      // the rows' scales, while the tile is computed; each warp its own copy, so that one
-      // that gives up leaves none waiting
-      float* const by_row = row_scales[quad];
-      __syncwarp();
-      for (int b = lane; b < t.cnt; b += 32) {
-        int source = g.p2u == nullptr ? t.start + b : g.p2u[t.start + b];
-        if (g.p2u != nullptr && source >= 0) source = token_of(g, source);
-        by_row[b] = source >= 0 ? args.x_scales[source] : 0.0f;
+    // a tile's scales are asked for a tile ahead; each warp has its own copy of the rows', so
+    // that one that gives up leaves none waiting
+    float* const by_row = row_scales[quad];
+    float scale[S::kTileB / 32], next_channel = 0.0f;
+    Tile nt{};
+    auto look = [&](int tile) {
+      nt = find(tile);
+      int source[S::kTileB / 32];
+#pragma unroll
+      for (int j = 0; j < S::kTileB / 32; ++j) {
+        const int b = lane + 32 * j;
+        source[j] = b >= nt.cnt ? -1 : g.p2u == nullptr ? nt.start + b : g.p2u[nt.start + b];
       }
-      const int row = t.a0 + static_cast<int>(rank) * kRowsA + quad * 32 + lane;
-      const float channel =
-          row < g.N ? args.w_scales[static_cast<size_t>(t.e) * g.N + row] : 0.0f;
+      const int row = nt.a0 + static_cast<int>(rank) * kRowsA + quad * 32 + lane;
+      next_channel = row < g.N ? args.w_scales[static_cast<size_t>(nt.e) * g.N + row] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < S::kTileB / 32; ++j) {
+        if (g.p2u != nullptr && source[j] >= 0) source[j] = token_of(g, source[j]);
+        scale[j] = source[j] >= 0 ? args.x_scales[source[j]] : 0.0f;
+      }
+    };
+    if (first < tiles) look(first);
+    for (int i = first; i < tiles && ok; i += step) {
+      const Tile t = nt;
+      const float channel = next_channel;
+      __syncwarp();  // all lanes have used the rows' scales of the tile before
+#pragma unroll
+      for (int j = 0; j < S::kTileB / 32; ++j) by_row[lane + 32 * j] = scale[j];
       __syncwarp();
+      const int row = t.a0 + static_cast<int>(rank) * kRowsA + quad * 32 + lane;
+      if (i + step < tiles) look(i + step);
       for (int first_slice = 0; first_slice == 0 || first_slice < slices;) {
         const bool add = first_slice > 0;  // fp32 only: to what this thread stored before
         const int buf = n & 1;
@@ -368,6 +446,14 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
         for (int c = 0; c < t.cnt; c += 32) {
           uint32_t v[32];
           tmem_load_32(acc + c, v);
+          if (c + 32 >= t.cnt) {  // the accumulator is free before the last stores
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (CG == 2 && rank == 1) mbar_arrive_relaxed(map_to_rank(smem_addr(&drained[buf]), 0));
+              else mbar_arrive(&drained[buf]);
+            }
+          }
           const size_t o = static_cast<size_t>(t.start + c) * g.N + row;
           if (row < g.N) {
             if constexpr (F32) {
@@ -390,11 +476,6 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
           }
           __syncwarp();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0)
-          mbar_arrive_cluster(CG == 2 ? map_to_rank(smem_addr(&drained[buf]), 0)
-                                      : smem_addr(&drained[buf]));
         ++n;
         first_slice += max(segment, 1);
       }
@@ -459,6 +540,7 @@ int launch_typed(const W8Args& a, cudaStream_t st) {
   g.x_scales = a.x_scales;
   g.w_scales = a.w_scales;
   const long long ta = (a.N + S::kTileA - 1) / S::kTileA;
+  g.inv_a = inverse_of(static_cast<int>(ta));
   const long long tb = static_cast<long long>(a.E < a.P ? a.E : a.P) + a.P / S::kTileB;
   const long long clusters = ta * tb < resident ? ta * tb : resident;
   cudaLaunchConfig_t cfg = {};

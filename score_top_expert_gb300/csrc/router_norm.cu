@@ -21,8 +21,8 @@
 // mean(v yh), is over g_x, which holds the first; but it is linear in it:
 //   sum c g_x = sum c (grad_sum + r_pre u) - r_pre mean(u xh) sum c xh,
 // so all sums of a row are taken together behind one barrier.  A team keeps the
-// columns' sums for the weights' gradients of all its rows and leaves them as one row;
-// a second kernel adds those up in order: repeated calls give the same bits.
+// columns' sums for the weights' gradients of all its rows, a block leaves its teams' as one
+// row; a second kernel adds those up in order: repeated calls give the same bits.
 #include <atomic>
 #include <climits>
 
@@ -46,7 +46,7 @@ constexpr int kBlockWarps = 8;    // of a block whose rows take fewer
 #define FWD_MIN(U) (U == 1 ? 4 : U == 2 ? 3 : 1)
 #endif
 constexpr int kFwdWarps = 8;      // most warps of a row whose lanes hold one or two pieces
-constexpr int kSumThreads = 512;
+constexpr int kSumThreads = 1024;
 
 enum { GATE_NONE = 0, GATE_TOKEN = 1, GATE_VALUE = 2 };
 
@@ -328,7 +328,7 @@ __host__ __device__ constexpr int stage_bytes(int threads, int pieces, bool valu
 
 template <typename P, int U, bool VALUE>
 struct Ring {
-  static constexpr int kQuads = P::kN / 4;  // of a piece's columns
+  [[maybe_unused]] static constexpr int kQuads = P::kN / 4;  // of a piece's columns
   uint32_t base, weights;
   int threads, thread, lane, stage_size;
   int team_threads, team_thread;
@@ -453,7 +453,10 @@ __global__ __launch_bounds__(32 * (LONG ? kMaxWarps : kBlockWarps), U <= 2 ? 2 :
     if (ahead < a.T) ring.load(a, ahead, stage == 0 ? stages - 1 : stage - 1, col);
     ahead += step;
     copies_commit_group();
-    copies_wait_group(stages - 1);
+    if (stages == 4) copies_wait_group<3>();
+    else if (stages == 3) copies_wait_group<2>();
+    else if (stages == 2) copies_wait_group<1>();
+    else copies_wait_group<0>();
     __syncwarp();
     const float r_post = a.rstd != nullptr ? ring.factor(stage, 0) : 1.0f;
     const float r_pre = a.rstd != nullptr ? ring.factor(stage, 1) : 1.0f;
@@ -546,23 +549,37 @@ __global__ __launch_bounds__(32 * (LONG ? kMaxWarps : kBlockWarps), U <= 2 ? 2 :
     if (++stage == stages) stage = 0;
   }
   if (a.partial == nullptr) return;
-  float* const mine = a.partial + static_cast<size_t>(first) * 2 * a.D;
+  // one row of sums a block: the teams' added up in the place of the rows under way
+  float* out = a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.D;
+  float* const part = reinterpret_cast<float*>(dynamic_smem);
+  if (r.teams > 1) {
+    __syncthreads();
+    out = part + r.team * 2 * a.D;
+  }
 #pragma unroll
   for (int q = 0; q < U; ++q)
 #pragma unroll
     for (int j = 0; j < P::kN; ++j) {
       const int c = P::column(col[q], j / P::kEach, lane) + j % P::kEach;
       if (c < a.D) {
-        if (post) mine[c] = by_post[q][j];
-        if (pre) mine[a.D + c] = by_pre[q][j];
+        out[c] = by_post[q][j];
+        out[a.D + c] = by_pre[q][j];
       }
     }
+  if (r.teams > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.D; c += blockDim.x) {
+      float v = part[c];
+      for (int w = 1; w < r.teams; ++w) v += part[w * 2 * a.D + c];
+      a.partial[static_cast<size_t>(blockIdx.x) * 2 * a.D + c] = v;
+    }
+  }
 }
 
-// The teams' rows added up: 32 columns of one of the two a block, 16 warps on every
-// 16th row each.
+// The blocks' rows added up: 32 columns of one of the two a block, 32 warps on every
+// 32nd row each.
 __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(const float* __restrict__ partial,
-                                                               int teams, int D, float* post,
+                                                               int rows, int D, float* post,
                                                                float* pre) {
   __shared__ float part[kSumThreads / 32][33];
   pdl_enter();
@@ -574,7 +591,7 @@ __global__ __launch_bounds__(kSumThreads) void norm_sum_kernel(const float* __re
   if (c < D) {
     const float* at = partial + static_cast<size_t>(blockIdx.y) * D + c;
 #pragma unroll 8
-    for (int i = warp; i < teams; i += kSumThreads / 32)
+    for (int i = warp; i < rows; i += kSumThreads / 32)
       s += __ldcg(at + static_cast<size_t>(i) * 2 * D);
   }
   part[warp][lane] = s;
@@ -629,12 +646,8 @@ int bwd_blocks(int T, const Split& s) {
   return most < resident ? most : resident;
 }
 
-// Rows of partial sums for any alignment (narrow accesses take more warps a row, so
-// fewer teams).
-size_t partial_rows(int T) {
-  const size_t most = static_cast<size_t>(kBwdBlocks) * kBlockWarps;
-  return static_cast<size_t>(T) + kBlockWarps < most ? static_cast<size_t>(T) + kBlockWarps : most;
-}
+// Rows of partial sums: a block's each, at any alignment (and so any number of teams).
+size_t partial_rows(int T) { return T < kBwdBlocks ? T : kBwdBlocks; }
 
 template <int DT, int BYTES, int U>
 cudaError_t launch_fwd_pieces(const NormArgs& a, const Split& s, cudaStream_t st) {
@@ -686,7 +699,7 @@ int launch_bwd(NormArgs a, cudaStream_t st) {
                                             : launch_bwd_rows<DT, BYTES, false>(a, s, blocks, st);
   if (e == cudaSuccess && a.partial != nullptr)
     e = launch_kernel(norm_sum_kernel, dim3((a.D + 31) / 32, 2), dim3(kSumThreads), 0, st,
-                      static_cast<const float*>(a.partial), blocks * s.teams, a.D, a.grad_post,
+                      static_cast<const float*>(a.partial), blocks, a.D, a.grad_post,
                       a.grad_pre);
   return e == cudaSuccess ? MR_OK : MR_ERR_CUDA;
 }

@@ -22,12 +22,10 @@ __device__ __forceinline__ void copies_commit_group() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// Until at most `pending` (0 to 3) of the thread's groups are on their way.
-__device__ __forceinline__ void copies_wait_group(int pending) {
-  if (pending >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-  else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+// Until at most PENDING of the thread's groups are on their way.
+template <int PENDING>
+__device__ __forceinline__ void copies_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
 // What a lane holds of a stretch of 32 kN columns of a row, as it was loaded (so

@@ -191,7 +191,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
   __shared__ int tmp[33];
   __shared__ int prefix[MR_MAX_EXPERTS + 1];
   __shared__ int offs[MR_MAX_EXPERTS + 1];  // the offsets, clamped to [0, P]
-  __shared__ float row_scales[4][S::kTileB];  // of each storing warp
+  __shared__ __align__(16) float row_scales[4][S::kTileB];  // of each storing warp
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
@@ -454,24 +454,45 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
               else mbar_arrive(&drained[buf]);
             }
           }
+          // scaled in place first: reads of the rows' scales between the stores wait for one
+          // another (110 cycles a store)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(by_row + c + j);
+            v[j] = __float_as_uint(__uint_as_float(v[j]) * f.x * channel);
+            v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f.y * channel);
+            v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f.z * channel);
+            v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) * f.w * channel);
+          }
           const size_t o = static_cast<size_t>(t.start + c) * g.N + row;
+          const bool whole = c + 32 <= t.cnt;
           if (row < g.N) {
             if constexpr (F32) {
               float* out = static_cast<float*>(g.out) + o;
+              if (add) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j, out += g.N)
-                if (c + j < t.cnt) {
-                  const float r = __uint_as_float(v[j]) * by_row[c + j] * channel;
-                  if (add) red_add(out, r);
-                  else *out = r;
-                }
+                for (int j = 0; j < 32; ++j, out += g.N)
+                  if (c + j < t.cnt) red_add(out, __uint_as_float(v[j]));
+              } else if (whole) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j, out += g.N) *out = __uint_as_float(v[j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j, out += g.N)
+                  if (c + j < t.cnt) *out = __uint_as_float(v[j]);
+              }
             } else {
               unsigned short* out = static_cast<unsigned short*>(g.out) + o;
+              if (whole) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j, out += g.N)
-                if (c + j < t.cnt)
-                  *out = static_cast<unsigned short>(
-                      f32_to_bf16_bits(__uint_as_float(v[j]) * by_row[c + j] * channel));
+                for (int j = 0; j < 32; ++j, out += g.N)
+                  *out = static_cast<unsigned short>(f32_to_bf16_bits(__uint_as_float(v[j])));
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j, out += g.N)
+                  if (c + j < t.cnt)
+                    *out = static_cast<unsigned short>(f32_to_bf16_bits(__uint_as_float(v[j])));
+              }
             }
           }
           __syncwarp();

@@ -25,8 +25,10 @@ int check_product(int T, int P, int E, int N, int D, bool mapped) {
 constexpr int kFewRows = 36;
 constexpr int kFewColumns = 512;
 
-// Rows an expert, on average, up to which 8-bit operands take the few-rows kernel.
-constexpr int kFewRowsW8 = 4;
+// Rows an expert, on average, up to which 8-bit operands take the few-rows kernel: 2.3 rows of
+// 2048 -> 1024 take 56 us there and 70 in the tensor-core pipeline, 8 rows 124 and 128, of 4096
+// -> 1024 115 and 131.
+constexpr int kFewRowsW8 = 8;
 
 int run_product(int form, const ExpertArgs& a, mr_stream_t stream) {
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

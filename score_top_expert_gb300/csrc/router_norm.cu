@@ -36,15 +36,6 @@ namespace {
 
 constexpr int kMaxWarps = 16;     // of a row
 constexpr int kBlockWarps = 8;    // of a block whose rows take fewer
-#ifndef FWD_AHEAD
-#define FWD_AHEAD 8
-#endif
-#ifndef FWD_ONEPIECE
-#define FWD_ONEPIECE 8
-#endif
-#ifndef FWD_MIN
-#define FWD_MIN(U) (U == 1 ? 4 : U == 2 ? 3 : 1)
-#endif
 constexpr int kFwdWarps = 8;      // most warps of a row whose lanes hold one or two pieces
 constexpr int kSumThreads = 1024;
 
@@ -169,10 +160,10 @@ __device__ __forceinline__ void load_wide(const void* base, int row, int col0, i
 // ONE: a block is one team (and has one barrier: sixteen a block, which barriers of teams
 // take, leave room for four blocks on an SM).
 template <int DT, int BYTES, int U, bool ONE>
-__global__ __launch_bounds__(32 * (U == 4 ? kMaxWarps : kFwdWarps), FWD_MIN(U))
+__global__ __launch_bounds__(32 * (U == 4 ? kMaxWarps : kFwdWarps), U == 1 ? 4 : U == 2 ? 3 : 1)
     void norm_fwd_kernel(const NormArgs a) {
   using P = Piece<DT, BYTES>;
-  constexpr int kAhead = FWD_AHEAD / U;  // rows of z in flight
+  constexpr int kAhead = 8 / U;  // rows of z in flight
   __shared__ float cells[2][kMaxWarps];
   pdl_enter();
   RowTeam r = row_team(a.warps);
@@ -630,7 +621,7 @@ struct Split {
 Split split_of(int D, int columns, bool forward) {
   const int stretches = (D + columns - 1) / columns;
   int pieces;
-  if (forward) pieces = stretches <= FWD_ONEPIECE ? 1 : stretches <= 2 * kFwdWarps ? 2 : 4;
+  if (forward) pieces = stretches <= kFwdWarps ? 1 : stretches <= 2 * kFwdWarps ? 2 : 4;
   else pieces = stretches == 1 ? 1 : stretches <= 2 * kBlockWarps ? 2 : 4;
   const int warps = (stretches + pieces - 1) / pieces;
   return Split{warps, pieces, warps >= kBlockWarps ? 1 : kBlockWarps / warps};

@@ -463,7 +463,7 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_fwd_k
 template <int GROUPS, int WIDE, int WARPS>
 __global__ __launch_bounds__(32 * WARPS) void balance_finish_kernel(const BalanceArgs a) {
   constexpr int kCols = 32 * WIDE, kItems = WARPS / GROUPS;
-  __shared__ float sums[GROUPS == 1 ? 1 : GROUPS][kCols];
+  __shared__ double sums[GROUPS == 1 ? 1 : GROUPS][kCols];
   __shared__ int counts[GROUPS == 1 ? 1 : GROUPS][kCols];
   __shared__ float shared[2][WARPS];
   __shared__ int last;
@@ -480,11 +480,11 @@ __global__ __launch_bounds__(32 * WARPS) void balance_finish_kernel(const Balanc
     int lo, hi;
     sequence_range(a, s, &lo, &hi);
     const int b0 = lo / a.rows, b1 = hi > lo ? (hi - 1) / a.rows : b0 - 1;
-    float v[WIDE];
+    double v[WIDE];  // (a long batch has hundreds of thousands of slots)
     int n[WIDE];
 #pragma unroll
     for (int u = 0; u < WIDE; ++u) {
-      v[u] = 0.0f;
+      v[u] = 0.0;
       n[u] = 0;
     }
     if (vec) {
@@ -538,7 +538,7 @@ __global__ __launch_bounds__(32 * WARPS) void balance_finish_kernel(const Balanc
         if (c + u < a.E) {
           a.counts[static_cast<size_t>(s) * a.E + c + u] = n[u];
           // c_se P_se / n_s^2 (the factors that all share come last)
-          share = fmaf(static_cast<float>(n[u]) * by_tokens, v[u] * by_tokens, share);
+          share = fmaf(static_cast<float>(n[u]) * by_tokens, static_cast<float>(v[u]) * by_tokens, share);
         }
     }
   }
@@ -720,12 +720,15 @@ int blocks_per_sm(const Shape& sh, size_t smem) {
   return n < 1 ? 1 : n > kMostPerSm ? kMostPerSm : n;
 }
 
-// Tokens of a block: `per_sm` blocks on each of 152 SMs, two rows a team at least.
-// A function of the sizes alone, so that sums have the same order on every GPU.
+// Tokens of a block: `per_sm` blocks on each of 152 SMs, two rows a team at least, and 256 at
+// most, since a team adds its rows up one after the other in fp32.  A function of the
+// sizes alone, so that sums have the same order on every GPU.
+constexpr int kMostRows = 256;
+
 int rows_of(int T, int teams, int per_sm) {
   const int blocks = 152 * per_sm;
-  const int rows = (T + blocks - 1) / blocks;
-  return (rows < 2 * teams ? 2 * teams : (rows + teams - 1) / teams * teams);
+  const int each = ((T + blocks - 1) / blocks + teams - 1) / teams;  // of a team
+  return teams * (each < 2 ? 2 : each > kMostRows ? kMostRows : each);
 }
 
 constexpr int kFinishBlocks = 608;

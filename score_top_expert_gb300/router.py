@@ -1088,7 +1088,7 @@ def router_balance_loss_fwd(logits: torch.Tensor, topk_indices: torch.Tensor,
         if workspace.get_device() != idx or not workspace.is_contiguous():
             _bad("workspace", f"a contiguous tensor on cuda:{idx}")
         nbytes = workspace.numel() * workspace.element_size()
-    sf = _score(score_func)
+    sf, coeff, z_coeff = _score(score_func), float(coeff), float(z_coeff)
     if idx == _cur_dev():
         rc = calls.router_balance_loss_fwd(
             x.data_ptr(), _DTYPE[dt], choices.data_ptr(), ld, seq_ptr, T, E, K, S, sf, coeff,
@@ -1127,7 +1127,7 @@ def router_balance_loss_bwd(grad_loss: torch.Tensor, logits: torch.Tensor,
         _bad("row_stats", f"a contiguous float32 [{T}, 2] tensor on cuda:{idx}")
     out = _empty((T, E), dtype=dt, device=x.device) if grad_logits is None \
         else _out(grad_logits, (T, E), dt, x.device, "grad_logits")
-    sf = _score(score_func)
+    sf, K, coeff, z_coeff = _score(score_func), int(K), float(coeff), float(z_coeff)
     call = (_fast or _calls()).router_balance_loss_bwd
     if idx == _cur_dev():
         rc = call(g.data_ptr(), x.data_ptr(), _DTYPE[dt], counts.data_ptr(), stats.data_ptr(),
@@ -1236,13 +1236,13 @@ def router_combine_norm_fwd(expert_out: torch.Tensor, residual: torch.Tensor,
     call = (_fast or _calls()).router_combine_norm_fwd
     if idx == _cur_dev():
         rc = call(z.data_ptr(), _DTYPE[dt], u2p_ptr, w_ptr, ld, res.data_ptr(), post_ptr, gate_ptr,
-                  kind, residual_scale, pre_ptr, eps, T, K, D, sum.data_ptr(), normed_ptr,
+                  kind, float(residual_scale), pre_ptr, float(eps), T, K, D, sum.data_ptr(), normed_ptr,
                   block_ptr, rstd_ptr, _raw_stream(idx))
     else:
         with torch.cuda.device(idx):
             rc = call(z.data_ptr(), _DTYPE[dt], u2p_ptr, w_ptr, ld, res.data_ptr(), post_ptr,
-                      gate_ptr, kind, residual_scale, pre_ptr, eps, T, K, D, sum.data_ptr(),
-                      normed_ptr, block_ptr, rstd_ptr, _raw_stream(idx))
+                      gate_ptr, kind, float(residual_scale), pre_ptr, float(eps), T, K, D,
+                      sum.data_ptr(), normed_ptr, block_ptr, rstd_ptr, _raw_stream(idx))
     if rc != 0:
         raise RouterError("router_combine_norm_fwd", rc)
     return sum, normed, block_out, rstd
@@ -1330,7 +1330,7 @@ def router_combine_norm_bwd(grad_sum: torch.Tensor | None, grad_normed: torch.Te
     grad_residual = _empty(shape, dtype=dt, device=dev) if grad_residual is None \
         else _out(grad_residual, shape, dt, dev, "grad_residual")
     args = (gs_ptr, gn_ptr, _DTYPE[dt], y_ptr, x_ptr, rstd_ptr, post_ptr, gate_ptr, kind,
-            residual_scale, pre_ptr, T, D, grad_block.data_ptr(), grad_residual.data_ptr(),
+            float(residual_scale), pre_ptr, T, D, grad_block.data_ptr(), grad_residual.data_ptr(),
             ggate_ptr, gpost_ptr, gpre_ptr, ws_ptr, nbytes)
     if idx == _cur_dev():
         rc = calls.router_combine_norm_bwd(*args, _raw_stream(idx))

@@ -80,6 +80,36 @@ def test_balance(R, T, E, K, S, pad, score, z, dtype):
     check_balance(R, T, E, K, sequences(T, S, pad, T + E), score, z, dtype, T + 3 * E)
 
 
+def test_balance_of_many_short_sequences(R):
+    check_balance(R, 2000, 40, 2, sequences(2000, 1000, 30, 3), "softmax", 1e-3, "f32", 4)
+    check_balance(R, 600, 2304, 3, sequences(600, 300, 0, 4), "sigmoid", 0.0, "f32", 5)
+
+
+@pytest.mark.parametrize("T,E,K,seq", [(600_001, 4, 2, None), (3_000_000, 1, 1, (0, 2_999_990)),
+                                       (500_000, 60, 2, (5, 250_001, 499_999))])
+def test_balance_of_long_batches(R, T, E, K, seq):
+    """Sums over up to millions of tokens, against the definition in 64 bits: no team adds up more
+    than 256 rows in fp32 (and 32 such sums as one block), what is behind is in 64 bits."""
+    gen = torch.Generator(device=DEV).manual_seed(E)
+    x = torch.randn(T, E, generator=gen, device=DEV)
+    idx = torch.randint(0, E, (T, K), generator=gen, device=DEV, dtype=torch.int32)
+    sd = None if seq is None else torch.tensor(seq, dtype=torch.int32, device=DEV)
+    loss, counts, _ = R.router_balance_loss_fwd(x, idx, "softmax", 1.0, 0.5, sd)
+    ends = (0, T) if seq is None else seq
+    want, z = 0.0, 0.0
+    for s, (a, b) in enumerate(zip(ends, ends[1:])):
+        lse = x[a:b].double().logsumexp(1, keepdim=True)
+        c = torch.bincount(idx[a:b].reshape(-1).long(), minlength=E)
+        assert torch.equal(c.int(), counts[s])
+        want += float(((x[a:b].double() - lse).exp().sum(0) * c).sum()) * E / (K * (b - a) ** 2)
+        z += float(lse.square().sum())
+    got = loss.double().tolist()
+    # a score's own error (softmax of values within 6 of the largest) is random: far below
+    # its bound of 50 half steps in such a sum; the additions' as well
+    assert abs(got[0] - want / (len(ends) - 1)) <= 64 * STEP * want
+    assert abs(got[1] - 0.5 * z / (ends[-1] - ends[0])) <= 512 * STEP * 0.5 * z / (ends[-1] - ends[0]) + 1e-9
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_balance_without_offsets_dropped_choices_wide_logits(R, score):
     check_balance(R, 333, 96, 5, None, score, 1e-3, "f32", 5, scale=8.0, drop=0.3)

@@ -50,12 +50,9 @@ __host__ __device__ constexpr int ring_rows(int nv, int bytes) {
 }
 constexpr int registers_of(int nv) { return nv <= 4 ? 80 : nv <= 6 ? 128 : 168; }
 
-// Shared memory of the rows and (8 bytes a thread) of the choices under way.
+// Shared memory of the rows under way.
 __host__ __device__ constexpr int ring_bytes(bool vec, int nv, int bytes) {
   return vec ? ring_rows(nv, bytes) * nv * threads_of(nv) * bytes : 0;
-}
-__host__ __device__ constexpr int choice_bytes(bool vec, int nv, int bytes) {
-  return vec ? ring_rows(nv, bytes) * threads_of(nv) * 8 : 0;
 }
 
 struct BalanceArgs {
@@ -210,38 +207,29 @@ __device__ __forceinline__ void blank_outside(const Team& t, int E, Row<NV>* r) 
 // The rows of the block's range on their way to the team, through places in shared memory
 // that belong to the thread: the thread waits for its own copies, no barrier is needed,
 // and several rows are under way where registers held one.  They are asked for before it
-// is known which sequences they belong to.  A row's choices come along, to the team's
-// first warp.  (Rows that are not aligned are loaded when they are needed.)
-template <int DT, bool VEC, int NV, bool CHOICES>
+// is known which sequences they belong to.  (Rows that are not aligned are loaded when
+// they are needed.)
+template <int DT, bool VEC, int NV>
 struct RowRing {
   static constexpr int kBytes = DT == DT_F32 ? 16 : 8;  // of four logits
   static constexpr int kRing = ring_rows(NV, kBytes);
-  [[maybe_unused]] static constexpr uint32_t kWidth = threads_of(NV) * kBytes;  // of a block's pieces j
-  [[maybe_unused]] static constexpr uint32_t kChoiceWidth = threads_of(NV) * 8;
   uint32_t base;          // the thread's first place
   int taken, asked;       // of the next row to take and to ask for, in rows
-  uint32_t choice_base;
   const uint8_t* from;    // the thread's first four logits of the latter
-  const int32_t* choose;  // the lane's choice of the latter
-  size_t stride, choice_stride;  // from one row of the team to the next, in bytes and choices
+  size_t stride;          // from one row of the team to the next, in bytes
   int row, hi;            // the latter's number
 
   __device__ __forceinline__ void request(const BalanceArgs& a, const Team& t) {
     if constexpr (VEC) {
+      constexpr uint32_t kWidth = threads_of(NV) * kBytes;  // of a block's pieces j
       if (row < hi) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (column_of(t, j) < a.E)
             copy_async<kBytes>(base + (asked * NV + j) * kWidth, from + j * t.warps * (32 * kBytes));
-        if (CHOICES && t.warp == 0) {
-          const uint32_t to = choice_base + asked * kChoiceWidth;
-          if (t.lane < a.K) copy_async<4>(to, choose);
-          if (t.lane + 32 < a.K) copy_async<4>(to + 4, choose + 32);
-        }
       }
       row += t.teams;
       from += stride;
-      choose += choice_stride;
       if (++asked == kRing) asked = 0;
       copies_commit_group();
     }
@@ -250,15 +238,11 @@ struct RowRing {
   __device__ __forceinline__ void begin(const BalanceArgs& a, const Team& t, void* smem, int lo,
                                         int stop) {
     base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * kBytes;
-    choice_base = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
-                  ring_bytes(VEC, NV, kBytes) + threadIdx.x * 8;
     row = lo + t.team;
     hi = stop;
     stride = static_cast<size_t>(t.teams) * a.E * (kBytes / 4);
-    choice_stride = t.teams * a.ld_choices;
     from = static_cast<const uint8_t*>(a.logits) +
            (static_cast<size_t>(row) * a.E + column_of(t, 0)) * (kBytes / 4);
-    choose = a.choices + row * a.ld_choices + t.lane;
     taken = asked = 0;
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) request(a, t);
@@ -270,10 +254,10 @@ struct RowRing {
     if (++taken == kRing) taken = 0;
   }
 
-  // Row `at_row`, the team's next, and (first warp) its choices: -1 behind the last.
-  __device__ __forceinline__ void take(const BalanceArgs& a, const Team& t, int at_row, Row<NV>* r,
-                                       int* c0, int* c1) {
+  // Row `at_row`, the team's next.
+  __device__ __forceinline__ void take(const BalanceArgs& a, const Team& t, int at_row, Row<NV>* r) {
     if constexpr (VEC) {
+      constexpr uint32_t kWidth = threads_of(NV) * kBytes;
       request(a, t);
       copies_wait_group<kRing - 1>();
 #pragma unroll
@@ -292,21 +276,9 @@ struct RowRing {
           r->v[j][3] = __uint_as_float(y & 0xffff0000u);
         }
       }
-      if (CHOICES && t.warp == 0) {
-        int x, y;
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                     : "=r"(x), "=r"(y) : "r"(choice_base + taken * kChoiceWidth) : "memory");
-        *c0 = t.lane < a.K ? x : -1;
-        *c1 = t.lane + 32 < a.K ? y : -1;
-      }
       if (++taken == kRing) taken = 0;
     } else {
       load_row<DT, false>(a, t, at_row, r);
-      if (CHOICES && t.warp == 0) {
-        const int32_t* const c = a.choices + at_row * a.ld_choices + t.lane;
-        *c0 = t.lane < a.K ? c[0] : -1;
-        *c1 = t.lane + 32 < a.K ? c[32] : -1;
-      }
     }
     if (a.E < 128 * NV * t.warps) blank_outside<VEC>(t, a.E, r);
   }
@@ -315,7 +287,7 @@ struct RowRing {
 template <int DT, bool VEC, int NV, int SF>
 __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_fwd_kernel(
     const BalanceArgs a, int warps) {
-  // the rows and choices under way; [E] column sums; [E] counts
+  // the rows under way; [E] column sums; [E] counts
   extern __shared__ __align__(16) uint8_t dynamic_smem[];
   __shared__ float xch[2 * kMostWarps * 2];
   __shared__ float z_warp[kMostWarps];
@@ -324,10 +296,10 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_fwd_k
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   Team t = make_team(warps, xch);
   const int t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
-  RowRing<DT, VEC, NV, true> ring;
+  RowRing<DT, VEC, NV> ring;
   ring.begin(a, t, dynamic_smem, t0, t1);
   float* const block_sums = reinterpret_cast<float*>(
-      dynamic_smem + ring_bytes(VEC, NV, ring.kBytes) + choice_bytes(VEC, NV, ring.kBytes));
+      dynamic_smem + ring_bytes(VEC, NV, ring.kBytes));
   int* const hist = reinterpret_cast<int*>(block_sums + a.E);
   if (threadIdx.x < 32) {
     const int s = first_sequence(a, t0);
@@ -347,16 +319,35 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_fwd_k
     if (hi <= lo) continue;
     p = hi;
     for (; row < lo; row += t.teams) ring.skip(a, t);
-    // ---- column sums of q, and counts ----------------------------------------------------
+    // ---- counts: the choices of the range's tokens, while the rows are on their way ---------
+    const int32_t* const chosen = a.choices + lo * a.ld_choices;
+    const int n = (hi - lo) * a.K;
+    auto count = [&](int e) {
+      if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(hist + e, 1);
+    };
+    if (a.ld_choices == a.K) {
+      constexpr int kAtOnce = 8;
+      int i = threadIdx.x;
+      for (; i + (kAtOnce - 1) * static_cast<int>(blockDim.x) < n; i += kAtOnce * blockDim.x) {
+        int e[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) e[u] = __ldcs(chosen + i + u * blockDim.x);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) count(e[u]);
+      }
+#pragma unroll 4
+      for (; i < n; i += blockDim.x) count(__ldcs(chosen + i));
+    } else {
+      for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int at = i / a.K;
+        count(chosen[at * a.ld_choices + (i - at * a.K)]);
+      }
+    }
+    // ---- column sums of q ------------------------------------------------------------------
     Row<NV> sums{};
     for (; row < hi; row += t.teams) {
       Row<NV> r;
-      int c0 = -1, c1 = -1;
-      ring.take(a, t, row, &r, &c0, &c1);
-      if (t.warp == 0) {
-        if (static_cast<unsigned>(c0) < static_cast<unsigned>(a.E)) atomicAdd(hist + c0, 1);
-        if (static_cast<unsigned>(c1) < static_cast<unsigned>(a.E)) atomicAdd(hist + c1, 1);
-      }
+      ring.take(a, t, row, &r);
       float top = -INFINITY, total = 0.0f, factor;
       if (SF == SF_SOFTMAX || want_z) {
 #pragma unroll
@@ -463,8 +454,9 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_fwd_k
 template <int GROUPS, int WIDE, int WARPS>
 __global__ __launch_bounds__(32 * WARPS) void balance_finish_kernel(const BalanceArgs a) {
   constexpr int kCols = 32 * WIDE, kItems = WARPS / GROUPS;
-  __shared__ double sums[GROUPS == 1 ? 1 : GROUPS][kCols];
-  __shared__ int counts[GROUPS == 1 ? 1 : GROUPS][kCols];
+  static_assert(GROUPS == 1 || (GROUPS == 32 && WARPS == 32 && WIDE == 1), "a warp a column");
+  __shared__ float sums[GROUPS == 1 ? 1 : GROUPS][kCols + 1];
+  __shared__ int counts[GROUPS == 1 ? 1 : GROUPS][kCols + 1];
   __shared__ float shared[2][WARPS];
   __shared__ int last;
   pdl_enter();
@@ -480,13 +472,20 @@ __global__ __launch_bounds__(32 * WARPS) void balance_finish_kernel(const Balanc
     int lo, hi;
     sequence_range(a, s, &lo, &hi);
     const int b0 = lo / a.rows, b1 = hi > lo ? (hi - 1) / a.rows : b0 - 1;
-    double v[WIDE];  // (a long batch has hundreds of thousands of slots)
+    // fp32 sums with what each addition left over (a long batch has 100000 slots)
+    float v[WIDE], rest[WIDE];
     int n[WIDE];
 #pragma unroll
     for (int u = 0; u < WIDE; ++u) {
-      v[u] = 0.0;
+      v[u] = rest[u] = 0.0f;
       n[u] = 0;
     }
+    auto add = [&](int u, float x, int k) {
+      const float y = x - rest[u], next = v[u] + y;
+      rest[u] = (next - v[u]) - y;
+      v[u] = next;
+      n[u] += k;
+    };
     if (vec) {
       if (c < a.E) {
 #pragma unroll 4
@@ -494,10 +493,11 @@ __global__ __launch_bounds__(32 * WARPS) void balance_finish_kernel(const Balanc
           const size_t at = (static_cast<size_t>(b) + s) * a.E + c;
           const float4 x = __ldcg(reinterpret_cast<const float4*>(a.slot_sums + at));
           const int4 k = __ldcg(reinterpret_cast<const int4*>(a.slot_counts + at));
-          v[0] += x.x; n[0] += k.x;
+          add(0, x.x, k.x);
           if constexpr (WIDE == 4) {
-            v[1] += x.y; v[2] += x.z; v[3] += x.w;
-            n[1] += k.y; n[2] += k.z; n[3] += k.w;
+            add(1, x.y, k.y);
+            add(2, x.z, k.z);
+            add(3, x.w, k.w);
           }
         }
       }
@@ -507,46 +507,35 @@ __global__ __launch_bounds__(32 * WARPS) void balance_finish_kernel(const Balanc
         const size_t at = (static_cast<size_t>(b) + s) * a.E + c;
 #pragma unroll
         for (int u = 0; u < WIDE; ++u)
-          if (c + u < a.E) {
-            v[u] += __ldcg(a.slot_sums + at + u);
-            n[u] += __ldcg(a.slot_counts + at + u);
-          }
+          if (c + u < a.E) add(u, __ldcg(a.slot_sums + at + u), __ldcg(a.slot_counts + at + u));
       }
     }
     const float by_tokens = 1.0f / static_cast<float>(max(hi - lo, 1));
-    if constexpr (GROUPS > 1) {
-#pragma unroll
-      for (int u = 0; u < WIDE; ++u) {
-        sums[group][WIDE * lane + u] = v[u];
-        counts[group][WIDE * lane + u] = n[u];
-      }
+    // c_se P_se / n_s^2 (the factors that all share come last)
+    auto finish = [&](int e, float p, int k) {
+      a.counts[static_cast<size_t>(s) * a.E + e] = k;
+      share = fmaf(static_cast<float>(k) * by_tokens, p * by_tokens, share);
+    };
+    if constexpr (GROUPS > 1) {  // warp w adds up column w of the item
+      sums[group][lane] = v[0];
+      counts[group][lane] = n[0];
       __syncthreads();
-      if (warp == 0) {
-        const int groups = min(GROUPS, b1 - b0 + 1);
-        for (int g = 1; g < groups; ++g)
-#pragma unroll
-          for (int u = 0; u < WIDE; ++u) {
-            v[u] += sums[g][WIDE * lane + u];
-            n[u] += counts[g][WIDE * lane + u];
-          }
-      }
+      const float p = seg_sum<32>(sums[lane][warp]);
+      const int k = __reduce_add_sync(0xffffffffu, counts[lane][warp]);
+      const int e = c - lane + warp;
+      if (lane == 0 && e < a.E) finish(e, p, k);
       __syncthreads();
-    }
-    if (group == 0) {
+    } else {
 #pragma unroll
       for (int u = 0; u < WIDE; ++u)
-        if (c + u < a.E) {
-          a.counts[static_cast<size_t>(s) * a.E + c + u] = n[u];
-          // c_se P_se / n_s^2 (the factors that all share come last)
-          share = fmaf(static_cast<float>(n[u]) * by_tokens, static_cast<float>(v[u]) * by_tokens, share);
-        }
+        if (c + u < a.E) finish(c + u, v[u], n[u]);
     }
   }
   share = seg_sum<32>(share);
   if (lane == 0) shared[0][warp] = share;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = GROUPS; w < WARPS; w += GROUPS) share += shared[0][w];
+    for (int w = 1; w < WARPS; ++w) share += shared[0][w];
     a.parts[blockIdx.x] = share;
     __threadfence();
     last = atomicAdd(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
@@ -589,7 +578,7 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_bwd_k
   pdl_enter();
   Team t = make_team(warps, xch);
   const int t0 = blockIdx.x * a.rows, t1 = min(t0 + a.rows, a.T);
-  RowRing<DT, VEC, NV, false> ring;
+  RowRing<DT, VEC, NV> ring;
   ring.begin(a, t, dynamic_smem, t0, t1);
   if (threadIdx.x < 32) {
     const int s = first_sequence(a, t0);
@@ -644,8 +633,7 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_bwd_k
       const float2 st = next_st;
       if (row + t.teams < hi) next_st = a.stats[row + t.teams];
       Row<NV> r;
-      int none0, none1;
-      ring.take(a, t, row, &r, &none0, &none1);
+      ring.take(a, t, row, &r);
       const float inv = rcp_approx(SF == SF_SOFTMAX ? st.y : st.x);
       const float shift = (SF == SF_SOFTMAX ? st.x : st.y) * kLog2e;
       float z = 0.0f;
@@ -706,7 +694,7 @@ Shape shape_of(int E) {
 
 size_t smem_of(int E, const Shape& sh, bool vec, int bytes, bool forward) {
   const size_t ring = ring_bytes(vec, sh.nv, bytes);
-  return forward ? ring + choice_bytes(vec, sh.nv, bytes) + static_cast<size_t>(E) * 8 : ring;
+  return forward ? ring + static_cast<size_t>(E) * 8 : ring;
 }
 
 // Blocks that an SM holds, by registers and shared memory: a block more than that would run

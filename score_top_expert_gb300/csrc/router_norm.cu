@@ -319,7 +319,6 @@ __host__ __device__ constexpr int stage_bytes(int threads, int pieces, bool valu
 
 template <typename P, int U, bool VALUE>
 struct Ring {
-  [[maybe_unused]] static constexpr int kQuads = P::kN / 4;  // of a piece's columns
   uint32_t base, weights;
   int threads, thread, lane, stage_size;
   int team_threads, team_thread;
@@ -331,7 +330,7 @@ struct Ring {
     return base + (stage + 1) * stage_size - (threads / 32 - (thread >> 5)) * 16;
   }
   __device__ __forceinline__ uint32_t weight_at(int which, int q, int h) const {
-    return weights + (((which * U + q) * kQuads + h) * team_threads + team_thread) * 16;
+    return weights + (((which * U + q) * (P::kN / 4) + h) * team_threads + team_thread) * 16;
   }
 
   __device__ __forceinline__ void load(const NormArgs& a, int t, int stage, const int (&col)[U]) const {
@@ -372,7 +371,7 @@ struct Ring {
                                          float (&v)[P::kN]) const {
     if constexpr (BYTES == 16) {
 #pragma unroll
-      for (int h = 0; h < kQuads; ++h)
+      for (int h = 0; h < P::kN / 4; ++h)
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                      : "=f"(v[4 * h]), "=f"(v[4 * h + 1]), "=f"(v[4 * h + 2]), "=f"(v[4 * h + 3])
                      : "r"(weight_at(which, q, h)));
@@ -424,7 +423,7 @@ __global__ __launch_bounds__(32 * (LONG ? kMaxWarps : kBlockWarps), U <= 2 ? 2 :
           for (int j = 0; j < P::kN; ++j) v[j] = 1.0f;
           if (w != nullptr) vector_at<P, BYTES>(w, col[q], lane, a.D, v);
 #pragma unroll
-          for (int h = 0; h < ring.kQuads; ++h)
+          for (int h = 0; h < P::kN / 4; ++h)
             asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(ring.weight_at(which, q, h)),
                          "f"(v[4 * h]), "f"(v[4 * h + 1]), "f"(v[4 * h + 2]), "f"(v[4 * h + 3])
                          : "memory");

@@ -76,6 +76,25 @@ struct RowTeam {
     else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
   }
 
+  // The same for three values with cells [3][kMaxWarps] of the team's own, 16-byte aligned and zero
+  // behind its warps: four warps' a read.
+  __device__ __forceinline__ void sum3(float* mine, float (&v)[3]) const {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = seg_sum<32>(v[i]);
+    if (warps == 1) return;
+    if (lane < 3) mine[lane * kMaxWarps + warp] = lane == 0 ? v[0] : lane == 1 ? v[1] : v[2];
+    sync();
+#pragma unroll
+    for (int i = 0; i < 3; ++i) v[i] = 0.0f;
+    for (int w = 0; w < warps; w += 4) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const float4 c = *reinterpret_cast<const float4*>(mine + i * kMaxWarps + w);
+        v[i] += (c.x + c.y) + (c.z + c.w);
+      }
+    }
+  }
+
   // N values summed over the team, the same in all its threads.  With two sets of cells in
   // turn one barrier is enough: who writes a set has passed the barrier behind its last
   // reading.
@@ -310,40 +329,51 @@ __global__ __launch_bounds__(32 * (U == 4 ? kMaxWarps : kFwdWarps), U == 1 ? 4 :
 // The rows of a backward on their way through shared memory: a thread's pieces go to places
 // of its own, so that it waits for its own copies and no barrier is needed; each warp's
 // first lane brings the row's factors and gate.  Both weights lie behind the ring, in the order
-// in which a warp reads them (16-byte accesses only).
+// in which a warp reads them.
 enum { ROW_GS = 0, ROW_GN = 1, ROW_X = 2, ROW_Y = 3, ROW_GATE = 4 };
 
-__host__ __device__ constexpr int stage_bytes(int threads, int pieces, bool value) {
-  return threads * 16 * pieces * (4 + value) + threads / 32 * 16;
+// Places for 256 threads (512 in the blocks of long rows) whatever a block has, so that a
+// thread's places lie at fixed distances.
+__host__ __device__ constexpr int places_of(bool is_long) { return 32 * (is_long ? kMaxWarps : kBlockWarps); }
+__host__ __device__ constexpr int stage_bytes(bool is_long, int pieces, bool value) {
+  return places_of(is_long) * 16 * pieces * (4 + value) + places_of(is_long) / 32 * 16;
 }
 
-template <typename P, int U, bool VALUE>
+// Both weights are kept in shared memory for 16-byte accesses (long rows fill it).
+__host__ __device__ constexpr bool weights_kept(int bytes, bool is_long) {
+  return bytes == 16 && !is_long;
+}
+
+template <typename P, int U, bool VALUE, bool LONG>
 struct Ring {
-  uint32_t base, weights;
-  int threads, thread, lane, stage_size;
-  int team_threads, team_thread;
+  static constexpr int kPitch = places_of(LONG) * 16;
+  static constexpr int kStage = stage_bytes(LONG, U, VALUE);
+  static constexpr bool kWeights = weights_kept(P::kBytes, LONG);  // in shared memory
+  uint32_t base, factors, weights;  // the thread's, its warp's, and its weights' places
+  int lane;
 
   __device__ __forceinline__ uint32_t at(int stage, int array, int q) const {
-    return base + stage * stage_size + ((array * U + q) * threads + thread) * 16;
+    return base + stage * kStage + (array * U + q) * kPitch;
   }
-  __device__ __forceinline__ uint32_t factors_at(int stage) const {
-    return base + (stage + 1) * stage_size - (threads / 32 - (thread >> 5)) * 16;
-  }
+  __device__ __forceinline__ uint32_t factors_at(int stage) const { return factors + stage * kStage; }
   __device__ __forceinline__ uint32_t weight_at(int which, int q, int h) const {
-    return weights + (((which * U + q) * (P::kN / 4) + h) * team_threads + team_thread) * 16;
+    return weights + ((which * U + q) * (P::kN / 4) + h) * kPitch;
   }
 
+  template <bool FULL>
   __device__ __forceinline__ void load(const NormArgs& a, int t, int stage, const int (&col)[U]) const {
     const size_t row = static_cast<size_t>(t) * a.D;
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       if (!any_inside<P>(col[q], lane, a.D)) continue;
-      if (a.grad_sum != nullptr) P::load_async(at(stage, ROW_GS, q), a.grad_sum, row, col[q], lane, a.D);
-      if (a.pre_weight != nullptr) {
+      if (FULL || a.grad_sum != nullptr)
+        P::load_async(at(stage, ROW_GS, q), a.grad_sum, row, col[q], lane, a.D);
+      if (FULL || a.pre_weight != nullptr) {
         P::load_async(at(stage, ROW_GN, q), a.grad_normed, row, col[q], lane, a.D);
         P::load_async(at(stage, ROW_X, q), a.sum, row, col[q], lane, a.D);
       }
-      if (a.block != nullptr) P::load_async(at(stage, ROW_Y, q), a.block, row, col[q], lane, a.D);
+      if (FULL || a.block != nullptr)
+        P::load_async(at(stage, ROW_Y, q), a.block, row, col[q], lane, a.D);
       if constexpr (VALUE)
         P::load_async(at(stage, ROW_GATE, q), a.gate, row, col[q], lane, a.D);
     }
@@ -369,7 +399,7 @@ struct Ring {
   template <int BYTES>
   __device__ __forceinline__ void weight(const float* w, int which, int q, int col, int D,
                                          float (&v)[P::kN]) const {
-    if constexpr (BYTES == 16) {
+    if constexpr (kWeights) {
 #pragma unroll
       for (int h = 0; h < P::kN / 4; ++h)
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -387,31 +417,36 @@ struct Ring {
 // and then, with m = r_pre^2 mean(u x) and f = scale gate_token r_post,
 //   g_x = grad_sum + r_pre u - r_pre m x,  g_y = (f g_x) gate post_weight - y r_post mean_v r_post,
 //   the weights' sums take (r_pre grad_normed) x and (f g_x gate) y.
-template <int DT, int BYTES, int U, bool VALUE, bool LONG>
+// FULL: both norms, grad_sum given, known when the kernel is built (which saves a seventh of its
+// instructions; they bound it with bf16 rows).
+template <int DT, int BYTES, int U, bool VALUE, bool LONG, bool FULL>
 __global__ __launch_bounds__(32 * (LONG ? kMaxWarps : kBlockWarps), U <= 2 ? 2 : 1)
     void norm_bwd_kernel(const NormArgs a, int stages) {
   using P = Piece<DT, BYTES>;
   extern __shared__ __align__(16) uint8_t dynamic_smem[];
-  __shared__ float cells[2][3 * kMaxWarps];
+  __shared__ __align__(16) float cells[2][kBlockWarps][3 * kMaxWarps];  // [.][team]
   pdl_enter();
   const RowTeam r = row_team(a.warps);
   const int first = blockIdx.x * r.teams + r.team, step = gridDim.x * r.teams;
   const int lane = r.lane;
   const uint32_t smem = static_cast<uint32_t>(__cvta_generic_to_shared(dynamic_smem));
-  const int stage_size = stage_bytes(blockDim.x, U, VALUE);
-  const Ring<P, U, VALUE> ring{smem, smem + stages * stage_size, static_cast<int>(blockDim.x),
-                               static_cast<int>(threadIdx.x), lane, stage_size, a.warps * 32,
-                               r.warp * 32 + lane};
+  using R = Ring<P, U, VALUE, LONG>;
+  const R ring{smem + threadIdx.x * 16, smem + R::kStage - (places_of(LONG) / 32 - (threadIdx.x >> 5)) * 16,
+               smem + stages * R::kStage + (r.warp * 32 + lane) * 16, lane};
+  for (int i = threadIdx.x; i < 2 * kBlockWarps * 3 * kMaxWarps; i += blockDim.x) cells[0][0][i] = 0.0f;
+  __syncthreads();
   int col[U];
 #pragma unroll
   for (int q = 0; q < U; ++q) col[q] = (r.warp + q * a.warps) * 32 * P::kN;
-  const bool pre = a.pre_weight != nullptr, post = a.post_weight != nullptr;
+  const bool pre = FULL || a.pre_weight != nullptr, post = FULL || a.post_weight != nullptr;
+  const bool summed = FULL || a.grad_sum != nullptr, block = FULL || a.block != nullptr;
+  const float by_columns = 1.0f / static_cast<float>(a.D);
   int ahead = first;  // the next row to ask for
   for (int s = 0; s < stages - 1; ++s, ahead += step) {
-    if (ahead < a.T) ring.load(a, ahead, s, col);
+    if (ahead < a.T) ring.template load<FULL>(a, ahead, s, col);
     copies_commit_group();
   }
-  if constexpr (BYTES == 16) {
+  if constexpr (R::kWeights) {
     if (r.team == 0) {
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
@@ -440,7 +475,7 @@ __global__ __launch_bounds__(32 * (LONG ? kMaxWarps : kBlockWarps), U <= 2 ? 2 :
   int stage = 0, flip = 0;
   for (int t = first; t < a.T; t += step, flip ^= 1) {
     __syncwarp();  // the lanes have read the factors of the stage that is filled again
-    if (ahead < a.T) ring.load(a, ahead, stage == 0 ? stages - 1 : stage - 1, col);
+    if (ahead < a.T) ring.template load<FULL>(a, ahead, stage == 0 ? stages - 1 : stage - 1, col);
     ahead += step;
     copies_commit_group();
     if (stages == 4) copies_wait_group<3>();
@@ -456,22 +491,24 @@ __global__ __launch_bounds__(32 * (LONG ? kMaxWarps : kBlockWarps), U <= 2 ? 2 :
     for (int q = 0; q < U; ++q) {
       if (!any_inside<P>(col[q], lane, a.D)) continue;
       float x[P::kN], v[P::kN], w[P::kN];
+      if (!FULL) {
 #pragma unroll
-      for (int j = 0; j < P::kN; ++j) g[q][j] = x[j] = 0.0f;
-      if (a.grad_sum != nullptr) ring.widened(stage, ROW_GS, q, g[q]);
+        for (int j = 0; j < P::kN; ++j) g[q][j] = x[j] = 0.0f;
+      }
+      if (summed) ring.widened(stage, ROW_GS, q, g[q]);
       if (pre) {
         ring.widened(stage, ROW_X, q, x);
         ring.widened(stage, ROW_GN, q, v);
         ring.template weight<BYTES>(a.pre_weight, 1, q, col[q], a.D, w);
 #pragma unroll
         for (int j = 0; j < P::kN; ++j) {
-          const float gn = r_pre * v[j];
+          const float gn = r_pre * v[j], u = gn * w[j];
           by_pre[q][j] = fmaf(gn, x[j], by_pre[q][j]);
-          s[0] = fmaf(gn * w[j], x[j], s[0]);
-          g[q][j] = fmaf(gn, w[j], g[q][j]);
+          s[0] = fmaf(u, x[j], s[0]);
+          g[q][j] += u;
         }
       }
-      if (a.block != nullptr) {
+      if (block) {
         ring.widened(stage, ROW_Y, q, v);
         if constexpr (VALUE) {
           ring.widened(stage, ROW_GATE, q, w);
@@ -490,13 +527,13 @@ __global__ __launch_bounds__(32 * (LONG ? kMaxWarps : kBlockWarps), U <= 2 ? 2 :
         }
       }
     }
-    if (pre || post || a.gate_kind == GATE_TOKEN) r.sum(cells[flip], s);
+    if (pre || post || a.gate_kind == GATE_TOKEN) r.sum3(cells[flip][r.team], s);
     // s[0] = r_pre sum u x;  g_x = g - k x
-    const float k = pre ? r_pre * r_pre * (s[0] / a.D) : 0.0f;
+    const float k = pre ? r_pre * r_pre * (s[0] * by_columns) : 0.0f;
     const float whole = r_post * fmaf(-k, s[2], s[1]);  // sum c g_x, of yh
     const float by = a.gate_kind == GATE_TOKEN ? a.scale * ring.factor(stage, 2) : a.scale;
     const float f = by * r_post;
-    const float back = post ? r_post * r_post * (by * whole / a.D) : 0.0f;
+    const float back = post ? r_post * r_post * (by * whole * by_columns) : 0.0f;
     if (a.gate_kind == GATE_TOKEN && r.warp == 0 && lane == 0)
       static_cast<float*>(a.grad_gate)[t] = a.scale * whole;
     const size_t at = static_cast<size_t>(t) * a.D;
@@ -510,7 +547,7 @@ __global__ __launch_bounds__(32 * (LONG ? kMaxWarps : kBlockWarps), U <= 2 ? 2 :
         for (int j = 0; j < P::kN; ++j) g[q][j] = fmaf(-k, v[j], g[q][j]);
       }
       P::store(a.grad_residual, at, col[q], lane, a.D, g[q]);
-      if (a.block != nullptr) ring.widened(stage, ROW_Y, q, v);
+      if (block) ring.widened(stage, ROW_Y, q, v);
       if (post) ring.template weight<BYTES>(a.post_weight, 0, q, col[q], a.D, w);
       if constexpr (VALUE) {
         float gate[P::kN], gg[P::kN];
@@ -657,27 +694,39 @@ int launch_fwd(NormArgs a, cudaStream_t st) {
 }
 
 // Rows on their way: as many as the blocks' shares of shared memory hold, four at most.
+template <int DT, int BYTES, int U, bool VALUE, bool LONG, bool FULL>
+cudaError_t launch_bwd_kernel(const NormArgs& a, const Split& s, int blocks, cudaStream_t st) {
+  static std::atomic<int> granted[kSmemDevs];
+  constexpr int size = stage_bytes(LONG, U, VALUE);
+  constexpr int weights = weights_kept(BYTES, LONG) ? 2 * U * (Piece<DT, BYTES>::kN / 4) * places_of(LONG) * 16 : 0;
+  constexpr int fit = ((U <= 2 ? 110 : 222) * 1024 - weights) / size;
+  constexpr int stages = fit > 4 ? 4 : fit < 1 ? 1 : fit;
+  constexpr size_t smem = static_cast<size_t>(stages) * size + weights;
+  static_assert(smem > 48 * 1024 && smem <= 222 * 1024, "opted in, and within an SM's");
+  const auto kern = norm_bwd_kernel<DT, BYTES, U, VALUE, LONG, FULL>;
+  const cudaError_t e = allow_smem(kern, smem, granted);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(blocks), dim3(32 * s.warps * s.teams), smem, st, a, stages);
+}
+
 template <int DT, int BYTES, int U, bool VALUE, bool LONG>
 cudaError_t launch_bwd_pieces(const NormArgs& a, const Split& s, int blocks, cudaStream_t st) {
-  static std::atomic<int> granted[kSmemDevs];
-  const int threads = 32 * s.warps * s.teams;
-  const int size = stage_bytes(threads, U, VALUE);
-  const int weights = BYTES == 16 ? 2 * U * Piece<DT, BYTES>::kN * 4 * 32 * s.warps : 0;
-  int stages = ((U <= 2 ? 112 : 224) * 1024 - weights) / size;
-  stages = stages > 4 ? 4 : stages < 1 ? 1 : stages;
-  const size_t smem = static_cast<size_t>(stages) * size + weights;
-  const auto kern = norm_bwd_kernel<DT, BYTES, U, VALUE, LONG>;
-  const cudaError_t e = allow_smem(kern, smem > 40 * 1024 && smem <= 48 * 1024 ? 49168 : smem, granted);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(blocks), dim3(threads), smem, st, a, stages);
+  if constexpr (BYTES == 16) {
+    if (a.pre_weight != nullptr && a.post_weight != nullptr && a.grad_sum != nullptr)
+      return launch_bwd_kernel<DT, BYTES, U, VALUE, LONG, true>(a, s, blocks, st);
+  }
+  return launch_bwd_kernel<DT, BYTES, U, VALUE, LONG, false>(a, s, blocks, st);
 }
 
 template <int DT, int BYTES, bool VALUE>
 cudaError_t launch_bwd_rows(const NormArgs& a, const Split& s, int blocks, cudaStream_t st) {
   if (s.pieces == 1) return launch_bwd_pieces<DT, BYTES, 1, VALUE, false>(a, s, blocks, st);
   if (s.pieces == 2) return launch_bwd_pieces<DT, BYTES, 2, VALUE, false>(a, s, blocks, st);
-  return s.warps <= kBlockWarps ? launch_bwd_pieces<DT, BYTES, 4, VALUE, false>(a, s, blocks, st)
-                                : launch_bwd_pieces<DT, BYTES, 4, VALUE, true>(a, s, blocks, st);
+  // (8192 bf16 columns are 32 stretches of 256, or 64 of 128 as fp32 and by single values)
+  if constexpr (Piece<DT, BYTES>::kN == 4) {
+    if (s.warps > kBlockWarps) return launch_bwd_pieces<DT, BYTES, 4, VALUE, true>(a, s, blocks, st);
+  }
+  return launch_bwd_pieces<DT, BYTES, 4, VALUE, false>(a, s, blocks, st);
 }
 
 template <int DT, int BYTES>

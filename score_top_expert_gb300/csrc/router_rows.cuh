@@ -34,6 +34,7 @@ __device__ __forceinline__ void copies_wait_group() {
 // four accesses 32 lanes apart, so that each is contiguous over the warp.
 template <int DT, int BYTES>
 struct Piece {
+  static constexpr int kBytes = BYTES;
   static constexpr int kSize = DT == DT_F32 ? 4 : 2;
   static constexpr int kEach = BYTES / kSize;                          // columns per access
   static constexpr int kAccesses = BYTES == 16 ? 1 : 4;

@@ -1,7 +1,8 @@
-// Products grouped by expert for few rows per expert (decoding), on bf16 or
+// Products grouped by expert for few rows per expert (decoding), on bf16, 8-bit or
 // 4-bit weights:
 //
 //   out[p, n] = sum_d w[e, n, d] x[row(p), d]
+//   8-bit: integers x and w, the sum times the row's and the output channel's scale
 //   4-bit: w[e, n, d] = s[e, n, g] (q[e, n, d] - z[e, n, g]),  d in group g
 //
 // The weights of the experts that have rows are the traffic and are read once
@@ -44,6 +45,12 @@
 // pairs that meet in a fragment are (i, i + 4).  Thread t of a quad takes the
 // words t V .. t V + V - 1 of each group (V = group / 32), so that a product's 16
 // columns lie in one group.
+//
+// 8-bit arithmetic.  Both operands are widened to fp16 (exact), x when it is staged, the
+// weights between shared memory and the product; a chunk of 256 columns is a sum of its own,
+// exact below 2^24.  mma.sync's own 8-bit products run at a quarter of the fp16 rate
+// (259 against 1009 multiply-adds a cycle and SM).  32 tokens, 256 experts, 8 choices, 2048 ->
+// 1024: 57 us, 4.2 TB/s of weights.
 #include <atomic>
 #include <climits>
 

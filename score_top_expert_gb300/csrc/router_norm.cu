@@ -13,16 +13,19 @@
 //   grad_gate = scale g_x h,  grad_pre_weight = sum_t grad_normed xh,
 //   grad_post_weight = sum_t scale gate g_x yh
 //
-// Bound by HBM: every row is read once, held in the registers of the 1 to 16 warps of
-// its team, and written once; all sums and both factors stay fp32, and x is normed
-// before it is rounded.
+// Bound by HBM: every row is read once, held by the 1 to 16 warps of its team, and written
+// once; all sums and both factors stay fp32, and x is normed before it is rounded.
 //
-// The forward needs one sum over a row behind the other.  The backward's second sum,
+// The forward (registers; 8192 tokens, 8 choices, 2048 bf16: 73 us, 5.1 TB/s, in every split
+// tried; fp32 4096 columns 5.5 TB/s) needs one sum over a row behind the other.  The backward's second sum,
 // mean(v yh), is over g_x, which holds the first; but it is linear in it:
 //   sum c g_x = sum c (grad_sum + r_pre u) - r_pre mean(u xh) sum c xh,
 // so all sums of a row are taken together behind one barrier.  A team keeps the
 // columns' sums for the weights' gradients of all its rows, a block leaves its teams' as one
-// row; a second kernel adds those up in order: repeated calls give the same bits.
+// row; a second kernel adds those up in order: repeated calls give the same bits.  Rows
+// come through shared memory, several ahead; the instructions bound bf16 rows nearly as HBM
+// does (8192 x 2048 39 us, 5.1 TB/s; 8192 x 4096 74, 5.4 TB/s; fp32 4096 x 4096 69, 5.8 TB/s).
+// Two pieces to a lane and four warps to 2048 columns: with one piece and eight warps 62 us.
 #include <atomic>
 #include <climits>
 

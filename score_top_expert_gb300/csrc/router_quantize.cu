@@ -3,7 +3,9 @@
 //   scale = max |x| / 127,   q = x / scale to the nearest integer, ties to even
 //
 // Bound by HBM: a row is read once, held in the registers of the 1 to 16 warps of its
-// team (of more than 64 pieces a lane's later ones are read again), and written once.
+// team (what goes beyond 16 warps' pieces is read again), and written once; a team's next
+// row is asked for before the present one is done.  8192 x 2048 bf16: 12.5 us, 4.0 TB/s;
+// 22066 x 504 9.1 us.
 //
 // The quotient is the exact one's rounding.  x (1 / scale) is off by 2^-23 of itself, 1.6e-5
 // at 127, which matters only beside a half.
@@ -196,7 +198,7 @@ int launch_pieces(QuantizeArgs a, int stretches, cudaStream_t st) {
 
 // Few rows: a piece to a lane, up to 16 warps to a row, for the latency (one row of 2048 bf16
 // 2.4 us against 3.8 with eight pieces to a lane of one warp).  Many: more pieces to
-// a lane, so fewer barriers and divisions.
+// a lane, so fewer barriers and divisions (8192 rows: one piece 27 us).
 template <int DT, int BYTES>
 int launch_typed(const QuantizeArgs& a, cudaStream_t st) {
   constexpr int columns = 32 * Piece<DT, BYTES>::kN;

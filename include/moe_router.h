@@ -428,7 +428,8 @@ MR_API int router_aux_loss_fwd_noalloc(const float* aux_scores, const uint8_t* r
  * row_stats         [T, 2] float, output for the backward, 8-byte aligned (only the
  *                   tokens of sequences are written)
  * workspace         router_balance_loss_workspace_bytes(T, E, S) bytes, 16-byte
- *                   aligned; needs no initialisation
+ *                   aligned; needs no initialisation; calls (and captured graphs) that
+ *                   overlap on the GPU need one each
  * Two kernels; repeated calls give the same bits.  T = 0 writes zeros to the loss
  * and the counts.  The backward takes the forward's logits, counts, row_stats and
  * other arguments, and writes all T rows of grad_logits [T, E] dtype; it may not
@@ -694,7 +695,8 @@ MR_API int router_combine_norm_fwd(const void* expert_out, mr_dtype dtype,
  * grad_gate     like gate, output (ignored without one)
  * grad_post_weight, grad_pre_weight  [D] float, outputs with the weight
  * workspace     router_combine_norm_bwd_workspace_bytes(T, D) bytes, 16-byte aligned,
- *               with either weight; needs no initialisation
+ *               with either weight; needs no initialisation; calls (and captured
+ *               graphs) that overlap on the GPU need one each
  * Two kernels with a weight, one without; repeated calls give the same bits.  T = 0
  * writes zeros to the weights' gradients.  Errors: as the forward.
  */

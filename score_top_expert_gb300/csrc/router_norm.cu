@@ -72,15 +72,14 @@ struct NormArgs {
 // A row's team of warps, and sums over it.
 struct RowTeam {
   int warps, team, teams, warp, lane;
-  float* cells;  // [teams, warps, kSums]
 
   __device__ __forceinline__ void sync() const {
     if (teams == 1) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(warps * 32) : "memory");
   }
 
-  // The same for three values with cells [3][kMaxWarps] of the team's own, 16-byte aligned and zero
-  // behind its warps: four warps' a read.
+  // Three values (below: one) summed over the team, with cells [3][kMaxWarps] of its own, 16-byte
+  // aligned and zero behind its warps: four warps' a read.
   __device__ __forceinline__ void sum3(float* mine, float (&v)[3]) const {
 #pragma unroll
     for (int i = 0; i < 3; ++i) v[i] = seg_sum<32>(v[i]);
@@ -98,28 +97,18 @@ struct RowTeam {
     }
   }
 
-  // N values summed over the team, the same in all its threads.  With two sets of cells in
-  // turn one barrier is enough: who writes a set has passed the barrier behind its last
-  // reading.
-  template <int N>
-  __device__ __forceinline__ void sum(float* cells_at, float (&v)[N]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = seg_sum<32>(v[i]);
-    if (warps == 1) return;
-    float* const mine = cells_at + team * warps * N;
-    if (lane < N) {
-      float mineth = v[0];
-#pragma unroll
-      for (int i = 1; i < N; ++i) mineth = lane == i ? v[i] : mineth;
-      mine[warp * N + lane] = mineth;
-    }
+  // A value summed over the team, the same in all its threads; cells: one for each warp of the
+  // block.  With two sets of cells in turn one barrier is enough: who writes a set has
+  // passed the barrier behind its last reading.
+  __device__ __forceinline__ float sum(float* cells, float v) const {
+    v = seg_sum<32>(v);
+    if (warps == 1) return v;
+    float* const mine = cells + team * warps;
+    if (lane == 0) mine[warp] = v;
     sync();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float s = 0.0f;
-      for (int w = 0; w < warps; ++w) s += mine[w * N + i];
-      v[i] = s;
-    }
+    v = 0.0f;
+    for (int w = 0; w < warps; ++w) v += mine[w];
+    return v;
   }
 };
 
@@ -269,19 +258,18 @@ __global__ __launch_bounds__(32 * (U == 4 ? kMaxWarps : kFwdWarps), U == 1 ? 4 :
   float by = a.scale;
   if (a.gate_kind == GATE_TOKEN) by *= static_cast<const float*>(a.gate)[t];
   if (a.post_weight != nullptr) {
-    float s[1] = {0.0f};
+    float s = 0.0f;
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       float w[P::kN];
       vector_at<P, BYTES>(a.post_weight, col[q], lane, a.D, w);
 #pragma unroll
       for (int j = 0; j < P::kN; ++j) {
-        s[0] = fmaf(y[q][j], y[q][j], s[0]);
+        s = fmaf(y[q][j], y[q][j], s);
         y[q][j] *= w[j];
       }
     }
-    r.sum(cells[0], s);
-    r_post = __frsqrt_rn(s[0] / a.D + a.eps);
+    r_post = __frsqrt_rn(r.sum(cells[0], s) / a.D + a.eps);
   }
   by *= r_post;
   float x[U][P::kN];
@@ -306,19 +294,18 @@ __global__ __launch_bounds__(32 * (U == 4 ? kMaxWarps : kFwdWarps), U == 1 ? 4 :
 
   // ---- the norm before the next block -----------------------------------------------------
   if (a.pre_weight != nullptr) {
-    float s[1] = {0.0f};
+    float s = 0.0f;
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       float w[P::kN];
       vector_at<P, BYTES>(a.pre_weight, col[q], lane, a.D, w);
 #pragma unroll
       for (int j = 0; j < P::kN; ++j) {
-        s[0] = fmaf(x[q][j], x[q][j], s[0]);
+        s = fmaf(x[q][j], x[q][j], s);
         x[q][j] *= w[j];
       }
     }
-    r.sum(cells[1], s);
-    r_pre = __frsqrt_rn(s[0] / a.D + a.eps);
+    r_pre = __frsqrt_rn(r.sum(cells[1], s) / a.D + a.eps);
 #pragma unroll
     for (int q = 0; q < U; ++q) {
 #pragma unroll

@@ -311,6 +311,9 @@ W8 = [
     (515, 4, 2, 257, 260, "f32", True), (70, 300, 6, 24, 40, "f32", True),
     (50, 2304, 36, 16, 32, "bf16", True), (300, 2, 2, 130, 2000, "f32", True),
     (300, 2, 2, 130, 2000, "bf16", False), (600, 3, 1, 384, 1984, "f32", True),
+    # several tiles to a CTA and more than one use of every stage, pairs and single CTAs
+    (6000, 4, 2, 600, 704, "f32", True), (3000, 40, 3, 1100, 388, "bf16", False),
+    (2000, 256, 5, 530, 1040, "bf16", True), (1500, 100, 12, 700, 120, "f32", True),
 ]
 
 

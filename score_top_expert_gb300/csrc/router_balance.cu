@@ -409,9 +409,12 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_fwd_k
 #pragma unroll
         for (int u = 0; u < 4; ++u) sums.v[j][u] = fmaf(r.v[j][u], factor, sums.v[j][u]);
     }
-    // ---- the slot of this block and sequence: the teams' sums one after the other --------
-    for (int w = 0; w < t.teams; ++w) {
-      if (t.team == w) {
+    // ---- the slot of this block and sequence: the sums of the teams that had a row of it, one
+    // after the other from the first row's ----------------------------------------------------
+    const int adding = min(hi - lo, t.teams);
+    const int place = (t.team + t.teams - (lo - t0) % t.teams) % t.teams;
+    for (int w = 0; w < adding; ++w) {
+      if (place == w) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           const int c = column_of(t, j);

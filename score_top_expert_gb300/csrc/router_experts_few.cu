@@ -50,7 +50,7 @@
 // weights between shared memory and the product; a chunk of 256 columns is a sum of its own,
 // exact below 2^24.  mma.sync's own 8-bit products run at a quarter of the fp16 rate
 // (259 against 1009 multiply-adds a cycle and SM).  32 tokens, 256 experts, 8 choices, 2048 ->
-// 1024: 57 us, 4.2 TB/s of weights.
+// 1024: 54 us, 4.5 TB/s of weights (57 with each task, its rows and scales looked up when needed).
 #include <atomic>
 #include <climits>
 
@@ -212,12 +212,40 @@ __device__ __forceinline__ Task task_of(const FewArgs& g, const int* prefix, int
   return t;
 }
 
-// 8 bits: the scale of a permuted row times that of a weight row.
-__device__ __forceinline__ float scale_of(const FewArgs& g, const Task& k, int token, int n) {
-  const int src = source_row(g.p2u, g.T, k.p0 + token);
-  return (src >= 0 ? g.x_scales[src] : 0.0f) *
-         static_cast<const float*>(g.scales)[static_cast<size_t>(k.e) * g.N + n];
-}
+// 8 bits: a task and the rows of x behind its permuted ones (-1: none), looked up by one warp
+// while the block multiplies the task before.
+struct Ahead {
+  Task task;
+  int rows[kTokens];
+
+  // The lane's entry of the map, asked for before the products and used behind them.
+  __device__ __forceinline__ static int entry(const FewArgs& g, const Task& k, int lane) {
+    return lane >= k.cnt ? -1 : g.p2u == nullptr ? k.p0 + lane : g.p2u[k.p0 + lane];
+  }
+
+  __device__ __forceinline__ void put(const FewArgs& g, const Task& k, int entry, int lane) {
+    if (lane == 0) task = k;
+    if (lane < kTokens) rows[lane] = entry < 0 ? -1 : g.p2u == nullptr ? entry : entry % g.T;
+  }
+};
+
+// 8 bits: the scales that a thread's sums take, asked for when its task begins.
+template <bool SHARED>
+struct RowScales {
+  static constexpr int kHeld = SHARED ? 1 : 2;
+  float x[kHeld], w[kHeld];
+
+  // tokens token .. token + kHeld - 1, weight rows n and (two held) n + 8
+  __device__ __forceinline__ void load(const FewArgs& g, const Ahead& k, int token, int n) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      const int src = k.rows[token + j], at = n + 8 * j;
+      x[j] = src >= 0 ? g.x_scales[src] : 0.0f;
+      w[j] = at < g.N ? static_cast<const float*>(
+                            g.scales)[static_cast<size_t>(k.task.e) * g.N + at] : 0.0f;
+    }
+  }
+};
 
 // Scales (low half) and zero points of one chunk of 16 weight rows: the quad's
 // lanes hold every fourth group of both of its rows and hand them round.
@@ -262,6 +290,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
   int* prefix = reinterpret_cast<int*>(xs + kTokens * pitch);
   __shared__ int tmp[33];
   __shared__ float part[SHARED ? kWarps : 1][kTokens][kRows + 1];
+  __shared__ Ahead ahead;  // 8 bits
 
   pdl_enter();
   const int row_tiles = (g.N + kRows - 1) / kRows;
@@ -334,8 +363,23 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
   const unsigned short* __restrict__ x = static_cast<const unsigned short*>(g.x);
   const uint8_t* const x_at = xs + gq * pitch + t * 16;
   int stage = 0;
+  if (V == 8 && warp == 0 && static_cast<int>(blockIdx.x) < tasks) {
+    const Task k = task_of(g, prefix, blockIdx.x, spans, span, row_tiles);
+    ahead.put(g, k, Ahead::entry(g, k, lane), lane);
+  }
   for (int i = blockIdx.x; i < tasks; i += gridDim.x) {
-    const Task k = task_of(g, prefix, i, spans, span, row_tiles);
+    Task k;
+    [[maybe_unused]] Task after;
+    [[maybe_unused]] int after_entry = -1;
+    const int next = i + static_cast<int>(gridDim.x);
+    const bool look = V == 8 && warp == 0 && next < tasks;
+    [[maybe_unused]] RowScales<SHARED> scales;
+    if constexpr (V == 8) {
+      __syncthreads();  // the task is known, the panel before has been read
+      k = ahead.task;
+    } else {
+      k = task_of(g, prefix, i, spans, span, row_tiles);
+    }
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     Meta<V> meta, coming;
     // this warp's tile: a span has one for each team, so that a tile's sums stay
@@ -345,15 +389,18 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
     const size_t ra = (row + min(tile * kRows + gq, g.N - 1)) * groups;
     const size_t rb = (row + min(tile * kRows + gq + 8, g.N - 1)) * groups;
     if (tile < k.last && c0 < c1) meta.template load<ZEROS>(g, ra, rb, c0, groups, t);
+    if constexpr (V == 8)
+      scales.load(g, ahead, SHARED ? member * 2 + (lane >> 4) : 2 * t,
+                  tile < k.last ? tile * kRows + (SHARED ? lane & 15 : gq) : g.N);
     for (int d0 = 0; d0 < g.D; d0 += kPanel) {
       // ---- this panel of x ---------------------------------------------------------
       const int cols = min(kPanel, g.D - d0);
       // of 8 columns, whole steps of 32 (8 bits: 64)
       const int pieces = V == 8 ? (cols + 63) / 64 * 8 : (cols + 31) / 32 * 4;
-      __syncthreads();  // the panel before has been read
+      if (V != 8 || d0 > 0) __syncthreads();  // the panel before has been read
       for (int q = threadIdx.x; q < k.cnt * pieces; q += kThreads) {
         const int token = q / pieces, at = q - token * pieces;
-        const int src = source_row(g.p2u, g.T, k.p0 + token);
+        const int src = V == 8 ? ahead.rows[token] : source_row(g.p2u, g.T, k.p0 + token);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (V == 8) {
           // piece q of a step's eight goes to thread q / 2 as its first or second
@@ -381,6 +428,10 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
         *reinterpret_cast<uint4*>(xs + token * pitch + place * 16) = v;
       }
       __syncthreads();
+      if (look && d0 + kPanel >= g.D) {
+        after = task_of(g, prefix, next, spans, span, row_tiles);
+        after_entry = Ahead::entry(g, after, lane);
+      }
 
       // ---- products ------------------------------------------------------------------
       const int b0 = max(c0, d0 / L::kPerChunk);
@@ -482,7 +533,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
             float v = sums[0][token][n];
 #pragma unroll
             for (int w = 1; w < kShare; ++w) v += sums[w][token][n];
-            if constexpr (V == 8) v *= scale_of(g, k, token, n0 + n);
+            if constexpr (V == 8) v *= scales.x[0] * scales.w[0];
             store_value(g, static_cast<size_t>(k.p0 + token) * g.N + n0 + n, v);
           }
           team_sync(team + 1);
@@ -491,13 +542,14 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
           for (int j = 0; j < 4; ++j) {
             const int token = 2 * t + (j & 1), n = n0 + gq + (j >> 1) * 8;
             if (token < k.cnt && n < g.N) {
-              if constexpr (V == 8) acc[j] *= scale_of(g, k, token, n);
+              if constexpr (V == 8) acc[j] *= scales.x[j & 1] * scales.w[j >> 1];
               store_value(g, static_cast<size_t>(k.p0 + token) * g.N + n, acc[j]);
             }
           }
         }
       }
     }
+    if (look) ahead.put(g, after, after_entry, lane);
   }
 }
 

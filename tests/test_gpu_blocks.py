@@ -314,6 +314,8 @@ W8 = [
     # several tiles to a CTA and more than one use of every stage, pairs and single CTAs
     (6000, 4, 2, 600, 704, "f32", True), (3000, 40, 3, 1100, 388, "bf16", False),
     (2000, 256, 5, 530, 1040, "bf16", True), (1500, 100, 12, 700, 120, "f32", True),
+    # few rows: several tasks to a block, rows in two parts
+    (640, 80, 1, 520, 4128, "f32", True), (600, 400, 5, 250, 48, "bf16", True),
 ]
 
 

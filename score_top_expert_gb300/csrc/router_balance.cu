@@ -251,9 +251,11 @@ struct RowRing {
     for (int i = 0; i < kRing - 1; ++i) request(a, t);
   }
 
-  // The team's next row is one of padding.
+  // The team's next row is one of padding.  Its copy is waited for like any other: the next
+  // request goes to its place, and nothing orders two copies to one place that are both under way.
   __device__ __forceinline__ void skip(const BalanceArgs& a, const Team& t) {
     request(a, t);
+    if constexpr (VEC) copies_wait_group<kRing - 1>();
     if (++taken == kRing) taken = 0;
   }
 

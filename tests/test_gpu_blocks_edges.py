@@ -1,0 +1,121 @@
+"""The operators around the routed experts where batches, scales and logits are unusual,
+against the definitions in 64 bits."""
+import numpy as np
+import pytest
+
+from blocks_cases import HALF_STEP, STEP, normals, score_error
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+DEV = "cuda:0"
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module")
+def R():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from score_top_expert_gb300 import build
+    build.build()
+    import score_top_expert_gb300.router as r
+    r.lib()
+    return r
+
+
+def up(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+    return t if dtype is None else t.to(DT[dtype])
+
+
+# ---- balance loss -------------------------------------------------------------------
+def exact_balance(x, idx, g, score, coeff, z, seq):
+    """(loss [2], counts, stats, grad, mag of grad) of sequences seq, in 64 bits; stats and
+    grad of padding are zeros."""
+    T, E = x.shape
+    K, S = idx.shape[1], len(seq) - 1
+    x = x.double()
+    n = max(seq[-1] - seq[0], 1)
+    loss = torch.zeros(2, dtype=torch.float64, device=DEV)
+    counts = torch.zeros(S, E, dtype=torch.int32, device=DEV)
+    stats = torch.zeros(T, 2, dtype=torch.float64, device=DEV)
+    grad, mag = torch.zeros_like(x), torch.zeros_like(x)
+    for s, (a, b) in enumerate(zip(seq, seq[1:])):
+        if a == b:
+            continue
+        r = x[a:b]
+        top = r.amax(1, keepdim=True)
+        total = (r - top).exp().sum(1, keepdim=True)
+        lse = top + total.log()
+        soft, sig = (r - top).exp() / total, torch.sigmoid(r)
+        norm = sig.sum(1, keepdim=True)
+        q = soft if score == "softmax" else sig / norm
+        w = soft if score == "softmax" else sig * torch.sigmoid(-r) / norm
+        stats[a:b] = torch.cat((top, total) if score == "softmax" else (norm, lse), 1)
+        chosen = idx[a:b].reshape(-1).long()
+        c = torch.bincount(chosen[(chosen >= 0) & (chosen < E)], minlength=E)
+        counts[s] = c.int()
+        c = c.double()
+        by = coeff * E / (S * K * (b - a) ** 2)
+        loss[0] += by * (q.sum(0) * c).sum()
+        loss[1] += z / n * lse.square().sum()
+        dz = g[1] * z * 2 / n * lse * soft
+        grad[a:b] = g[0] * by * w * (c - (q * c).sum(1, keepdim=True)) + dz
+        c = (c - (b - a) * K / E).abs()  # a constant less changes nothing
+        mag[a:b] = abs(g[0] * by) * w * (c + (q * c).sum(1, keepdim=True)) + dz.abs()
+    return loss, counts, stats, grad, mag
+
+
+def within(got, want, tol, name):
+    off = (got.double() - want).abs() - tol
+    assert not bool(torch.isnan(got).any()), name
+    assert float(off.max()) <= 0.0, (name, float(off.max()))
+
+
+def check_rows(x, idx, score, z, seq, out, dtype, g):
+    """Each row's kept numbers and gradient, and the counts."""
+    _, counts, stats, grad = out
+    _, want_counts, want_stats, want, mag = exact_balance(x, idx, g, score, 0.01, z, seq)
+    assert torch.equal(counts, want_counts)
+    error = score_error(x.double().cpu().numpy(), score)
+    inside = slice(seq[0], seq[-1])
+    if score == "softmax":
+        assert torch.equal(stats[inside, 0].double(), want_stats[inside, 0])  # the maximum
+    else:
+        within(stats[inside, 0], want_stats[inside, 0], error * want_stats[inside, 0], "stats")
+    if score == "softmax":
+        within(stats[inside, 1], want_stats[inside, 1], error * want_stats[inside, 1], "stats")
+    both = 2 * error + score_error(x.double().cpu().numpy(), "softmax")
+    tol = (both + 48 * STEP) * mag  # as for rows without padding
+    within(grad, want, tol + HALF_STEP[dtype] * (want.abs() + tol) + 1e-37, "grad")
+
+
+# Padding in front of the first sequence, more rows to a team than it has under way (3 at 2304
+# experts, 4 or 8 at 512): the rows behind it are not computed from those of the padding.
+@pytest.mark.parametrize("T,E,K,front,score,z,dtype", [
+    (65536, 512, 22, 100, "softmax", 1e-3, "f32"), (65536, 512, 22, 5003, "sigmoid", 0.0, "f32"),
+    (65536, 512, 22, 131, "softmax", 1e-3, "bf16"), (65536, 512, 22, 9999, "sigmoid", 1e-3, "bf16"),
+    (8192, 2304, 36, 101, "softmax", 1e-3, "f32"), (8192, 2304, 36, 3005, "sigmoid", 1e-3, "bf16"),
+    (30000, 64, 4, 70, "softmax", 0.0, "f32"), (30000, 66, 4, 70, "softmax", 1e-3, "f32"),
+])
+def test_balance_of_left_padded_batches(R, T, E, K, front, score, z, dtype):
+    gen = torch.Generator(device=DEV).manual_seed(T + E + front)
+    x = torch.randn(T, E, generator=gen, device=DEV).to(DT[dtype])
+    idx = torch.randint(0, E, (T, K), generator=gen, device=DEV, dtype=torch.int32)
+    seq = [front, front, front + 1, (front + T) // 2, T - 7, T - 7]
+    sd = torch.tensor(seq, dtype=torch.int32, device=DEV)
+    g = [0.75, 1.25]
+    first = None
+    for other in (0.0, 30.0, -5.0):  # what the padding's rows hold changes no bit
+        x[:front] = other + torch.randn(front, E, generator=gen, device=DEV).to(DT[dtype])
+        idx[:front] = torch.randint(0, E, (front, K), generator=gen, device=DEV, dtype=torch.int32)
+        loss, counts, stats = R.router_balance_loss_fwd(x, idx, score, 0.01, z, sd)
+        grad = torch.full((T, E), 77.0, dtype=DT[dtype], device=DEV)
+        R.router_balance_loss_bwd(torch.tensor(g, device=DEV), x, counts, stats, K, score, 0.01, z,
+                                  sd, grad_logits=grad)
+        got = [loss, counts, stats[front:T - 7], grad]
+        if first is None:
+            first = got
+            check_rows(x, idx, score, z, seq, (loss, counts, stats, grad), dtype, g)
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+        assert not bool(grad[:front].any()) and not bool(grad[T - 7:].any())

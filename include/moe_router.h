@@ -90,6 +90,7 @@ typedef enum {
 #define MR_MAX_GROUPS 32
 #define MR_MAX_FEATURES 65536 /* columns of the expert-side operators */
 #define MR_MAX_NORM_FEATURES 8192 /* columns of the norms around a block */
+#define MR_MAX_ROWS 2000000000    /* rows of the balance loss (T), the products (P) and the norms (T) */
 
 /*
  * router_topk_fwd — score, select and emit the top-K experts of each token.
@@ -439,7 +440,7 @@ MR_API int router_aux_loss_fwd_noalloc(const float* aux_scores, const uint8_t* r
  *   without seq_offsets, T E or T K > INT_MAX, an unknown dtype, a score_func
  *   other than MR_SOFTMAX and MR_SIGMOID, ld_indices < K, a NULL tensor that the call
  *   reads or writes, a small or misaligned workspace, misaligned row_stats.
- * MR_ERR_UNSUPPORTED: E > MR_MAX_EXPERTS, K > MR_MAX_TOPK.
+ * MR_ERR_UNSUPPORTED: E > MR_MAX_EXPERTS, K > MR_MAX_TOPK, T > MR_MAX_ROWS.
  */
 MR_API size_t router_balance_loss_workspace_bytes(int T, int E, int S);
 MR_API int router_balance_loss_fwd(const void* logits, mr_dtype dtype, const int32_t* topk_indices,
@@ -487,7 +488,8 @@ MR_API int router_balance_loss_bwd(const float* grad_loss, const void* logits, m
  *
  * MR_ERR_INVALID: a negative size, E, N, D or K < 1, unknown dtypes, a NULL
  * tensor that the call reads or writes.  MR_ERR_UNSUPPORTED: E >
- * MR_MAX_EXPERTS, K > MR_MAX_TOPK, N or D > MR_MAX_FEATURES.
+ * MR_MAX_EXPERTS, K > MR_MAX_TOPK, N or D > MR_MAX_FEATURES, in the products P >
+ * MR_MAX_ROWS.
  */
 
 /*
@@ -671,7 +673,7 @@ MR_API int router_quantize_rows(const void* x, mr_dtype dtype, int R, int D, int
  *   or gate_kind, a gate that gate_kind does not name, ld_weights < K with weights,
  *   K != 1 or weights without a map, a NULL tensor that the call reads or writes,
  *   a misaligned rstd.
- * MR_ERR_UNSUPPORTED: K > MR_MAX_TOPK, D > MR_MAX_NORM_FEATURES.
+ * MR_ERR_UNSUPPORTED: K > MR_MAX_TOPK, D > MR_MAX_NORM_FEATURES, T > MR_MAX_ROWS.
  */
 typedef enum { MR_GATE_NONE = 0, MR_GATE_TOKEN = 1, MR_GATE_VALUE = 2 } mr_gate;
 MR_API int router_combine_norm_fwd(const void* expert_out, mr_dtype dtype,

@@ -758,6 +758,7 @@ int check(int dtype, int T, int E, int K, int S, bool packed, int score_func) {
   if (static_cast<long long>(T) * E > INT_MAX || static_cast<long long>(T) * K > INT_MAX)
     return MR_ERR_INVALID;
   if (E > MR_MAX_EXPERTS || K > MR_MAX_TOPK) return MR_ERR_UNSUPPORTED;
+  if (T > MR_MAX_ROWS) return MR_ERR_UNSUPPORTED;  // (a block's rows end behind T, still as an int)
   return MR_OK;
 }
 
@@ -828,7 +829,7 @@ using namespace moe_router;
 extern "C" {
 
 size_t router_balance_loss_workspace_bytes(int T, int E, int S) {
-  if (T < 0 || E < 1 || E > MR_MAX_EXPERTS || S < 1) return 0;
+  if (T < 0 || T > MR_MAX_ROWS || E < 1 || E > MR_MAX_EXPERTS || S < 1) return 0;
   return workspace_of(T, E, S).bytes;
 }
 

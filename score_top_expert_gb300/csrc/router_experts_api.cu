@@ -17,6 +17,8 @@ int check_product(int T, int P, int E, int N, int D, bool mapped) {
   if (mapped && (T < 0 || (T == 0 && P > 0))) return MR_ERR_INVALID;
   if (E > MR_MAX_EXPERTS || N > MR_MAX_FEATURES || D > MR_MAX_FEATURES)
     return MR_ERR_UNSUPPORTED;
+  // an expert's rows and its row tiles are added up as ints
+  if (P > MR_MAX_ROWS) return MR_ERR_UNSUPPORTED;
   return MR_OK;
 }
 

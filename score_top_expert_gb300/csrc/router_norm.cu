@@ -738,6 +738,7 @@ int check(int dtype, int T, int K, int D, float eps) {
   if (T < 0 || K < 1 || D < 1 || static_cast<long long>(T) * K > INT_MAX) return MR_ERR_INVALID;
   if (!(eps > 0.0f)) return MR_ERR_INVALID;
   if (K > MR_MAX_TOPK || D > MR_MAX_NORM_FEATURES) return MR_ERR_UNSUPPORTED;
+  if (T > MR_MAX_ROWS) return MR_ERR_UNSUPPORTED;  // (rows are stepped past T as ints)
   return MR_OK;
 }
 
@@ -798,7 +799,7 @@ int router_combine_norm_fwd(const void* expert_out, mr_dtype dtype,
 }
 
 size_t router_combine_norm_bwd_workspace_bytes(int T, int D) {
-  if (T <= 0 || D < 1 || D > MR_MAX_NORM_FEATURES) return 0;
+  if (T <= 0 || T > MR_MAX_ROWS || D < 1 || D > MR_MAX_NORM_FEATURES) return 0;
   return partial_rows(T) * 2 * D * sizeof(float);
 }
 

@@ -108,6 +108,15 @@ __device__ __forceinline__ int first_sequence(const BalanceArgs& a, int t) {
   return lo;
 }
 
+// exp(x - max) of a row as 2^(x by - max by).  Where max log2 e could leave fp32's range no other
+// logit lies within 2^76 of the largest: 1 for it and 0 for the others then is exp by any factor.
+struct Shifted {
+  float by, shift;
+  __device__ __forceinline__ explicit Shifted(float top)
+      : by(fabsf(top) < 0x1p100f ? kLog2e : 1.0f), shift(top * by) {}
+  __device__ __forceinline__ float exp(float x) const { return ex2_approx(fmaf(x, by, -shift)); }
+};
+
 // Largest of a warp's values, in one instruction.
 __device__ __forceinline__ float warp_max(float v) {
   float m;
@@ -362,13 +371,14 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_fwd_k
         top = warp_max(top);
       }
       // (a warp without columns: its maximum is minus infinity, its sum zero)
-      const float own = top, shift = top == -INFINITY ? 0.0f : top * kLog2e;
+      const float own = top;
+      const Shifted from(top == -INFINITY ? 0.0f : top);
       if constexpr (SF == SF_SOFTMAX) {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            r.v[j][u] = exp_shifted(r.v[j][u], shift);
+            r.v[j][u] = from.exp(r.v[j][u]);
             total += r.v[j][u];
           }
         total = seg_sum<32>(total);
@@ -388,7 +398,7 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_fwd_k
 #pragma unroll
           for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) total += exp_shifted(r.v[j][u], shift);
+            for (int u = 0; u < 4; ++u) total += from.exp(r.v[j][u]);
           total = seg_sum<32>(total);
           t.softmax_stats(&top, &total);
           lse = top + logf(total);
@@ -643,7 +653,7 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_bwd_k
       Row<NV> r;
       ring.take(a, t, row, &r);
       const float inv = rcp_approx(SF == SF_SOFTMAX ? st.y : st.x);
-      const float shift = (SF == SF_SOFTMAX ? st.x : st.y) * kLog2e;
+      const Shifted from(SF == SF_SOFTMAX ? st.x : st.y);
       float z = 0.0f;
       if (by_z != 0.0f) z = by_z * (SF == SF_SOFTMAX ? st.x + logf(st.y) : st.y);
       // r becomes exp(x - max), q times the row's sum; sigmoid: sigma(-|x|) with the sign of
@@ -656,7 +666,7 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_bwd_k
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           if constexpr (SF == SF_SOFTMAX) {
-            r.v[j][u] = exp_shifted(r.v[j][u], shift);
+            r.v[j][u] = from.exp(r.v[j][u]);
             dot = fmaf(c.v[j][u], r.v[j][u], dot);
           } else {
             const float e = ex2_approx(-fabsf(r.v[j][u]) * kLog2e);
@@ -676,7 +686,7 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_bwd_k
         for (int u = 0; u < 4; ++u) {
           const float w = SF == SF_SOFTMAX ? r.v[j][u] : fmaf(-r.v[j][u], r.v[j][u], r.v[j][u]);
           g[u] = w * fmaf(by, c.v[j][u], less);
-          if (SF != SF_SOFTMAX && by_z != 0.0f) g[u] = fmaf(z, exp_shifted(x.v[j][u], shift), g[u]);
+          if (SF != SF_SOFTMAX && by_z != 0.0f) g[u] = fmaf(z, from.exp(x.v[j][u]), g[u]);
         }
         if (col < a.E) store4<DT, VEC>(a.grad, static_cast<size_t>(row) * a.E, col, a.E, g);
       }

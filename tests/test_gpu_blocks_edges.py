@@ -72,12 +72,21 @@ def within(got, want, tol, name):
     assert float(off.max()) <= 0.0, (name, float(off.max()))
 
 
+def errors(x, score):
+    """score_error of the logits, and of the softmax, without those whose score is zero in any
+    arithmetic (and minus infinity)."""
+    x = x.double()
+    top = x.amax(1, keepdim=True)
+    x = torch.where(x < top - 200.0, top, x).cpu().numpy()
+    return score_error(x, score), score_error(x, "softmax")
+
+
 def check_rows(x, idx, score, z, seq, out, dtype, g):
     """Each row's kept numbers and gradient, and the counts."""
     _, counts, stats, grad = out
     _, want_counts, want_stats, want, mag = exact_balance(x, idx, g, score, 0.01, z, seq)
     assert torch.equal(counts, want_counts)
-    error = score_error(x.double().cpu().numpy(), score)
+    error, soft_error = errors(x, score)
     inside = slice(seq[0], seq[-1])
     if score == "softmax":
         assert torch.equal(stats[inside, 0].double(), want_stats[inside, 0])  # the maximum
@@ -85,8 +94,7 @@ def check_rows(x, idx, score, z, seq, out, dtype, g):
         within(stats[inside, 0], want_stats[inside, 0], error * want_stats[inside, 0], "stats")
     if score == "softmax":
         within(stats[inside, 1], want_stats[inside, 1], error * want_stats[inside, 1], "stats")
-    both = 2 * error + score_error(x.double().cpu().numpy(), "softmax")
-    tol = (both + 48 * STEP) * mag  # as for rows without padding
+    tol = (2 * error + soft_error + 48 * STEP) * mag  # as for rows without padding
     within(grad, want, tol + HALF_STEP[dtype] * (want.abs() + tol) + 1e-37, "grad")
 
 
@@ -119,3 +127,59 @@ def test_balance_of_left_padded_batches(R, T, E, K, front, score, z, dtype):
             check_rows(x, idx, score, z, seq, (loss, counts, stats, grad), dtype, g)
         assert all(torch.equal(a, b) for a, b in zip(first, got))
         assert not bool(grad[:front].any()) and not bool(grad[T - 7:].any())
+
+
+# Masked experts: the type's lowest value, minus infinity, or far below the others.  At 2304 experts a
+# row is two warps': with all but 128 neighbouring experts masked one of them has none left.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score,z", [("softmax", 1e-3), ("softmax", 0.0), ("sigmoid", 1e-3),
+                                     ("sigmoid", 0.0)])
+@pytest.mark.parametrize("E,left", [(2304, range(128, 256)), (2304, range(0, 100)),
+                                    (2303, range(1300, 1400)), (512, range(7, 9)), (96, range(95, 96))])
+def test_balance_of_masked_experts(R, E, left, score, z, dtype):
+    T, K = 150, min(4, len(left))
+    x = up(normals((T, E), E, "f32"))
+    gen = torch.Generator(device=DEV).manual_seed(E)
+    idx = left[0] + torch.randint(0, len(left), (T, K), generator=gen, device=DEV, dtype=torch.int32)
+    off = torch.ones(E, dtype=torch.bool, device=DEV)
+    off[left[0]:left[-1] + 1] = False
+    for mask in (torch.finfo(DT[dtype]).min, -float("inf"), -1e4):
+        x[:, off] = mask
+        xd = x.to(DT[dtype])
+        loss, counts, stats = R.router_balance_loss_fwd(xd, idx, score, 0.01, z)
+        g = [0.75, 1.25]
+        grad = R.router_balance_loss_bwd(torch.tensor(g, device=DEV), xd, counts, stats, K, score,
+                                         0.01, z)
+        check_rows(xd, idx, score, z, [0, T], (loss, counts, stats, grad), dtype, g)
+        want = exact_balance(xd, idx, g, score, 0.01, z, [0, T])[0]
+        error, soft = errors(xd, score)
+        # 150 tokens are added up one behind the other at most; the z loss takes two errors of lse,
+        # which is below 10 and, as a mean of squares here, above 0.1
+        assert float((loss[0] - want[0]).abs()) <= (error + 150 * STEP) * float(want[0])
+        assert float((loss[1] - want[1]).abs()) <= (20 * soft + 160 * STEP) * float(want[1]) + 1e-37
+
+
+@pytest.mark.parametrize("E", [64, 1000, 2304])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_balance_of_rows_at_the_ends_of_the_type(R, dtype, E):
+    """Rows with every expert masked by the lowest value, or with logits next to the largest: the
+    softmax of equal logits, or of one above all others."""
+    T, K = 24, 2
+    x = up(normals((T, E), E, "f32"))
+    ends = torch.finfo(DT[dtype])
+    x[1] = ends.min
+    x[2] = ends.max
+    x[3] = ends.min
+    x[3, E - 1] = ends.max
+    x[4] = 2.0 ** 120
+    x[4, 5] = 2.0 ** 121
+    x[5] = -2.0 ** 99
+    x[6] = -2.0 ** 100
+    x[6, 0] = -2.0 ** 101
+    xd = x.to(DT[dtype])
+    idx = torch.arange(T * K, device=DEV, dtype=torch.int32).view(T, K) % E
+    loss, counts, stats = R.router_balance_loss_fwd(xd, idx, "softmax", 0.01)
+    grad = R.router_balance_loss_bwd(torch.ones(2, device=DEV), xd, counts, stats, K, "softmax", 0.01)
+    check_rows(xd, idx, "softmax", 0.0, [0, T], (loss, counts, stats, grad), dtype, [1.0, 1.0])
+    want = exact_balance(xd, idx, [1.0, 1.0], "softmax", 0.01, 0.0, [0, T])[0]
+    assert float((loss[0] - want[0]).abs()) <= (errors(xd, "softmax")[0] + 64 * STEP) * float(want[0])

@@ -581,7 +581,8 @@ MR_API int router_expert_matmul_w4(const void* x, const uint8_t* qweight, const 
  * average: sums of 256 terms, whatever the output.)
  *
  * x              [T, D] or [P, D] int8 (map as in router_expert_matmul)
- * x_scales       [T] or [P] float, of x's rows, e.g. from router_quantize_rows
+ * x_scales       [T] or [P] float, of x's rows, e.g. from router_quantize_rows (the sum is
+ *                multiplied by the channel's scale, then by the row's)
  * weight         [E, N, D] int8, any values
  * weight_scales  [E, N] float
  * out            [P, N] out_dtype

@@ -533,7 +533,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
             float v = sums[0][token][n];
 #pragma unroll
             for (int w = 1; w < kShare; ++w) v += sums[w][token][n];
-            if constexpr (V == 8) v *= scales.x[0] * scales.w[0];
+            if constexpr (V == 8) v = scaled_sum(v, scales.w[0], scales.x[0]);
             store_value(g, static_cast<size_t>(k.p0 + token) * g.N + n0 + n, v);
           }
           team_sync(team + 1);
@@ -542,7 +542,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
           for (int j = 0; j < 4; ++j) {
             const int token = 2 * t + (j & 1), n = n0 + gq + (j >> 1) * 8;
             if (token < k.cnt && n < g.N) {
-              if constexpr (V == 8) acc[j] *= scales.x[j & 1] * scales.w[j >> 1];
+              if constexpr (V == 8) acc[j] = scaled_sum(acc[j], scales.w[j >> 1], scales.x[j & 1]);
               store_value(g, static_cast<size_t>(k.p0 + token) * g.N + n, acc[j]);
             }
           }

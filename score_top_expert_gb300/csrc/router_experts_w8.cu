@@ -471,10 +471,10 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(by_row + c + j);
-            v[j] = __float_as_uint(__uint_as_float(v[j]) * f.x * channel);
-            v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) * f.y * channel);
-            v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) * f.z * channel);
-            v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) * f.w * channel);
+            v[j] = __float_as_uint(scaled_sum(__uint_as_float(v[j]), channel, f.x));
+            v[j + 1] = __float_as_uint(scaled_sum(__uint_as_float(v[j + 1]), channel, f.y));
+            v[j + 2] = __float_as_uint(scaled_sum(__uint_as_float(v[j + 2]), channel, f.z));
+            v[j + 3] = __float_as_uint(scaled_sum(__uint_as_float(v[j + 3]), channel, f.w));
           }
           const size_t o = static_cast<size_t>(t.start + c) * g.N + row;
           const bool whole = c + 32 <= t.cnt;

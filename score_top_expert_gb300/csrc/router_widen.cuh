@@ -1,4 +1,4 @@
-// 8-bit integers as fp16, for the products on the 16-bit tensor cores.
+// 8-bit integers as fp16, for the products on the 16-bit tensor cores, and their scales.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -22,6 +22,14 @@ __device__ __forceinline__ uint4 widen_eight(uint32_t a, uint32_t b) {
   b ^= 0x80808080u;
   return make_uint4(widen_two(a, 0x4140), widen_two(a, 0x4342), widen_two(b, 0x4140),
                     widen_two(b, 0x4342));
+}
+
+// A sum of integers with its output channel's and its row's scale, in both 8-bit kernels.  One
+// after the other: the product of the scales alone may be subnormal or infinite where the output
+// is an ordinary number (a row of 2^-126, the quantiser's smallest).  The channel's first: it is
+// a parameter of ordinary size, while a row's may lie anywhere, and the sum is a whole number.
+__device__ __forceinline__ float scaled_sum(float sum, float channel, float row) {
+  return sum * channel * row;
 }
 
 }  // namespace moe_router

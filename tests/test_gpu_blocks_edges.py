@@ -183,3 +183,35 @@ def test_balance_of_rows_at_the_ends_of_the_type(R, dtype, E):
     check_rows(xd, idx, "softmax", 0.0, [0, T], (loss, counts, stats, grad), dtype, [1.0, 1.0])
     want = exact_balance(xd, idx, [1.0, 1.0], "softmax", 0.01, 0.0, [0, T])[0]
     assert float((loss[0] - want[0]).abs()) <= (errors(xd, "softmax")[0] + 64 * STEP) * float(want[0])
+
+
+# ---- 8-bit products --------------------------------------------------------------------
+# up to eight rows an expert, 30 and 350: the kernel of few rows, single CTAs and pairs
+@pytest.mark.parametrize("T,E", [(3, 2), (40, 8), (640, 80), (60, 2), (700, 2)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_w8_of_very_small_and_very_large_rows(R, T, E, out):
+    """Scales whose product is subnormal or infinite where the output is a number."""
+    from blocks_cases import B, route
+    N, D = 72, 128
+    m = route(T, E, 1, T)
+    rng = np.random.default_rng(T)
+    x, w = rng.integers(-128, 128, (T, D)).astype(np.int8), rng.integers(-128, 128, (E, N, D)).astype(np.int8)
+    xs = rng.uniform(0.5, 1.0, T).astype(np.float32)
+    ws = rng.uniform(0.5, 1.0, (E, N)).astype(np.float32)
+    xs[0], xs[1], xs[2] = 2.0 ** -126, 8e-37, 8e35
+    xs[3:] *= np.float32(2.0) ** rng.integers(-100, 100, T - 3).astype(np.float32)
+    ws[:, ::3] *= np.float32(1e-6)
+    ws[:, 1::3] *= np.float32(1e3)
+    w[:, 1] = 0  # sums of zero stay zero beside scales of 8e35 and 1e3
+    y = R.router_expert_matmul_w8(up(x), up(xs), up(w), up(ws), up(m["off"]), up(m["p2u"]), out_dtype=DT[out])
+    got = y.double().cpu().numpy()
+    ref, mag = B.expert_matmul_w8(x, xs, w, ws, m["off"], m["p2u"], T)
+    # the sums are exact (below 2^24): two products, each rounded to 2^-24 of itself or (the second
+    # one) half the smallest number
+    tol = 2 * STEP * np.abs(ref) + 2.0 ** -150
+    if out == "bf16":
+        tol = tol + HALF_STEP[out] * (np.abs(ref) + tol) + 2.0 ** -134
+    large = np.abs(ref) > 3.38e38  # infinite, or next to it
+    assert np.isinf(got[np.abs(ref) > 3.5e38]).all() and large.any() and not large.all()
+    assert (np.abs(got - ref) <= tol)[~large].all()
+    assert not got[:, 1].any()

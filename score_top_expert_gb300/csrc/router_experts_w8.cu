@@ -16,18 +16,24 @@
 // piece asked for two stages ahead in the registers that its predecessor has just left, widened
 // and stored in the layout that the tensor cores read.  One group's stores (half of the
 // shared memory's time) pass while the other fetches and waits: with all sixteen warps on
-// each stage, 8192 tokens, 8 experts, 4096 x 4096 took 390 us.
+// each stage, 8192 tokens, 8 experts, 4096 x 4096 took 390 us where this took 365.
 //
-// In a pair each CTA's loading warps arrive on its own barrier and one warp of the second
-// CTA passes that on to the leader's by an asynchronous store: an arrival with release
-// semantics of cluster scope held it for about 1500 cycles a stage.  A tile's lookup and its
-// scales' loads are made a tile ahead: made where they were needed they took 5000 of the
-// 10400 cycles of a tile with 43 rows and four stages.
+// In a pair each CTA's loading warps arrive on its own barrier, and a warp of the second CTA that
+// waits there passes that on to the leader's by an arrival with release semantics of cluster
+// scope: what it has seen is then ordered before the products.  Such an arrival holds its warp for
+// about 1500 cycles, so each stage has a warp of its own.  (The completion of an asynchronous store
+// is ordered behind that store alone, not behind what its thread has seen: 8192 tokens, 8 experts
+// took 355 us that way, and would not have been sound.)  The second CTA's storing warps hand
+// their accumulators back in the same way, through a fourth.
+//
+// A tile's lookup and its scales' loads are made a tile ahead: made where they were needed they
+// took 5000 of the 10400 cycles of a tile with 43 rows and four stages.
 //
 // Bound by the load pipe and shared memory: a stage's loads, widened stores and the tensor
-// cores' reads are 1280 cycles of its 128 bytes a cycle, the products 1024; a stage takes 1600.
-// 8192 tokens, 8 experts, 4096 x 4096 355 us (1549 TFLOP/s), 64 experts of 2048 x 2048 228, 256
-// experts of 2048 -> 1024 278; 1003 tokens, 512 experts, 504 -> 1000, fp32 out 118 (3.1 TB/s).
+// cores' reads are 1280 cycles of its 128 bytes a cycle, the products 1024; a stage takes 1750 (1600
+// without the second CTA's arrivals, whose latency three stages do not hide).
+// 8192 tokens, 8 experts, 4096 x 4096 388 us (1417 TFLOP/s), 64 experts of 2048 x 2048 241, 256
+// experts of 2048 -> 1024 294; 1003 tokens, 512 experts, 504 -> 1000, fp32 out 118 (3.1 TB/s).
 #include <atomic>
 
 #include "router_experts_tiles.cuh"
@@ -109,14 +115,6 @@ __device__ __forceinline__ void store_wide(uint32_t at, uint32_t a, uint32_t b) 
                "r"(v.w) : "memory");
 }
 
-// One word to the other CTA of the pair, which completes four bytes on its barrier.  The
-// barrier's phase is ordered behind what this thread has seen, as by an arrival with
-// release semantics of cluster scope, but the thread goes on at once.
-__device__ __forceinline__ void announce(uint32_t word, uint32_t bar) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];"
-               ::"r"(word), "r"(1u), "r"(bar) : "memory");
-}
-
 // Waits for data that the other CTA of the pair has published.
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -140,13 +138,6 @@ __device__ __forceinline__ bool wait_cluster(const Waiter& w, uint64_t* bar, uin
   *reinterpret_cast<volatile int*>(w.gave_up) = 1;
   atomicExch(w.status, kDeviceWaitTimeout);
   return false;
-}
-
-// Arrives on a barrier of the pair's leader once the warp's tensor-memory loads are complete.
-// Relaxed: nothing else is published, and an arrival with release semantics waits for the
-// output's stores.
-__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // find_tile by a whole warp: 32 probes at a time, and divisions only for an expert of
@@ -190,8 +181,9 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
   using S = Shape<CG>;
   const TcArgs& g = args.t;
   extern __shared__ uint8_t dynamic_smem[];
-  __shared__ __align__(8) uint64_t full[kStages], peer[kStages], empty[kStages], done[2], drained[2];
-  __shared__ uint32_t tmem_at, heard;
+  __shared__ __align__(8) uint64_t full[kStages], peer[kStages], empty[kStages];
+  __shared__ __align__(8) uint64_t done[2], drained[2], read[2];
+  __shared__ uint32_t tmem_at;
   __shared__ int gave_up;
   __shared__ int tmp[33];
   __shared__ int prefix[MR_MAX_EXPERTS + 1];
@@ -210,7 +202,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&done[i], 1);
-      mbar_init(&drained[i], 4 * CG);  // one arrival per storing warp
+      mbar_init(&drained[i], 4 + (CG - 1));  // one arrival per storing warp, one for the second CTA's
+      mbar_init(&read[i], 4);                // the second CTA's storing warps
     }
     gave_up = 0;
     fence_mbar_init();
@@ -315,7 +308,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
       // An operand's stores before its next loads, one after the other: with each load right
       // behind its own piece's stores 8192 tokens and 256 experts took 285 us instead of 278 and
       // 8 experts of 4096 x 4096 368 instead of 355 (1003 tokens of 504 columns 116 instead of 118);
-      // all loads behind all stores 305 and more.
+      // all loads behind all stores 305 and more (with the asynchronous store between the CTAs).
 #pragma unroll
       for (int h = 0; h < kOwn; ++h) store_piece(at + h * 4096, a[h]);
       if (more) {
@@ -340,22 +333,37 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
         parity ^= 1;
       }
     }
-  } else if (warp == 3 && CG == 2 && rank == 1) {
-    // ---- the second CTA's stages, announced to the leader ----------------------------
+  } else if (CG == 2 && rank == 1 && warp != 2 && warp < 4) {
+    // ---- the second CTA's stages, announced to the leader, by a warp each -------------
+    const int own = warp == 3 ? 2 : warp;
     int stage = 0;
     uint32_t parity = 0;
     bool ok = true;
     for (int i = first; i < tiles && ok; i += step)
       for (int s = 0; s < slices && ok; ++s) {
-        ok = __all_sync(0xffffffffu, wait(&full[stage], parity));
-        if (!ok) break;
-        if (lane == 0)
-          announce(map_to_rank(smem_addr(&heard), 0), map_to_rank(smem_addr(&peer[stage]), 0));
-        __syncwarp();
+        if (stage == own) {
+          ok = __all_sync(0xffffffffu, wait(&full[stage], parity));
+          if (ok && lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&peer[stage]), 0));
+          __syncwarp();
+        }
         if (++stage == kStages) {
           stage = 0;
           parity ^= 1;
         }
+      }
+  } else if (CG == 2 && rank == 1 && warp == 2) {
+    // ---- its accumulators that have been read ---------------------------------------
+    int n = 0;
+    bool ok = true;
+    const int segment = segment_of<F32>(slices, kMostStages);
+    for (int i = first; i < tiles && ok; i += step)
+      for (int s0 = 0; s0 < slices && ok; s0 += segment, ++n) {
+        ok = __all_sync(0xffffffffu, wait(&read[n & 1], (n >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        tc_fence_before();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&drained[n & 1]), 0));
+        __syncwarp();
       }
   } else if (warp == 1 && rank == 0) {
     // ---- products ----------------------------------------------------------------
@@ -363,8 +371,6 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
     uint32_t parity = 0;
     bool ok = true;
     const int segment = segment_of<F32>(slices, kMostStages);
-    if (CG == 2 && lane == 0)
-      for (int i = 0; i < kStages; ++i) mbar_expect_tx_cluster(smem_addr(&peer[i]), 4);
     Tile t{};
     if (first < tiles) t = find(first);
     for (int i = first; i < tiles && ok; i += step) {
@@ -375,7 +381,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
         const int end = min(s0 + segment, slices);
         const int buf = n & 1;
         // an accumulator that the storing warps are done with
-        ok = __all_sync(0xffffffffu, wait(&drained[buf], ((n >> 1) & 1) ^ 1));
+        ok = __all_sync(0xffffffffu, CG == 2 ? wait_cluster(wait, &drained[buf], ((n >> 1) & 1) ^ 1)
+                                             : wait(&drained[buf], ((n >> 1) & 1) ^ 1));
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + buf * S::kTileB;
@@ -394,7 +401,6 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
               if (16 * k < g.D - s * kWide)
                 tc_product<CG>(d, da + by, db + by, desc, s > s0 || k > 0);
             }
-            if (CG == 2) mbar_expect_tx_cluster(smem_addr(&peer[stage]), 4);  // of its next phase
             tc_commit<CG>(&empty[stage]);
             if (s == end - 1) tc_commit<CG>(&done[buf]);
           }
@@ -461,10 +467,7 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
           if (c + 32 >= t.cnt) {  // the accumulator is free before the last stores
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              if (CG == 2 && rank == 1) mbar_arrive_relaxed(map_to_rank(smem_addr(&drained[buf]), 0));
-              else mbar_arrive(&drained[buf]);
-            }
+            if (lane == 0) mbar_arrive(CG == 2 && rank == 1 ? &read[buf] : &drained[buf]);
           }
           // scaled in place first: reads of the rows' scales between the stores wait for one
           // another (110 cycles a store)

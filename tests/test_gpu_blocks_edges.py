@@ -215,3 +215,21 @@ def test_w8_of_very_small_and_very_large_rows(R, T, E, out):
     assert np.isinf(got[np.abs(ref) > 3.5e38]).all() and large.any() and not large.all()
     assert (np.abs(got - ref) <= tol)[~large].all()
     assert not got[:, 1].any()
+
+
+@pytest.mark.parametrize("T,E,N,D", [(6000, 2, 600, 960), (3000, 40, 1100, 384), (4096, 4, 512, 128)])
+def test_w8_of_many_tiles_to_a_pair_is_exact(R, T, E, N, D):
+    """Every integer of many stages that pass between the CTAs of a pair, on data that change from
+    call to call: sums below 2^24 are exact, and a second call gives the same."""
+    per = T // E
+    off = torch.arange(E + 1, device=DEV, dtype=torch.int32) * per
+    gen = torch.Generator(device=DEV).manual_seed(D)
+    for _ in range(6):
+        x = torch.randint(-128, 128, (T, D), generator=gen, device=DEV, dtype=torch.int8)
+        w = torch.randint(-128, 128, (E, N, D), generator=gen, device=DEV, dtype=torch.int8)
+        one, ones = torch.ones(T, device=DEV), torch.ones(E, N, device=DEV)
+        y = R.router_expert_matmul_w8(x, one, w, ones, off, out_dtype=torch.float32)
+        want = torch.bmm(x.view(E, per, D).double(), w.double().transpose(1, 2)).view(T, N)
+        assert torch.equal(y.double(), want)
+        assert torch.equal(y, R.router_expert_matmul_w8(x, one, w, ones, off, out_dtype=torch.float32))
+    assert R.device_status() == 0

@@ -233,3 +233,30 @@ def test_w8_of_many_tiles_to_a_pair_is_exact(R, T, E, N, D):
         assert torch.equal(y.double(), want)
         assert torch.equal(y, R.router_expert_matmul_w8(x, one, w, ones, off, out_dtype=torch.float32))
     assert R.device_status() == 0
+
+
+# One sequence of nearly all tokens among short ones, in front, behind and between them: the
+# second kernel's warps add its slots up together.  (E 66: rows that are not aligned.)
+@pytest.mark.parametrize("T,E,K,S,place,dtype", [
+    (65536, 64, 6, 64, 0, "f32"), (65536, 64, 6, 64, 63, "bf16"), (65536, 66, 6, 80, 40, "f32"),
+    (8192, 2304, 4, 64, 5, "f32"), (30000, 130, 3, 700, 699, "f32"), (30000, 128, 3, 700, 350, "f32"),
+])
+def test_balance_of_one_long_sequence_among_short_ones(R, T, E, K, S, place, dtype):
+    gen = torch.Generator(device=DEV).manual_seed(T + S)
+    x = torch.randn(T, E, generator=gen, device=DEV).to(DT[dtype])
+    idx = torch.randint(0, E, (T, K), generator=gen, device=DEV, dtype=torch.int32)
+    short = 5
+    seq = [i * short for i in range(place + 1)] + [T - (S - 1 - i) * short for i in range(place, S)]
+    sd = torch.tensor(seq, dtype=torch.int32, device=DEV)
+    g = [0.75, 1.25]
+    loss, counts, stats = R.router_balance_loss_fwd(x, idx, "softmax", 0.01, 1e-3, sd)
+    grad = R.router_balance_loss_bwd(torch.tensor(g, device=DEV), x, counts, stats, K, "softmax", 0.01,
+                                     1e-3, sd)
+    check_rows(x, idx, "softmax", 1e-3, seq, (loss, counts, stats, grad), dtype, g)
+    want = exact_balance(x, idx, g, "softmax", 0.01, 1e-3, seq)[0]
+    # at most 256 rows behind one another in a team's sums, and some 50 additions behind those
+    error, soft = errors(x, "softmax")
+    assert float((loss[0] - want[0]).abs()) <= (error + 306 * STEP) * float(want[0])
+    assert float((loss[1] - want[1]).abs()) <= (soft + 320 * STEP) * float(want[1])
+    again = R.router_balance_loss_fwd(x, idx, "softmax", 0.01, 1e-3, sd)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], counts)

@@ -21,7 +21,11 @@
 // sums and one of counts for each sequence that its range touches ("slot": block + sequence,
 // which rises by one or more from each to the next, so no two share one).  A
 // second kernel adds a sequence's slots up in order; its last block to finish adds the
-// blocks' shares.  No floating-point atomics: repeated calls give the same bits.
+// blocks' shares.  No floating-point atomics: repeated calls give the same bits.  All sums are fp32:
+// a team's rows (256 at most, one after the other) and a block's teams plain; a warp's slots with
+// what each addition leaves over; then plain again, in trees, 32 warps' partial sums, the shares
+// (a thread's one after the other) and the ranges' z.  Remainders carried through those as well cost
+// 0.4 to 1.6 us and moved no result by a step that a test could see.
 //
 // Few warps to a row: what a row costs beside its values (two reductions, a barrier, its
 // copies' addresses) is paid once a warp.  8192 x 2304 with six warps a row and 12 logits to a

@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <climits>
+
 #include "moe_router.h"
 
 namespace moe_router {
@@ -53,6 +55,7 @@ struct W8Args {
   const int32_t* p2u;
   void* out;
   int T, P, E, N, D, out_dtype;
+  int least, most;  // rows of the experts that a launch takes
 };
 
 struct CombineArgs {
@@ -100,10 +103,11 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int P
 // expert of n rows has ceil(n / rows_per_tile).  Every thread of the block (a
 // multiple of 32 threads, at most 1024) calls it; prefix (E + 1 ints) and tmp
 // (33 ints) are in shared memory.  Thread i adds up a contiguous run of
-// experts; the runs' sums are scanned by warp shuffles.
+// experts; the runs' sums are scanned by warp shuffles.  Experts of fewer than
+// `least` or more than `most` rows have no tiles.
 __device__ __forceinline__ int expert_tile_prefix(const int32_t* __restrict__ offsets, int E,
-                                                  int P, int rows_per_tile, int* prefix,
-                                                  int* tmp) {
+                                                  int P, int rows_per_tile, int* prefix, int* tmp,
+                                                  int least = 0, int most = INT_MAX) {
   const int nthreads = blockDim.x;
   const int per = (E + nthreads - 1) / nthreads;
   const int b0 = threadIdx.x * per;
@@ -116,7 +120,8 @@ __device__ __forceinline__ int expert_tile_prefix(const int32_t* __restrict__ of
       // the expert's own range, clamped as in expert_rows
       const int hi = min(max(offsets[e + 1], 0), P);
       prefix[e] = local;
-      local += (max(hi - lo, 0) + rows_per_tile - 1) / rows_per_tile;
+      const int n = max(hi - lo, 0);
+      if (n >= least && n <= most) local += (n + rows_per_tile - 1) / rows_per_tile;
       lo = hi;
     }
   }

@@ -32,6 +32,15 @@ constexpr int kFewColumns = 512;
 // -> 1024 115 and 131.
 constexpr int kFewRowsW8 = 8;
 
+// The few-rows kernel reads an expert's weights again for every eight of its rows.  In calls of
+// more than 2^31 multiply-adds, where all rows in one expert would cost it 43 us or more, experts
+// of more than 32 rows are left to the tensor-core pipeline, in a launch of its own: 16384 rows, 2304
+// experts of 1024 x 1024 evenly 533 us (530 by the few-rows kernel alone, 595 by the pipeline alone),
+// by a power law 411 (559, 509), half of them in one expert 443 (576, 601), all of them 56 (331,
+// 54).  64 rows instead of 32: by the power law 427.
+constexpr int kHotRowsW8 = 32;
+constexpr double kHotWorkW8 = 2147483648.0;
+
 int run_product(int form, const ExpertArgs& a, mr_stream_t stream) {
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // One token's rows: 4 experts of 1024 x 1024 take 10 us here and 14 us in the
@@ -127,11 +136,18 @@ int router_expert_matmul_w8(const int8_t* x, const float* x_scales, const int8_t
       expert_first_token_offset == nullptr || out == nullptr)
     return MR_ERR_INVALID;
   const W8Args a{x, x_scales, weight, weight_scales, expert_first_token_offset,
-                 permuted_to_unpermuted, out, T, P, E, N, D, out_dtype};
+                 permuted_to_unpermuted, out, T, P, E, N, D, out_dtype, 0, INT_MAX};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return P <= kFewRowsW8 * static_cast<long long>(E) && expert_matmul_w8_few_ok(a)
-             ? launch_expert_matmul_w8_few(a, st)
-             : launch_expert_matmul_w8_tc(a, st);
+  if (P > kFewRowsW8 * static_cast<long long>(E) || !expert_matmul_w8_few_ok(a))
+    return launch_expert_matmul_w8_tc(a, st);
+  if (P > kHotRowsW8 && 1.0 * P * N * D > kHotWorkW8) {
+    W8Args hot = a, rest = a;
+    hot.least = kHotRowsW8 + 1;
+    rest.most = kHotRowsW8;
+    const int code = launch_expert_matmul_w8_tc(hot, st);
+    return code != MR_OK ? code : launch_expert_matmul_w8_few(rest, st);
+  }
+  return launch_expert_matmul_w8_few(a, st);
 }
 
 // Sizes of the combination: every row index stays below 2^31.

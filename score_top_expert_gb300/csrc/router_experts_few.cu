@@ -177,6 +177,7 @@ struct FewArgs {
   const int32_t* p2u;
   void* out;
   int T, P, E, N, D, out_dtype;
+  int most;  // 8 bits: rows of an expert, above which it is left to the tensor-core pipeline
 };
 
 __device__ __forceinline__ void store_value(const FewArgs& g, size_t i, float v) {
@@ -295,7 +296,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_few_kernel(FewArgs 
   pdl_enter();
   const int row_tiles = (g.N + kRows - 1) / kRows;
   const int spans = (row_tiles + span - 1) / span;
-  const int tasks = expert_tile_prefix(g.offsets, g.E, g.P, kTokens, prefix, tmp) * spans;
+  const int tasks = expert_tile_prefix(g.offsets, g.E, g.P, kTokens, prefix, tmp, 0,
+                                       V == 8 ? g.most : INT_MAX) * spans;
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int team = SHARED ? warp / kShare : warp, member = SHARED ? warp % kShare : 0;
@@ -591,13 +593,13 @@ bool expert_matmul_few_ok(const ExpertArgs& a) {
 
 int launch_expert_matmul_few(const ExpertArgs& a, cudaStream_t st) {
   const FewArgs g{a.a, nullptr, static_cast<const uint8_t*>(a.b), nullptr, nullptr, a.offsets, a.p2u,
-                  a.out, a.T, a.P, a.E, a.N, a.D, a.out_dtype};
+                  a.out, a.T, a.P, a.E, a.N, a.D, a.out_dtype, 0};
   return launch_typed<0, false>(g, st);
 }
 
 int launch_expert_matmul_w4(const W4Args& a, cudaStream_t st) {
   const FewArgs g{a.x, nullptr, a.q, a.scales, a.zeros, a.offsets, a.p2u, a.out, a.T, a.P, a.E, a.N, a.D,
-                  a.out_dtype};
+                  a.out_dtype, 0};
   if (a.group == 32) return a.zeros ? launch_typed<1, true>(g, st) : launch_typed<1, false>(g, st);
   if (a.group == 64) return a.zeros ? launch_typed<2, true>(g, st) : launch_typed<2, false>(g, st);
   return a.zeros ? launch_typed<4, true>(g, st) : launch_typed<4, false>(g, st);
@@ -610,7 +612,7 @@ bool expert_matmul_w8_few_ok(const W8Args& a) {
 
 int launch_expert_matmul_w8_few(const W8Args& a, cudaStream_t st) {
   const FewArgs g{a.x, a.x_scales, reinterpret_cast<const uint8_t*>(a.w), a.w_scales, nullptr,
-                  a.offsets, a.p2u, a.out, a.T, a.P, a.E, a.N, a.D, a.out_dtype};
+                  a.offsets, a.p2u, a.out, a.T, a.P, a.E, a.N, a.D, a.out_dtype, a.most};
   return launch_typed<8, false>(g, st);
 }
 

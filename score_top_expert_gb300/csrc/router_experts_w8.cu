@@ -71,6 +71,7 @@ struct W8TcArgs {
   const float* x_scales;
   const float* w_scales;
   uint32_t inv_a;  // inverse_of the weight's slices
+  int least;       // rows of an expert, below which it is left to the few-rows kernel
 };
 
 // 16 consecutive bytes of a row, VB bytes an access, of which `left` (a multiple of VB, or
@@ -212,7 +213,8 @@ __global__ __launch_bounds__(kThreads, 1) void expert_matmul_w8_kernel(const W8T
   pdl_enter();
   for (int e = threadIdx.x; e <= g.E; e += blockDim.x) offs[e] = min(max(g.offsets[e], 0), g.P);
   const int slices_a = (g.N + S::kTileA - 1) / S::kTileA;
-  const int tiles = expert_tile_prefix(g.offsets, g.E, g.P, S::kTileB, prefix, tmp) * slices_a;
+  const int tiles =
+      expert_tile_prefix(g.offsets, g.E, g.P, S::kTileB, prefix, tmp, args.least) * slices_a;
   tc_fence_before();
   if constexpr (CG == 2) cluster_sync(); else __syncthreads();
   tc_fence_after();
@@ -575,6 +577,7 @@ int launch_typed(const W8Args& a, cudaStream_t st) {
   g.w = a.w;
   g.x_scales = a.x_scales;
   g.w_scales = a.w_scales;
+  g.least = a.least;
   const long long ta = (a.N + S::kTileA - 1) / S::kTileA;
   g.inv_a = inverse_of(static_cast<int>(ta));
   const long long tb = static_cast<long long>(a.E < a.P ? a.E : a.P) + a.P / S::kTileB;

@@ -260,3 +260,40 @@ def test_balance_of_one_long_sequence_among_short_ones(R, T, E, K, S, place, dty
     assert float((loss[1] - want[1]).abs()) <= (soft + 320 * STEP) * float(want[1])
     again = R.router_balance_loss_fwd(x, idx, "softmax", 0.01, 1e-3, sd)
     assert torch.equal(again[0], loss) and torch.equal(again[1], counts)
+
+
+# Up to eight rows an expert on average with some experts of many: two kernels share the experts.
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("sizes,N,D", [
+    ((32, 33, 0, 1, 700, 31, 0, 129, 2, 64), 1024, 1008), ((1200,), 1030, 1024), ((), 2048, 512),
+    ((33,) * 40, 1000, 1024), ((300, 32, 32, 500), 600, 4096)])
+def test_w8_of_a_few_hot_experts(R, sizes, N, D, gather):
+    E = 320
+    rng = np.random.default_rng(len(sizes) + N)
+    n = rng.integers(0, 8, E)
+    n[rng.permutation(E)[:len(sizes)]] = sizes
+    P, owned = 2400, int(n.sum())
+    assert owned <= P <= 8 * E and P * N * D > 2 ** 31
+    off = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(N)
+    T = 300 if gather else P
+    x = torch.randint(-127, 128, (T, D), generator=gen, device=DEV, dtype=torch.int8)
+    w = torch.randint(-127, 128, (E, N, D), generator=gen, device=DEV, dtype=torch.int8)
+    p2u = torch.randperm(P, generator=gen, device=DEV).int() if gather else None
+    one, ones = torch.ones(T, device=DEV), torch.ones(E, N, device=DEV)
+    y = torch.full((P, N), 0.5, device=DEV)
+    R.router_expert_matmul_w8(x, one, w, ones, off, p2u, out=y, out_dtype=torch.float32)
+    rows = x[p2u.long() % T] if gather else x
+    cut = off.tolist()
+    for e in range(E):
+        a, b = cut[e], cut[e + 1]
+        want = rows[a:b].double() @ w[e].double().t()
+        if D <= 1024:  # sums below 2^24
+            assert torch.equal(y[a:b].double(), want), e
+        elif b > a:  # parts of at least 256 terms, added up in round-to-nearest
+            mag = rows[a:b].double().abs() @ w[e].double().abs().t()
+            within(y[a:b], want, (D // 256 + 1) * STEP * mag, e)
+    assert bool((y[owned:] == 0.5).all())
+    again = R.router_expert_matmul_w8(x, one, w, ones, off, p2u, out=torch.full_like(y, 0.5),
+                                      out_dtype=torch.float32)
+    assert torch.equal(y, again) and R.device_status() == 0

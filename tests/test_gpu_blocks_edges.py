@@ -297,3 +297,38 @@ def test_w8_of_a_few_hot_experts(R, sizes, N, D, gather):
     again = R.router_expert_matmul_w8(x, one, w, ones, off, p2u, out=torch.full_like(y, 0.5),
                                       out_dtype=torch.float32)
     assert torch.equal(y, again) and R.device_status() == 0
+
+
+# ---- norms ---------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,gate", [(24, "none"), (257, "token"), (2048, "value"), (4100, "token")])
+def test_norms_keep_nan_and_infinities_in_their_rows(R, D, gate, dtype):
+    """Forward and backward: the rows without one get the same bits as beside ordinary rows."""
+    T = 61
+    bad = {3: float("nan"), 17: float("inf"), 60: -float("inf")}
+    ok = torch.ones(T, dtype=torch.bool, device=DEV)
+    ok[list(bad)] = False
+    clean = {k: up(normals((T, D), 10 + i, dtype), dtype) for i, k in enumerate(("z", "res", "gs", "gn"))}
+    wpost, wpre = up(1 + 0.1 * normals((D,), 1, "f32")), up(1 + 0.1 * normals((D,), 2, "f32"))
+    g = {"none": None, "token": up(np.abs(normals((T,), 3, "f32"))),
+         "value": up(normals((T, D), 3, dtype), dtype)}[gate]
+
+    def run(t):
+        x, n, y, r = R.router_combine_norm_fwd(t["z"], t["res"], post_weight=wpost, gate=g,
+                                               residual_scale=0.5, pre_weight=wpre, save=True)
+        gb, gr, gg, _, _ = R.router_combine_norm_bwd(t["gs"], t["gn"], y, x, r, post_weight=wpost, gate=g,
+                                                     residual_scale=0.5, pre_weight=wpre)
+        return [v for v in (x, n, y, r, gb, gr, gg) if v is not None]
+
+    want = run(clean)
+    for name in clean:
+        dirty = dict(clean)
+        dirty[name] = clean[name].clone()
+        for row, value in bad.items():
+            dirty[name][row, (row * 7) % D] = value
+        got = run(dirty)
+        for a, b in zip(want, got):
+            assert torch.equal(a[ok], b[ok]), name
+        # and where they are they show: x for the forward's inputs, the residual's gradient behind
+        shown = got[0] if name in ("z", "res") else got[5]
+        assert not bool(torch.isfinite(shown[~ok]).all(1).any()), name

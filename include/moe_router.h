@@ -578,7 +578,7 @@ MR_API int router_expert_matmul_w4(const void* x, const uint8_t* qweight, const 
  * Products are exact.  So are sums below 2^24 in any order, and with fp32 outputs
  * segments of at most 960 terms, added up in round-to-nearest; a bf16 output is
  * one sum, above 2^24 rounded as a bf16 product's.  (Up to eight rows an expert on
- * average, for experts of up to 32: sums of 256 terms, whatever the output.)  One
+ * average, for experts of up to 128: sums of 256 terms, whatever the output.)  One
  * kernel, or two that share the experts.
  *
  * x              [T, D] or [P, D] int8 (map as in router_expert_matmul)

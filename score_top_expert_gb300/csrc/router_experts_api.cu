@@ -34,11 +34,13 @@ constexpr int kFewRowsW8 = 8;
 
 // The few-rows kernel reads an expert's weights again for every eight of its rows.  In calls of
 // more than 2^31 multiply-adds, where all rows in one expert would cost it 43 us or more, experts
-// of more than 32 rows are left to the tensor-core pipeline, in a launch of its own: 16384 rows, 2304
-// experts of 1024 x 1024 evenly 533 us (530 by the few-rows kernel alone, 595 by the pipeline alone),
-// by a power law 411 (559, 509), half of them in one expert 443 (576, 601), all of them 56 (331,
-// 54).  64 rows instead of 32: by the power law 427.
-constexpr int kHotRowsW8 = 32;
+// of more rows than a tile holds are left to the tensor-core pipeline, in a launch of its own.
+// 16384 rows, 2304 experts of 1024 x 1024, us by both, the few-rows kernel alone, the pipeline alone:
+// evenly 536, 532, 595; by a power law 455, 563, 509; half of them in one expert 443, 580, 601; all
+// of them 57, 331, 54.  1024 rows, 128 experts of 4096 -> 1024, where a long tile has nothing beside
+// it, by both and the few-rows kernel: 109, 107; 132, 124; 125, 127; 29, 74.  From 32 rows instead:
+// 411 by the power law at 2304 experts, but 123 for 107 with slightly uneven ones at 4096 -> 1024.
+constexpr int kHotRowsW8 = 128;
 constexpr double kHotWorkW8 = 2147483648.0;
 
 int run_product(int form, const ExpertArgs& a, mr_stream_t stream) {

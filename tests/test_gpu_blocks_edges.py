@@ -265,8 +265,8 @@ def test_balance_of_one_long_sequence_among_short_ones(R, T, E, K, S, place, dty
 # Up to eight rows an expert on average with some experts of many: two kernels share the experts.
 @pytest.mark.parametrize("gather", [True, False])
 @pytest.mark.parametrize("sizes,N,D", [
-    ((32, 33, 0, 1, 700, 31, 0, 129, 2, 64), 1024, 1008), ((1200,), 1030, 1024), ((), 2048, 512),
-    ((33,) * 40, 1000, 1024), ((300, 32, 32, 500), 600, 4096)])
+    ((32, 33, 0, 1, 600, 31, 0, 129, 2, 128), 1024, 1008), ((1200,), 1030, 1024), ((), 2048, 512),
+    ((33,) * 40, 1000, 1024), ((300, 128, 127, 500), 600, 4096)])
 def test_w8_of_a_few_hot_experts(R, sizes, N, D, gather):
     E = 320
     rng = np.random.default_rng(len(sizes) + N)

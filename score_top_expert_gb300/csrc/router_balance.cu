@@ -32,8 +32,9 @@
 // lane took 242 instructions a warp and row, 29 us.
 //
 // Backward: the same ranges; a team keeps its sequence's counts in registers.  They
-// enter as c_sj - K n_s / E: a constant less changes nothing, since q sums to one,
-// and leaves the difference c_sj - sum c q without the cancellation of two large numbers.
+// enter less the whole part of K n_s / E: a constant less changes nothing, since q sums to one,
+// and leaves the difference c_sj - sum c q without the cancellation of two large numbers (in
+// integers: a count above 2^24 is no fp32 number).
 #include <atomic>
 #include <climits>
 
@@ -693,7 +694,8 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_bwd_k
   for (int s = first_s, p = t0; s < a.S && p < t1; ++s) {
     int lo, hi;
     sequence_range(a, s, &lo, &hi);
-    const float tokens = static_cast<float>(hi - lo);
+    const int all = hi - lo;
+    const float tokens = static_cast<float>(all);
     lo = max(lo, p);
     hi = min(hi, t1);
     if (lo >= t1) break;
@@ -701,7 +703,7 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_bwd_k
     p = hi;
     clear(lo);
     const float scale = by_balance * (static_cast<float>(a.E) / a.K) / tokens / tokens;
-    const float mean = tokens * a.K / a.E;
+    const int mean = static_cast<int>(static_cast<long long>(all) * a.K / a.E);
     Row<NV> c;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -709,7 +711,7 @@ __global__ __launch_bounds__(threads_of(NV), NV <= 4 ? 3 : 2) void balance_bwd_k
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         c.v[j][u] = col + u < a.E
-                        ? static_cast<float>(a.counts[static_cast<size_t>(s) * a.E + col + u]) - mean
+                        ? static_cast<float>(a.counts[static_cast<size_t>(s) * a.E + col + u] - mean)
                         : 0.0f;
     }
     float2 next_st = row < hi ? a.stats[row] : make_float2(0.0f, 1.0f);

@@ -185,6 +185,27 @@ def test_balance_of_rows_at_the_ends_of_the_type(R, dtype, E):
     assert float((loss[0] - want[0]).abs()) <= (errors(xd, "softmax")[0] + 64 * STEP) * float(want[0])
 
 
+def test_balance_gradient_of_counts_above_2_to_the_24(R):
+    """Two experts that are chosen nearly alike by 40 million tokens: the gradient is of the
+    difference of two counts that fp32 does not hold."""
+    T, E = 40_000_000, 2
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.rand(T, E, generator=gen, device=DEV)
+    idx = torch.zeros(T, 1, dtype=torch.int32, device=DEV)
+    idx[:T // 2 - 501] = 1
+    _, counts, stats = R.router_balance_loss_fwd(x, idx, "softmax", 1.0)
+    assert counts.tolist() == [[T // 2 + 501, T // 2 - 501]]
+    grad = R.router_balance_loss_bwd(torch.tensor([1e12, 0.0], device=DEV), x, counts, stats, 1, "softmax", 1.0)
+    error = score_error(np.array([[0.0, 1.0]]), "softmax")  # logits within one of each other
+    for a in range(0, T, 8_000_000):
+        q = x[a:a + 8_000_000].double().softmax(1)
+        c = torch.tensor([501.0, -501.0], dtype=torch.float64, device=DEV)  # less their mean
+        by = 1e12 * E / T ** 2
+        inner = (q * c).sum(1, keepdim=True)
+        mag = by * q * (c.abs() + (q * c.abs()).sum(1, keepdim=True))
+        within(grad[a:a + 8_000_000], by * q * (c - inner), (3 * error + 48 * STEP) * mag, "grad")
+
+
 # ---- 8-bit products --------------------------------------------------------------------
 # up to eight rows an expert, 30 and 350: the kernel of few rows, single CTAs and pairs
 @pytest.mark.parametrize("T,E", [(3, 2), (40, 8), (640, 80), (60, 2), (700, 2)])

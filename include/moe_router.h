@@ -417,7 +417,10 @@ MR_API int router_aux_loss_fwd_noalloc(const float* aux_scores, const uint8_t* r
  *   loss[0] = coeff / S sum_s E / (K n_s^2) sum_e c_se P_se
  *   loss[1] = z_coeff / n sum_t (log sum_e exp x_te)^2,  n = sum_s n_s
  * (a sequence without tokens adds zero; for one sequence of all tokens loss[0] is
- * router_aux_loss_fwd's).  The counts carry no gradient:
+ * router_aux_loss_fwd's).  A masked expert's logit may be the type's lowest value.
+ * A row whose sigmoids are all below 2^-126 (logits below -87) has no fp32 sum, here
+ * as in router_aux_scores_fwd: its losses and gradients are NaN.  The counts carry
+ * no gradient:
  *   grad_x_tj = grad_loss[0] coeff / S E / (K n_s^2) sum_e (c_se) dq_te/dx_tj
  *             + grad_loss[1] z_coeff 2 lse_t / n softmax(x_t)_j
  *
@@ -576,7 +579,7 @@ MR_API int router_expert_matmul_w4(const void* x, const uint8_t* qweight, const 
  *   out[p, n] = x_scales[row(p)] weight_scales[e, n]
  *               sum_d weight[e, n, d] x[row(p), d]
  * Products are exact.  So are sums below 2^24 in any order, and with fp32 outputs
- * segments of at most 960 terms, added up in round-to-nearest; a bf16 output is
+ * segments of at most 896 terms, added up in round-to-nearest; a bf16 output is
  * one sum, above 2^24 rounded as a bf16 product's.  (Up to eight rows an expert on
  * average, for experts of up to 128: sums of 256 terms, whatever the output.)  One
  * kernel, or two that share the experts.
@@ -658,7 +661,9 @@ MR_API int router_quantize_rows(const void* x, mr_dtype dtype, int R, int D, int
  *   x = residual + residual_scale gate h
  *   n = x / sqrt(mean(x^2) + eps) pre_weight       (only with pre_weight)
  * all in fp32; x and y are rounded once, where they are stored, and n is of the
- * unrounded x.
+ * unrounded x.  (A row whose squares add up to more than fp32 holds, values of about
+ * 1e19, has a factor of 0.)  NaN and infinities stay in their rows; the weights'
+ * gradients are sums over all rows.
  *
  * expert_out    [T K, D] (or [T, D]) dtype, residual [T, D] dtype
  * post_weight, pre_weight  [D] float or NULL

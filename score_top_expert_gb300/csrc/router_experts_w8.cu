@@ -4,9 +4,9 @@
 //   out[p, n] = x_scales[row(p)] weight_scales[e, n] sum_d weight[e, n, d] x[row(p), d]
 //
 // sm_103a's tcgen05 has no integer products.  An 8-bit integer is exact in fp16, a product
-// of two in fp32, and a sum of 960 of them stays below 2^24: so the operands are widened to
-// fp16 on their way to shared memory and multiplied at the 16-bit rate.  A fp32 output is
-// summed in segments of at most 960 terms, each exact; a bf16 output is one sum, exact
+// of two in fp32, and a sum of 896 of them (seven stages) stays below 2^24: so the operands are
+// widened to fp16 on their way to shared memory and multiplied at the 16-bit rate.  A fp32 output
+// is summed in segments of at most 896 terms, each exact; a bf16 output is one sum, exact
 // while it stays below 2^24 (and off by about 2^-30 of its value a term above that).
 //
 // The tiles and their order are those of router_experts_tc.cu's forward: 128 or 256 weight

@@ -16,8 +16,9 @@
 // Bound by HBM: every row is read once, held by the 1 to 16 warps of its team, and written
 // once; all sums and both factors stay fp32, and x is normed before it is rounded.
 //
-// The forward (registers; 8192 tokens, 8 choices, 2048 bf16: 73 us, 5.1 TB/s, in every split
-// tried; fp32 4096 columns 5.5 TB/s) needs one sum over a row behind the other.  The backward's second sum,
+// The forward (registers, of which rows of one piece to a lane spill 12 to 48 bytes a thread at 64; 8192
+// tokens, 8 choices, 2048 bf16: 73 us, 5.1 TB/s, in every split tried, three to five blocks an SM
+// alike; fp32 4096 columns 5.5 TB/s) needs one sum over a row behind the other.  The backward's second sum,
 // mean(v yh), is over g_x, which holds the first; but it is linear in it:
 //   sum c g_x = sum c (grad_sum + r_pre u) - r_pre mean(u xh) sum c xh,
 // so all sums of a row are taken together behind one barrier.  A team keeps the
@@ -61,7 +62,7 @@ struct NormArgs {
   void* grad_block;          // [T, D]
   void* grad_residual;       // [T, D]
   void* grad_gate;           // like gate
-  float* partial;            // [teams, 2, D]
+  float* partial;            // [blocks, 2, D]
   float* grad_post;          // [D]
   float* grad_pre;           // [D]
   long long ld_w;

@@ -353,3 +353,54 @@ def test_norms_keep_nan_and_infinities_in_their_rows(R, D, gate, dtype):
         # and where they are they show: x for the forward's inputs, the residual's gradient behind
         shown = got[0] if name in ("z", "res") else got[5]
         assert not bool(torch.isfinite(shown[~ok]).all(1).any()), name
+
+
+# ---- captured -------------------------------------------------------------------------------
+def test_replays_follow_the_offsets(R):
+    """What the kernels decide on the device (hot experts, a long sequence, padding in front) is
+    decided again by each replay: a graph captured on even batches, two replays under way at once."""
+    E, P, N, D, T, S, K = 320, 2400, 1024, 1008, 20000, 64, 4
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randint(-127, 128, (P, D), generator=gen, device=DEV, dtype=torch.int8)
+    w = torch.randint(-127, 128, (E, N, D), generator=gen, device=DEV, dtype=torch.int8)
+    xs = torch.rand(P, generator=gen, device=DEV)
+    ws = torch.rand(E, N, generator=gen, device=DEV)
+    logits = torch.randn(T, 64, generator=gen, device=DEV)
+    idx = torch.randint(0, 64, (T, K), generator=gen, device=DEV, dtype=torch.int32)
+    hot = np.full(E, 2)
+    hot[[7, 200]] = 1100, 400
+    offsets = [np.concatenate([[0], np.cumsum(n)]).clip(max=P) for n in (np.full(E, 7), hot, np.eye(E)[9] * P)]
+    seqs = [np.arange(S + 1) * (T // S), np.concatenate([[500], 600 + 5 * np.arange(S - 1), [T - 3]]),
+            np.concatenate([[0], T - 5 * np.arange(S - 1, -1, -1)])]
+    states = [(up(offsets[0]).int(), up(seqs[0]).int()) for _ in range(2)]
+    one = torch.ones(2, device=DEV)
+
+    def call(off, seq):
+        y = R.router_expert_matmul_w8(x, xs, w, ws, off)
+        loss, counts, stats = R.router_balance_loss_fwd(logits, idx, "softmax", 0.01, 1e-3, seq)
+        return y, loss, counts, R.router_balance_loss_bwd(one, logits, counts, stats, K, "softmax", 0.01,
+                                                          1e-3, seq)
+
+    call(*states[0])
+    graphs, held = [], []
+    for state in states:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(call(*state))
+    side = torch.cuda.Stream()
+    for a, b in ((0, 1), (1, 2), (2, 0)):
+        want = []
+        for (off, seq), i in zip(states, (a, b)):
+            off.copy_(up(offsets[i]))
+            seq.copy_(up(seqs[i]))
+            want.append(call(off, seq))
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for got, exp, i in zip(held, want, (a, b)):
+            owned = int(offsets[i][-1])
+            assert torch.equal(got[0][:owned], exp[0][:owned])
+            assert all(torch.equal(p, q) for p, q in zip(got[1:], exp[1:]))
+    assert R.device_status() == 0
